@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmoeq.so")
 SOURCES = ["moeq_api.cu", "moeq_stream.cu", "moeq_stream_mma.cu", "moeq_token.cu", "moeq_mtok.cu", "moeq_tp.cu", "moeq_quant.cu",
-           "moeq_route.cu"]
+           "moeq_route.cu", "moeq_rows_api.cu", "moeq_rows.cu", "moeq_mx4.cu", "moeq_mx4_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "-I", os.path.join(ROOT, "include")]

@@ -1,0 +1,567 @@
+// Operators on any number of tokens around the experts' products: the
+// router's top-k and its gradient, the stable sort of (token, slot) pairs by
+// expert, and the movement of rows to expert order and back, with gradients.
+// All of them move each byte once; what bounds them is HBM (large) or the
+// launch (small).
+#include <cooperative_groups.h>
+#include <float.h>
+
+#include "moeq_device.cuh"
+#include "moeq_rows.h"
+
+namespace moeq {
+namespace cg = cooperative_groups;
+namespace {
+
+constexpr int kMaxK = MOEQ_MAX_TOPK;
+
+// --------------------------------------------------------------- elements
+__device__ __forceinline__ void st1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void st1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Eight consecutive elements, as they sit in memory (raw) and as floats.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
+    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        a = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void store(float* p) const {
+        reinterpret_cast<float4*>(p)[0] = a;
+        reinterpret_cast<float4*>(p)[1] = b;
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+        a = make_float4(v[0], v[1], v[2], v[3]);
+        b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+// One element, for widths and addresses that eight at a time do not fit.
+template <typename T>
+struct Raw1 {
+    T a;
+    __device__ __forceinline__ void load(const T* p) { a = __ldg(p); }
+    __device__ __forceinline__ void store(T* p) const { *p = a; }
+    __device__ __forceinline__ void zero() { st1(&a, 0.f); }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = static_cast<float>(a); }
+    __device__ __forceinline__ void set(const float (&v)[1]) { st1(&a, v[0]); }
+};
+template <typename T, int V>
+struct RawOf {
+    using type = Raw1<T>;
+};
+template <typename T>
+struct RawOf<T, 8> {
+    using type = Raw8<T>;
+};
+template <typename T, int V>
+using Raw = typename RawOf<T, V>::type;
+
+// ------------------------------------------------------------------ router
+// A logit as an unsigned key that orders as the logit does; 0 for one that
+// is never picked (-inf, NaN).  +inf counts as the largest finite number, so
+// that the softmax over the picks stays finite.
+__device__ __forceinline__ uint32_t logit_key(float f) {
+    if (!(f > -INFINITY)) return 0u;
+    const uint32_t u = __float_as_uint(fminf(f, FLT_MAX) + 0.0f);  // -0 folds onto +0
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float logit_of_key(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+// One warp a row: lane l holds the keys of experts l, l + 32, ...; a round
+// takes the largest key and the lowest id that holds it (two warp
+// reductions), and lane j keeps round j's pick for the softmax.
+template <int NPER>
+__global__ void __launch_bounds__(128) route_rows_kernel(const float* __restrict__ logits, int64_t ld, int T, int E,
+                                                         int k, int32_t* __restrict__ id, float* __restrict__ w) {
+    const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (t >= T) return;
+    const float* row = logits + t * ld;
+    uint32_t key[NPER];
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+        const int e = lane + 32 * i;
+        key[i] = e < E ? logit_key(__ldg(row + e)) : 0u;
+    }
+    int my_id = -1;
+    float my_v = 0.f;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = key[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < NPER; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (!top) break;  // nothing left that may be picked
+        const int e = __reduce_min_sync(0xffffffffu, best == top ? lane + 32 * at : 0x7fffffff);
+        if ((e & 31) == lane) {
+#pragma unroll
+            for (int i = 0; i < NPER; ++i)
+                if (i == (e >> 5)) key[i] = 0u;
+        }
+        if (lane == j) {
+            my_id = e;
+            my_v = logit_of_key(top);
+        }
+    }
+    const float v0 = __shfl_sync(0xffffffffu, my_v, 0);
+    const float p = my_id >= 0 ? expf(my_v - v0) : 0.f;
+    float sum = p;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane < k) {
+        id[static_cast<int64_t>(t) * k + lane] = my_id;
+        w[static_cast<int64_t>(t) * k + lane] = my_id >= 0 ? __fdiv_rn(p, sum) : 0.f;
+    }
+}
+
+// dl[id_j] = w_j (dw_j - sum_i w_i dw_i), zero elsewhere.  One warp a row:
+// zeros first, then the picks (ordered by the warp barrier).
+__global__ void __launch_bounds__(128) route_rows_grad_kernel(const float* __restrict__ dw,
+                                                              const int32_t* __restrict__ id,
+                                                              const float* __restrict__ w, int T, int E, int k,
+                                                              float* __restrict__ dl, int64_t ld, int vec) {
+    const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (t >= T) return;
+    float* row = dl + t * ld;
+    float g = 0.f, p = 0.f;
+    int e = -1;
+    if (lane < k) {
+        const int64_t i = static_cast<int64_t>(t) * k + lane;
+        e = id[i];
+        p = w[i];
+        g = dw[i];
+    }
+    const bool live = e >= 0 && e < E;
+    float s = live ? p * g : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (vec) {
+        for (int c = lane * 4; c < E; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+        for (int c = lane; c < E; c += 32) row[c] = 0.f;
+    }
+    __syncwarp();
+    if (live) row[e] = p * (g - s);
+}
+
+// -------------------------------------------------------------------- sort
+// Stable counting sort of the pairs by expert in ONE launch: one cluster of
+// CTAs, each warp owning a contiguous run of pairs.
+//   1 each warp counts its run's experts (shared memory, its own bins);
+//   2 the bins are scanned over the CTA's warps, over the cluster's CTAs
+//     (their totals read through distributed shared memory) and over the
+//     experts, which gives every warp its first row of every expert;
+//   3 each warp walks its run again, 32 pairs at a time: the rank among
+//     equal experts in the 32 comes from a match, so the order is the pairs'.
+// No atomic decides an order, so the result is the same every time.
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+
+__global__ void __launch_bounds__(kSortThreads) expert_sort_kernel(const int32_t* __restrict__ id, int P, int E,
+                                                                   int warps, int run, int32_t* __restrict__ offs,
+                                                                   int32_t* __restrict__ pair_row,
+                                                                   int32_t* __restrict__ row_pair) {
+    extern __shared__ int sm[];
+    int* bins = sm;                // [warps][E]
+    int* total = sm + warps * E;   // [E] this CTA's counts
+    int* first = total + E;        // [E] first row of each expert
+    __shared__ int scan[kSortWarps + 1];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = cluster.block_rank(), ctas = cluster.num_blocks();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    for (int i = tid; i < warps * E; i += kSortThreads) bins[i] = 0;
+    __syncthreads();
+    const int64_t p0 = (static_cast<int64_t>(rank) * warps + warp) * run;
+    const int64_t p1 = min(p0 + run, static_cast<int64_t>(P));
+    int* mine = bins + warp * E;
+    if (warp < warps) {
+        for (int64_t p = p0 + lane; p < p1; p += 32) {
+            const int e = __ldg(id + p);
+            if (e >= 0 && e < E) atomicAdd(mine + e, 1);
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += kSortThreads) {
+        int run_sum = 0;
+        for (int i = 0; i < warps; ++i) {
+            const int c = bins[i * E + e];
+            bins[i * E + e] = run_sum;
+            run_sum += c;
+        }
+        total[e] = run_sum;
+    }
+    cluster.sync();
+    // One expert a thread (E <= MOEQ_MAX_EXPERTS = kSortThreads).
+    int before = 0, all = 0;
+    if (tid < E) {
+        for (int c = 0; c < ctas; ++c) {
+            const int v = cluster.map_shared_rank(total, c)[tid];
+            if (c < rank) before += v;
+            all += v;
+        }
+    }
+    int inc = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        int v = scan[lane];
+        const int own = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        scan[lane] = v - own;
+        if (lane == 31) scan[32] = v;
+    }
+    __syncthreads();
+    const int kept = scan[kSortWarps];
+    if (tid < E) {
+        const int start = scan[warp] + inc - all;
+        first[tid] = start + before;
+        if (rank == 0) offs[tid] = start;
+    }
+    if (rank == 0 && tid == 0) offs[E] = kept;
+    cluster.sync();  // every CTA has read this one's totals; first[] is written
+    if (warp < warps) {
+        for (int e = lane; e < E; e += 32) mine[e] += first[e];
+        __syncwarp();
+        for (int64_t b = p0; b < p1; b += 32) {
+            const int64_t p = b + lane;
+            int e = p < p1 ? __ldg(id + p) : -1;
+            if (e < 0 || e >= E) e = -1;
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            const int ahead = __popc(same & ((1u << lane) - 1u));
+            int row = -1;
+            if (e >= 0) row = mine[e] + ahead;
+            __syncwarp();
+            if (e >= 0 && ahead == 0) mine[e] += __popc(same);
+            __syncwarp();
+            if (p < p1) pair_row[p] = row;
+            if (row >= 0) row_pair[row] = static_cast<int32_t>(p);
+        }
+    }
+    for (int64_t r = kept + static_cast<int64_t>(rank) * kSortThreads + tid; r < P;
+         r += static_cast<int64_t>(ctas) * kSortThreads)
+        row_pair[r] = -1;
+}
+
+// ------------------------------------------------------------------ gather
+// xs[pair_row[t, j]] = x[t].  Token-major: each of x's elements is read once
+// and written to its rows (reading row-major would read it top_k times).
+// Blocks past the tokens' zero the rows from offs[E] on.
+constexpr int kTailBlocks = 64;
+
+template <typename T, int V>
+__global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ x, int64_t ld_x, int nt, int H, int k,
+                                                          const int32_t* __restrict__ offs, int E, int64_t R,
+                                                          const int32_t* __restrict__ pair_row, T* __restrict__ xs,
+                                                          int64_t ld_xs) {
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    if (c >= H) return;
+    if (blockIdx.x < nt) {
+        const int64_t t = blockIdx.x;
+        Raw<T, V> v;
+        v.load(x + t * ld_x + c);
+        const int32_t* pr = pair_row + t * k;
+        for (int j = 0; j < k; ++j) {
+            const int r = __ldg(pr + j);
+            if (r >= 0 && r < R) v.store(xs + r * ld_xs + c);
+        }
+    } else {
+        Raw<T, V> z;
+        z.zero();
+        for (int64_t r = max(__ldg(offs + E), 0) + (blockIdx.x - nt); r < R; r += kTailBlocks)
+            z.store(xs + r * ld_xs + c);
+    }
+}
+
+// ----------------------------------------------------------------- combine
+// out[t] = base[t] + sum_j w[t, j] y[pair_row[t, j]], fp32 in slot order
+// (the base first), rounded once.  Each thread holds the loads of up to
+// eight rows in flight; slots without a row add nothing.
+template <typename TY, typename TO, int V, bool kWeighted>
+__global__ void __launch_bounds__(256) combine_rows_kernel(const TY* __restrict__ y, int64_t ld_y, int H, int k,
+                                                           int64_t R, const int32_t* __restrict__ pair_row,
+                                                           const float* __restrict__ w, const TO* __restrict__ base,
+                                                           int64_t ld_base, TO* __restrict__ out, int64_t ld_out) {
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    if (c >= H) return;
+    const int64_t t = blockIdx.x;
+    const int32_t* pr = pair_row + t * k;
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    if (base) {
+        Raw<TO, V> b;
+        b.load(base + t * ld_base + c);
+        b.get(acc);
+    }
+    for (int j0 = 0; j0 < k; j0 += 8) {
+        Raw<TY, V> v[8];
+        float ww[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            ww[j] = 0.f;
+            v[j].zero();
+            if (j0 + j < k) {
+                const int r = __ldg(pr + j0 + j);
+                if (r >= 0 && r < R) {
+                    v[j].load(y + r * ld_y + c);
+                    ww[j] = kWeighted ? __ldg(w + t * k + j0 + j) : 1.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float f[V];
+            v[j].get(f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(ww[j], f[i], acc[i]);
+        }
+    }
+    Raw<TO, V> o;
+    o.set(acc);
+    o.store(out + t * ld_out + c);
+}
+
+// ---------------------------------------------------------- combine's grad
+// dy[pair_row[t, j]] = w[t, j] dout[t] and dw[t, j] = <dout[t], y[..]>: one
+// block a token, so that dout is read once for all its slots and the dot
+// products end in one block reduction (a fixed tree).  Blocks past the
+// tokens' zero the rows of dy from offs[E] on.
+template <typename TY, typename TO, int V, int KM>
+__global__ void __launch_bounds__(256) combine_rows_grad_kernel(
+    const TO* __restrict__ dout, int64_t ld_do, const TY* __restrict__ y, int64_t ld_y, int nt, int H, int k,
+    const int32_t* __restrict__ offs, int E, int64_t R, const int32_t* __restrict__ pair_row,
+    const float* __restrict__ w, TY* __restrict__ dy, int64_t ld_dy, float* __restrict__ dw) {
+    const int tid = threadIdx.x;
+    if (blockIdx.x >= nt) {
+        Raw<TY, V> z;
+        z.zero();
+        for (int64_t r = max(__ldg(offs + E), 0) + (blockIdx.x - nt); r < R; r += kTailBlocks)
+            for (int c = tid * V; c < H; c += blockDim.x * V) z.store(dy + r * ld_dy + c);
+        return;
+    }
+    __shared__ float red[8][KM];
+    const int64_t t = blockIdx.x;
+    int row[KM];
+    float ww[KM], dot[KM];
+#pragma unroll
+    for (int j = 0; j < KM; ++j) {
+        row[j] = -1;
+        ww[j] = dot[j] = 0.f;
+        if (j < k) {
+            const int r = __ldg(pair_row + t * k + j);
+            if (r >= 0 && r < R) {
+                row[j] = r;
+                ww[j] = __ldg(w + t * k + j);
+            }
+        }
+    }
+    for (int c = tid * V; c < H; c += blockDim.x * V) {
+        Raw<TO, V> d;
+        d.load(dout + t * ld_do + c);
+        Raw<TY, V> v[KM];
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            v[j].zero();
+            if (row[j] >= 0) v[j].load(y + row[j] * ld_y + c);
+        }
+        float df[V];
+        d.get(df);
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            if (row[j] < 0) continue;
+            float f[V], g[V];
+            v[j].get(f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                dot[j] = fmaf(df[i], f[i], dot[j]);
+                g[i] = ww[j] * df[i];
+            }
+            Raw<TY, V> o;
+            o.set(g);
+            o.store(dy + row[j] * ld_dy + c);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < KM; ++j) {
+        float s = dot[j];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if ((tid & 31) == 0) red[tid >> 5][j] = s;
+    }
+    __syncthreads();
+    if (tid < k) {
+        float s = 0.f;
+        for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += red[i][tid];
+        dw[t * k + tid] = s;
+    }
+}
+
+// Eight elements at a time fit when rows start and step on 16 bytes.
+bool fits8(const void* p, int64_t ld, int f32) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (f32 ? 4 : 8) == 0;
+}
+
+template <typename F>
+cudaError_t by_type(int f32, F f) {
+    return f32 ? f(static_cast<float*>(nullptr)) : f(static_cast<__nv_bfloat16*>(nullptr));
+}
+
+}  // namespace
+
+cudaError_t launch_route_rows(const float* logits, int64_t ld, int T, int E, int k, int32_t* id, float* w,
+                              cudaStream_t stream) {
+    const int grid = (T + 3) / 4;
+    if (E <= 64)
+        route_rows_kernel<2><<<grid, 128, 0, stream>>>(logits, ld, T, E, k, id, w);
+    else if (E <= 256)
+        route_rows_kernel<8><<<grid, 128, 0, stream>>>(logits, ld, T, E, k, id, w);
+    else
+        route_rows_kernel<32><<<grid, 128, 0, stream>>>(logits, ld, T, E, k, id, w);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_route_rows_grad(const float* dw, const int32_t* id, const float* w, int T, int E, int k,
+                                   float* dlogits, int64_t ld, cudaStream_t stream) {
+    const int vec = E % 4 == 0 && fits8(dlogits, ld, 1);
+    route_rows_grad_kernel<<<(T + 3) / 4, 128, 0, stream>>>(dw, id, w, T, E, k, dlogits, ld, vec);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* offs, int32_t* pair_row,
+                               int32_t* row_pair, cudaStream_t stream) {
+    const int P = T * k;
+    const int ctas = P <= 2048 ? 1 : 8;
+    const int warps = min(kSortWarps, max(1, (P + ctas * 32 - 1) / (ctas * 32)));
+    const int run = (P + ctas * warps - 1) / (ctas * warps);
+    const size_t smem = (static_cast<size_t>(warps) * E + 2 * E) * sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (kSortWarps + 2) * MOEQ_MAX_EXPERTS * static_cast<int>(sizeof(int)));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, expert_sort_kernel, id, P, E, warps, run, offs, pair_row, row_pair);
+}
+
+cudaError_t launch_gather_rows(RowsIn x, int T, int H, int k, const int32_t* offs, int E, const int32_t* pair_row,
+                               RowsOut xs, cudaStream_t stream) {
+    const bool v8 = H % 8 == 0 && fits8(x.p, x.ld, x.f32) && fits8(xs.p, xs.ld, x.f32);
+    return by_type(x.f32, [&](auto* tag) {
+        using Ty = std::remove_pointer_t<decltype(tag)>;
+        const int nv = v8 ? H / 8 : H, threads = nv >= 256 ? 256 : (nv + 31) / 32 * 32;
+        const dim3 grid(T + kTailBlocks, (nv + threads - 1) / threads);
+        const Ty* xp = static_cast<const Ty*>(x.p);
+        Ty* sp = static_cast<Ty*>(xs.p);
+        if (v8)
+            gather_rows_kernel<Ty, 8><<<grid, threads, 0, stream>>>(xp, x.ld, T, H, k, offs, E,
+                                                                    static_cast<int64_t>(T) * k, pair_row, sp, xs.ld);
+        else
+            gather_rows_kernel<Ty, 1><<<grid, threads, 0, stream>>>(xp, x.ld, T, H, k, offs, E,
+                                                                    static_cast<int64_t>(T) * k, pair_row, sp, xs.ld);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_combine_rows(RowsIn y, int T, int H, int k, const int32_t* pair_row, const float* w, RowsIn base,
+                                RowsOut out, cudaStream_t stream) {
+    const bool v8 = H % 8 == 0 && fits8(y.p, y.ld, y.f32) && fits8(out.p, out.ld, out.f32) &&
+                    (!base.p || fits8(base.p, base.ld, out.f32));
+    const int64_t R = static_cast<int64_t>(T) * k;
+    return by_type(y.f32, [&](auto* ty) {
+        return by_type(out.f32, [&](auto* to) {
+            using TY = std::remove_pointer_t<decltype(ty)>;
+            using TO = std::remove_pointer_t<decltype(to)>;
+            const int nv = v8 ? H / 8 : H, threads = nv >= 256 ? 256 : (nv + 31) / 32 * 32;
+            const dim3 grid(T, (nv + threads - 1) / threads);
+            const TY* yp = static_cast<const TY*>(y.p);
+            const TO* bp = static_cast<const TO*>(base.p);
+            TO* op = static_cast<TO*>(out.p);
+            auto go = [&](auto kern) {
+                kern<<<grid, threads, 0, stream>>>(yp, y.ld, H, k, R, pair_row, w, bp, base.ld, op, out.ld);
+                return cudaGetLastError();
+            };
+            if (v8) return w ? go(combine_rows_kernel<TY, TO, 8, true>) : go(combine_rows_kernel<TY, TO, 8, false>);
+            return w ? go(combine_rows_kernel<TY, TO, 1, true>) : go(combine_rows_kernel<TY, TO, 1, false>);
+        });
+    });
+}
+
+cudaError_t launch_combine_rows_grad(RowsIn dout, RowsIn y, int T, int H, int k, const int32_t* offs, int E,
+                                     const int32_t* pair_row, const float* w, RowsOut dy, float* dw,
+                                     cudaStream_t stream) {
+    const bool v8 = H % 8 == 0 && fits8(y.p, y.ld, y.f32) && fits8(dout.p, dout.ld, dout.f32) &&
+                    fits8(dy.p, dy.ld, y.f32);
+    const int64_t R = static_cast<int64_t>(T) * k;
+    return by_type(y.f32, [&](auto* ty) {
+        return by_type(dout.f32, [&](auto* to) {
+            using TY = std::remove_pointer_t<decltype(ty)>;
+            using TO = std::remove_pointer_t<decltype(to)>;
+            const int grid = T + kTailBlocks;
+            auto go = [&](auto kern) {
+                kern<<<grid, 256, 0, stream>>>(static_cast<const TO*>(dout.p), dout.ld, static_cast<const TY*>(y.p),
+                                               y.ld, T, H, k, offs, E, R, pair_row, w, static_cast<TY*>(dy.p), dy.ld,
+                                               dw);
+                return cudaGetLastError();
+            };
+            if (k <= 8)
+                return v8 ? go(combine_rows_grad_kernel<TY, TO, 8, 8>) : go(combine_rows_grad_kernel<TY, TO, 1, 8>);
+            return v8 ? go(combine_rows_grad_kernel<TY, TO, 8, kMaxK>) : go(combine_rows_grad_kernel<TY, TO, 1, kMaxK>);
+        });
+    });
+}
+
+}  // namespace moeq

@@ -1,0 +1,89 @@
+// Host launchers of the operators that take any number of tokens (routing,
+// the sort by expert, row movement, MXFP4).  moeq_rows_api.cu validates the
+// arguments of the C ABI and calls these.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/moeq.h"
+
+namespace moeq {
+
+// A matrix of rows: base, leading dimension in elements, element type.
+struct RowsIn {
+    const void* p;
+    int64_t ld;
+    int f32;
+};
+struct RowsOut {
+    void* p;
+    int64_t ld;
+    int f32;
+};
+
+cudaError_t launch_route_rows(const float* logits, int64_t ld, int T, int E, int k, int32_t* id, float* w,
+                              cudaStream_t stream);
+cudaError_t launch_route_rows_grad(const float* dw, const int32_t* id, const float* w, int T, int E, int k,
+                                   float* dlogits, int64_t ld, cudaStream_t stream);
+cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* offs, int32_t* pair_row,
+                               int32_t* row_pair, cudaStream_t stream);
+cudaError_t launch_gather_rows(RowsIn x, int T, int H, int k, const int32_t* offs, int E, const int32_t* pair_row,
+                               RowsOut xs, cudaStream_t stream);
+// out[t] = base[t] + sum_j w[t, j] * y[pair_row[t, j]]; w == NULL: weights 1.
+cudaError_t launch_combine_rows(RowsIn y, int T, int H, int k, const int32_t* pair_row, const float* w, RowsIn base,
+                                RowsOut out, cudaStream_t stream);
+cudaError_t launch_combine_rows_grad(RowsIn dout, RowsIn y, int T, int H, int k, const int32_t* offs, int E,
+                                     const int32_t* pair_row, const float* w, RowsOut dy, float* dw,
+                                     cudaStream_t stream);
+
+// ------------------------------------------------------------------ MXFP4
+// Weights are tile-major: tile (e, nb, kb) is the 128 x 256 block of rows
+// nb*128.. and columns kb*256.. of expert e: 16 KiB of codes (rows of 128
+// bytes, the 16-byte chunk c of row r stored at chunk c ^ (r % 8)) and 1 KiB
+// of scales: per 128 columns 512 bytes, the word of row r (its four scale
+// bytes, lowest column first) at word (r % 32) * 4 + r / 32.  Rows and
+// columns past N and K are zero.
+constexpr int kMx4TileRows = 128, kMx4TileCols = 256, kMx4TileBytes = 16384, kMx4TileScaleBytes = 1024;
+
+// Activations: codes [rows, K/2], scales [rows, pitch] bytes (eight for every
+// 256 columns; those past K are zero).
+__host__ __device__ constexpr int mx4_scale_pitch(int K) { return (K + kMx4TileCols - 1) / kMx4TileCols * 8; }
+__host__ __device__ constexpr int mx4_kb(int K) { return (K + kMx4TileCols - 1) / kMx4TileCols; }
+__host__ __device__ constexpr int mx4_nb(int N) { return (N + kMx4TileRows - 1) / kMx4TileRows; }
+
+// act: x is [rows, 2K] and silu(x[:, :K]) * x[:, K:] is quantised.
+cudaError_t launch_mx4_quant_act(RowsIn x, int rows, int K, int act, uint8_t* codes, uint8_t* scales,
+                                 cudaStream_t stream);
+cudaError_t launch_mx4_dequant_act(const uint8_t* codes, const uint8_t* scales, int rows, int K, RowsOut out,
+                                   cudaStream_t stream);
+cudaError_t launch_mx4_quant_weight(const void* w, int w_f32, int E, int N, int K, uint8_t* tiles, uint8_t* stiles,
+                                    cudaStream_t stream);
+cudaError_t launch_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, uint8_t* tiles,
+                                   uint8_t* stiles, cudaStream_t stream);
+
+struct Mx4GemmArgs {
+    const uint8_t* w;       // tiles
+    const uint8_t* sw;      // scale tiles
+    const uint8_t* a;       // activation codes [a_rows, K/2]
+    const uint8_t* sa;      // activation scales [a_rows, pitch]
+    const int32_t* offs;    // [E + 1]
+    const int32_t* row_pair;  // [R] or NULL: row r reads activation row r
+    void* y;
+    int64_t ld_y;
+    int y_f32;
+    int a_rows, K, N, E, R, top_k;
+    int nt;                 // most rows of one token tile (multiple of 16)
+    int stages;
+    int* tickets;           // kMx4Tickets, zero between launches
+    float* part;            // 2 * grid slots of nt * 128 floats
+    int* status;
+};
+constexpr int kMx4Tickets = 4096;
+// Most rows of one token tile for R rows over E experts.
+int mx4_tile_rows(int R, int E);
+cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stream);
+
+}  // namespace moeq

@@ -25,6 +25,9 @@ MOEQ_ERR_TIMEOUT = 5
 MOEQ_ERR_DEVICE = 6
 MOEQ_BF16 = 0
 MOEQ_F32 = 1
+MOEQ_MX4 = 2
+MOEQ_ACT_NONE = 0
+MOEQ_ACT_SWIGLU = 1
 MOEQ_GROUP = 128
 MOEQ_MAX_TOKENS = 16
 MOEQ_MAX_LAYERS = 256
@@ -40,6 +43,10 @@ EXPORTS = [
     "moeq_dense_ffn_workspace_size", "moeq_dense_ffn", "moeq_stack_workspace_size", "moeq_moe_stack",
     "moeq_stack_plan", "moeq_stack_release_graphs", "moeq_tp_shard_weights", "moeq_moe_layer_shard",
     "moeq_tp_reduce", "moeq_layer_ws_count_offset", "moeq_gemm_ws_count_offset",
+    "moeq_route_rows", "moeq_route_rows_grad", "moeq_expert_sort", "moeq_gather_rows", "moeq_gather_rows_grad",
+    "moeq_combine_rows", "moeq_combine_rows_grad", "moeq_mx4_scale_pitch", "moeq_mx4_weight_bytes",
+    "moeq_mx4_weight_scale_bytes", "moeq_mx4_quant_act", "moeq_mx4_dequant_act", "moeq_mx4_quant_weight",
+    "moeq_mx4_pack_weight", "moeq_mx4_expert_gemm_workspace_size", "moeq_mx4_expert_gemm",
 ]
 
 
@@ -58,6 +65,7 @@ _lib = None
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_ll = ctypes.c_int64
 
 
 def load(path: str = LIB_PATH):
@@ -105,6 +113,24 @@ def load(path: str = LIB_PATH):
         "moeq_moe_layer": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp,
                                 ctypes.POINTER(moeq_route_plan), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                 _sz, _vp]),
+        "moeq_route_rows": (_i, [_vp, _ll, _i, _i, _i, _vp, _vp, _vp]),
+        "moeq_route_rows_grad": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _ll, _vp]),
+        "moeq_expert_sort": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
+        "moeq_gather_rows": (_i, [_vp, _i, _ll, _i, _i, _i, _vp, _i, _vp, _vp, _ll, _vp]),
+        "moeq_gather_rows_grad": (_i, [_vp, _i, _ll, _i, _i, _i, _vp, _vp, _ll, _vp]),
+        "moeq_combine_rows": (_i, [_vp, _i, _ll, _i, _i, _i, _vp, _vp, _vp, _ll, _vp, _i, _ll, _vp]),
+        "moeq_combine_rows_grad": (_i, [_vp, _i, _ll, _vp, _i, _ll, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _ll, _vp,
+                                        _vp]),
+        "moeq_mx4_scale_pitch": (_i, [_i]),
+        "moeq_mx4_weight_bytes": (_sz, [_i, _i, _i]),
+        "moeq_mx4_weight_scale_bytes": (_sz, [_i, _i, _i]),
+        "moeq_mx4_quant_act": (_i, [_vp, _i, _ll, _i, _i, _i, _vp, _vp, _vp]),
+        "moeq_mx4_dequant_act": (_i, [_vp, _vp, _i, _i, _vp, _i, _ll, _vp]),
+        "moeq_mx4_quant_weight": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp]),
+        "moeq_mx4_pack_weight": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp]),
+        "moeq_mx4_expert_gemm_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+        "moeq_mx4_expert_gemm": (_i, [_vp, _i, _ll, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _i,
+                                      _ll, _vp, _sz, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -374,3 +400,204 @@ def moeq_layer_ws_count_offset(M, H, I, n_experts_incl_shared, top_k, which) -> 
 
 def moeq_gemm_ws_count_offset(rows_out, K, rows_in, max_uniq, is_gate_up, which) -> int:
     return int(load().moeq_gemm_ws_count_offset(rows_out, K, rows_in, max_uniq, is_gate_up, which))
+
+
+# ------------------------------------------------- any number of tokens
+def _ld(t, name: str = "matrix") -> int:
+    """Leading dimension, in elements, of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: a 2-D tensor with contiguous rows is wanted, got shape {tuple(t.shape)}, "
+                         f"strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def _packed(t, dtype, shape, name: str):
+    """A contiguous tensor of this dtype and shape, or an error that says which is not."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} is wanted, got {t.dtype} "
+                         f"{tuple(t.shape)}, strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _same(cond: bool, what: str) -> None:
+    if not cond:
+        raise ValueError(what)
+
+
+def moeq_route_rows(logits, topk_id, topk_w, stream=None) -> None:
+    """Top-k experts of every row of logits [T, E] fp32: topk_id [T, k] int32
+    (-1: the row has no expert left), topk_w [T, k] fp32."""
+    T, E = logits.shape
+    k = topk_id.shape[1]
+    _same(logits.dtype == torch.float32, "logits: fp32 is wanted")
+    _check("moeq_route_rows", load().moeq_route_rows(
+        logits.data_ptr(), _ld(logits, "logits"), T, E, k, _packed(topk_id, torch.int32, (T, k), "topk_id"),
+        _packed(topk_w, torch.float32, (T, k), "topk_w"), _stream(stream)))
+
+
+def moeq_route_rows_grad(d_topk_w, topk_id, topk_w, d_logits, stream=None) -> None:
+    T, E = d_logits.shape
+    k = topk_id.shape[1]
+    _same(d_logits.dtype == torch.float32, "d_logits: fp32 is wanted")
+    _check("moeq_route_rows_grad", load().moeq_route_rows_grad(
+        _packed(d_topk_w, torch.float32, (T, k), "d_topk_w"), _packed(topk_id, torch.int32, (T, k), "topk_id"),
+        _packed(topk_w, torch.float32, (T, k), "topk_w"), T, E, k, d_logits.data_ptr(), _ld(d_logits, "d_logits"),
+        _stream(stream)))
+
+
+def moeq_expert_sort(topk_id, E, offs, pair_row, row_pair, stream=None) -> None:
+    """Stable sort of the (token, slot) pairs of topk_id [T, k] by expert:
+    offs [E + 1], pair_row [T, k], row_pair [T * k], all int32."""
+    T, k = topk_id.shape
+    _check("moeq_expert_sort", load().moeq_expert_sort(
+        _packed(topk_id, torch.int32, (T, k), "topk_id"), T, k, E, _packed(offs, torch.int32, (E + 1,), "offs"),
+        _packed(pair_row, torch.int32, (T, k), "pair_row"), _packed(row_pair, torch.int32, (T * k,), "row_pair"),
+        _stream(stream)))
+
+
+def _pairs(pair_row):
+    T, k = pair_row.shape
+    return T, k, _packed(pair_row, torch.int32, (T, k), "pair_row")
+
+
+def _offs(offs):
+    return offs.shape[0] - 1, _packed(offs, torch.int32, offs.shape[:1], "offs")
+
+
+def moeq_gather_rows(x, offs, pair_row, xs, stream=None) -> None:
+    """xs[pair_row[t, j]] = x[t]; rows of xs from offs[E] on are zeroed."""
+    T, k, pr = _pairs(pair_row)
+    E, of = _offs(offs)
+    H = x.shape[1]
+    _same(tuple(x.shape) == (T, H) and tuple(xs.shape) == (T * k, H) and x.dtype == xs.dtype,
+          f"x [{T}, H] and xs [{T * k}, H] of one type are wanted, got {tuple(x.shape)} and {tuple(xs.shape)}")
+    _check("moeq_gather_rows", load().moeq_gather_rows(
+        x.data_ptr(), _dtype(x), _ld(x, "x"), T, H, k, of, E, pr, xs.data_ptr(), _ld(xs, "xs"), _stream(stream)))
+
+
+def moeq_gather_rows_grad(d_xs, pair_row, d_x, stream=None) -> None:
+    """d_x[t] = sum_j d_xs[pair_row[t, j]]."""
+    T, k, pr = _pairs(pair_row)
+    H = d_x.shape[1]
+    _same(tuple(d_x.shape) == (T, H) and tuple(d_xs.shape) == (T * k, H) and d_x.dtype == d_xs.dtype,
+          f"d_x [{T}, H] and d_xs [{T * k}, H] of one type are wanted, got {tuple(d_x.shape)} and {tuple(d_xs.shape)}")
+    _check("moeq_gather_rows_grad", load().moeq_gather_rows_grad(
+        d_xs.data_ptr(), _dtype(d_xs), _ld(d_xs, "d_xs"), T, H, k, pr, d_x.data_ptr(), _ld(d_x, "d_x"),
+        _stream(stream)))
+
+
+def moeq_combine_rows(y, pair_row, topk_w, out, base=None, stream=None) -> None:
+    """out[t] = base[t] + sum_j topk_w[t, j] * y[pair_row[t, j]]."""
+    T, k, pr = _pairs(pair_row)
+    H = out.shape[1]
+    _same(tuple(out.shape) == (T, H) and tuple(y.shape) == (T * k, H),
+          f"out [{T}, H] and y [{T * k}, H] are wanted, got {tuple(out.shape)} and {tuple(y.shape)}")
+    _same(base is None or (tuple(base.shape) == (T, H) and base.dtype == out.dtype), "base: out's shape and type")
+    _check("moeq_combine_rows", load().moeq_combine_rows(
+        y.data_ptr(), _dtype(y), _ld(y, "y"), T, H, k, pr, _packed(topk_w, torch.float32, (T, k), "topk_w"), _p(base),
+        _ld(base, "base") if base is not None else 0, out.data_ptr(), _dtype(out), _ld(out, "out"), _stream(stream)))
+
+
+def moeq_combine_rows_grad(d_out, y, offs, pair_row, topk_w, d_y, d_topk_w, stream=None) -> None:
+    """d_y[pair_row[t, j]] = topk_w[t, j] * d_out[t] (rows from offs[E] on
+    zeroed) and d_topk_w[t, j] = <d_out[t], y[pair_row[t, j]]>."""
+    T, k, pr = _pairs(pair_row)
+    E, of = _offs(offs)
+    H = d_out.shape[1]
+    _same(tuple(d_out.shape) == (T, H) and tuple(y.shape) == (T * k, H) and tuple(d_y.shape) == (T * k, H) and
+          d_y.dtype == y.dtype, f"d_out [{T}, H], y and d_y [{T * k}, H] are wanted, got {tuple(d_out.shape)}, "
+          f"{tuple(y.shape)} and {tuple(d_y.shape)}")
+    _check("moeq_combine_rows_grad", load().moeq_combine_rows_grad(
+        d_out.data_ptr(), _dtype(d_out), _ld(d_out, "d_out"), y.data_ptr(), _dtype(y), _ld(y, "y"), T, H, k, of, E, pr,
+        _packed(topk_w, torch.float32, (T, k), "topk_w"), d_y.data_ptr(), _ld(d_y, "d_y"),
+        _packed(d_topk_w, torch.float32, (T, k), "d_topk_w"), _stream(stream)))
+
+
+def moeq_mx4_scale_pitch(K) -> int:
+    return load().moeq_mx4_scale_pitch(K)
+
+
+def moeq_mx4_weight_bytes(E, N, K) -> int:
+    return int(load().moeq_mx4_weight_bytes(E, N, K))
+
+
+def moeq_mx4_weight_scale_bytes(E, N, K) -> int:
+    return int(load().moeq_mx4_weight_scale_bytes(E, N, K))
+
+
+def mx4_weight_buffers(E, N, K, device="cuda"):
+    """Device buffers for the tiles and scale tiles of E experts of [N, K]."""
+    nbytes = moeq_mx4_weight_bytes(E, N, K)
+    if not nbytes:
+        raise MoeqError("moeq_mx4_weight_bytes", MOEQ_ERR_UNSUPPORTED_SHAPE)
+    return (torch.empty(nbytes, dtype=torch.uint8, device=device),
+            torch.empty(moeq_mx4_weight_scale_bytes(E, N, K), dtype=torch.uint8, device=device))
+
+
+def moeq_mx4_quant_act(x, codes, scales, act=MOEQ_ACT_NONE, stream=None) -> None:
+    """x [rows, K] ([rows, 2K] with MOEQ_ACT_SWIGLU) -> codes [rows, K/2],
+    scales [rows, moeq_mx4_scale_pitch(K)], uint8."""
+    rows, K = x.shape[0], x.shape[1] // (2 if act == MOEQ_ACT_SWIGLU else 1)
+    L = load()
+    _check("moeq_mx4_quant_act", L.moeq_mx4_quant_act(
+        x.data_ptr(), _dtype(x), _ld(x, "x"), rows, K, act, _packed(codes, torch.uint8, (rows, K // 2), "codes"),
+        _packed(scales, torch.uint8, (rows, L.moeq_mx4_scale_pitch(K)), "scales"), _stream(stream)))
+
+
+def moeq_mx4_dequant_act(codes, scales, out, stream=None) -> None:
+    rows, K = out.shape
+    L = load()
+    _check("moeq_mx4_dequant_act", L.moeq_mx4_dequant_act(
+        _packed(codes, torch.uint8, (rows, K // 2), "codes"),
+        _packed(scales, torch.uint8, (rows, L.moeq_mx4_scale_pitch(K)), "scales"), rows, K, out.data_ptr(),
+        _dtype(out), _ld(out, "out"), _stream(stream)))
+
+
+def _tiles(tiles, scale_tiles, E, N, K):
+    return (_packed(tiles, torch.uint8, (moeq_mx4_weight_bytes(E, N, K),), "tiles"),
+            _packed(scale_tiles, torch.uint8, (moeq_mx4_weight_scale_bytes(E, N, K),), "scale_tiles"))
+
+
+def moeq_mx4_quant_weight(w, tiles, scale_tiles, stream=None) -> None:
+    """w [E, N, K] bf16 or fp32 -> tiles and scale tiles (mx4_weight_buffers)."""
+    E, N, K = w.shape
+    _same(w.is_contiguous(), "w: a contiguous tensor is wanted")
+    _check("moeq_mx4_quant_weight", load().moeq_mx4_quant_weight(
+        w.data_ptr(), _dtype(w), E, N, K, *_tiles(tiles, scale_tiles, E, N, K), _stream(stream)))
+
+
+def moeq_mx4_pack_weight(codes, scales, tiles, scale_tiles, stream=None) -> None:
+    """Row-major MXFP4 codes [E, N, K/2] and scales [E, N, K/32] -> tiles."""
+    E, N, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
+    _check("moeq_mx4_pack_weight", load().moeq_mx4_pack_weight(
+        _packed(codes, torch.uint8, (E, N, K // 2), "codes"), _packed(scales, torch.uint8, (E, N, K // 32), "scales"),
+        E, N, K, *_tiles(tiles, scale_tiles, E, N, K), _stream(stream)))
+
+
+def moeq_mx4_expert_gemm_workspace_size(rows, K, N, E, R) -> int:
+    return int(load().moeq_mx4_expert_gemm_workspace_size(rows, K, N, E, R))
+
+
+def moeq_mx4_expert_gemm(x, w, w_scales, offs, y, ws: Workspace, row_pair=None, top_k=1, act=MOEQ_ACT_NONE,
+                         x_scales=None, stream=None) -> None:
+    """y[r] = W[e(r)] . q(x[row(r)]) for rows sorted by expert (offs [E + 1]).
+    x [rows, K] bf16 or fp32, or uint8 codes [rows, K/2] with x_scales; row r
+    reads x[row_pair[r] // top_k], or x[r] without row_pair.  y [R, N]."""
+    E, of = _offs(offs)
+    R, N = y.shape
+    rows, K = x.shape
+    L = load()
+    if x_scales is not None:
+        K *= 2
+        dt, ld = MOEQ_MX4, 0
+        _packed(x, torch.uint8, (rows, K // 2), "x")
+        _packed(x_scales, torch.uint8, (rows, L.moeq_mx4_scale_pitch(K)), "x_scales")
+    else:
+        if act == MOEQ_ACT_SWIGLU:
+            K //= 2
+        dt, ld = _dtype(x), _ld(x, "x")
+    tp, sp = _tiles(w, w_scales, E, N, K)
+    _check("moeq_mx4_expert_gemm", L.moeq_mx4_expert_gemm(
+        x.data_ptr(), dt, ld, _p(x_scales), rows, K, act, tp, sp, N, of, E, R,
+        _packed(row_pair, torch.int32, (R,), "row_pair") if row_pair is not None else None, top_k, y.data_ptr(),
+        _dtype(y), _ld(y, "y"), ws.ptr, ws.nbytes, _stream(stream)))

@@ -70,7 +70,7 @@ typedef enum moeq_status {
     MOEQ_ERR_DEVICE = 6             /* no CUDA device, or not a compute capability 10.3 part */
 } moeq_status;
 
-typedef enum moeq_dtype { MOEQ_BF16 = 0, MOEQ_F32 = 1 } moeq_dtype;
+typedef enum moeq_dtype { MOEQ_BF16 = 0, MOEQ_F32 = 1, MOEQ_MX4 = 2 } moeq_dtype;
 
 #define MOEQ_GROUP 128          /* quantisation group along K, and weight block edge */
 #define MOEQ_MAX_TOKENS 16      /* M limit: decode plus draft verification */
@@ -475,6 +475,123 @@ moeq_status moeq_stack_plan(void* ws, size_t ws_bytes, int L, int M, int H, int 
 /* Destroy every graph moeq_moe_stack keeps (a graph still running is freed */
 /* when it completes).  The next stack call captures again.                 */
 moeq_status moeq_stack_release_graphs(void);
+
+/* ======================================================================== */
+/* Any number of tokens: the router, the sort of tokens by expert, rows to  */
+/* the experts and back (with gradients), and MXFP4 products.  The calls    */
+/* above stop at MOEQ_MAX_TOKENS; these serve prompts, batches and the      */
+/* training of the routing.  A layer is                                     */
+/*   moeq_route_rows -> moeq_expert_sort ->                                 */
+/*   moeq_mx4_expert_gemm (gate and up) -> moeq_mx4_expert_gemm (down, with */
+/*   MOEQ_ACT_SWIGLU) -> moeq_combine_rows.                                 */
+/* Conventions beyond those above: T, rows and R may be 0; matrices have a  */
+/* leading dimension in elements (rows at least their width apart) and need */
+/* only their elements' alignment (16-byte rows run faster); T * top_k and  */
+/* R are at most 2^30.  Device-side indices out of range read and write     */
+/* nothing out of range.                                                    */
+/* ======================================================================== */
+/* The element type MOEQ_MX4 (moeq_mx4_expert_gemm's x alone): MXFP4 codes.  */
+typedef enum moeq_act { MOEQ_ACT_NONE = 0, MOEQ_ACT_SWIGLU = 1 } moeq_act;
+
+/* moeq_route_rows -- top-k of each row of logits [T, E] (fp32).            */
+/*   topk_id [T, top_k]   falling logit, ties to the lower id               */
+/*   topk_w  [T, top_k]   softmax over the picks                            */
+/* -inf and NaN mask an expert: it is never picked, and the slots a row     */
+/* cannot fill get id -1 and weight 0.  +inf counts as the largest finite   */
+/* number.  top_k <= min(E, MOEQ_MAX_TOPK), E <= MOEQ_MAX_EXPERTS.          */
+moeq_status moeq_route_rows(const float* logits, int64_t ld, int T, int E, int top_k,
+                            int32_t* topk_id, float* topk_w, void* stream);
+/* Its gradient: d_logits[t, id_j] = w_j (d_w_j - sum_i w_i d_w_i), zero     */
+/* elsewhere (every element is written).  A row's ids are distinct or -1,   */
+/* as moeq_route_rows leaves them.                                          */
+moeq_status moeq_route_rows_grad(const float* d_topk_w, const int32_t* topk_id, const float* topk_w,
+                                 int T, int E, int top_k, float* d_logits, int64_t ld, void* stream);
+
+/* moeq_expert_sort -- the (token, slot) pairs sorted by expert, stable.    */
+/*   offs     [E + 1]     rows of expert e are offs[e] .. offs[e + 1] - 1   */
+/*   pair_row [T, top_k]  the row of a slot, -1 if its id is outside [0, E) */
+/*                        (no pick, or an expert held elsewhere)            */
+/*   row_pair [T * top_k] the pair t * top_k + j of a row, -1 from offs[E]  */
+moeq_status moeq_expert_sort(const int32_t* topk_id, int T, int top_k, int E,
+                             int32_t* offs, int32_t* pair_row, int32_t* row_pair, void* stream);
+
+/* moeq_gather_rows -- xs[pair_row[t, j]] = x[t]; xs [T * top_k, H], its    */
+/* rows from offs[E] on are zeroed.  bf16 or fp32.                          */
+moeq_status moeq_gather_rows(const void* x, moeq_dtype dtype, int64_t ld_x, int T, int H, int top_k,
+                             const int32_t* offs, int E, const int32_t* pair_row,
+                             void* xs, int64_t ld_xs, void* stream);
+/* Its gradient: d_x[t] = sum_j d_xs[pair_row[t, j]], fp32 sums in slot order. */
+moeq_status moeq_gather_rows_grad(const void* d_xs, moeq_dtype dtype, int64_t ld_xs, int T, int H, int top_k,
+                                  const int32_t* pair_row, void* d_x, int64_t ld_x, void* stream);
+
+/* moeq_combine_rows -- out[t] = base[t] + sum_j topk_w[t, j] *             */
+/* y[pair_row[t, j]], fp32 in slot order, rounded once; slots without a row */
+/* add nothing.  base_opt (the shared expert's output, or a residual) has   */
+/* out's type.                                                              */
+moeq_status moeq_combine_rows(const void* y, moeq_dtype y_dtype, int64_t ld_y, int T, int H, int top_k,
+                              const int32_t* pair_row, const float* topk_w,
+                              const void* base_opt, int64_t ld_base,
+                              void* out, moeq_dtype out_dtype, int64_t ld_out, void* stream);
+/* Its gradients: d_y[pair_row[t, j]] = topk_w[t, j] * d_out[t] (rows from  */
+/* offs[E] on zeroed) and d_topk_w[t, j] = <d_out[t], y[pair_row[t, j]]>    */
+/* (0 for a slot without a row).  base's gradient is d_out itself.          */
+moeq_status moeq_combine_rows_grad(const void* d_out, moeq_dtype out_dtype, int64_t ld_out,
+                                   const void* y, moeq_dtype y_dtype, int64_t ld_y, int T, int H, int top_k,
+                                   const int32_t* offs, int E, const int32_t* pair_row, const float* topk_w,
+                                   void* d_y, int64_t ld_dy, float* d_topk_w, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* MXFP4 (OCP microscaling): blocks of 32 along K share a scale 2^s, stored */
+/* as the byte s + 127, s = max(floor(log2 amax) - 2, -127); an element is  */
+/* the E2M1 code of x * 2^-s (0, .5, 1, 1.5, 2, 3, 4, 6 and their           */
+/* negatives), rounded to nearest even, saturating.  A block with a NaN or  */
+/* an infinity gets the scale 255 (NaN).  Two codes a byte, the lower       */
+/* column in the low bits.  K is a multiple of 32 up to MOEQ_MAX_K, N any.  */
+/*   activations: codes [rows, K/2], scales [rows, moeq_mx4_scale_pitch(K)] */
+/*           (8 bytes for every 256 columns, those past K zero)             */
+/*   weights: tile-major.  Tile (e, nb, kb) -- rows nb*128.., columns       */
+/*           kb*256.. of expert e -- is 16 KiB of codes (rows of 128 bytes, */
+/*           16-byte chunk c of row r at chunk c ^ (r % 8)) and 1 KiB of    */
+/*           scales (per 128 columns 512 bytes: the four bytes of row r at  */
+/*           word (r % 32) * 4 + r / 32); zero past N and K.                */
+/* ------------------------------------------------------------------------ */
+int moeq_mx4_scale_pitch(int K);                          /* 0 on a K out of range */
+size_t moeq_mx4_weight_bytes(int E, int N, int K);        /* 0 on invalid arguments */
+size_t moeq_mx4_weight_scale_bytes(int E, int N, int K);
+/* x [rows, K] -> codes and scales.  With MOEQ_ACT_SWIGLU x is [rows, 2K],  */
+/* gate then up, and silu(gate) * up is quantised.                          */
+moeq_status moeq_mx4_quant_act(const void* x, moeq_dtype dtype, int64_t ld, int rows, int K, moeq_act act,
+                               uint8_t* codes, uint8_t* scales, void* stream);
+/* The values that codes and scales stand for (exact in both types).        */
+moeq_status moeq_mx4_dequant_act(const uint8_t* codes, const uint8_t* scales, int rows, int K,
+                                 void* out, moeq_dtype dtype, int64_t ld, void* stream);
+/* w [E, N, K] -> tiles.                                                    */
+moeq_status moeq_mx4_quant_weight(const void* w, moeq_dtype dtype, int E, int N, int K,
+                                  uint8_t* tiles, uint8_t* scale_tiles, void* stream);
+/* Row-major codes [E, N, K/2] and scales [E, N, K/32] -> tiles.            */
+moeq_status moeq_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, int E, int N, int K,
+                                 uint8_t* tiles, uint8_t* scale_tiles, void* stream);
+
+/* moeq_mx4_expert_gemm -- y[r] = W[e] . q(x[row(r)]) for the rows r of     */
+/* every expert e, fp32 accumulation on the tensor cores.                   */
+/*   x       [rows, K] bf16 or fp32 (x_scales NULL), quantised here; or     */
+/*           MOEQ_MX4 codes with x_scales.  MOEQ_ACT_SWIGLU as above        */
+/*   w, w_scales  tiles of E experts of [N, K]                              */
+/*   offs    [E + 1] on the device, as moeq_expert_sort leaves it; a dense  */
+/*           product is E = 1, offs = {0, R}                                */
+/*   row_pair_opt [R]: row r reads x[row_pair[r] / top_k]; NULL: x[r]       */
+/*   y       [R, N] bf16 or fp32; rows from offs[E] on are zeroed           */
+/*   ws      moeq_mx4_expert_gemm_workspace_size(rows, K, N, E, R) bytes,   */
+/*           zeroed once (moeq_workspace_init); the status word is as for   */
+/*           the other calls.  The size depends on the device's SM count.   */
+size_t moeq_mx4_expert_gemm_workspace_size(int rows, int K, int N, int E, int R);
+moeq_status moeq_mx4_expert_gemm(const void* x, moeq_dtype x_dtype, int64_t ld_x, const uint8_t* x_scales,
+                                 int rows, int K, moeq_act act,
+                                 const uint8_t* w, const uint8_t* w_scales, int N,
+                                 const int32_t* offs, int E, int R,
+                                 const int32_t* row_pair_opt, int top_k,
+                                 void* y, moeq_dtype y_dtype, int64_t ld_y,
+                                 void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

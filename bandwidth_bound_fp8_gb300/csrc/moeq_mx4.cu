@@ -5,6 +5,7 @@
 // either way), so codes and scales are the definition's bit for bit.  A block
 // that holds a NaN or an infinity gets the scale 255, E8M0's NaN.
 #include "moeq_device.cuh"
+#include "moeq_mx4_plan.cuh"
 #include "moeq_rows.h"
 
 namespace moeq {
@@ -82,12 +83,15 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) 
     }
 }
 
+// silu(g) * u.  The fast exponential and division are within a few ulp times
+// |g|, far below the 4-bit rounding that follows.
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
 // Rows of activations.  A thread takes eight elements (one or two 16-byte
 // loads, four bytes of codes written), four lanes a block.
 template <bool kF32, bool kVec, bool kSwiglu>
 __global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__ x, int64_t ld, int64_t items, int K,
                                                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t item = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const bool in = item < items;
     const int per_row = K >> 3;
@@ -102,7 +106,7 @@ __global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__
             float u[8];
             load8<kF32, kVec>(x, row * ld + K + c, u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fdividef(v[i], 1.f + __expf(-v[i])) * u[i];
+            for (int i = 0; i < 8; ++i) v[i] = swiglu(v[i], u[i]);
         }
     }
     uint32_t s;
@@ -222,6 +226,74 @@ __global__ void __launch_bounds__(256) pack_weight_kernel(const uint8_t* __restr
     }
 }
 
+// The token tiles of a product: rows gathered into expert order, quantised on
+// the way (or copied from codes), and laid out as the tensor core reads them,
+// so that the product fetches a stage with plain bulk copies.  An item is a
+// row's 1024 columns, one warp each; the columns past K of its last block of
+// 256 are zeroed (padding rows of a tile are not: they only reach rows of the
+// product that are not stored).
+constexpr int kSegment = 4;  // K blocks of 256 columns an item
+
+template <int kSrc, bool kVec, bool kSwiglu>  // kSrc: 0 bf16, 1 fp32, 2 codes
+__global__ void __launch_bounds__(kPlanThreads) act_tiles_kernel(Mx4Source src, Mx4Plan p, int K,
+                                                                 uint8_t* __restrict__ tiles,
+                                                                 uint8_t* __restrict__ stiles) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ PlanShared plan;
+    plan_scan(p, plan);
+    const int lane = threadIdx.x & 31, kb_all = mx4_kb(K), segs = (kb_all + kSegment - 1) / kSegment;
+    const int r_end = plan.first[p.E];
+    const int64_t items = static_cast<int64_t>(r_end) * segs, step = static_cast<int64_t>(gridDim.x) * (kPlanThreads / 32);
+    const int sb = mx4_tile_scale_bytes(p.nt), chunk_bytes = sb / 2;
+    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kPlanThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
+        const int r = static_cast<int>(it / segs), seg = static_cast<int>(it - static_cast<int64_t>(r) * segs);
+        if (r < plan.first[0]) continue;
+        const int a_row = min(p.row_pair ? max(__ldg(p.row_pair + r), 0) / p.top_k : r, p.rows - 1);
+        float v[kSegment][8], u[kSegment][8];
+        uint32_t q[kSegment], s[kSegment];
+#pragma unroll
+        for (int i = 0; i < kSegment; ++i) {
+            const int c = (seg * kSegment + i) * kMx4TileCols + lane * 8;
+            q[i] = s[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = u[i][j] = 0.f;
+            if (c >= K) continue;
+            if constexpr (kSrc == 2) {
+                q[i] = __ldg(reinterpret_cast<const uint32_t*>(src.codes + static_cast<int64_t>(a_row) * (K >> 1) + (c >> 1)));
+                s[i] = __ldg(src.scales + static_cast<int64_t>(a_row) * mx4_scale_pitch(K) + (c >> 5));
+            } else {
+                load8<kSrc == 1, kVec>(src.x.p, a_row * src.x.ld + c, v[i]);
+                if constexpr (kSwiglu) load8<kSrc == 1, kVec>(src.x.p, a_row * src.x.ld + K + c, u[i]);
+            }
+        }
+        // where the row lies: its expert, tile and place in it
+        const int e = plan_find(plan.first, p.E, r);
+        const int per = plan_rows_per_tile(plan.first[e + 1] - plan.first[e], p.nt);
+        const int in_e = r - plan.first[e], t = in_e / per, pos = in_e - t * per;
+        const int64_t block0 = static_cast<int64_t>(plan.tile[e] + t) * kb_all + seg * kSegment;
+        const int at = pos * 128 + (((lane >> 2) ^ (pos & 7)) << 4) + (lane & 3) * 4;
+        const int s_at = (lane >> 4) * chunk_bytes + (pos >> 7) * 512 + (pos & 31) * 16 + ((pos >> 5) & 3) * 4;
+#pragma unroll
+        for (int i = 0; i < kSegment; ++i) {
+            if (seg * kSegment + i >= kb_all) break;
+            if constexpr (kSrc != 2) {
+                if constexpr (kSwiglu) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] = swiglu(v[i][j], u[i][j]);
+                }
+                const bool in = (seg * kSegment + i) * kMx4TileCols + lane * 8 < K;
+                q[i] = mx4_block(v[i], &s[i]);
+                if (!in) s[i] = 0;
+            }
+            uint32_t word = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) word |= __shfl_sync(0xffffffffu, s[i], (lane & 16) + 4 * j) << (8 * j);
+            *reinterpret_cast<uint32_t*>(tiles + (block0 + i) * p.nt * 128 + at) = q[i];
+            if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(stiles + (block0 + i) * sb + s_at) = word;
+        }
+    }
+}
+
 bool fits(const void* p, int64_t ld, int f32) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (f32 ? 4 : 8) == 0;
 }
@@ -276,6 +348,25 @@ cudaError_t launch_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, 
     const dim3 grid(mx4_kb(K), mx4_nb(N), E);
     pack_weight_kernel<<<grid, 256, 0, stream>>>(codes, scales, N, K, tiles, stiles);
     return cudaGetLastError();
+}
+
+cudaError_t launch_mx4_act_tiles(const Mx4Source& src, const Mx4Plan& plan, int K, uint8_t* tiles, uint8_t* stiles,
+                                 int sms, cudaStream_t stream) {
+    const int segs = (mx4_kb(K) + kSegment - 1) / kSegment;
+    const int64_t want = (static_cast<int64_t>(plan.R) * segs + 7) / 8;
+    const unsigned grid = static_cast<unsigned>(want < sms * 8 ? want : sms * 8);
+    const bool vec = src.codes || fits(src.x.p, src.x.ld, src.x.f32);
+    auto go = [&](auto kern) {
+        kern<<<grid, kPlanThreads, 0, stream>>>(src, plan, K, tiles, stiles);
+        return cudaGetLastError();
+    };
+    if (src.codes) return go(act_tiles_kernel<2, true, false>);
+    if (src.x.f32) {
+        if (src.act) return vec ? go(act_tiles_kernel<1, true, true>) : go(act_tiles_kernel<1, false, true>);
+        return vec ? go(act_tiles_kernel<1, true, false>) : go(act_tiles_kernel<1, false, false>);
+    }
+    if (src.act) return vec ? go(act_tiles_kernel<0, true, true>) : go(act_tiles_kernel<0, false, true>);
+    return vec ? go(act_tiles_kernel<0, true, false>) : go(act_tiles_kernel<0, false, false>);
 }
 
 }  // namespace moeq

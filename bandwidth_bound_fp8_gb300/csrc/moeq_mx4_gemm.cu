@@ -7,10 +7,9 @@
 // are the MMA's 128-row operand and tokens its N operand, so a decode batch
 // (one or two rows an expert) wastes no tensor time on padding and the same
 // kernel serves one token and a prompt: N is the tile's rows, rounded to 16.
-//   warp 0      weight tiles (one 16 KiB and one 1 KiB bulk copy a stage) and
-//               the tokens' codes (TMA gathers, four rows each)
+//   warp 0      copies: a stage is a weight tile (16 KiB), a token tile's K
+//               block and both scale blocks, all contiguous (bulk copies)
 //   warp 1      issues the MMAs (one thread)
-//   warps 2, 3  the tokens' block scales, to the order the tensor core reads
 //   warps 4..7  epilogue: TMEM -> y, behind the next unit's MMAs (two
 //               accumulators)
 // Work split: with many units each CTA takes whole ones, round robin.  With
@@ -19,19 +18,23 @@
 // arrives last sums them in the order of K, so the result does not depend on
 // which one that is.  No CTA ever waits for another.
 #include "moeq_device.cuh"
+#include "moeq_mx4_plan.cuh"
 #include "moeq_rows.h"
 
 namespace moeq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kPlanThreads;
 constexpr int kMaxStages = 12;
-constexpr int kMaxTileRows = 240;
 // Whole units from this many a CTA on (below, the stages are dealt evenly).
 constexpr int kWholeWaves = 8;
 // TMEM columns: accumulators at 0 and 256, the tokens' scales in between and
 // the weights' behind.
 constexpr int kTmemCols = 512, kAcc1 = 256, kColSfb = 240, kColSfa = 496;
+
+__host__ __device__ constexpr int stage_bytes_of(int nt) {
+    return (kMx4TileBytes + nt * 128 + kMx4TileScaleBytes + mx4_tile_scale_bytes(nt) + 1023) / 1024 * 1024;
+}
 
 struct Sched {
     int units, kb, grid, cta;
@@ -39,16 +42,15 @@ struct Sched {
     long long s0, s1;   // this CTA's stages (dealt mode)
 };
 struct Part {
-    int u, n0, r0, n, kb0, kb1, e, nb;
+    int u, n0, r0, n, kb0, kb1, tile, e, nb;
 };
 
 __device__ __forceinline__ long long deal(long long stages, int c, int grid) { return stages * c / grid; }
 
-__device__ __forceinline__ int offs_clamped(const int32_t* offs, int e, int R) { return min(max(__ldg(offs + e), 0), R); }
-
-// The i-th part of this CTA; false past its last.  cum[e] = units before
-// expert e.
-__device__ __forceinline__ bool part_at(const Sched& s, const Mx4GemmArgs& a, const int* cum, int i, Part& p) {
+// The i-th part of this CTA; false past its last.  A unit's number counts
+// experts, then weight blocks, then token tiles: neighbours read the same
+// weights.
+__device__ __forceinline__ bool part_at(const Sched& s, const Mx4GemmArgs& a, const PlanShared& plan, int i, Part& p) {
     if (s.whole) {
         p.u = s.cta + i * s.grid;
         if (p.u >= s.units) return false;
@@ -63,39 +65,19 @@ __device__ __forceinline__ bool part_at(const Sched& s, const Mx4GemmArgs& a, co
         p.kb0 = static_cast<int>(lo - u * s.kb);
         p.kb1 = static_cast<int>(hi - u * s.kb);
     }
-    int lo = 0, hi = a.E;  // the expert: cum[lo] <= u < cum[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= p.u)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    const int r0 = offs_clamped(a.offs, lo, a.R), cnt = max(offs_clamped(a.offs, lo + 1, a.R) - r0, 0);
-    const int tiles = max((cnt + a.nt - 1) / a.nt, 1);
-    const int per = ((cnt + tiles - 1) / tiles + 15) & ~15;
-    const int local = p.u - cum[lo];
-    p.e = lo;
+    const int nbt = mx4_nb(a.N), nt = a.plan.nt;
+    const int e = plan_find(plan.tile, a.plan.E, p.u / nbt);  // experts without tiles are never the last such
+    const int r0 = plan.first[e], cnt = plan.first[e + 1] - r0;
+    const int tiles = plan.tile[e + 1] - plan.tile[e], per = plan_rows_per_tile(cnt, nt);
+    const int local = p.u - plan.tile[e] * nbt;
+    p.e = e;
     p.nb = local / tiles;
     p.n0 = p.nb * kMx4TileRows;
-    const int t0 = (local - p.nb * tiles) * per;
-    p.r0 = r0 + t0;
-    p.n = min(per, cnt - t0);
+    const int t = local - p.nb * tiles;
+    p.tile = plan.tile[e] + t;
+    p.r0 = r0 + t * per;
+    p.n = min(per, cnt - t * per);
     return true;
-}
-
-__device__ __forceinline__ int act_row(const Mx4GemmArgs& a, int r) {
-    const int row = a.row_pair ? max(__ldg(a.row_pair + r), 0) / a.top_k : r;
-    return min(row, a.a_rows - 1);
-}
-
-__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, int col, int r0, int r1, int r2, int r3,
-                                        uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-        "%5, %6}], [%7];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
-        : "memory");
 }
 
 // 512 bytes of scales (32 rows of 16 bytes) into four TMEM columns of all four
@@ -136,24 +118,23 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
 }
 
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const Mx4GemmArgs a, const __grid_constant__ CUtensorMap map) {
+__global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4GemmArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full_tx[kMaxStages], full_sf[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_base_s;
-    __shared__ int abort_s, go_s[2], last_s[2], warp_sum[kThreads / 32];
-    __shared__ int cum[MOEQ_MAX_EXPERTS + 1];
+    __shared__ int abort_s, go_s[2], last_s[2];
+    __shared__ PlanShared plan;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int sfb_chunk = a.nt > 128 ? 1024 : 512;
-    const int off_b = kMx4TileBytes, off_sfa = off_b + a.nt * 128, off_sfb = off_sfa + kMx4TileScaleBytes;
-    const int stage_bytes = (off_sfb + 2 * sfb_chunk + 1023) & ~1023;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nt = a.plan.nt;
+    const int sfb_bytes = mx4_tile_scale_bytes(nt), sfb_chunk = sfb_bytes / 2;
+    const int off_b = kMx4TileBytes, off_sfa = off_b + nt * 128, off_sfb = off_sfa + kMx4TileScaleBytes;
+    const int stage_bytes = stage_bytes_of(nt);
     volatile int* abort = &abort_s;
 
     if (tid == 0) {
         abort_s = 0;
         for (int s = 0; s < a.stages; ++s) {
-            mbar_init(&full_tx[s], 1);
-            mbar_init(&full_sf[s], 1);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -167,39 +148,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const Mx4GemmArgs
         tmem_alloc(&tmem_base_s, kTmemCols);
         tc_fence_before();
     }
-    // Units before each expert: four experts a thread, scanned over the block.
-    const int nbt = mx4_nb(a.N);
-    int mine[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = tid * 4 + i;
-        mine[i] = sum;
-        if (e < a.E) {
-            const int lo = offs_clamped(a.offs, e, a.R);
-            sum += (max(offs_clamped(a.offs, e + 1, a.R) - lo, 0) + a.nt - 1) / a.nt * nbt;
-        }
-    }
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    int before = inc - sum, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        total += warp_sum[w];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (tid * 4 + i < a.E) cum[tid * 4 + i] = before + mine[i];
-    if (tid == 0) cum[a.E] = total;
-    __syncthreads();
+    plan_scan(a.plan, plan);  // ends in a block barrier
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
+    const int nbt = mx4_nb(a.N), total = plan.tile[a.plan.E] * nbt;
 
     Sched s;
     s.units = total;
@@ -220,59 +172,57 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const Mx4GemmArgs
     };
 
     if (warp == 0) {
-        // ------------------------------------------------------ producer
-        pdl_wait();
-        const uint64_t policy = l2_evict_first_policy();
-        int it = 0;
-        Part p;
-        for (int i = 0; !*abort && part_at(s, a, cum, i, p); ++i) {
-            const int n16 = (p.n + 15) & ~15;
-            int row[8];  // gather lane, and lane + 32: four rows each (past the tile: its first row again)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = (j >> 2) * 128 + lane * 4 + (j & 3);
-                row[j] = c < n16 ? act_row(a, p.r0 + (c < p.n ? c : 0)) : 0;
-            }
-            const int64_t tile0 = (static_cast<int64_t>(p.e) * nbt + p.nb) * s.kb;
-            for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
-                const int st = it % a.stages;
-                if (it >= a.stages) {
-                    bool ok = lane != 0 || mbar_wait_bounded(&empty[st], ((it / a.stages) - 1) & 1, abort);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) {
-                        if (lane == 0) give_up();
-                        __syncwarp();
-                        break;
+        // -------------------------------------------------------- copies
+        if (lane == 0) {
+            const uint64_t once = l2_evict_first_policy(), keep = l2_evict_last_policy();
+            auto weights = [&](const Part& p, int kb, int st) {
+                const int64_t tile = (static_cast<int64_t>(p.e) * nbt + p.nb) * s.kb + kb;
+                const int n16 = (p.n + 15) & ~15;
+                mbar_arrive_expect_tx(&full[st], kMx4TileBytes + kMx4TileScaleBytes + n16 * 128 + sfb_bytes);
+                bulk_load(stage_at(st), a.w + tile * kMx4TileBytes, kMx4TileBytes, &full[st], once);
+                bulk_load(stage_at(st) + off_sfa, a.sw + tile * kMx4TileScaleBytes, kMx4TileScaleBytes, &full[st], once);
+            };
+            auto tokens = [&](const Part& p, int kb, int st) {
+                const int64_t block = static_cast<int64_t>(p.tile) * s.kb + kb;
+                const int n16 = (p.n + 15) & ~15;
+                bulk_load(stage_at(st) + off_b, a.a + block * nt * 128, n16 * 128, &full[st], keep);
+                bulk_load(stage_at(st) + off_sfb, a.sa + block * sfb_bytes, sfb_bytes, &full[st], keep);
+            };
+            // The first stages' weights need not wait for the kernel ahead,
+            // which writes the token tiles.
+            Part p;
+            int it = 0, ahead = 0;
+            for (int i = 0; ahead < a.stages && part_at(s, a, plan, i, p); ++i)
+                for (int kb = p.kb0; kb < p.kb1 && ahead < a.stages; ++kb) weights(p, kb, ahead++);
+            pdl_wait();
+            for (int i = 0; (it < ahead || !*abort) && part_at(s, a, plan, i, p); ++i)
+                for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
+                    const int st = it % a.stages;
+                    if (it >= ahead) {
+                        if (!mbar_wait_bounded(&empty[st], ((it / a.stages) - 1) & 1, abort)) {
+                            give_up();
+                            break;
+                        }
+                        weights(p, kb, st);
+                    }
+                    tokens(p, kb, st);
+                }
+            // copies in flight land before the CTA may end
+            if (*abort)
+                for (int j = max(0, it - a.stages); j < it; ++j) {
+                    const unsigned long long t0 = global_timer_ns();
+                    while (!mbar_try_wait(&full[j % a.stages], (j / a.stages) & 1) &&
+                           global_timer_ns() - t0 < kWaitLimitNs) {
                     }
                 }
-                uint8_t* sp = stage_at(st);
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&full_tx[st], kMx4TileBytes + kMx4TileScaleBytes + n16 * 128);
-                    bulk_load(sp, a.w + (tile0 + kb) * kMx4TileBytes, kMx4TileBytes, &full_tx[st], policy);
-                    bulk_load(sp + off_sfa, a.sw + (tile0 + kb) * kMx4TileScaleBytes, kMx4TileScaleBytes, &full_tx[st],
-                              policy);
-                }
-                __syncwarp();
-                if (lane * 4 < n16)
-                    gather4(sp + off_b + lane * 512, &map, kb * 128, row[0], row[1], row[2], row[3], &full_tx[st]);
-                if (128 + lane * 4 < n16)
-                    gather4(sp + off_b + 16384 + lane * 512, &map, kb * 128, row[4], row[5], row[6], row[7],
-                            &full_tx[st]);
-            }
         }
-        // copies in flight land before the CTA may end
-        if (*abort && lane == 0)
-            for (int j = max(0, it - a.stages); j < it; ++j) {
-                const unsigned long long t0 = global_timer_ns();
-                while (!mbar_try_wait(&full_tx[j % a.stages], (j / a.stages) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
-                }
-            }
+        __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMAs
         if (lane == 0) {
             int it = 0;
             Part p;
-            for (int i = 0; !*abort && part_at(s, a, cum, i, p); ++i) {
+            for (int i = 0; !*abort && part_at(s, a, plan, i, p); ++i) {
                 const int buf = i & 1;
                 if (i >= 2 && !mbar_wait_bounded(&acc_empty[buf], ((i >> 1) - 1) & 1, abort)) {
                     give_up();
@@ -285,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const Mx4GemmArgs
                 for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
                     const int st = it % a.stages;
                     const uint32_t ph = (it / a.stages) & 1;
-                    if (!mbar_wait_bounded(&full_tx[st], ph, abort) || !mbar_wait_bounded(&full_sf[st], ph, abort)) {
+                    if (!mbar_wait_bounded(&full[st], ph, abort)) {
                         give_up();
                         break;
                     }
@@ -315,62 +265,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const Mx4GemmArgs
             }
         }
         __syncwarp();
-    } else if (warp < 4) {
-        // ------------------------------------------------- tokens' scales
-        pdl_wait();
-        const int pitch = mx4_scale_pitch(a.K);
-        int it = 0;
-        Part p;
-        for (int i = 0; !*abort && part_at(s, a, cum, i, p); ++i) {
-            const int n16 = (p.n + 15) & ~15;
-            const uint8_t* src[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = j * 32 + lane;
-                src[j] = c < n16 ? a.sa + static_cast<int64_t>(act_row(a, p.r0 + (c < p.n ? c : 0))) * pitch : nullptr;
-            }
-            const int n_stage = p.kb1 - p.kb0, first = ((warp - 2) ^ it) & 1;
-            uint2 next[8];
-            auto fetch = [&](int k) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    next[j] = src[j] ? __ldg(reinterpret_cast<const uint2*>(src[j] + (p.kb0 + k) * 8)) : make_uint2(0, 0);
-            };
-            if (first < n_stage) fetch(first);
-            for (int k = first; k < n_stage; k += 2) {
-                uint2 cur[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) cur[j] = next[j];
-                if (k + 2 < n_stage) fetch(k + 2);
-                const int g = it + k, st = g % a.stages;
-                if (g >= a.stages) {
-                    bool ok = lane != 0 || mbar_wait_bounded(&empty[st], ((g / a.stages) - 1) & 1, abort);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) {
-                        if (lane == 0) give_up();
-                        __syncwarp();
-                        break;
-                    }
-                }
-                uint8_t* sf = stage_at(st) + off_sfb + lane * 16;
-                *reinterpret_cast<uint4*>(sf) = make_uint4(cur[0].x, cur[1].x, cur[2].x, cur[3].x);
-                *reinterpret_cast<uint4*>(sf + sfb_chunk) = make_uint4(cur[0].y, cur[1].y, cur[2].y, cur[3].y);
-                if (n16 > 128) {
-                    *reinterpret_cast<uint4*>(sf + 512) = make_uint4(cur[4].x, cur[5].x, cur[6].x, cur[7].x);
-                    *reinterpret_cast<uint4*>(sf + sfb_chunk + 512) = make_uint4(cur[4].y, cur[5].y, cur[6].y, cur[7].y);
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full_sf[st]);
-            }
-            it += n_stage;
-        }
-    } else {
+    } else if (warp >= 4) {
         // ------------------------------------------------------- epilogue
         pdl_wait();
         const int q = warp - 4;
         Part p;
-        for (int i = 0; part_at(s, a, cum, i, p); ++i) {
+        for (int i = 0; part_at(s, a, plan, i, p); ++i) {
             const int buf = i & 1;
             if (lane == 0 && !mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1, abort)) give_up();
             __syncwarp();
@@ -387,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const Mx4GemmArgs
             const uint32_t acc = tmem + buf * kAcc1 + (static_cast<uint32_t>(q * 32) << 16);
             const int n = p.n0 + q * 32 + lane;
             const bool cut = p.kb0 > 0 || p.kb1 < s.kb;
-            const size_t slot_floats = static_cast<size_t>(a.nt) * 128;
+            const size_t slot_floats = static_cast<size_t>(nt) * 128;
             float* slot = a.part + (static_cast<size_t>(2 * s.cta) + (!s.whole && p.u != s.s0 / s.kb)) * slot_floats +
                           q * 32 + lane;
             for (int c0 = 0; c0 < p.n; c0 += 16) {
@@ -439,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const Mx4GemmArgs
         }
         // rows that belong to no expert
         const int t = tid - 128;
-        for (int64_t r = static_cast<int64_t>(offs_clamped(a.offs, a.E, a.R)) + blockIdx.x; r < a.R; r += gridDim.x)
+        for (int64_t r = static_cast<int64_t>(plan.first[a.plan.E]) + blockIdx.x; r < a.plan.R; r += gridDim.x)
             for (int c = t; c < a.N; c += 128) store_y<kF32>(a.y, r * a.ld_y + c, 0.f);
     }
     tc_fence_before();
@@ -450,30 +350,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const Mx4GemmArgs
     }
 }
 
-int stage_bytes_of(int nt) {
-    const int b = kMx4TileBytes + nt * 128 + kMx4TileScaleBytes + 2 * (nt > 128 ? 1024 : 512);
-    return (b + 1023) / 1024 * 1024;
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder (the library links the runtime only).
-EncodeTiled encode_tiled() {
-    static const EncodeTiled f = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return f;
-}
-
 }  // namespace
 
 // Rows of a token tile.  About twice the average of an expert, so that most
@@ -482,24 +358,14 @@ EncodeTiled encode_tiled() {
 int mx4_tile_rows(int R, int E) {
     const long long want = 2LL * R / E + 16;
     const int r16 = (R + 15) / 16 * 16;
-    const int w16 = static_cast<int>(want > kMaxTileRows ? kMaxTileRows : (want + 15) / 16 * 16);
+    const int w16 = static_cast<int>(want > kMx4MaxTileRows ? kMx4MaxTileRows : (want + 15) / 16 * 16);
     const int nt = E == 1 ? r16 : w16;
-    return nt < r16 ? (nt > kMaxTileRows ? kMaxTileRows : nt) : (r16 > kMaxTileRows ? kMaxTileRows : r16);
+    return nt < r16 ? (nt > kMx4MaxTileRows ? kMx4MaxTileRows : nt) : (r16 > kMx4MaxTileRows ? kMx4MaxTileRows : r16);
 }
 
 cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stream) {
-    CUtensorMap map;
-    const EncodeTiled enc = encode_tiled();
-    if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K / 2), static_cast<cuuint64_t>(a.a_rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.K / 2)};
-    const cuuint32_t box[2] = {128, 1}, es[2] = {1, 1};
-    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.a), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    const int sb = stage_bytes_of(a.nt);
-    const int budget = 220 * 1024;
+    const int sb = stage_bytes_of(a.plan.nt);
+    const int budget = 216 * 1024;  // of 227 KiB, with the static arrays and the alignment
     a.stages = budget / sb < kMaxStages ? budget / sb : kMaxStages;
     const int smem = a.stages * sb + 1024;
     auto kern = a.y_f32 ? mx4_gemm_kernel<true> : mx4_gemm_kernel<false>;
@@ -515,7 +381,7 @@ cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stre
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, a, map);
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace moeq

@@ -3,7 +3,6 @@
 // arguments of the C ABI and calls these.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -64,26 +63,55 @@ cudaError_t launch_mx4_quant_weight(const void* w, int w_f32, int E, int N, int 
 cudaError_t launch_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, uint8_t* tiles,
                                    uint8_t* stiles, cudaStream_t stream);
 
-struct Mx4GemmArgs {
-    const uint8_t* w;       // tiles
-    const uint8_t* sw;      // scale tiles
-    const uint8_t* a;       // activation codes [a_rows, K/2]
-    const uint8_t* sa;      // activation scales [a_rows, pitch]
-    const int32_t* offs;    // [E + 1]
+// A product's rows, quantised and laid out in token tiles as the tensor core
+// reads them: tile g of expert e holds up to nt of its rows; K block kb of it
+// is nt rows of 128 bytes at ((g * KB + kb) * nt) * 128 (chunks rotated as in
+// a weight tile), its scales mx4_tile_scale_bytes(nt) at (g * KB + kb) times
+// that (a weight tile's order, one more 512 bytes for rows 128..).
+constexpr int kMx4MaxTileRows = 240;
+constexpr int kMx4Tickets = 4096;
+__host__ __device__ constexpr int mx4_tile_scale_bytes(int nt) { return nt > 128 ? 2048 : 1024; }
+// Most rows of one token tile for R rows over E experts (a multiple of 16).
+int mx4_tile_rows(int R, int E);
+// Most token tiles there can be.
+__host__ __device__ constexpr int64_t mx4_max_tiles(int R, int E, int nt) { return R / nt + (E < R ? E : R); }
+
+// Which activation row each row reads, and where it lies.
+struct Mx4Plan {
+    const int32_t* offs;      // [E + 1]
     const int32_t* row_pair;  // [R] or NULL: row r reads activation row r
+    int E, R, top_k, rows;    // rows: activation rows
+    int nt;
+};
+
+// Source of the tiles: a matrix to quantise (act as in
+// launch_mx4_quant_act), or codes and scales made beforehand.
+struct Mx4Source {
+    RowsIn x;
+    int act;
+    const uint8_t* codes;     // NULL: x is quantised
+    const uint8_t* scales;
+};
+cudaError_t launch_mx4_act_tiles(const Mx4Source& src, const Mx4Plan& plan, int K, uint8_t* tiles, uint8_t* stiles,
+                                 int sms, cudaStream_t stream);
+
+struct Mx4GemmArgs {
+    const uint8_t* w;       // weight tiles and their scales
+    const uint8_t* sw;
+    const uint8_t* a;       // token tiles and their scales
+    const uint8_t* sa;
+    Mx4Plan plan;
     void* y;
     int64_t ld_y;
     int y_f32;
-    int a_rows, K, N, E, R, top_k;
-    int nt;                 // most rows of one token tile (multiple of 16)
+    int K, N;
     int stages;
     int* tickets;           // kMx4Tickets, zero between launches
     float* part;            // 2 * grid slots of nt * 128 floats
     int* status;
 };
-constexpr int kMx4Tickets = 4096;
-// Most rows of one token tile for R rows over E experts.
-int mx4_tile_rows(int R, int E);
+// pdl: start while the kernel ahead on the stream (which writes the token
+// tiles, and nothing else of the arguments) runs.
 cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stream);
 
 }  // namespace moeq

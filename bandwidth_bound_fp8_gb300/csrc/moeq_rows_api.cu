@@ -40,6 +40,10 @@ Device current_device() {
 
 constexpr int64_t kMaxPairs = int64_t(1) << 30;  // T * top_k and R: row numbers stay in 31 bits
 constexpr int kMaxWidth = 1 << 20;               // H and N
+// Rows of a gathered product from which the activations are quantised once,
+// in token order, and their codes gathered; below, each row is quantised as
+// it is gathered (one launch less, top_k times the arithmetic).
+constexpr int kQuantOnceRows = 4096;
 
 inline bool al(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
 inline bool type_ok(moeq_dtype t) { return t == MOEQ_BF16 || t == MOEQ_F32; }
@@ -58,16 +62,24 @@ bool rows_ok(const void* p, moeq_dtype t, int64_t ld, int64_t width) {
     return type_ok(t) && al(p, size_of(t)) && ld >= width;
 }
 
+// A product's workspace: the header (status word), the tickets of units cut
+// between CTAs, row-major codes and scales (rows quantised once before they
+// are gathered), the token tiles and their scales, and the parts' sums.
 struct Mx4Ws {
-    size_t tickets, codes, scales, part, end;
+    size_t tickets, codes, scales, tiles, stiles, part, end;
+    int nt;
 };
 Mx4Ws mx4_ws(int64_t rows, int K, int E, int R, int sms) {
     Mx4Ws l;
-    l.tickets = 256;  // the header: the status word
+    l.nt = mx4_tile_rows(R > 0 ? R : 1, E);
+    const size_t blocks = static_cast<size_t>(mx4_max_tiles(R > 0 ? R : 1, E, l.nt)) * mx4_kb(K);
+    l.tickets = 256;
     l.codes = l.tickets + up256(kMx4Tickets * sizeof(int));
     l.scales = l.codes + up256(static_cast<size_t>(rows) * (K / 2));
-    l.part = l.scales + up256(static_cast<size_t>(rows) * mx4_scale_pitch(K));
-    l.end = l.part + static_cast<size_t>(2 * sms) * mx4_tile_rows(R > 0 ? R : 1, E) * 128 * sizeof(float);
+    l.tiles = l.scales + up256(static_cast<size_t>(rows) * mx4_scale_pitch(K));
+    l.stiles = l.tiles + up256(blocks * l.nt * 128);
+    l.part = l.stiles + up256(blocks * mx4_tile_scale_bytes(l.nt));
+    l.end = l.part + static_cast<size_t>(2 * sms) * l.nt * 128 * sizeof(float);
     return l;
 }
 
@@ -241,38 +253,37 @@ moeq_status moeq_mx4_expert_gemm(const void* x, moeq_dtype x_dtype, int64_t ld_x
     if (!dev.ok) return MOEQ_ERR_DEVICE;
     const Mx4Ws l = mx4_ws(codes_in ? 0 : rows, K, E, R, dev.sms);
     if (!al(ws, 16) || ws_bytes < l.end) return MOEQ_ERR_WORKSPACE;
-    char* base = static_cast<char*>(ws);
+    uint8_t* u8 = static_cast<uint8_t*>(ws);
+    cudaStream_t st = as_stream(stream);
+    Mx4Source src = {{x, ld_x, x_dtype == MOEQ_F32}, act, nullptr, nullptr};
+    if (codes_in) {
+        src.codes = static_cast<const uint8_t*>(x);
+        src.scales = x_scales;
+    } else if (row_pair_opt && R >= kQuantOnceRows && rows < R) {
+        src.codes = u8 + l.codes;
+        src.scales = u8 + l.scales;
+        if (launch_mx4_quant_act(src.x, rows, K, act, u8 + l.codes, u8 + l.scales, st) != cudaSuccess) return MOEQ_ERR_CUDA;
+    }
     Mx4GemmArgs a = {};
+    a.plan = {offs, row_pair_opt, E, R, top_k, rows, l.nt};
+    if (launch_mx4_act_tiles(src, a.plan, K, u8 + l.tiles, u8 + l.stiles, dev.sms, st) != cudaSuccess)
+        return MOEQ_ERR_CUDA;
     a.w = w;
     a.sw = w_scales;
-    a.a = codes_in ? static_cast<const uint8_t*>(x) : reinterpret_cast<uint8_t*>(base + l.codes);
-    a.sa = codes_in ? x_scales : reinterpret_cast<uint8_t*>(base + l.scales);
-    a.offs = offs;
-    a.row_pair = row_pair_opt;
+    a.a = u8 + l.tiles;
+    a.sa = u8 + l.stiles;
     a.y = y;
     a.ld_y = ld_y;
     a.y_f32 = y_dtype == MOEQ_F32;
-    a.a_rows = rows;
     a.K = K;
     a.N = N;
-    a.E = E;
-    a.R = R;
-    a.top_k = top_k;
-    a.nt = mx4_tile_rows(R, E);
-    a.status = reinterpret_cast<int*>(base);
-    a.tickets = reinterpret_cast<int*>(base + l.tickets);
-    a.part = reinterpret_cast<float*>(base + l.part);
-    if (!codes_in) {
-        const moeq_status st = cuda_status(launch_mx4_quant_act({x, ld_x, x_dtype == MOEQ_F32}, rows, K, act,
-                                                                reinterpret_cast<uint8_t*>(base + l.codes),
-                                                                reinterpret_cast<uint8_t*>(base + l.scales),
-                                                                as_stream(stream)));
-        if (st != MOEQ_OK) return st;
-    }
-    // The product may start while the quantiser right ahead of it runs: it
-    // waits for it before it reads a code, and everything before the
-    // quantiser has ended by then.
-    return cuda_status(launch_mx4_gemm(a, dev.sms, !codes_in, as_stream(stream)));
+    a.status = reinterpret_cast<int*>(u8);
+    a.tickets = reinterpret_cast<int*>(u8 + l.tickets);
+    a.part = reinterpret_cast<float*>(u8 + l.part);
+    // The product may start while the kernel right ahead of it, which fills
+    // the token tiles, runs: it waits for it before it reads one, and
+    // everything before that kernel has ended by then.
+    return cuda_status(launch_mx4_gemm(a, dev.sms, true, st));
 }
 
 }  // extern "C"

@@ -55,69 +55,116 @@ __device__ __forceinline__ uint32_t mx4_block(const float (&v)[8], uint32_t* sca
     return b == kNanScale ? 0u : e2m1x8(v, mx4_inverse(b));
 }
 
-template <bool kF32, bool kVec>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
-    if constexpr (kF32) {
-        const float* f = static_cast<const float*>(p) + at;
+// Eight consecutive elements as they sit in memory: loaded early, converted
+// when they are used.
+template <bool kF32>
+struct Raw8 {
+    uint4 a, b;  // b: fp32 alone
+    template <bool kVec>
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
         if constexpr (kVec) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(f)), b = __ldg(reinterpret_cast<const float4*>(f) + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * (kF32 ? 4 : 2));
+            a = __ldg(q);
+            if constexpr (kF32) b = __ldg(q + 1);
         } else {
+            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __ldg(f + i);
+            for (int i = 0; i < (kF32 ? 8 : 4); ++i) {
+                if constexpr (kF32) {
+                    w[i] = __ldg(static_cast<const uint32_t*>(p) + at + i);
+                } else {
+                    const uint16_t* h = static_cast<const uint16_t*>(p) + at + 2 * i;
+                    w[i] = __ldg(h) | static_cast<uint32_t>(__ldg(h + 1)) << 16;
+                }
+            }
+            a = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (kF32) b = make_uint4(w[4], w[5], w[6], w[7]);
         }
-    } else {
-        const __nv_bfloat16* f = static_cast<const __nv_bfloat16*>(p) + at;
-        if constexpr (kVec) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(f));
-            const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+    }
+    __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < (kF32 ? 8 : 4); ++i) {
+            if constexpr (kF32) {
+                v[i] = __uint_as_float(u[i]);
+            } else {
                 v[2 * i] = __uint_as_float(u[i] << 16);
                 v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(__ldg(f + i));
         }
     }
-}
+};
 
 // silu(g) * u.  The fast exponential and division are within a few ulp times
 // |g|, far below the 4-bit rounding that follows.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
-// Rows of activations.  A thread takes eight elements (one or two 16-byte
-// loads, four bytes of codes written), four lanes a block.
+// A warp's segment of a row: kSegment K blocks of 256 columns, eight of each
+// a lane (its loads all issued before the first is used).
+constexpr int kSegment = 4;
+__host__ __device__ constexpr int segments(int K) { return (mx4_kb(K) + kSegment - 1) / kSegment; }
+
 template <bool kF32, bool kVec, bool kSwiglu>
-__global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__ x, int64_t ld, int64_t items, int K,
-                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const bool in = item < items;
-    const int per_row = K >> 3;
-    const int64_t row = in ? item / per_row : 0;
-    const int c = in ? static_cast<int>(item - row * per_row) * 8 : 0;
-    float v[8];
+struct Segment {
+    Raw8<kF32> v[kSegment], u[kSwiglu ? kSegment : 1];
+    __device__ __forceinline__ void load(const void* x, int64_t row0, int seg, int lane, int K) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    if (in) {
-        load8<kF32, kVec>(x, row * ld + c, v);
-        if constexpr (kSwiglu) {
-            float u[8];
-            load8<kF32, kVec>(x, row * ld + K + c, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = swiglu(v[i], u[i]);
+        for (int i = 0; i < kSegment; ++i) {
+            const int c = (seg * kSegment + i) * kMx4TileCols + lane * 8;
+            v[i].zero();
+            if constexpr (kSwiglu) u[i].zero();
+            if (c < K) {
+                v[i].template load<kVec>(x, row0 + c);
+                if constexpr (kSwiglu) u[i].template load<kVec>(x, row0 + K + c);
+            }
         }
     }
-    uint32_t s;
-    const uint32_t q = mx4_block(v, &s);
-    if (!in) return;
-    *reinterpret_cast<uint32_t*>(codes + row * (K >> 1) + (c >> 1)) = q;
-    if ((c & 31) == 0) {
-        uint8_t* sr = scales + row * mx4_scale_pitch(K);
-        sr[c >> 5] = static_cast<uint8_t>(s);
-        if (c + 32 == K)  // the row's scales end on eight bytes
-            for (int i = K >> 5; i < mx4_scale_pitch(K); ++i) sr[i] = 0;
+    // Codes and scale byte of K block i; a column past K gives zeros.
+    __device__ __forceinline__ uint32_t quant(int i, bool in, uint32_t* s) const {
+        float f[8];
+        v[i].get(f);
+        if constexpr (kSwiglu) {
+            float g[8];
+            u[i].get(g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = swiglu(f[j], g[j]);
+        }
+        const uint32_t q = mx4_block(f, s);
+        if (!in) *s = 0;
+        return in ? q : 0u;
+    }
+};
+
+// The four scale bytes of this lane's 128 columns (lanes 0..15, 16..31).
+__device__ __forceinline__ uint32_t scale_word(uint32_t s, int lane) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) word |= __shfl_sync(0xffffffffu, s, (lane & 16) + 4 * j) << (8 * j);
+    return word;
+}
+
+// Rows of activations, one warp a segment.
+template <bool kF32, bool kVec, bool kSwiglu>
+__global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__ x, int64_t ld, int rows, int K,
+                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+    const int lane = threadIdx.x & 31, segs = segments(K);
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t row = item / segs;
+    const int seg = static_cast<int>(item - row * segs);
+    if (row >= rows) return;
+    Segment<kF32, kVec, kSwiglu> g;
+    g.load(x, row * ld, seg, lane, K);
+#pragma unroll
+    for (int i = 0; i < kSegment; ++i) {
+        const int kb = seg * kSegment + i, c = kb * kMx4TileCols + lane * 8;
+        if (kb * kMx4TileCols >= K) break;
+        uint32_t s;
+        const uint32_t q = g.quant(i, c < K, &s);
+        if (c < K) *reinterpret_cast<uint32_t*>(codes + row * (K >> 1) + (c >> 1)) = q;
+        const uint32_t word = scale_word(s, lane);
+        if ((lane & 15) == 0)
+            *reinterpret_cast<uint32_t*>(scales + row * mx4_scale_pitch(K) + kb * 8 + (lane >> 4) * 4) = word;
     }
 }
 
@@ -125,51 +172,63 @@ __global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__
 // significant bits) times a power of two: exact in bf16 and in fp32 (a
 // subnormal of at least 2^-128 fits both).  The scale is applied in two
 // halves, because 2^-127 is no normal number.
-template <typename T>
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) dequant_act_kernel(const uint8_t* __restrict__ codes,
-                                                          const uint8_t* __restrict__ scales, int64_t items, int K,
-                                                          T* __restrict__ out, int64_t ld, int vec) {
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (item >= items) return;
-    const int per_row = K >> 3;
-    const int64_t row = item / per_row;
-    const int c = static_cast<int>(item - row * per_row) * 8;
-    const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (K >> 1) + (c >> 1)));
-    const uint32_t s = __ldg(scales + row * mx4_scale_pitch(K) + (c >> 5));
-    const int half = (static_cast<int>(s) - 127) >> 1, rest = static_cast<int>(s) - 127 - half;
-    const float f0 = pow2_bits(half + 127), f1 = pow2_bits(rest + 127);
-    float v[8];
+                                                          const uint8_t* __restrict__ scales, int rows, int K,
+                                                          T* __restrict__ out, int64_t ld) {
+    const int lane = threadIdx.x & 31, segs = segments(K);
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t row = item / segs;
+    const int seg = static_cast<int>(item - row * segs);
+    if (row >= rows) return;
+    uint32_t q[kSegment], sc[kSegment];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t n = (q >> (4 * i)) & 15u;
-        const uint32_t m = n & 7u;
-        // 0, .5, 1, 1.5, 2, 3, 4, 6: m < 2 has no implicit one
-        float a = m < 2 ? 0.5f * m : pow2_bits(126 + static_cast<int>(m >> 1)) * (1.f + 0.5f * (m & 1u));
-        a = a * f0 * f1;
-        a = s == kNanScale ? __uint_as_float(0x7FFFFFFFu) : a;
-        v[i] = (n & 8u) ? -a : a;
+    for (int i = 0; i < kSegment; ++i) {
+        const int c = (seg * kSegment + i) * kMx4TileCols + lane * 8;
+        q[i] = sc[i] = 0;
+        if (c < K) {
+            q[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (K >> 1) + (c >> 1)));
+            sc[i] = __ldg(scales + row * mx4_scale_pitch(K) + (c >> 5));
+        }
     }
-    T* o = out + row * ld + c;
-    if constexpr (sizeof(T) == 4) {
-        if (vec) {
-            reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = v[i];
-        }
-    } else {
-        uint32_t u[4];
+    for (int i = 0; i < kSegment; ++i) {
+        const int c = (seg * kSegment + i) * kMx4TileCols + lane * 8;
+        if (c >= K) break;
+        const int half = (static_cast<int>(sc[i]) - 127) >> 1, rest = static_cast<int>(sc[i]) - 127 - half;
+        const float f0 = pow2_bits(half + 127), f1 = pow2_bits(rest + 127);
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int j = 0; j < 4; ++j) {
+            uint32_t h;  // two codes to two exact halves
+            asm("{\n .reg .b8 b;\n cvt.u8.u32 b, %1;\n cvt.rn.f16x2.e2m1x2 %0, b;\n}" : "=r"(h) : "r"((q[i] >> (8 * j)) & 0xFFu));
+            const float2 f = f16x2_to_f32x2(h);
+            v[2 * j] = f.x * f0 * f1;
+            v[2 * j + 1] = f.y * f0 * f1;
         }
-        if (vec) {
+        if (sc[i] == kNanScale)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(0x7FFFFFFFu);
+        T* o = out + row * ld + c;
+        if constexpr (sizeof(T) == 4) {
+            if constexpr (kVec) {
+                reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = v[j];
+            }
+        } else if constexpr (kVec) {
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                u[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
             *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __float2bfloat16_rn(v[i]);
+            for (int j = 0; j < 8; ++j) o[j] = __float2bfloat16_rn(v[j]);
         }
     }
 }
@@ -179,9 +238,7 @@ __global__ void __launch_bounds__(256) dequant_act_kernel(const uint8_t* __restr
 __device__ __forceinline__ void store_tile(uint8_t* tile, uint8_t* stile, int r, int lane, uint32_t q, uint32_t s) {
     const int chunk = lane >> 2;
     *reinterpret_cast<uint32_t*>(tile + r * 128 + ((chunk ^ (r & 7)) << 4) + (lane & 3) * 4) = q;
-    uint32_t word = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) word |= __shfl_sync(0xffffffffu, s, (lane & 16) + 4 * i) << (8 * i);
+    const uint32_t word = scale_word(s, lane);
     if ((lane & 15) == 0)
         *reinterpret_cast<uint32_t*>(stile + (lane >> 4) * 512 + (r & 31) * 16 + (r >> 5) * 4) = word;
 }
@@ -196,11 +253,12 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(const void* __restric
 #pragma unroll 4
     for (int r = threadIdx.x >> 5; r < kMx4TileRows; r += 8) {
         const int n = nb * kMx4TileRows + r;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        Raw8<kF32> raw;
+        raw.zero();
         const bool in = n < N && c < K;
-        if (in) load8<kF32, kVec>(w, (static_cast<int64_t>(e) * N + n) * K + c, v);
+        if (in) raw.template load<kVec>(w, (static_cast<int64_t>(e) * N + n) * K + c);
+        float v[8];
+        raw.get(v);
         uint32_t s;
         const uint32_t q = mx4_block(v, &s);
         store_tile(tiles + t * kMx4TileBytes, stiles + t * kMx4TileScaleBytes, r, lane, in ? q : 0u, in ? s : 0u);
@@ -228,68 +286,109 @@ __global__ void __launch_bounds__(256) pack_weight_kernel(const uint8_t* __restr
 
 // The token tiles of a product: rows gathered into expert order, quantised on
 // the way (or copied from codes), and laid out as the tensor core reads them,
-// so that the product fetches a stage with plain bulk copies.  An item is a
-// row's 1024 columns, one warp each; the columns past K of its last block of
-// 256 are zeroed (padding rows of a tile are not: they only reach rows of the
-// product that are not stored).
-constexpr int kSegment = 4;  // K blocks of 256 columns an item
+// so that the product fetches a stage with plain bulk copies.  The columns
+// past K of a row's last block of 256 are zeroed (padding rows of a tile are
+// not: they only reach rows of the product that are not stored).
+struct Place {
+    int64_t block0;  // the row's tile's first K block
+    int pos;         // the row's place in its tile
+};
+__device__ __forceinline__ Place place_of(const PlanShared& plan, const Mx4Plan& p, int r, int kb_all) {
+    const int e = plan_find(plan.first, p.E, r);
+    const int per = plan_rows_per_tile(plan.first[e + 1] - plan.first[e], p.nt);
+    const int in_e = r - plan.first[e], t = in_e / per;
+    return {static_cast<int64_t>(plan.tile[e] + t) * kb_all, in_e - t * per};
+}
+// Byte offset, inside a K block's scales, of the word of row `pos` and the
+// block's 128-column half `kc`.
+__device__ __forceinline__ int scale_at(int pos, int kc, int sb) {
+    return kc * (sb >> 1) + (pos >> 7) * 512 + (pos & 31) * 16 + ((pos >> 5) & 3) * 4;
+}
+__device__ __forceinline__ int act_row(const Mx4Plan& p, int r) {
+    return min(p.row_pair ? max(__ldg(p.row_pair + r), 0) / p.top_k : r, p.rows - 1);
+}
 
-template <int kSrc, bool kVec, bool kSwiglu>  // kSrc: 0 bf16, 1 fp32, 2 codes
-__global__ void __launch_bounds__(kPlanThreads) act_tiles_kernel(Mx4Source src, Mx4Plan p, int K,
-                                                                 uint8_t* __restrict__ tiles,
+// From rows to quantise: a warp takes a segment of a row at a time.  The
+// first one's loads are issued before the plan is known (they need only the
+// row number).
+template <bool kF32, bool kVec, bool kSwiglu>
+__global__ void __launch_bounds__(kPlanThreads) act_tiles_kernel(RowsIn x, Mx4Plan p, int K, uint8_t* __restrict__ tiles,
                                                                  uint8_t* __restrict__ stiles) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ PlanShared plan;
+    const int lane = threadIdx.x & 31, kb_all = mx4_kb(K), segs = segments(K), sb = mx4_tile_scale_bytes(p.nt);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPlanThreads / 32);
+    int64_t it = static_cast<int64_t>(blockIdx.x) * (kPlanThreads / 32) + (threadIdx.x >> 5);
+    auto row_of = [&](int64_t i) { return static_cast<int>(i / segs); };
+    Segment<kF32, kVec, kSwiglu> g;
+    auto load = [&] {
+        const int r = row_of(it);
+        g.load(x.p, act_row(p, r) * x.ld, static_cast<int>(it - static_cast<int64_t>(r) * segs), lane, K);
+    };
+    const int64_t most = static_cast<int64_t>(p.R) * segs;
+    if (it < most) load();
     plan_scan(p, plan);
-    const int lane = threadIdx.x & 31, kb_all = mx4_kb(K), segs = (kb_all + kSegment - 1) / kSegment;
-    const int r_end = plan.first[p.E];
-    const int64_t items = static_cast<int64_t>(r_end) * segs, step = static_cast<int64_t>(gridDim.x) * (kPlanThreads / 32);
-    const int sb = mx4_tile_scale_bytes(p.nt), chunk_bytes = sb / 2;
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kPlanThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
-        const int r = static_cast<int>(it / segs), seg = static_cast<int>(it - static_cast<int64_t>(r) * segs);
-        if (r < plan.first[0]) continue;
-        const int a_row = min(p.row_pair ? max(__ldg(p.row_pair + r), 0) / p.top_k : r, p.rows - 1);
-        float v[kSegment][8], u[kSegment][8];
-        uint32_t q[kSegment], s[kSegment];
+    const int64_t items = static_cast<int64_t>(plan.first[p.E]) * segs;
+    while (it < items) {
+        const int r = row_of(it), seg = static_cast<int>(it - static_cast<int64_t>(r) * segs);
+        if (r >= plan.first[0]) {
+            const Place at = place_of(plan, p, r, kb_all);
+            const int c_at = at.pos * 128 + (((lane >> 2) ^ (at.pos & 7)) << 4) + (lane & 3) * 4;
 #pragma unroll
-        for (int i = 0; i < kSegment; ++i) {
-            const int c = (seg * kSegment + i) * kMx4TileCols + lane * 8;
-            q[i] = s[i] = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = u[i][j] = 0.f;
-            if (c >= K) continue;
-            if constexpr (kSrc == 2) {
-                q[i] = __ldg(reinterpret_cast<const uint32_t*>(src.codes + static_cast<int64_t>(a_row) * (K >> 1) + (c >> 1)));
-                s[i] = __ldg(src.scales + static_cast<int64_t>(a_row) * mx4_scale_pitch(K) + (c >> 5));
-            } else {
-                load8<kSrc == 1, kVec>(src.x.p, a_row * src.x.ld + c, v[i]);
-                if constexpr (kSwiglu) load8<kSrc == 1, kVec>(src.x.p, a_row * src.x.ld + K + c, u[i]);
+            for (int i = 0; i < kSegment; ++i) {
+                const int kb = seg * kSegment + i;
+                if (kb >= kb_all) break;
+                uint32_t s;
+                const uint32_t q = g.quant(i, kb * kMx4TileCols + lane * 8 < K, &s);
+                const uint32_t word = scale_word(s, lane);
+                *reinterpret_cast<uint32_t*>(tiles + (at.block0 + kb) * p.nt * 128 + c_at) = q;
+                if ((lane & 15) == 0)
+                    *reinterpret_cast<uint32_t*>(stiles + (at.block0 + kb) * sb + scale_at(at.pos, lane >> 4, sb)) = word;
             }
         }
-        // where the row lies: its expert, tile and place in it
-        const int e = plan_find(plan.first, p.E, r);
-        const int per = plan_rows_per_tile(plan.first[e + 1] - plan.first[e], p.nt);
-        const int in_e = r - plan.first[e], t = in_e / per, pos = in_e - t * per;
-        const int64_t block0 = static_cast<int64_t>(plan.tile[e] + t) * kb_all + seg * kSegment;
-        const int at = pos * 128 + (((lane >> 2) ^ (pos & 7)) << 4) + (lane & 3) * 4;
-        const int s_at = (lane >> 4) * chunk_bytes + (pos >> 7) * 512 + (pos & 31) * 16 + ((pos >> 5) & 3) * 4;
+        it += step;
+        if (it < items) load();
+    }
+}
+
+// From codes: a warp moves a row, 16 bytes of codes and four scale bytes a
+// lane at a time.
+__global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t* __restrict__ codes,
+                                                                  const uint8_t* __restrict__ scales, Mx4Plan p, int K,
+                                                                  uint8_t* __restrict__ tiles,
+                                                                  uint8_t* __restrict__ stiles) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ PlanShared plan;
+    plan_scan(p, plan);
+    const int lane = threadIdx.x & 31, kb_all = mx4_kb(K), sb = mx4_tile_scale_bytes(p.nt), pitch = mx4_scale_pitch(K);
+    const int chunks = K >> 5, all_chunks = kb_all * 8, r_end = plan.first[p.E];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPlanThreads / 32);
+    for (int64_t r64 = static_cast<int64_t>(blockIdx.x) * (kPlanThreads / 32) + (threadIdx.x >> 5); r64 < r_end;
+         r64 += step) {
+        const int r = static_cast<int>(r64);
+        if (r < plan.first[0]) continue;
+        const int64_t row = act_row(p, r);
+        const uint4* src = reinterpret_cast<const uint4*>(codes + row * (K >> 1));
+        const uint32_t* ssrc = reinterpret_cast<const uint32_t*>(scales + row * pitch);
+        const Place at = place_of(plan, p, r, kb_all);
+        for (int c0 = 0; c0 < all_chunks; c0 += 128) {
+            uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < kSegment; ++i) {
-            if (seg * kSegment + i >= kb_all) break;
-            if constexpr (kSrc != 2) {
-                if constexpr (kSwiglu) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] = swiglu(v[i][j], u[i][j]);
-                }
-                const bool in = (seg * kSegment + i) * kMx4TileCols + lane * 8 < K;
-                q[i] = mx4_block(v[i], &s[i]);
-                if (!in) s[i] = 0;
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + i * 32 + lane;
+                v[i] = c < chunks ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
             }
-            uint32_t word = 0;
+            const int word = c0 / 4 + lane;  // 32 words of 128 columns for 128 chunks of 32
+            const uint32_t w = word * 4 < pitch ? __ldg(ssrc + word) : 0u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) word |= __shfl_sync(0xffffffffu, s[i], (lane & 16) + 4 * j) << (8 * j);
-            *reinterpret_cast<uint32_t*>(tiles + (block0 + i) * p.nt * 128 + at) = q[i];
-            if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(stiles + (block0 + i) * sb + s_at) = word;
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + i * 32 + lane;
+                if (c < all_chunks)
+                    *reinterpret_cast<uint4*>(tiles + ((at.block0 + (c >> 3)) * p.nt + at.pos) * 128 +
+                                              (((c & 7) ^ (at.pos & 7)) << 4)) = v[i];
+            }
+            if (word * 4 < pitch)
+                *reinterpret_cast<uint32_t*>(stiles + (at.block0 + (word >> 1)) * sb + scale_at(at.pos, word & 1, sb)) = w;
         }
     }
 }
@@ -302,12 +401,11 @@ bool fits(const void* p, int64_t ld, int f32) {
 
 cudaError_t launch_mx4_quant_act(RowsIn x, int rows, int K, int act, uint8_t* codes, uint8_t* scales,
                                  cudaStream_t stream) {
-    const int64_t items = static_cast<int64_t>(rows) * (K / 8);
-    const unsigned grid = static_cast<unsigned>((items + 255) / 256);
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(rows) * segments(K) + 7) / 8);
     // the second half of a SwiGLU row starts K elements on: K is a multiple of 32
     const bool vec = fits(x.p, x.ld, x.f32);
     auto go = [&](auto kern) {
-        kern<<<grid, 256, 0, stream>>>(x.p, x.ld, items, K, codes, scales);
+        kern<<<grid, 256, 0, stream>>>(x.p, x.ld, rows, K, codes, scales);
         return cudaGetLastError();
     };
     if (x.f32) {
@@ -320,15 +418,18 @@ cudaError_t launch_mx4_quant_act(RowsIn x, int rows, int K, int act, uint8_t* co
 
 cudaError_t launch_mx4_dequant_act(const uint8_t* codes, const uint8_t* scales, int rows, int K, RowsOut out,
                                    cudaStream_t stream) {
-    const int64_t items = static_cast<int64_t>(rows) * (K / 8);
-    const unsigned grid = static_cast<unsigned>((items + 255) / 256);
-    const int vec = fits(out.p, out.ld, out.f32);
-    if (out.f32)
-        dequant_act_kernel<<<grid, 256, 0, stream>>>(codes, scales, items, K, static_cast<float*>(out.p), out.ld, vec);
-    else
-        dequant_act_kernel<<<grid, 256, 0, stream>>>(codes, scales, items, K, static_cast<__nv_bfloat16*>(out.p),
-                                                     out.ld, vec);
-    return cudaGetLastError();
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(rows) * segments(K) + 7) / 8);
+    const bool vec = fits(out.p, out.ld, out.f32);
+    auto go = [&](auto* o, auto kern) {
+        kern<<<grid, 256, 0, stream>>>(codes, scales, rows, K, o, out.ld);
+        return cudaGetLastError();
+    };
+    if (out.f32) {
+        float* o = static_cast<float*>(out.p);
+        return vec ? go(o, dequant_act_kernel<float, true>) : go(o, dequant_act_kernel<float, false>);
+    }
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out.p);
+    return vec ? go(o, dequant_act_kernel<__nv_bfloat16, true>) : go(o, dequant_act_kernel<__nv_bfloat16, false>);
 }
 
 cudaError_t launch_mx4_quant_weight(const void* w, int w_f32, int E, int N, int K, uint8_t* tiles, uint8_t* stiles,
@@ -352,21 +453,27 @@ cudaError_t launch_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, 
 
 cudaError_t launch_mx4_act_tiles(const Mx4Source& src, const Mx4Plan& plan, int K, uint8_t* tiles, uint8_t* stiles,
                                  int sms, cudaStream_t stream) {
-    const int segs = (mx4_kb(K) + kSegment - 1) / kSegment;
-    const int64_t want = (static_cast<int64_t>(plan.R) * segs + 7) / 8;
-    const unsigned grid = static_cast<unsigned>(want < sms * 8 ? want : sms * 8);
-    const bool vec = src.codes || fits(src.x.p, src.x.ld, src.x.f32);
+    // one wave of resident blocks: each scans the plan once
+    auto grid_of = [&](int64_t warps, int per_sm) {
+        const int64_t blocks = (warps + 7) / 8;
+        return static_cast<unsigned>(blocks < static_cast<int64_t>(sms) * per_sm ? blocks : sms * per_sm);
+    };
+    if (src.codes) {
+        code_tiles_kernel<<<grid_of(plan.R, 8), kPlanThreads, 0, stream>>>(src.codes, src.scales, plan, K, tiles, stiles);
+        return cudaGetLastError();
+    }
+    const bool vec = fits(src.x.p, src.x.ld, src.x.f32);
     auto go = [&](auto kern) {
-        kern<<<grid, kPlanThreads, 0, stream>>>(src, plan, K, tiles, stiles);
+        kern<<<grid_of(static_cast<int64_t>(plan.R) * segments(K), 6), kPlanThreads, 0, stream>>>(src.x, plan, K, tiles,
+                                                                                               stiles);
         return cudaGetLastError();
     };
-    if (src.codes) return go(act_tiles_kernel<2, true, false>);
     if (src.x.f32) {
-        if (src.act) return vec ? go(act_tiles_kernel<1, true, true>) : go(act_tiles_kernel<1, false, true>);
-        return vec ? go(act_tiles_kernel<1, true, false>) : go(act_tiles_kernel<1, false, false>);
+        if (src.act) return vec ? go(act_tiles_kernel<true, true, true>) : go(act_tiles_kernel<true, false, true>);
+        return vec ? go(act_tiles_kernel<true, true, false>) : go(act_tiles_kernel<true, false, false>);
     }
-    if (src.act) return vec ? go(act_tiles_kernel<0, true, true>) : go(act_tiles_kernel<0, false, true>);
-    return vec ? go(act_tiles_kernel<0, true, false>) : go(act_tiles_kernel<0, false, false>);
+    if (src.act) return vec ? go(act_tiles_kernel<false, true, true>) : go(act_tiles_kernel<false, false, true>);
+    return vec ? go(act_tiles_kernel<false, true, false>) : go(act_tiles_kernel<false, false, false>);
 }
 
 }  // namespace moeq

@@ -42,7 +42,7 @@ struct Sched {
     long long s0, s1;   // this CTA's stages (dealt mode)
 };
 struct Part {
-    int u, n0, r0, n, kb0, kb1, tile, e, nb;
+    int u, n0, r0, n, kb0, kb1, tile, tiles, e, nb;
 };
 
 __device__ __forceinline__ long long deal(long long stages, int c, int grid) { return stages * c / grid; }
@@ -71,6 +71,7 @@ __device__ __forceinline__ bool part_at(const Sched& s, const Mx4GemmArgs& a, co
     const int tiles = plan.tile[e + 1] - plan.tile[e], per = plan_rows_per_tile(cnt, nt);
     const int local = p.u - plan.tile[e] * nbt;
     p.e = e;
+    p.tiles = tiles;
     p.nb = local / tiles;
     p.n0 = p.nb * kMx4TileRows;
     const int t = local - p.nb * tiles;
@@ -107,6 +108,11 @@ __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <bool kF32>
@@ -115,6 +121,85 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
         static_cast<float*>(y)[at] = v;
     else
         static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
+}
+
+// v += the other CTAs' parts of 16 columns, all in the order of K (this CTA's
+// own comes from TMEM): four parts' loads in flight at a time.
+__device__ __forceinline__ void sum_parts(const Mx4GemmArgs& a, const Sched& s, const Part& p, long long all_stages,
+                                          int c_lo, int c_hi, size_t slot_floats, int c0, int row, float (&v)[16]) {
+    float sum[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) sum[c] = 0.f;
+    for (int k0 = c_lo; k0 <= c_hi; k0 += 4) {
+        float4 f[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = k0 + j;
+            if (k > c_hi || k == s.cta) continue;
+            const int second = p.u != deal(all_stages, k, s.grid) / s.kb;
+            const float4* slot = reinterpret_cast<const float4*>(a.part + (static_cast<size_t>(2 * k) + second) * slot_floats) +
+                                 c0 / 4 * 128 + row;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) f[j][c] = __ldcg(slot + c * 128);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = k0 + j;
+            if (k > c_hi) continue;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                sum[4 * c] += k == s.cta ? v[4 * c] : f[j][c].x;
+                sum[4 * c + 1] += k == s.cta ? v[4 * c + 1] : f[j][c].y;
+                sum[4 * c + 2] += k == s.cta ? v[4 * c + 2] : f[j][c].z;
+                sum[4 * c + 3] += k == s.cta ? v[4 * c + 3] : f[j][c].w;
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 16; ++c) v[c] = sum[c];
+}
+
+// 16 rows of y (columns of the accumulator) by the four epilogue warps, lane
+// = weight row.  They pass through shared memory, so that a row's 128 values
+// leave as 16-byte pieces; one barrier a call, with the two buffers the
+// caller alternates.  Where y's rows do not divide so, element by element.
+constexpr int kEpiPitch16 = 320, kEpiPitch32 = 528;  // bytes a row: neighbours in other banks
+constexpr int kEpiBytes = 16 * kEpiPitch32;
+template <bool kF32>
+__device__ __forceinline__ void store_chunk(const Mx4GemmArgs& a, const Part& p, int c0, int q, int lane, int n,
+                                            const float (&v)[16], uint8_t* buf, bool vec) {
+    if (!vec) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c0 + c < p.n && n < a.N) store_y<kF32>(a.y, static_cast<int64_t>(p.r0 + c0 + c) * a.ld_y + n, v[c]);
+        return;
+    }
+    constexpr int kPitch = kF32 ? kEpiPitch32 : kEpiPitch16;
+    if constexpr (kF32) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) *reinterpret_cast<float*>(buf + c * kPitch + (q * 32 + lane) * 4) = v[c];
+    } else {
+        // a lane pair swaps halves: the even one keeps row c, the odd c + 1
+        const bool odd = lane & 1;
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
+            const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(got, v[c + 1]) : __floats2bfloat162_rn(v[c], got);
+            *reinterpret_cast<__nv_bfloat162*>(buf + (c + odd) * kPitch + (q * 32 + (lane & ~1)) * 2) = h;
+        }
+    }
+    named_sync(1, 128);
+    constexpr int kPer = kF32 ? 4 : 8, kPieces = 128 / kPer;  // elements of a piece, pieces of a row
+    const int t = q * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < 16 * kPieces / 128; ++i) {
+        const int c = (i * 128 + t) / kPieces, piece = (i * 128 + t) % kPieces;
+        if (c0 + c < p.n && p.n0 + piece * kPer < a.N) {
+            const uint4 w = *reinterpret_cast<const uint4*>(buf + c * kPitch + piece * 16);
+            const int64_t at = static_cast<int64_t>(p.r0 + c0 + c) * a.ld_y + p.n0 + piece * kPer;
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.y) + at * (kF32 ? 4 : 2)) = w;
+        }
+    }
 }
 
 template <bool kF32>
@@ -174,19 +259,22 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
     if (warp == 0) {
         // -------------------------------------------------------- copies
         if (lane == 0) {
-            const uint64_t once = l2_evict_first_policy(), keep = l2_evict_last_policy();
+            // weights that one token tile reads are not read again; those of
+            // several, and the token tiles, come from L2 the next time
+            const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
             auto weights = [&](const Part& p, int kb, int st) {
                 const int64_t tile = (static_cast<int64_t>(p.e) * nbt + p.nb) * s.kb + kb;
+                const uint64_t policy = p.tiles > 1 ? again : once;
                 const int n16 = (p.n + 15) & ~15;
                 mbar_arrive_expect_tx(&full[st], kMx4TileBytes + kMx4TileScaleBytes + n16 * 128 + sfb_bytes);
-                bulk_load(stage_at(st), a.w + tile * kMx4TileBytes, kMx4TileBytes, &full[st], once);
-                bulk_load(stage_at(st) + off_sfa, a.sw + tile * kMx4TileScaleBytes, kMx4TileScaleBytes, &full[st], once);
+                bulk_load(stage_at(st), a.w + tile * kMx4TileBytes, kMx4TileBytes, &full[st], policy);
+                bulk_load(stage_at(st) + off_sfa, a.sw + tile * kMx4TileScaleBytes, kMx4TileScaleBytes, &full[st], policy);
             };
             auto tokens = [&](const Part& p, int kb, int st) {
                 const int64_t block = static_cast<int64_t>(p.tile) * s.kb + kb;
                 const int n16 = (p.n + 15) & ~15;
-                bulk_load(stage_at(st) + off_b, a.a + block * nt * 128, n16 * 128, &full[st], keep);
-                bulk_load(stage_at(st) + off_sfb, a.sa + block * sfb_bytes, sfb_bytes, &full[st], keep);
+                bulk_load(stage_at(st) + off_b, a.a + block * nt * 128, n16 * 128, &full[st], again);
+                bulk_load(stage_at(st) + off_sfb, a.sa + block * sfb_bytes, sfb_bytes, &full[st], again);
             };
             // The first stages' weights need not wait for the kernel ahead,
             // which writes the token tiles.
@@ -269,6 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
         // ------------------------------------------------------- epilogue
         pdl_wait();
         const int q = warp - 4;
+        uint8_t* stage_y = smem + a.stages * stage_bytes;
+        // rows of y in 16-byte pieces
+        const bool vec_y = a.N % (kF32 ? 4 : 8) == 0 && a.ld_y % (kF32 ? 4 : 8) == 0 &&
+                           (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
         Part p;
         for (int i = 0; part_at(s, a, plan, i, p); ++i) {
             const int buf = i & 1;
@@ -279,63 +371,64 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
             // last unit's.)
             if (tid == 128) {
                 go_s[buf] = !*abort;
-                last_s[buf] = 0;
             }
             named_sync(1, 128);
             if (!go_s[buf]) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * kAcc1 + (static_cast<uint32_t>(q * 32) << 16);
             const int n = p.n0 + q * 32 + lane;
-            const bool cut = p.kb0 > 0 || p.kb1 < s.kb;
             const size_t slot_floats = static_cast<size_t>(nt) * 128;
-            float* slot = a.part + (static_cast<size_t>(2 * s.cta) + (!s.whole && p.u != s.s0 / s.kb)) * slot_floats +
-                          q * 32 + lane;
-            for (int c0 = 0; c0 < p.n; c0 += 16) {
-                uint32_t r[16];
-                tmem_ld_nowait<16>(acc + c0, r);
-                tmem_wait_ld();
+            const bool cut = p.kb0 > 0 || p.kb1 < s.kb;
+            // the CTAs that hold the unit's stages: c_lo .. c_hi
+            int c_lo = s.cta, c_hi = s.cta;
+            bool join = false;  // every other part is in the workspace: this CTA sums them
+            if (cut) {
+                const long long f = static_cast<long long>(p.u) * s.kb, l = f + s.kb - 1;
+                while (deal(all_stages, c_lo, s.grid) > f) --c_lo;
+                while (deal(all_stages, c_hi + 1, s.grid) <= l) ++c_hi;
+                if (tid == 128) last_s[buf] = ld_acquire(a.tickets + p.u) == c_hi - c_lo;
+                named_sync(1, 128);
+                join = last_s[buf];
+                if (!join) {
+                    float4* slot = reinterpret_cast<float4*>(
+                                       a.part + (static_cast<size_t>(2 * s.cta) + (p.u != s.s0 / s.kb)) * slot_floats) +
+                                   q * 32 + lane;
+                    for (int c0 = 0; c0 < p.n; c0 += 16) {
+                        uint32_t r[16];
+                        tmem_ld_nowait<16>(acc + c0, r);
+                        tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    if (c0 + c >= p.n) break;
-                    if (cut)
-                        __stcg(slot + (c0 + c) * 128, __uint_as_float(r[c]));
-                    else if (n < a.N)
-                        store_y<kF32>(a.y, static_cast<int64_t>(p.r0 + c0 + c) * a.ld_y + n, __uint_as_float(r[c]));
+                        for (int c = 0; c < 16; c += 4)
+                            __stcg(slot + (c0 + c) / 4 * 128,
+                                   make_float4(__uint_as_float(r[c]), __uint_as_float(r[c + 1]),
+                                               __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])));
+                    }
+                    __threadfence();
+                    named_sync(1, 128);
+                    if (tid == 128) last_s[buf] = atom_add_acq_rel(a.tickets + p.u, 1) == c_hi - c_lo;
+                    named_sync(1, 128);
+                    join = last_s[buf];
+                }
+                if (join) {
+                    __threadfence();
+                    if (tid == 128) a.tickets[p.u] = 0;
+                }
+            }
+            if (!cut || join) {
+                for (int c0 = 0; c0 < p.n; c0 += 16) {
+                    uint32_t r[16];
+                    tmem_ld_nowait<16>(acc + c0, r);
+                    tmem_wait_ld();
+                    float v[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(r[c]);
+                    if (cut) sum_parts(a, s, p, all_stages, c_lo, c_hi, slot_floats, c0, q * 32 + lane, v);
+                    store_chunk<kF32>(a, p, c0, q, lane, n, v, stage_y + ((c0 >> 4) & 1) * kEpiBytes, vec_y);
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[buf]);
-            if (cut) {
-                // the CTAs that hold the unit's stages, and this one's turn
-                const long long f = static_cast<long long>(p.u) * s.kb, l = f + s.kb - 1;
-                int c_lo = static_cast<int>(f * s.grid / all_stages), c_hi = static_cast<int>(l * s.grid / all_stages);
-                while (deal(all_stages, c_lo + 1, s.grid) <= f) ++c_lo;
-                while (deal(all_stages, c_lo, s.grid) > f) --c_lo;
-                while (deal(all_stages, c_hi + 1, s.grid) <= l) ++c_hi;
-                while (deal(all_stages, c_hi, s.grid) > l) --c_hi;
-                __threadfence();
-                named_sync(1, 128);
-                if (tid == 128) {
-                    const int turn = atom_add_acq_rel(a.tickets + p.u, 1);
-                    if (turn == c_hi - c_lo) {
-                        a.tickets[p.u] = 0;
-                        last_s[buf] = 1;
-                    }
-                }
-                named_sync(1, 128);
-                if (last_s[buf]) {
-                    __threadfence();
-                    for (int c = 0; c < p.n; ++c) {
-                        float v = 0.f;
-                        for (int k = c_lo; k <= c_hi; ++k) {
-                            const int second = p.u != deal(all_stages, k, s.grid) / s.kb;
-                            v += __ldcg(a.part + (static_cast<size_t>(2 * k) + second) * slot_floats + c * 128 + q * 32 + lane);
-                        }
-                        if (n < a.N) store_y<kF32>(a.y, static_cast<int64_t>(p.r0 + c) * a.ld_y + n, v);
-                    }
-                }
-            }
         }
         // rows that belong to no expert
         const int t = tid - 128;
@@ -365,9 +458,10 @@ int mx4_tile_rows(int R, int E) {
 
 cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stream) {
     const int sb = stage_bytes_of(a.plan.nt);
-    const int budget = 216 * 1024;  // of 227 KiB, with the static arrays and the alignment
+    // of 227 KiB: less the static arrays, the alignment and the epilogue's buffers
+    const int budget = 216 * 1024 - 2 * kEpiBytes;
     a.stages = budget / sb < kMaxStages ? budget / sb : kMaxStages;
-    const int smem = a.stages * sb + 1024;
+    const int smem = a.stages * sb + 2 * kEpiBytes + 1024;
     auto kern = a.y_f32 ? mx4_gemm_kernel<true> : mx4_gemm_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

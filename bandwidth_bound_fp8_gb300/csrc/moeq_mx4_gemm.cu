@@ -113,7 +113,35 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
     return pol;
 }
+// 16 accumulator columns of this thread's lane, valid after tmem_wait_ld and
+// (so that no use moves above the wait) tmem_use16.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_use16(float* v) {
+    asm volatile(""
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// One lane of a converged warp, the same each time.  tcgen05 instructions take
+// their operands from uniform registers: under an elected predicate the
+// compiler keeps them there, under `lane == 0` it moves them over one by one
+// (a stage of 6 scale copies and 4 MMAs of N = 240: 549 cycles against 717).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+    return p != 0;
+}
+// A bounded wait by a whole warp, with one answer for it.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
+}
 
 template <bool kF32>
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
@@ -123,35 +151,36 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
         static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
 }
 
-// v += the other CTAs' parts of 16 columns, all in the order of K (this CTA's
-// own comes from TMEM): four parts' loads in flight at a time.
-__device__ __forceinline__ void sum_parts(const Mx4GemmArgs& a, const Sched& s, const Part& p, long long all_stages,
-                                          int c_lo, int c_hi, size_t slot_floats, int c0, int row, float (&v)[16]) {
+// The sum of a unit's parts for 16 columns, all in the order of K: this CTA's
+// own (v) comes from TMEM, the others' from the workspace, two parts' loads
+// in flight at a time.  lo_second: the first CTA's part is in its second slot.
+__device__ __forceinline__ void sum_parts(const float* __restrict__ part, size_t slot_floats, int c_lo, int c_hi, int own,
+                                          int lo_second, int c0, int row, float (&v)[16]) {
     float sum[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) sum[c] = 0.f;
-    for (int k0 = c_lo; k0 <= c_hi; k0 += 4) {
-        float4 f[4][4];
+    const size_t at = static_cast<size_t>(c0) * 128 + row * 4;
+    for (int k0 = c_lo; k0 <= c_hi; k0 += 2) {
+        float4 f[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
             const int k = k0 + j;
-            if (k > c_hi || k == s.cta) continue;
-            const int second = p.u != deal(all_stages, k, s.grid) / s.kb;
-            const float4* slot = reinterpret_cast<const float4*>(a.part + (static_cast<size_t>(2 * k) + second) * slot_floats) +
-                                 c0 / 4 * 128 + row;
+            if (k > c_hi || k == own) continue;
+            // only the first of a unit's CTAs can have begun in another unit
+            const float* slot = part + (static_cast<size_t>(2 * k) + (k == c_lo ? lo_second : 0)) * slot_floats + at;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) f[j][c] = __ldcg(slot + c * 128);
+            for (int c = 0; c < 4; ++c) f[j][c] = __ldcg(reinterpret_cast<const float4*>(slot + c * 512));
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
             const int k = k0 + j;
             if (k > c_hi) continue;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                sum[4 * c] += k == s.cta ? v[4 * c] : f[j][c].x;
-                sum[4 * c + 1] += k == s.cta ? v[4 * c + 1] : f[j][c].y;
-                sum[4 * c + 2] += k == s.cta ? v[4 * c + 2] : f[j][c].z;
-                sum[4 * c + 3] += k == s.cta ? v[4 * c + 3] : f[j][c].w;
+                sum[4 * c] += k == own ? v[4 * c] : f[j][c].x;
+                sum[4 * c + 1] += k == own ? v[4 * c + 1] : f[j][c].y;
+                sum[4 * c + 2] += k == own ? v[4 * c + 2] : f[j][c].z;
+                sum[4 * c + 3] += k == own ? v[4 * c + 3] : f[j][c].w;
             }
         }
     }
@@ -159,51 +188,60 @@ __device__ __forceinline__ void sum_parts(const Mx4GemmArgs& a, const Sched& s, 
     for (int c = 0; c < 16; ++c) v[c] = sum[c];
 }
 
-// 16 rows of y (columns of the accumulator) by the four epilogue warps, lane
-// = weight row.  They pass through shared memory, so that a row's 128 values
-// leave as 16-byte pieces; one barrier a call, with the two buffers the
-// caller alternates.  Where y's rows do not divide so, element by element.
-constexpr int kEpiPitch16 = 320, kEpiPitch32 = 528;  // bytes a row: neighbours in other banks
-constexpr int kEpiBytes = 16 * kEpiPitch32;
+// A step of the epilogue: kCols rows of y (columns of the accumulator) by
+// four warps, lane = weight row.  They pass through shared memory, so that a
+// row's 128 values leave as 16-byte pieces; where y's rows do not divide so,
+// element by element.
 template <bool kF32>
-__device__ __forceinline__ void store_chunk(const Mx4GemmArgs& a, const Part& p, int c0, int q, int lane, int n,
-                                            const float (&v)[16], uint8_t* buf, bool vec) {
+struct Epi {
+    static constexpr int kCols = kF32 ? 32 : 64;
+    static constexpr int kPitch = kF32 ? 528 : 320;  // bytes a row: neighbours in other banks
+};
+constexpr int kEpiBytes = 64 * 320;
+static_assert(Epi<true>::kCols * Epi<true>::kPitch <= kEpiBytes, "one buffer serves both types");
+
+template <bool kF32, int kCols>
+__device__ __forceinline__ void store_step(const Mx4GemmArgs& a, const Part& p, int c0, int q, int lane, int n,
+                                           const float (&v)[kCols], uint8_t* buf, bool vec) {
+    constexpr int kPitch = Epi<kF32>::kPitch;
     if (!vec) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
+        for (int c = 0; c < kCols; ++c)
             if (c0 + c < p.n && n < a.N) store_y<kF32>(a.y, static_cast<int64_t>(p.r0 + c0 + c) * a.ld_y + n, v[c]);
         return;
     }
-    constexpr int kPitch = kF32 ? kEpiPitch32 : kEpiPitch16;
+    named_sync(1, 128);  // the step before has left the buffer
     if constexpr (kF32) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) *reinterpret_cast<float*>(buf + c * kPitch + (q * 32 + lane) * 4) = v[c];
+        for (int c = 0; c < kCols; ++c) *reinterpret_cast<float*>(buf + c * kPitch + (q * 32 + lane) * 4) = v[c];
     } else {
         // a lane pair swaps halves: the even one keeps row c, the odd c + 1
         const bool odd = lane & 1;
+        uint8_t* at = buf + odd * kPitch + (q * 32 + (lane & ~1)) * 2;
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) {
+        for (int c = 0; c < kCols; c += 2) {
             const float got = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
-            const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(got, v[c + 1]) : __floats2bfloat162_rn(v[c], got);
-            *reinterpret_cast<__nv_bfloat162*>(buf + (c + odd) * kPitch + (q * 32 + (lane & ~1)) * 2) = h;
+            *reinterpret_cast<__nv_bfloat162*>(at + c * kPitch) =
+                odd ? __floats2bfloat162_rn(got, v[c + 1]) : __floats2bfloat162_rn(v[c], got);
         }
     }
     named_sync(1, 128);
-    constexpr int kPer = kF32 ? 4 : 8, kPieces = 128 / kPer;  // elements of a piece, pieces of a row
-    const int t = q * 32 + lane;
+    constexpr int kPer = kF32 ? 4 : 8, kPieces = 128 / kPer, kRows = 128 / kPieces;  // of a piece; of a row; at a time
+    const int t = q * 32 + lane, piece = t % kPieces, c1 = t / kPieces;
+    if (p.n0 + piece * kPer >= a.N) return;
+    uint8_t* y = static_cast<uint8_t*>(a.y) +
+                 (static_cast<int64_t>(p.r0 + c0 + c1) * a.ld_y + p.n0 + piece * kPer) * (kF32 ? 4 : 2);
+    const int64_t step = a.ld_y * (kRows * (kF32 ? 4 : 2));
+    uint4 w[kCols / kRows];
 #pragma unroll
-    for (int i = 0; i < 16 * kPieces / 128; ++i) {
-        const int c = (i * 128 + t) / kPieces, piece = (i * 128 + t) % kPieces;
-        if (c0 + c < p.n && p.n0 + piece * kPer < a.N) {
-            const uint4 w = *reinterpret_cast<const uint4*>(buf + c * kPitch + piece * 16);
-            const int64_t at = static_cast<int64_t>(p.r0 + c0 + c) * a.ld_y + p.n0 + piece * kPer;
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.y) + at * (kF32 ? 4 : 2)) = w;
-        }
-    }
+    for (int i = 0; i < kCols / kRows; ++i) w[i] = *reinterpret_cast<const uint4*>(buf + (c1 + i * kRows) * kPitch + piece * 16);
+#pragma unroll
+    for (int i = 0; i < kCols / kRows; ++i)
+        if (c0 + c1 + i * kRows < p.n) *reinterpret_cast<uint4*>(y + i * step) = w[i];
 }
 
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4GemmArgs a) {
+__global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4GemmArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_base_s;
@@ -258,98 +296,108 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
 
     if (warp == 0) {
         // -------------------------------------------------------- copies
-        if (lane == 0) {
-            // weights that one token tile reads are not read again; those of
-            // several, and the token tiles, come from L2 the next time
-            const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
-            auto weights = [&](const Part& p, int kb, int st) {
-                const int64_t tile = (static_cast<int64_t>(p.e) * nbt + p.nb) * s.kb + kb;
-                const uint64_t policy = p.tiles > 1 ? again : once;
-                const int n16 = (p.n + 15) & ~15;
+        // weights that one token tile reads are not read again; those of
+        // several, and the token tiles, come from L2 the next time
+        const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
+        auto weights = [&](const Part& p, int kb, int st) {
+            const int64_t tile = (static_cast<int64_t>(p.e) * nbt + p.nb) * s.kb + kb;
+            const uint64_t policy = p.tiles > 1 ? again : once;
+            const int n16 = (p.n + 15) & ~15;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&full[st], kMx4TileBytes + kMx4TileScaleBytes + n16 * 128 + sfb_bytes);
                 bulk_load(stage_at(st), a.w + tile * kMx4TileBytes, kMx4TileBytes, &full[st], policy);
                 bulk_load(stage_at(st) + off_sfa, a.sw + tile * kMx4TileScaleBytes, kMx4TileScaleBytes, &full[st], policy);
-            };
-            auto tokens = [&](const Part& p, int kb, int st) {
-                const int64_t block = static_cast<int64_t>(p.tile) * s.kb + kb;
-                const int n16 = (p.n + 15) & ~15;
+            }
+        };
+        auto tokens = [&](const Part& p, int kb, int st) {
+            const int64_t block = static_cast<int64_t>(p.tile) * s.kb + kb;
+            const int n16 = (p.n + 15) & ~15;
+            if (elect_one()) {
                 bulk_load(stage_at(st) + off_b, a.a + block * nt * 128, n16 * 128, &full[st], again);
                 bulk_load(stage_at(st) + off_sfb, a.sa + block * sfb_bytes, sfb_bytes, &full[st], again);
-            };
-            // The first stages' weights need not wait for the kernel ahead,
-            // which writes the token tiles.
-            Part p;
-            int it = 0, ahead = 0;
-            for (int i = 0; ahead < a.stages && part_at(s, a, plan, i, p); ++i)
-                for (int kb = p.kb0; kb < p.kb1 && ahead < a.stages; ++kb) weights(p, kb, ahead++);
-            pdl_wait();
-            for (int i = 0; (it < ahead || !*abort) && part_at(s, a, plan, i, p); ++i)
-                for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
-                    const int st = it % a.stages;
-                    if (it >= ahead) {
-                        if (!mbar_wait_bounded(&empty[st], ((it / a.stages) - 1) & 1, abort)) {
-                            give_up();
-                            break;
-                        }
-                        weights(p, kb, st);
+            }
+        };
+        // The first stages' weights need not wait for the kernel ahead, which
+        // writes the token tiles.
+        Part p;
+        int ahead = 0;
+        for (int i = 0; ahead < a.stages && part_at(s, a, plan, i, p); ++i)
+            for (int kb = p.kb0; kb < p.kb1 && ahead < a.stages; ++kb) weights(p, kb, ahead++);
+        pdl_wait();
+        int it = 0, st = 0;
+        uint32_t phase = 1;  // of the ring's previous round
+        bool ok = true;
+        for (int i = 0; ok && part_at(s, a, plan, i, p); ++i)
+            for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
+                if (it >= ahead) {
+                    ok = warp_wait(&empty[st], phase, abort);
+                    if (!ok) {
+                        if (lane == 0) give_up();
+                        break;
                     }
-                    tokens(p, kb, st);
+                    weights(p, kb, st);
                 }
-            // copies in flight land before the CTA may end
-            if (*abort)
-                for (int j = max(0, it - a.stages); j < it; ++j) {
-                    const unsigned long long t0 = global_timer_ns();
-                    while (!mbar_try_wait(&full[j % a.stages], (j / a.stages) & 1) &&
-                           global_timer_ns() - t0 < kWaitLimitNs) {
-                    }
+                tokens(p, kb, st);
+                if (++st == a.stages) {
+                    st = 0;
+                    phase ^= 1;
                 }
-        }
+            }
+        // copies in flight land before the CTA may end
+        if (!ok && lane == 0)
+            for (int j = max(0, it - a.stages); j < it; ++j) {
+                const unsigned long long t0 = global_timer_ns();
+                while (!mbar_try_wait(&full[j % a.stages], (j / a.stages) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
+                }
+            }
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMAs
-        if (lane == 0) {
-            int it = 0;
-            Part p;
-            for (int i = 0; !*abort && part_at(s, a, plan, i, p); ++i) {
-                const int buf = i & 1;
-                if (i >= 2 && !mbar_wait_bounded(&acc_empty[buf], ((i >> 1) - 1) & 1, abort)) {
-                    give_up();
-                    break;
-                }
+        int st = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        Part p;
+        for (int i = 0; ok && part_at(s, a, plan, i, p); ++i) {
+            const int buf = i & 1;
+            if (i >= 2) ok = warp_wait(&acc_empty[buf], ((i >> 1) - 1) & 1, abort);
+            tc_fence_after();
+            const int n16 = (p.n + 15) & ~15;
+            const uint32_t d = tmem + buf * kAcc1;
+            const uint32_t id0 = idesc_mx4(n16, 0), id2 = idesc_mx4(n16, 2);
+            for (int kb = p.kb0; ok && kb < p.kb1; ++kb) {
+                ok = warp_wait(&full[st], phase, abort);
+                if (!ok) break;
                 tc_fence_after();
-                const int n16 = (p.n + 15) & ~15;
-                const uint32_t d = tmem + buf * kAcc1;
-                const uint32_t idesc[2] = {idesc_mx4(n16, 0), idesc_mx4(n16, 2)};
-                for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
-                    const int st = it % a.stages;
-                    const uint32_t ph = (it / a.stages) & 1;
-                    if (!mbar_wait_bounded(&full[st], ph, abort)) {
-                        give_up();
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sp = smem_u32(stage_at(st));
+                const uint32_t sp = smem_u32(stage_at(st));
+                const uint64_t fa = sf_desc(sp + off_sfa), fb = sf_desc(sp + off_sfb);
+                const uint64_t ad = umma_desc_sw128(sp), bd = umma_desc_sw128(sp + off_b);
+                if (elect_one()) {
 #pragma unroll
                     for (int kc = 0; kc < 2; ++kc) {
-                        sf_copy(tmem + kColSfa + kc * 4, sf_desc(sp + off_sfa + kc * 512));
-                        sf_copy(tmem + kColSfb + kc * 8, sf_desc(sp + off_sfb + kc * sfb_chunk));
-                        if (n16 > 128) sf_copy(tmem + kColSfb + kc * 8 + 4, sf_desc(sp + off_sfb + kc * sfb_chunk + 512));
+                        sf_copy(tmem + kColSfa + kc * 4, fa + kc * (512 >> 4));
+                        sf_copy(tmem + kColSfb + kc * 8, fb + kc * (sfb_chunk >> 4));
+                        if (n16 > 128) sf_copy(tmem + kColSfb + kc * 8 + 4, fb + kc * (sfb_chunk >> 4) + (512 >> 4));
                     }
-                    const uint64_t ad = umma_desc_sw128(sp), bd = umma_desc_sw128(sp + off_b);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)  // 64 columns = 32 bytes of a row
-                        mma_mx4(d, ad + j * 2, bd + j * 2, idesc[j & 1], tmem + kColSfa + (j >> 1) * 4,
+                        mma_mx4(d, ad + j * 2, bd + j * 2, j & 1 ? id2 : id0, tmem + kColSfa + (j >> 1) * 4,
                                 tmem + kColSfb + (j >> 1) * 8, kb > p.kb0 || j > 0);
                     umma_commit(&empty[st]);
+                    if (kb + 1 == p.kb1) umma_commit(&acc_full[buf]);
                 }
-                if (*abort) break;
-                umma_commit(&acc_full[buf]);
+                __syncwarp();
+                if (++st == a.stages) {
+                    st = 0;
+                    phase ^= 1;
+                }
             }
-            if (*abort) {
-                umma_commit(&drained);
-                const unsigned long long t0 = global_timer_ns();
-                while (!mbar_try_wait(&drained, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
-                }
+        }
+        if (!ok) {
+            if (lane == 0) give_up();
+            __syncwarp();
+            if (elect_one()) umma_commit(&drained);
+            const unsigned long long t0 = global_timer_ns();
+            while (!mbar_try_wait(&drained, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
         }
         __syncwarp();
@@ -394,14 +442,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
                                        a.part + (static_cast<size_t>(2 * s.cta) + (p.u != s.s0 / s.kb)) * slot_floats) +
                                    q * 32 + lane;
                     for (int c0 = 0; c0 < p.n; c0 += 16) {
-                        uint32_t r[16];
-                        tmem_ld_nowait<16>(acc + c0, r);
+                        float v[16];
+                        tmem_ld16(acc + c0, v);
                         tmem_wait_ld();
+                        tmem_use16(v);
 #pragma unroll
                         for (int c = 0; c < 16; c += 4)
-                            __stcg(slot + (c0 + c) / 4 * 128,
-                                   make_float4(__uint_as_float(r[c]), __uint_as_float(r[c + 1]),
-                                               __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])));
+                            __stcg(slot + (c0 + c) / 4 * 128, make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]));
                     }
                     __threadfence();
                     named_sync(1, 128);
@@ -414,21 +461,35 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
                     if (tid == 128) a.tickets[p.u] = 0;
                 }
             }
-            if (!cut || join) {
-                for (int c0 = 0; c0 < p.n; c0 += 16) {
-                    uint32_t r[16];
-                    tmem_ld_nowait<16>(acc + c0, r);
-                    tmem_wait_ld();
-                    float v[16];
+            auto release = [&] {  // the accumulator is read: the next unit but one may have it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            };
+            if (!cut) {
+                constexpr int kCols = Epi<kF32>::kCols;
+                for (int c0 = 0; c0 < p.n; c0 += kCols) {
+                    float v[kCols];  // columns past the tile's are read and not stored
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(r[c]);
-                    if (cut) sum_parts(a, s, p, all_stages, c_lo, c_hi, slot_floats, c0, q * 32 + lane, v);
-                    store_chunk<kF32>(a, p, c0, q, lane, n, v, stage_y + ((c0 >> 4) & 1) * kEpiBytes, vec_y);
+                    for (int j = 0; j < kCols; j += 16) tmem_ld16(acc + c0 + j, v + j);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < kCols; j += 16) tmem_use16(v + j);
+                    if (c0 + kCols >= p.n) release();
+                    store_step<kF32, kCols>(a, p, c0, q, lane, n, v, stage_y, vec_y);
                 }
+            } else {
+                const int lo_second = deal(all_stages, c_lo, s.grid) / s.kb != p.u;
+                for (int c0 = 0; join && c0 < p.n; c0 += 16) {
+                    float v[16];
+                    tmem_ld16(acc + c0, v);
+                    tmem_wait_ld();
+                    tmem_use16(v);
+                    sum_parts(a.part, slot_floats, c_lo, c_hi, s.cta, lo_second, c0, q * 32 + lane, v);
+                    store_step<kF32, 16>(a, p, c0, q, lane, n, v, stage_y, vec_y);
+                }
+                release();
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
         // rows that belong to no expert
         const int t = tid - 128;
@@ -459,9 +520,9 @@ int mx4_tile_rows(int R, int E) {
 cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stream) {
     const int sb = stage_bytes_of(a.plan.nt);
     // of 227 KiB: less the static arrays, the alignment and the epilogue's buffers
-    const int budget = 216 * 1024 - 2 * kEpiBytes;
+    const int budget = 216 * 1024 - kEpiBytes;
     a.stages = budget / sb < kMaxStages ? budget / sb : kMaxStages;
-    const int smem = a.stages * sb + 2 * kEpiBytes + 1024;
+    const int smem = a.stages * sb + kEpiBytes + 1024;
     auto kern = a.y_f32 ? mx4_gemm_kernel<true> : mx4_gemm_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

@@ -138,9 +138,20 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(p));
     return p != 0;
 }
-// A bounded wait by a whole warp, with one answer for it.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+// Wait (bounded) for what is in flight after a give-up.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs) {
+    }
 }
 
 template <bool kF32>
@@ -296,82 +307,81 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
 
     if (warp == 0) {
         // -------------------------------------------------------- copies
-        // weights that one token tile reads are not read again; those of
-        // several, and the token tiles, come from L2 the next time
-        const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
-        auto weights = [&](const Part& p, int kb, int st) {
-            const int64_t tile = (static_cast<int64_t>(p.e) * nbt + p.nb) * s.kb + kb;
-            const uint64_t policy = p.tiles > 1 ? again : once;
-            const int n16 = (p.n + 15) & ~15;
-            if (elect_one()) {
+        if (elect_one()) {
+            // weights that one token tile reads are not read again; those of
+            // several, and the token tiles, come from L2 the next time
+            const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
+            auto weights = [&](const Part& p, int kb, int st) {
+                const int64_t tile = (static_cast<int64_t>(p.e) * nbt + p.nb) * s.kb + kb;
+                const uint64_t policy = p.tiles > 1 ? again : once;
+                const int n16 = (p.n + 15) & ~15;
                 mbar_arrive_expect_tx(&full[st], kMx4TileBytes + kMx4TileScaleBytes + n16 * 128 + sfb_bytes);
                 bulk_load(stage_at(st), a.w + tile * kMx4TileBytes, kMx4TileBytes, &full[st], policy);
                 bulk_load(stage_at(st) + off_sfa, a.sw + tile * kMx4TileScaleBytes, kMx4TileScaleBytes, &full[st], policy);
-            }
-        };
-        auto tokens = [&](const Part& p, int kb, int st) {
-            const int64_t block = static_cast<int64_t>(p.tile) * s.kb + kb;
-            const int n16 = (p.n + 15) & ~15;
-            if (elect_one()) {
+            };
+            auto tokens = [&](const Part& p, int kb, int st) {
+                const int64_t block = static_cast<int64_t>(p.tile) * s.kb + kb;
+                const int n16 = (p.n + 15) & ~15;
                 bulk_load(stage_at(st) + off_b, a.a + block * nt * 128, n16 * 128, &full[st], again);
                 bulk_load(stage_at(st) + off_sfb, a.sa + block * sfb_bytes, sfb_bytes, &full[st], again);
-            }
-        };
-        // The first stages' weights need not wait for the kernel ahead, which
-        // writes the token tiles.
-        Part p;
-        int ahead = 0;
-        for (int i = 0; ahead < a.stages && part_at(s, a, plan, i, p); ++i)
-            for (int kb = p.kb0; kb < p.kb1 && ahead < a.stages; ++kb) weights(p, kb, ahead++);
-        pdl_wait();
-        int it = 0, st = 0;
-        uint32_t phase = 1;  // of the ring's previous round
-        bool ok = true;
-        for (int i = 0; ok && part_at(s, a, plan, i, p); ++i)
-            for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
-                if (it >= ahead) {
-                    ok = warp_wait(&empty[st], phase, abort);
-                    if (!ok) {
-                        if (lane == 0) give_up();
-                        break;
+            };
+            // The first stages' weights need not wait for the kernel ahead,
+            // which writes the token tiles.
+            Part p;
+            int ahead = 0;
+            for (int i = 0; ahead < a.stages && part_at(s, a, plan, i, p); ++i)
+                for (int kb = p.kb0; kb < p.kb1 && ahead < a.stages; ++kb) weights(p, kb, ahead++);
+            pdl_wait();
+            int it = 0, st = 0;
+            uint32_t phase = 1;  // of the ring's previous round
+            bool ok = true;
+            for (int i = 0; ok && part_at(s, a, plan, i, p); ++i)
+                for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
+                    if (it >= ahead) {
+                        ok = mbar_wait_bounded(&empty[st], phase, abort);
+                        if (!ok) break;
+                        weights(p, kb, st);
                     }
-                    weights(p, kb, st);
+                    tokens(p, kb, st);
+                    if (++st == a.stages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
-                tokens(p, kb, st);
-                if (++st == a.stages) {
-                    st = 0;
-                    phase ^= 1;
-                }
+            if (!ok) {
+                give_up();
+                // copies in flight land before the CTA may end
+                for (int j = max(0, it - a.stages); j < it; ++j) drain(&full[j % a.stages], (j / a.stages) & 1);
             }
-        // copies in flight land before the CTA may end
-        if (!ok && lane == 0)
-            for (int j = max(0, it - a.stages); j < it; ++j) {
-                const unsigned long long t0 = global_timer_ns();
-                while (!mbar_try_wait(&full[j % a.stages], (j / a.stages) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
-                }
-            }
+        }
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMAs
-        int st = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        Part p;
-        for (int i = 0; ok && part_at(s, a, plan, i, p); ++i) {
-            const int buf = i & 1;
-            if (i >= 2) ok = warp_wait(&acc_empty[buf], ((i >> 1) - 1) & 1, abort);
-            tc_fence_after();
-            const int n16 = (p.n + 15) & ~15;
-            const uint32_t d = tmem + buf * kAcc1;
-            const uint32_t id0 = idesc_mx4(n16, 0), id2 = idesc_mx4(n16, 2);
-            for (int kb = p.kb0; ok && kb < p.kb1; ++kb) {
-                ok = warp_wait(&full[st], phase, abort);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t sp = smem_u32(stage_at(st));
-                const uint64_t fa = sf_desc(sp + off_sfa), fb = sf_desc(sp + off_sfb);
-                const uint64_t ad = umma_desc_sw128(sp), bd = umma_desc_sw128(sp + off_b);
-                if (elect_one()) {
+        // The tensor core's queue holds little: the next stage's barrier is
+        // asked for while this one's last MMAs go out.
+        if (elect_one()) {
+            int st = 0;
+            uint32_t phase = 0;
+            bool ok = true, ready = false;
+            Part p;
+            for (int i = 0; ok && part_at(s, a, plan, i, p); ++i) {
+                const int buf = i & 1;
+                if (i >= 2) ok = mbar_wait_bounded(&acc_empty[buf], ((i >> 1) - 1) & 1, abort);
+                const int n16 = (p.n + 15) & ~15;
+                const uint32_t d = tmem + buf * kAcc1;
+                const uint32_t id0 = idesc_mx4(n16, 0), id2 = idesc_mx4(n16, 2);
+                for (int kb = p.kb0; ok && kb < p.kb1; ++kb) {
+                    if (!ready) ok = mbar_wait_bounded(&full[st], phase, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sp = smem_u32(stage_at(st));
+                    const uint64_t fa = sf_desc(sp + off_sfa), fb = sf_desc(sp + off_sfb);
+                    const uint64_t ad = umma_desc_sw128(sp), bd = umma_desc_sw128(sp + off_b);
+                    uint64_t* const done = &empty[st];
+                    if (++st == a.stages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
 #pragma unroll
                     for (int kc = 0; kc < 2; ++kc) {
                         sf_copy(tmem + kColSfa + kc * 4, fa + kc * (512 >> 4));
@@ -379,25 +389,19 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
                         if (n16 > 128) sf_copy(tmem + kColSfb + kc * 8 + 4, fb + kc * (sfb_chunk >> 4) + (512 >> 4));
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)  // 64 columns = 32 bytes of a row
+                    for (int j = 0; j < 4; ++j) {  // 64 columns = 32 bytes of a row
+                        if (j == 2) ready = mbar_test_wait(&full[st], phase);
                         mma_mx4(d, ad + j * 2, bd + j * 2, j & 1 ? id2 : id0, tmem + kColSfa + (j >> 1) * 4,
                                 tmem + kColSfb + (j >> 1) * 8, kb > p.kb0 || j > 0);
-                    umma_commit(&empty[st]);
-                    if (kb + 1 == p.kb1) umma_commit(&acc_full[buf]);
+                    }
+                    umma_commit(done);
                 }
-                __syncwarp();
-                if (++st == a.stages) {
-                    st = 0;
-                    phase ^= 1;
-                }
+                if (ok) umma_commit(&acc_full[buf]);
             }
-        }
-        if (!ok) {
-            if (lane == 0) give_up();
-            __syncwarp();
-            if (elect_one()) umma_commit(&drained);
-            const unsigned long long t0 = global_timer_ns();
-            while (!mbar_try_wait(&drained, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+            if (!ok) {
+                give_up();
+                umma_commit(&drained);
+                drain(&drained, 0);
             }
         }
         __syncwarp();

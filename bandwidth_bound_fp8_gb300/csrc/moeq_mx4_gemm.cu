@@ -27,7 +27,7 @@ namespace {
 constexpr int kThreads = kPlanThreads;
 constexpr int kMaxStages = 12;
 // Whole units from this many a CTA on (below, the stages are dealt evenly).
-constexpr int kWholeWaves = 8;
+constexpr int kWholeWaves = 4;
 // TMEM columns: accumulators at 0 and 256, the tokens' scales in between and
 // the weights' behind.
 constexpr int kTmemCols = 512, kAcc1 = 256, kColSfb = 240, kColSfa = 496;
@@ -528,7 +528,8 @@ cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stre
     a.stages = budget / sb < kMaxStages ? budget / sb : kMaxStages;
     const int smem = a.stages * sb + kEpiBytes + 1024;
     auto kern = a.y_f32 ? mx4_gemm_kernel<true> : mx4_gemm_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemOnce once[2];
+    const cudaError_t e = once[a.y_f32 != 0].raise(reinterpret_cast<const void*>(kern), budget + kEpiBytes + 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);

@@ -454,6 +454,18 @@ cudaError_t by_type(int f32, F f) {
 
 }  // namespace
 
+cudaError_t SmemOnce::raise(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev < 128;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (known && (done[dev >> 6].load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && known) done[dev >> 6].fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 cudaError_t launch_route_rows(const float* logits, int64_t ld, int T, int E, int k, int32_t* id, float* w,
                               cudaStream_t stream) {
     const int grid = (T + 3) / 4;
@@ -480,8 +492,9 @@ cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* 
     const int warps = min(kSortWarps, max(1, (P + ctas * 32 - 1) / (ctas * 32)));
     const int run = (P + ctas * warps - 1) / (ctas * warps);
     const size_t smem = (static_cast<size_t>(warps) * E + 2 * E) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (kSortWarps + 2) * MOEQ_MAX_EXPERTS * static_cast<int>(sizeof(int)));
+    static SmemOnce once;
+    const cudaError_t e = once.raise(reinterpret_cast<const void*>(expert_sort_kernel),
+                                     (kSortWarps + 2) * MOEQ_MAX_EXPERTS * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);

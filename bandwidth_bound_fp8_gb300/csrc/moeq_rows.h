@@ -7,9 +7,19 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/moeq.h"
 
 namespace moeq {
+
+// Raises a kernel's dynamic shared memory limit to `bytes` on the current
+// device, once a device and kernel (`done`: the kernel's own static, zero).
+// The call costs about a microsecond, a small launch's half.
+struct SmemOnce {
+    std::atomic<uint64_t> done[2]{};  // devices 0 .. 127
+    cudaError_t raise(const void* kernel, int bytes);
+};
 
 // A matrix of rows: base, leading dimension in elements, element type.
 struct RowsIn {

@@ -158,8 +158,16 @@ def _p(t):
     return t.data_ptr()
 
 
+# torch's current stream as a handle: the raw query where this torch has it
+# (0.2 us a call against 3 us through a Stream object).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -405,23 +413,18 @@ def moeq_gemm_ws_count_offset(rows_out, K, rows_in, max_uniq, is_gate_up, which)
 # ------------------------------------------------- any number of tokens
 def _ld(t, name: str = "matrix") -> int:
     """Leading dimension, in elements, of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: a 2-D tensor with contiguous rows is wanted, got shape {tuple(t.shape)}, "
-                         f"strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    sh, st = t.shape, t.stride()
+    if len(sh) != 2 or (st[1] != 1 and sh[1] > 1):
+        raise ValueError(f"{name}: a 2-D tensor with contiguous rows is wanted, got shape {tuple(sh)}, strides {st}")
+    return st[0] if sh[0] > 1 else max(sh[1], st[0])
 
 
 def _packed(t, dtype, shape, name: str):
     """A contiguous tensor of this dtype and shape, or an error that says which is not."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} is wanted, got {t.dtype} "
                          f"{tuple(t.shape)}, strides {t.stride()}")
     return t.data_ptr()
-
-
-def _same(cond: bool, what: str) -> None:
-    if not cond:
-        raise ValueError(what)
 
 
 def moeq_route_rows(logits, topk_id, topk_w, stream=None) -> None:
@@ -429,7 +432,8 @@ def moeq_route_rows(logits, topk_id, topk_w, stream=None) -> None:
     (-1: the row has no expert left), topk_w [T, k] fp32."""
     T, E = logits.shape
     k = topk_id.shape[1]
-    _same(logits.dtype == torch.float32, "logits: fp32 is wanted")
+    if logits.dtype is not torch.float32:
+        raise TypeError(f"unsupported logits dtype {logits.dtype}")
     _check("moeq_route_rows", load().moeq_route_rows(
         logits.data_ptr(), _ld(logits, "logits"), T, E, k, _packed(topk_id, torch.int32, (T, k), "topk_id"),
         _packed(topk_w, torch.float32, (T, k), "topk_w"), _stream(stream)))
@@ -438,7 +442,8 @@ def moeq_route_rows(logits, topk_id, topk_w, stream=None) -> None:
 def moeq_route_rows_grad(d_topk_w, topk_id, topk_w, d_logits, stream=None) -> None:
     T, E = d_logits.shape
     k = topk_id.shape[1]
-    _same(d_logits.dtype == torch.float32, "d_logits: fp32 is wanted")
+    if d_logits.dtype is not torch.float32:
+        raise TypeError(f"unsupported d_logits dtype {d_logits.dtype}")
     _check("moeq_route_rows_grad", load().moeq_route_rows_grad(
         _packed(d_topk_w, torch.float32, (T, k), "d_topk_w"), _packed(topk_id, torch.int32, (T, k), "topk_id"),
         _packed(topk_w, torch.float32, (T, k), "topk_w"), T, E, k, d_logits.data_ptr(), _ld(d_logits, "d_logits"),
@@ -469,8 +474,9 @@ def moeq_gather_rows(x, offs, pair_row, xs, stream=None) -> None:
     T, k, pr = _pairs(pair_row)
     E, of = _offs(offs)
     H = x.shape[1]
-    _same(tuple(x.shape) == (T, H) and tuple(xs.shape) == (T * k, H) and x.dtype == xs.dtype,
-          f"x [{T}, H] and xs [{T * k}, H] of one type are wanted, got {tuple(x.shape)} and {tuple(xs.shape)}")
+    if x.shape != (T, H) or xs.shape != (T * k, H) or x.dtype is not xs.dtype:
+        raise ValueError(f"x [{T}, H] and xs [{T * k}, H] of one type are wanted, got {tuple(x.shape)} and "
+                         f"{tuple(xs.shape)}")
     _check("moeq_gather_rows", load().moeq_gather_rows(
         x.data_ptr(), _dtype(x), _ld(x, "x"), T, H, k, of, E, pr, xs.data_ptr(), _ld(xs, "xs"), _stream(stream)))
 
@@ -479,8 +485,9 @@ def moeq_gather_rows_grad(d_xs, pair_row, d_x, stream=None) -> None:
     """d_x[t] = sum_j d_xs[pair_row[t, j]]."""
     T, k, pr = _pairs(pair_row)
     H = d_x.shape[1]
-    _same(tuple(d_x.shape) == (T, H) and tuple(d_xs.shape) == (T * k, H) and d_x.dtype == d_xs.dtype,
-          f"d_x [{T}, H] and d_xs [{T * k}, H] of one type are wanted, got {tuple(d_x.shape)} and {tuple(d_xs.shape)}")
+    if d_x.shape != (T, H) or d_xs.shape != (T * k, H) or d_x.dtype is not d_xs.dtype:
+        raise ValueError(f"d_x [{T}, H] and d_xs [{T * k}, H] of one type are wanted, got {tuple(d_x.shape)} and "
+                         f"{tuple(d_xs.shape)}")
     _check("moeq_gather_rows_grad", load().moeq_gather_rows_grad(
         d_xs.data_ptr(), _dtype(d_xs), _ld(d_xs, "d_xs"), T, H, k, pr, d_x.data_ptr(), _ld(d_x, "d_x"),
         _stream(stream)))
@@ -490,9 +497,10 @@ def moeq_combine_rows(y, pair_row, topk_w, out, base=None, stream=None) -> None:
     """out[t] = base[t] + sum_j topk_w[t, j] * y[pair_row[t, j]]."""
     T, k, pr = _pairs(pair_row)
     H = out.shape[1]
-    _same(tuple(out.shape) == (T, H) and tuple(y.shape) == (T * k, H),
-          f"out [{T}, H] and y [{T * k}, H] are wanted, got {tuple(out.shape)} and {tuple(y.shape)}")
-    _same(base is None or (tuple(base.shape) == (T, H) and base.dtype == out.dtype), "base: out's shape and type")
+    if out.shape != (T, H) or y.shape != (T * k, H):
+        raise ValueError(f"out [{T}, H] and y [{T * k}, H] are wanted, got {tuple(out.shape)} and {tuple(y.shape)}")
+    if base is not None and (base.shape != (T, H) or base.dtype is not out.dtype):
+        raise ValueError("base: out's shape and type are wanted")
     _check("moeq_combine_rows", load().moeq_combine_rows(
         y.data_ptr(), _dtype(y), _ld(y, "y"), T, H, k, pr, _packed(topk_w, torch.float32, (T, k), "topk_w"), _p(base),
         _ld(base, "base") if base is not None else 0, out.data_ptr(), _dtype(out), _ld(out, "out"), _stream(stream)))
@@ -504,9 +512,9 @@ def moeq_combine_rows_grad(d_out, y, offs, pair_row, topk_w, d_y, d_topk_w, stre
     T, k, pr = _pairs(pair_row)
     E, of = _offs(offs)
     H = d_out.shape[1]
-    _same(tuple(d_out.shape) == (T, H) and tuple(y.shape) == (T * k, H) and tuple(d_y.shape) == (T * k, H) and
-          d_y.dtype == y.dtype, f"d_out [{T}, H], y and d_y [{T * k}, H] are wanted, got {tuple(d_out.shape)}, "
-          f"{tuple(y.shape)} and {tuple(d_y.shape)}")
+    if d_out.shape != (T, H) or y.shape != (T * k, H) or d_y.shape != (T * k, H) or d_y.dtype is not y.dtype:
+        raise ValueError(f"d_out [{T}, H], y and d_y [{T * k}, H] are wanted, got {tuple(d_out.shape)}, "
+                         f"{tuple(y.shape)} and {tuple(d_y.shape)}")
     _check("moeq_combine_rows_grad", load().moeq_combine_rows_grad(
         d_out.data_ptr(), _dtype(d_out), _ld(d_out, "d_out"), y.data_ptr(), _dtype(y), _ld(y, "y"), T, H, k, of, E, pr,
         _packed(topk_w, torch.float32, (T, k), "topk_w"), d_y.data_ptr(), _ld(d_y, "d_y"),
@@ -561,7 +569,8 @@ def _tiles(tiles, scale_tiles, E, N, K):
 def moeq_mx4_quant_weight(w, tiles, scale_tiles, stream=None) -> None:
     """w [E, N, K] bf16 or fp32 -> tiles and scale tiles (mx4_weight_buffers)."""
     E, N, K = w.shape
-    _same(w.is_contiguous(), "w: a contiguous tensor is wanted")
+    if not w.is_contiguous():
+        raise ValueError("w: a contiguous tensor is wanted")
     _check("moeq_mx4_quant_weight", load().moeq_mx4_quant_weight(
         w.data_ptr(), _dtype(w), E, N, K, *_tiles(tiles, scale_tiles, E, N, K), _stream(stream)))
 

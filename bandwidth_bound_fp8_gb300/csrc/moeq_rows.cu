@@ -25,8 +25,8 @@ struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
     uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int, int) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p, int, int) const { *reinterpret_cast<uint4*>(p) = a; }
     __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         const uint32_t u[4] = {a.x, a.y, a.z, a.w};
@@ -49,11 +49,11 @@ struct Raw8<__nv_bfloat16> {
 template <>
 struct Raw8<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
+    __device__ __forceinline__ void load(const float* p, int, int) {
         a = __ldg(reinterpret_cast<const float4*>(p));
         b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
-    __device__ __forceinline__ void store(float* p) const {
+    __device__ __forceinline__ void store(float* p, int, int) const {
         reinterpret_cast<float4*>(p)[0] = a;
         reinterpret_cast<float4*>(p)[1] = b;
     }
@@ -67,19 +67,43 @@ struct Raw8<float> {
         b = make_float4(v[4], v[5], v[6], v[7]);
     }
 };
-// One element, for widths and addresses that eight at a time do not fit.
+// Four elements a block's width (`step`) apart, for widths and addresses that
+// sixteen bytes at a time do not fit: neighbouring threads still touch
+// neighbouring elements, and four loads are in flight (one at a time left a
+// 1001-wide fp32 movement at 39 % of the copy rate).  `left`: columns from
+// the first on.
 template <typename T>
-struct Raw1 {
-    T a;
-    __device__ __forceinline__ void load(const T* p) { a = __ldg(p); }
-    __device__ __forceinline__ void store(T* p) const { *p = a; }
-    __device__ __forceinline__ void zero() { st1(&a, 0.f); }
-    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = static_cast<float>(a); }
-    __device__ __forceinline__ void set(const float (&v)[1]) { st1(&a, v[0]); }
+struct RawS {
+    T a[4];
+    __device__ __forceinline__ void load(const T* p, int left, int step) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i * step < left)
+                a[i] = __ldg(p + i * step);
+            else
+                st1(&a[i], 0.f);
+    }
+    __device__ __forceinline__ void store(T* p, int left, int step) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i * step < left) p[i * step] = a[i];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st1(&a[i], 0.f);
+    }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(a[i]);
+    }
+    __device__ __forceinline__ void set(const float (&v)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st1(&a[i], v[i]);
+    }
 };
 template <typename T, int V>
 struct RawOf {
-    using type = Raw1<T>;
+    using type = RawS<T>;
 };
 template <typename T>
 struct RawOf<T, 8> {
@@ -87,6 +111,12 @@ struct RawOf<T, 8> {
 };
 template <typename T, int V>
 using Raw = typename RawOf<T, V>::type;
+// A thread's first column in block y of a row.
+template <int V>
+__device__ __forceinline__ int first_col(int y) {
+    return V == 8 ? (y * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8
+                  : y * static_cast<int>(blockDim.x) * 4 + static_cast<int>(threadIdx.x);
+}
 
 // ------------------------------------------------------------------ router
 // A logit as an unsigned key that orders as the logit does; 0 for one that
@@ -191,7 +221,22 @@ __global__ void __launch_bounds__(128) route_rows_grad_kernel(const float* __res
 //   3 each warp walks its run again, 32 pairs at a time: the rank among
 //     equal experts in the 32 comes from a match, so the order is the pairs'.
 // No atomic decides an order, so the result is the same every time.
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+// A warp's ids are loaded 16 at a time, all in flight, and a run that fits
+// stays in registers for both walks.  What is left is the scatter of
+// row_pair, one 4-byte sector a pair.
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBatch = 16;
+
+__device__ __forceinline__ void load_ids(const int32_t* __restrict__ id, int64_t b, int64_t end, int E, int lane,
+                                         int (&e)[kSortBatch]) {
+#pragma unroll
+    for (int i = 0; i < kSortBatch; ++i) {
+        const int64_t p = b + i * 32 + lane;
+        e[i] = p < end ? __ldg(id + p) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kSortBatch; ++i)
+        if (e[i] < 0 || e[i] >= E) e[i] = -1;
+}
 
 __global__ void __launch_bounds__(kSortThreads) expert_sort_kernel(const int32_t* __restrict__ id, int P, int E,
                                                                    int warps, int run, int32_t* __restrict__ offs,
@@ -205,27 +250,30 @@ __global__ void __launch_bounds__(kSortThreads) expert_sort_kernel(const int32_t
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = cluster.block_rank(), ctas = cluster.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t p0 = (static_cast<int64_t>(rank) * warps + warp) * run;
+    const int64_t p1 = warp < warps ? min(p0 + run, static_cast<int64_t>(P)) : p0;
+    int* mine = bins + warp * E;
 
+    int e[kSortBatch];
+    load_ids(id, p0, p1, E, lane, e);
     for (int i = tid; i < warps * E; i += kSortThreads) bins[i] = 0;
     __syncthreads();
-    const int64_t p0 = (static_cast<int64_t>(rank) * warps + warp) * run;
-    const int64_t p1 = min(p0 + run, static_cast<int64_t>(P));
-    int* mine = bins + warp * E;
-    if (warp < warps) {
-        for (int64_t p = p0 + lane; p < p1; p += 32) {
-            const int e = __ldg(id + p);
-            if (e >= 0 && e < E) atomicAdd(mine + e, 1);
-        }
+    for (int64_t b = p0; b < p1;) {
+#pragma unroll
+        for (int i = 0; i < kSortBatch; ++i)
+            if (e[i] >= 0) atomicAdd(mine + e[i], 1);
+        b += kSortBatch * 32;
+        if (b < p1) load_ids(id, b, p1, E, lane, e);
     }
     __syncthreads();
-    for (int e = tid; e < E; e += kSortThreads) {
-        int run_sum = 0;
+    for (int x = tid; x < E; x += kSortThreads) {
+        int sum = 0;
         for (int i = 0; i < warps; ++i) {
-            const int c = bins[i * E + e];
-            bins[i * E + e] = run_sum;
-            run_sum += c;
+            const int c = bins[i * E + x];
+            bins[i * E + x] = sum;
+            sum += c;
         }
-        total[e] = run_sum;
+        total[x] = sum;
     }
     cluster.sync();
     // One expert a thread (E <= MOEQ_MAX_EXPERTS = kSortThreads).
@@ -266,21 +314,24 @@ __global__ void __launch_bounds__(kSortThreads) expert_sort_kernel(const int32_t
     if (rank == 0 && tid == 0) offs[E] = kept;
     cluster.sync();  // every CTA has read this one's totals; first[] is written
     if (warp < warps) {
-        for (int e = lane; e < E; e += 32) mine[e] += first[e];
+        for (int x = lane; x < E; x += 32) mine[x] += first[x];
         __syncwarp();
-        for (int64_t b = p0; b < p1; b += 32) {
-            const int64_t p = b + lane;
-            int e = p < p1 ? __ldg(id + p) : -1;
-            if (e < 0 || e >= E) e = -1;
-            const unsigned same = __match_any_sync(0xffffffffu, e);
-            const int ahead = __popc(same & ((1u << lane) - 1u));
-            int row = -1;
-            if (e >= 0) row = mine[e] + ahead;
-            __syncwarp();
-            if (e >= 0 && ahead == 0) mine[e] += __popc(same);
-            __syncwarp();
-            if (p < p1) pair_row[p] = row;
-            if (row >= 0) row_pair[row] = static_cast<int32_t>(p);
+        if (p1 - p0 > kSortBatch * 32) load_ids(id, p0, p1, E, lane, e);
+        for (int64_t b = p0; b < p1;) {
+#pragma unroll
+            for (int i = 0; i < kSortBatch; ++i) {
+                const int64_t p = b + i * 32 + lane;
+                const unsigned same = __match_any_sync(0xffffffffu, e[i]);
+                const int ahead = __popc(same & ((1u << lane) - 1u));
+                const int row = e[i] >= 0 ? mine[e[i]] + ahead : -1;
+                __syncwarp();
+                if (e[i] >= 0 && ahead == 0) mine[e[i]] += __popc(same);
+                __syncwarp();
+                if (p < p1) pair_row[p] = row;
+                if (row >= 0) row_pair[row] = static_cast<int32_t>(p);
+            }
+            b += kSortBatch * 32;
+            if (b < p1) load_ids(id, b, p1, E, lane, e);
         }
     }
     for (int64_t r = kept + static_cast<int64_t>(rank) * kSortThreads + tid; r < P;
@@ -299,22 +350,22 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ 
                                                           const int32_t* __restrict__ offs, int E, int64_t R,
                                                           const int32_t* __restrict__ pair_row, T* __restrict__ xs,
                                                           int64_t ld_xs) {
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
-    if (c >= H) return;
+    const int c = first_col<V>(blockIdx.y), left = H - c, step = blockDim.x;
+    if (left <= 0) return;
     if (blockIdx.x < nt) {
         const int64_t t = blockIdx.x;
         Raw<T, V> v;
-        v.load(x + t * ld_x + c);
+        v.load(x + t * ld_x + c, left, step);
         const int32_t* pr = pair_row + t * k;
         for (int j = 0; j < k; ++j) {
             const int r = __ldg(pr + j);
-            if (r >= 0 && r < R) v.store(xs + r * ld_xs + c);
+            if (r >= 0 && r < R) v.store(xs + r * ld_xs + c, left, step);
         }
     } else {
         Raw<T, V> z;
         z.zero();
         for (int64_t r = max(__ldg(offs + E), 0) + (blockIdx.x - nt); r < R; r += kTailBlocks)
-            z.store(xs + r * ld_xs + c);
+            z.store(xs + r * ld_xs + c, left, step);
     }
 }
 
@@ -327,8 +378,8 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const TY* __restrict_
                                                            int64_t R, const int32_t* __restrict__ pair_row,
                                                            const float* __restrict__ w, const TO* __restrict__ base,
                                                            int64_t ld_base, TO* __restrict__ out, int64_t ld_out) {
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
-    if (c >= H) return;
+    const int c = first_col<V>(blockIdx.y), left = H - c, step = blockDim.x;
+    if (left <= 0) return;
     const int64_t t = blockIdx.x;
     const int32_t* pr = pair_row + t * k;
     float acc[V];
@@ -336,7 +387,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const TY* __restrict_
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     if (base) {
         Raw<TO, V> b;
-        b.load(base + t * ld_base + c);
+        b.load(base + t * ld_base + c, left, step);
         b.get(acc);
     }
     for (int j0 = 0; j0 < k; j0 += 8) {
@@ -349,7 +400,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const TY* __restrict_
             if (j0 + j < k) {
                 const int r = __ldg(pr + j0 + j);
                 if (r >= 0 && r < R) {
-                    v[j].load(y + r * ld_y + c);
+                    v[j].load(y + r * ld_y + c, left, step);
                     ww[j] = kWeighted ? __ldg(w + t * k + j0 + j) : 1.f;
                 }
             }
@@ -364,7 +415,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const TY* __restrict_
     }
     Raw<TO, V> o;
     o.set(acc);
-    o.store(out + t * ld_out + c);
+    o.store(out + t * ld_out + c, left, step);
 }
 
 // ---------------------------------------------------------- combine's grad
@@ -377,12 +428,12 @@ __global__ void __launch_bounds__(256) combine_rows_grad_kernel(
     const TO* __restrict__ dout, int64_t ld_do, const TY* __restrict__ y, int64_t ld_y, int nt, int H, int k,
     const int32_t* __restrict__ offs, int E, int64_t R, const int32_t* __restrict__ pair_row,
     const float* __restrict__ w, TY* __restrict__ dy, int64_t ld_dy, float* __restrict__ dw) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, step = blockDim.x;
     if (blockIdx.x >= nt) {
         Raw<TY, V> z;
         z.zero();
         for (int64_t r = max(__ldg(offs + E), 0) + (blockIdx.x - nt); r < R; r += kTailBlocks)
-            for (int c = tid * V; c < H; c += blockDim.x * V) z.store(dy + r * ld_dy + c);
+            for (int c = first_col<V>(0); c < H; c += step * V) z.store(dy + r * ld_dy + c, H - c, step);
         return;
     }
     __shared__ float red[8][KM];
@@ -401,14 +452,14 @@ __global__ void __launch_bounds__(256) combine_rows_grad_kernel(
             }
         }
     }
-    for (int c = tid * V; c < H; c += blockDim.x * V) {
+    for (int c = first_col<V>(0); c < H; c += step * V) {
         Raw<TO, V> d;
-        d.load(dout + t * ld_do + c);
+        d.load(dout + t * ld_do + c, H - c, step);
         Raw<TY, V> v[KM];
 #pragma unroll
         for (int j = 0; j < KM; ++j) {
             v[j].zero();
-            if (row[j] >= 0) v[j].load(y + row[j] * ld_y + c);
+            if (row[j] >= 0) v[j].load(y + row[j] * ld_y + c, H - c, step);
         }
         float df[V];
         d.get(df);
@@ -424,7 +475,7 @@ __global__ void __launch_bounds__(256) combine_rows_grad_kernel(
             }
             Raw<TY, V> o;
             o.set(g);
-            o.store(dy + row[j] * ld_dy + c);
+            o.store(dy + row[j] * ld_dy + c, H - c, step);
         }
     }
 #pragma unroll
@@ -485,10 +536,13 @@ cudaError_t launch_route_rows_grad(const float* dw, const int32_t* id, const flo
     return cudaGetLastError();
 }
 
+// One CTA up to kSortOneCta pairs, else the largest cluster.
+constexpr int kSortOneCta = 2048, kSortCtas = 16;
+
 cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* offs, int32_t* pair_row,
                                int32_t* row_pair, cudaStream_t stream) {
     const int P = T * k;
-    const int ctas = P <= 2048 ? 1 : 8;
+    const int ctas = P <= kSortOneCta ? 1 : kSortCtas;
     const int warps = min(kSortWarps, max(1, (P + ctas * 32 - 1) / (ctas * 32)));
     const int run = (P + ctas * warps - 1) / (ctas * warps);
     const size_t smem = (static_cast<size_t>(warps) * E + 2 * E) * sizeof(int);
@@ -496,6 +550,8 @@ cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* 
     const cudaError_t e = once.raise(reinterpret_cast<const void*>(expert_sort_kernel),
                                      (kSortWarps + 2) * MOEQ_MAX_EXPERTS * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
+    static const cudaError_t wide = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (wide != cudaSuccess) return wide;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kSortThreads);
@@ -515,7 +571,7 @@ cudaError_t launch_gather_rows(RowsIn x, int T, int H, int k, const int32_t* off
     const bool v8 = H % 8 == 0 && fits8(x.p, x.ld, x.f32) && fits8(xs.p, xs.ld, x.f32);
     return by_type(x.f32, [&](auto* tag) {
         using Ty = std::remove_pointer_t<decltype(tag)>;
-        const int nv = v8 ? H / 8 : H, threads = nv >= 256 ? 256 : (nv + 31) / 32 * 32;
+        const int nv = v8 ? H / 8 : (H + 3) / 4, threads = nv >= 256 ? 256 : (nv + 31) / 32 * 32;
         const dim3 grid(T + kTailBlocks, (nv + threads - 1) / threads);
         const Ty* xp = static_cast<const Ty*>(x.p);
         Ty* sp = static_cast<Ty*>(xs.p);
@@ -523,7 +579,7 @@ cudaError_t launch_gather_rows(RowsIn x, int T, int H, int k, const int32_t* off
             gather_rows_kernel<Ty, 8><<<grid, threads, 0, stream>>>(xp, x.ld, T, H, k, offs, E,
                                                                     static_cast<int64_t>(T) * k, pair_row, sp, xs.ld);
         else
-            gather_rows_kernel<Ty, 1><<<grid, threads, 0, stream>>>(xp, x.ld, T, H, k, offs, E,
+            gather_rows_kernel<Ty, 4><<<grid, threads, 0, stream>>>(xp, x.ld, T, H, k, offs, E,
                                                                     static_cast<int64_t>(T) * k, pair_row, sp, xs.ld);
         return cudaGetLastError();
     });
@@ -538,7 +594,7 @@ cudaError_t launch_combine_rows(RowsIn y, int T, int H, int k, const int32_t* pa
         return by_type(out.f32, [&](auto* to) {
             using TY = std::remove_pointer_t<decltype(ty)>;
             using TO = std::remove_pointer_t<decltype(to)>;
-            const int nv = v8 ? H / 8 : H, threads = nv >= 256 ? 256 : (nv + 31) / 32 * 32;
+            const int nv = v8 ? H / 8 : (H + 3) / 4, threads = nv >= 256 ? 256 : (nv + 31) / 32 * 32;
             const dim3 grid(T, (nv + threads - 1) / threads);
             const TY* yp = static_cast<const TY*>(y.p);
             const TO* bp = static_cast<const TO*>(base.p);
@@ -548,7 +604,7 @@ cudaError_t launch_combine_rows(RowsIn y, int T, int H, int k, const int32_t* pa
                 return cudaGetLastError();
             };
             if (v8) return w ? go(combine_rows_kernel<TY, TO, 8, true>) : go(combine_rows_kernel<TY, TO, 8, false>);
-            return w ? go(combine_rows_kernel<TY, TO, 1, true>) : go(combine_rows_kernel<TY, TO, 1, false>);
+            return w ? go(combine_rows_kernel<TY, TO, 4, true>) : go(combine_rows_kernel<TY, TO, 4, false>);
         });
     });
 }
@@ -571,8 +627,8 @@ cudaError_t launch_combine_rows_grad(RowsIn dout, RowsIn y, int T, int H, int k,
                 return cudaGetLastError();
             };
             if (k <= 8)
-                return v8 ? go(combine_rows_grad_kernel<TY, TO, 8, 8>) : go(combine_rows_grad_kernel<TY, TO, 1, 8>);
-            return v8 ? go(combine_rows_grad_kernel<TY, TO, 8, kMaxK>) : go(combine_rows_grad_kernel<TY, TO, 1, kMaxK>);
+                return v8 ? go(combine_rows_grad_kernel<TY, TO, 8, 8>) : go(combine_rows_grad_kernel<TY, TO, 4, 8>);
+            return v8 ? go(combine_rows_grad_kernel<TY, TO, 8, kMaxK>) : go(combine_rows_grad_kernel<TY, TO, 4, kMaxK>);
         });
     });
 }

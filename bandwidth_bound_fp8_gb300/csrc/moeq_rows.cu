@@ -131,6 +131,20 @@ __device__ __forceinline__ float logit_of_key(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+// key[i] = 0 on this lane, for an i that is the same on all: a tree of
+// branches, so that keys stay in registers at three branches a call.
+template <int N>
+__device__ __forceinline__ void clear_key(uint32_t* key, int i, bool me) {
+    if constexpr (N == 1) {
+        if (me) key[0] = 0u;
+    } else {
+        if (i < N / 2)
+            clear_key<N / 2>(key, i, me);
+        else
+            clear_key<N / 2>(key + N / 2, i - N / 2, me);
+    }
+}
+
 // One warp a row: lane l holds the keys of experts l, l + 32, ...; a round
 // takes the largest key and the lowest id that holds it (two warp
 // reductions), and lane j keeps round j's pick for the softmax.
@@ -160,11 +174,7 @@ __global__ void __launch_bounds__(128) route_rows_kernel(const float* __restrict
         const uint32_t top = __reduce_max_sync(0xffffffffu, best);
         if (!top) break;  // nothing left that may be picked
         const int e = __reduce_min_sync(0xffffffffu, best == top ? lane + 32 * at : 0x7fffffff);
-        if ((e & 31) == lane) {
-#pragma unroll
-            for (int i = 0; i < NPER; ++i)
-                if (i == (e >> 5)) key[i] = 0u;
-        }
+        clear_key<NPER>(key, e >> 5, (e & 31) == lane);
         if (lane == j) {
             my_id = e;
             my_v = logit_of_key(top);
@@ -214,17 +224,29 @@ __global__ void __launch_bounds__(128) route_rows_grad_kernel(const float* __res
 // -------------------------------------------------------------------- sort
 // Stable counting sort of the pairs by expert in ONE launch: one cluster of
 // CTAs, each warp owning a contiguous run of pairs.
-//   1 each warp counts its run's experts (shared memory, its own bins);
+//   1 each warp walks its run 32 pairs at a time, counting experts in bins of
+//     its own.  Ballots over the bits of the id find the equal ones among the
+//     32 (8 ballots for 256 experts; a match instruction took 3 times as
+//     long), so a pair's rank in the run is known as it is counted;
 //   2 the bins are scanned over the CTA's warps, over the cluster's CTAs
 //     (their totals read through distributed shared memory) and over the
 //     experts, which gives every warp its first row of every expert;
-//   3 each warp walks its run again, 32 pairs at a time: the rank among
-//     equal experts in the 32 comes from a match, so the order is the pairs'.
+//   3 a pair's row is its warp's first row of the expert plus its rank.
+//     row_pair is first sorted within the CTA in shared memory and leaves in
+//     runs: scattered, it costs a 4-byte sector a pair and a cycle each.
 // No atomic decides an order, so the result is the same every time.
-// A warp's ids are loaded 16 at a time, all in flight, and a run that fits
-// stays in registers for both walks.  What is left is the scatter of
-// row_pair, one 4-byte sector a pair.
+// A warp's ids are loaded 16 at a time, all in flight.  With up to
+// kSortBatch * 32 pairs a warp (16384 a CTA) ids, ranks and the CTA's sorted
+// pairs stay on the SM; longer runs keep their ranks in pair_row meanwhile
+// and scatter.
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBatch = 16;
+constexpr int kSortLocal = kSortWarps * kSortBatch * 32;  // pairs of a CTA that are sorted in shared memory
+// One CTA up to kSortOneCta pairs (no cluster to meet), else the largest cluster.
+constexpr int kSortOneCta = 2048, kSortCtas = 16;
+
+__host__ __device__ constexpr size_t sort_smem(int warps, int E, bool local) {
+    return (static_cast<size_t>(warps) * E + 3 * E) * sizeof(int) + (local ? 2 * kSortLocal * sizeof(uint16_t) : 0);
+}
 
 __device__ __forceinline__ void load_ids(const int32_t* __restrict__ id, int64_t b, int64_t end, int E, int lane,
                                          int (&e)[kSortBatch]) {
@@ -238,100 +260,144 @@ __device__ __forceinline__ void load_ids(const int32_t* __restrict__ id, int64_t
         if (e[i] < 0 || e[i] >= E) e[i] = -1;
 }
 
+// The lanes that hold this lane's id (ids of `bits` bits; -1 for none).
+__device__ __forceinline__ unsigned same_ids(int e, int bits) {
+    unsigned same = __ballot_sync(0xffffffffu, e >= 0);
+    for (int i = 0; i < bits; ++i) {
+        const unsigned set = __ballot_sync(0xffffffffu, (e >> i) & 1);
+        same &= (e >> i) & 1 ? set : ~set;
+    }
+    return same;
+}
+
+// Exclusive scan over the block of one int a thread; *total gets the sum.
+__device__ __forceinline__ int block_scan(int v, int* scratch, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    __syncthreads();  // scratch may still be read
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    int w = scratch[lane];
+    const int own = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += u;
+    }
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    return __shfl_sync(0xffffffffu, w - own, warp) + inc - v;
+}
+
+template <bool kLocal>
 __global__ void __launch_bounds__(kSortThreads) expert_sort_kernel(const int32_t* __restrict__ id, int P, int E,
-                                                                   int warps, int run, int32_t* __restrict__ offs,
+                                                                   int warps, int run, int bits,
+                                                                   int32_t* __restrict__ offs,
                                                                    int32_t* __restrict__ pair_row,
                                                                    int32_t* __restrict__ row_pair) {
     extern __shared__ int sm[];
     int* bins = sm;                // [warps][E]
     int* total = sm + warps * E;   // [E] this CTA's counts
-    int* first = total + E;        // [E] first row of each expert
-    __shared__ int scan[kSortWarps + 1];
+    int* first = total + E;        // [E] this CTA's first row of each expert
+    int* local = first + E;        // [E] its place in the CTA's sorted pairs
+    uint16_t* sorted = reinterpret_cast<uint16_t*>(local + E);  // the CTA's pairs (from its first on) by expert
+    uint16_t* sorted_e = sorted + kSortLocal;                   // and their experts
+    __shared__ int scratch[kSortWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = cluster.block_rank(), ctas = cluster.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t p0 = (static_cast<int64_t>(rank) * warps + warp) * run;
+    const int64_t cta0 = static_cast<int64_t>(rank) * warps * run, p0 = cta0 + static_cast<int64_t>(warp) * run;
     const int64_t p1 = warp < warps ? min(p0 + run, static_cast<int64_t>(P)) : p0;
     int* mine = bins + warp * E;
 
-    int e[kSortBatch];
+    int e[kSortBatch], ahead[kSortBatch];
     load_ids(id, p0, p1, E, lane, e);
     for (int i = tid; i < warps * E; i += kSortThreads) bins[i] = 0;
     __syncthreads();
     for (int64_t b = p0; b < p1;) {
 #pragma unroll
-        for (int i = 0; i < kSortBatch; ++i)
-            if (e[i] >= 0) atomicAdd(mine + e[i], 1);
+        for (int i = 0; i < kSortBatch; ++i) {
+            const unsigned same = same_ids(e[i], bits);
+            const int before = __popc(same & ((1u << lane) - 1u));
+            const int n = e[i] >= 0 ? mine[e[i]] : 0;
+            ahead[i] = n + before;
+            __syncwarp();
+            if (e[i] >= 0 && before == 0) mine[e[i]] = n + __popc(same);
+            __syncwarp();
+        }
+        if constexpr (!kLocal) {
+#pragma unroll
+            for (int i = 0; i < kSortBatch; ++i)
+                if (b + i * 32 + lane < p1) pair_row[b + i * 32 + lane] = ahead[i];
+        }
         b += kSortBatch * 32;
         if (b < p1) load_ids(id, b, p1, E, lane, e);
     }
     __syncthreads();
-    for (int x = tid; x < E; x += kSortThreads) {
+    if (tid < E) {  // one expert a thread: E <= MOEQ_MAX_EXPERTS = kSortThreads
         int sum = 0;
         for (int i = 0; i < warps; ++i) {
-            const int c = bins[i * E + x];
-            bins[i * E + x] = sum;
+            const int c = bins[i * E + tid];
+            bins[i * E + tid] = sum;
             sum += c;
         }
-        total[x] = sum;
+        total[tid] = sum;
     }
     cluster.sync();
-    // One expert a thread (E <= MOEQ_MAX_EXPERTS = kSortThreads).
-    int before = 0, all = 0;
-    if (tid < E) {
-        for (int c = 0; c < ctas; ++c) {
-            const int v = cluster.map_shared_rank(total, c)[tid];
-            if (c < rank) before += v;
-            all += v;
-        }
-    }
-    int inc = all;
+    int v[kSortCtas], before = 0, all = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
-    if (lane == 31) scan[warp] = inc;
-    __syncthreads();
-    if (warp == 0) {
-        int v = scan[lane];
-        const int own = v;
+    for (int c = 0; c < kSortCtas; ++c) v[c] = tid < E && c < ctas ? cluster.map_shared_rank(total, c)[tid] : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
-        }
-        scan[lane] = v - own;
-        if (lane == 31) scan[32] = v;
+    for (int c = 0; c < kSortCtas; ++c) {
+        if (c < rank) before += v[c];
+        all += v[c];
     }
-    __syncthreads();
-    const int kept = scan[kSortWarps];
+    int kept, in_cta;
+    const int start = block_scan(all, scratch, &kept);
+    const int place = block_scan(tid < E ? total[tid] : 0, scratch, &in_cta);
     if (tid < E) {
-        const int start = scan[warp] + inc - all;
         first[tid] = start + before;
+        local[tid] = place;
         if (rank == 0) offs[tid] = start;
     }
     if (rank == 0 && tid == 0) offs[E] = kept;
     cluster.sync();  // every CTA has read this one's totals; first[] is written
     if (warp < warps) {
-        for (int x = lane; x < E; x += 32) mine[x] += first[x];
-        __syncwarp();
-        if (p1 - p0 > kSortBatch * 32) load_ids(id, p0, p1, E, lane, e);
-        for (int64_t b = p0; b < p1;) {
+        for (int64_t b = p0; b < p1; b += kSortBatch * 32) {
+            if constexpr (!kLocal) {
+                load_ids(id, b, p1, E, lane, e);
+#pragma unroll
+                for (int i = 0; i < kSortBatch; ++i) {
+                    const int64_t p = b + i * 32 + lane;
+                    ahead[i] = p < p1 ? pair_row[p] : 0;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kSortBatch; ++i) {
                 const int64_t p = b + i * 32 + lane;
-                const unsigned same = __match_any_sync(0xffffffffu, e[i]);
-                const int ahead = __popc(same & ((1u << lane) - 1u));
-                const int row = e[i] >= 0 ? mine[e[i]] + ahead : -1;
-                __syncwarp();
-                if (e[i] >= 0 && ahead == 0) mine[e[i]] += __popc(same);
-                __syncwarp();
+                const int in_e = e[i] >= 0 ? mine[e[i]] + ahead[i] : 0;
+                const int row = e[i] >= 0 ? first[e[i]] + in_e : -1;
                 if (p < p1) pair_row[p] = row;
-                if (row >= 0) row_pair[row] = static_cast<int32_t>(p);
+                if (row < 0) continue;
+                if constexpr (kLocal) {
+                    const int at = local[e[i]] + in_e;
+                    sorted[at] = static_cast<uint16_t>(p - cta0);
+                    sorted_e[at] = static_cast<uint16_t>(e[i]);
+                } else {
+                    row_pair[row] = static_cast<int32_t>(p);
+                }
             }
-            b += kSortBatch * 32;
-            if (b < p1) load_ids(id, b, p1, E, lane, e);
+        }
+    }
+    if constexpr (kLocal) {
+        __syncthreads();
+        for (int i = tid; i < in_cta; i += kSortThreads) {
+            const int x = sorted_e[i];
+            row_pair[first[x] + i - local[x]] = static_cast<int32_t>(cta0 + sorted[i]);
         }
     }
     for (int64_t r = kept + static_cast<int64_t>(rank) * kSortThreads + tid; r < P;
@@ -357,9 +423,13 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ 
         Raw<T, V> v;
         v.load(x + t * ld_x + c, left, step);
         const int32_t* pr = pair_row + t * k;
-        for (int j = 0; j < k; ++j) {
-            const int r = __ldg(pr + j);
-            if (r >= 0 && r < R) v.store(xs + r * ld_xs + c, left, step);
+        for (int j0 = 0; j0 < k; j0 += 8) {
+            int r[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = j0 + j < k ? __ldg(pr + j0 + j) : -1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (r[j] >= 0 && r[j] < R) v.store(xs + r[j] * ld_xs + c, left, step);
         }
     } else {
         Raw<T, V> z;
@@ -455,27 +525,34 @@ __global__ void __launch_bounds__(256) combine_rows_grad_kernel(
     for (int c = first_col<V>(0); c < H; c += step * V) {
         Raw<TO, V> d;
         d.load(dout + t * ld_do + c, H - c, step);
-        Raw<TY, V> v[KM];
-#pragma unroll
-        for (int j = 0; j < KM; ++j) {
-            v[j].zero();
-            if (row[j] >= 0) v[j].load(y + row[j] * ld_y + c, H - c, step);
-        }
         float df[V];
         d.get(df);
+        // rows in flight at a time: eight 16-byte loads, or four of RawS's
+        // (which would need twice the registers)
+        constexpr int kGroup = V == 8 ? 8 : 4;
 #pragma unroll
-        for (int j = 0; j < KM; ++j) {
-            if (row[j] < 0) continue;
-            float f[V], g[V];
-            v[j].get(f);
+        for (int j0 = 0; j0 < KM; j0 += kGroup) {
+            if (j0 >= k) break;
+            Raw<TY, V> v[kGroup];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                dot[j] = fmaf(df[i], f[i], dot[j]);
-                g[i] = ww[j] * df[i];
+            for (int j = 0; j < kGroup; ++j) {
+                v[j].zero();
+                if (row[j0 + j] >= 0) v[j].load(y + row[j0 + j] * ld_y + c, H - c, step);
             }
-            Raw<TY, V> o;
-            o.set(g);
-            o.store(dy + row[j] * ld_dy + c, H - c, step);
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                if (row[j0 + j] < 0) continue;
+                float f[V], g[V];
+                v[j].get(f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    dot[j0 + j] = fmaf(df[i], f[i], dot[j0 + j]);
+                    g[i] = ww[j0 + j] * df[i];
+                }
+                Raw<TY, V> o;
+                o.set(g);
+                o.store(dy + row[j0 + j] * ld_dy + c, H - c, step);
+            }
         }
     }
 #pragma unroll
@@ -505,7 +582,7 @@ cudaError_t by_type(int f32, F f) {
 
 }  // namespace
 
-cudaError_t SmemOnce::raise(const void* kernel, int bytes) {
+cudaError_t SmemOnce::raise(const void* kernel, int bytes, bool wide_cluster) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -513,6 +590,9 @@ cudaError_t SmemOnce::raise(const void* kernel, int bytes) {
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (known && (done[dev >> 6].load(std::memory_order_acquire) & bit)) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // clusters of more than eight CTAs have to be asked for
+    if (e == cudaSuccess && wide_cluster)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess && known) done[dev >> 6].fetch_or(bit, std::memory_order_release);
     return e;
 }
@@ -536,26 +616,24 @@ cudaError_t launch_route_rows_grad(const float* dw, const int32_t* id, const flo
     return cudaGetLastError();
 }
 
-// One CTA up to kSortOneCta pairs, else the largest cluster.
-constexpr int kSortOneCta = 2048, kSortCtas = 16;
-
 cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* offs, int32_t* pair_row,
                                int32_t* row_pair, cudaStream_t stream) {
     const int P = T * k;
     const int ctas = P <= kSortOneCta ? 1 : kSortCtas;
     const int warps = min(kSortWarps, max(1, (P + ctas * 32 - 1) / (ctas * 32)));
     const int run = (P + ctas * warps - 1) / (ctas * warps);
-    const size_t smem = (static_cast<size_t>(warps) * E + 2 * E) * sizeof(int);
-    static SmemOnce once;
-    const cudaError_t e = once.raise(reinterpret_cast<const void*>(expert_sort_kernel),
-                                     (kSortWarps + 2) * MOEQ_MAX_EXPERTS * static_cast<int>(sizeof(int)));
+    const bool local = run <= kSortBatch * 32;
+    int bits = 0;
+    while ((1 << bits) < E) ++bits;
+    const auto kern = local ? expert_sort_kernel<true> : expert_sort_kernel<false>;
+    static SmemOnce once[2];
+    cudaError_t e = once[local].raise(reinterpret_cast<const void*>(kern),
+                                      static_cast<int>(sort_smem(kSortWarps, MOEQ_MAX_EXPERTS, local)), true);
     if (e != cudaSuccess) return e;
-    static const cudaError_t wide = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (wide != cudaSuccess) return wide;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = sort_smem(warps, E, local);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -563,7 +641,7 @@ cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, expert_sort_kernel, id, P, E, warps, run, offs, pair_row, row_pair);
+    return cudaLaunchKernelEx(&cfg, kern, id, P, E, warps, run, bits, offs, pair_row, row_pair);
 }
 
 cudaError_t launch_gather_rows(RowsIn x, int T, int H, int k, const int32_t* offs, int E, const int32_t* pair_row,

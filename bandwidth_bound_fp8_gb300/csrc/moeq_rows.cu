@@ -3,14 +3,12 @@
 // expert, and the movement of rows to expert order and back, with gradients.
 // All of them move each byte once; what bounds them is HBM (large) or the
 // launch (small).
-#include <cooperative_groups.h>
 #include <float.h>
 
 #include "moeq_device.cuh"
 #include "moeq_rows.h"
 
 namespace moeq {
-namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kMaxK = MOEQ_MAX_TOPK;
@@ -222,31 +220,34 @@ __global__ void __launch_bounds__(128) route_rows_grad_kernel(const float* __res
 }
 
 // -------------------------------------------------------------------- sort
-// Stable counting sort of the pairs by expert in ONE launch: one cluster of
-// CTAs, each warp owning a contiguous run of pairs.
+// Stable counting sort of the pairs by expert, with no memory but the outputs.
+// A block owns a contiguous chunk of the pairs, and each of its warps a
+// contiguous run.
 //   1 each warp walks its run 32 pairs at a time, counting experts in bins of
-//     its own.  Ballots over the bits of the id find the equal ones among the
-//     32 (8 ballots for 256 experts; a match instruction took 3 times as
-//     long), so a pair's rank in the run is known as it is counted;
-//   2 the bins are scanned over the CTA's warps, over the cluster's CTAs
-//     (their totals read through distributed shared memory) and over the
-//     experts, which gives every warp its first row of every expert;
-//   3 a pair's row is its warp's first row of the expert plus its rank.
-//     row_pair is first sorted within the CTA in shared memory and leaves in
-//     runs: scattered, it costs a 4-byte sector a pair and a cycle each.
-// No atomic decides an order, so the result is the same every time.
-// A warp's ids are loaded 16 at a time, all in flight.  With up to
-// kSortBatch * 32 pairs a warp (16384 a CTA) ids, ranks and the CTA's sorted
-// pairs stay on the SM; longer runs keep their ranks in pair_row meanwhile
-// and scatter.
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBatch = 16;
-constexpr int kSortLocal = kSortWarps * kSortBatch * 32;  // pairs of a CTA that are sorted in shared memory
-// One CTA up to kSortOneCta pairs (no cluster to meet), else the largest cluster.
-constexpr int kSortOneCta = 2048, kSortCtas = 16;
-
-__host__ __device__ constexpr size_t sort_smem(int warps, int E, bool local) {
-    return (static_cast<size_t>(warps) * E + 3 * E) * sizeof(int) + (local ? 2 * kSortLocal * sizeof(uint16_t) : 0);
-}
+//     its own (shared memory).  Ballots over the bits of the id find the equal
+//     ones among the 32 (a match instruction took 1.6 times as long), so a
+//     pair's rank in the run is known as it is counted, and scanning the bins
+//     over the warps gives its rank in the chunk.  Ranks go to pair_row,
+//     the chunk's counts to row_pair;
+//   2 every block adds up the counts of the chunks before its own and of all,
+//     scans them over the experts, and turns its ranks into rows;
+//   3 row_pair is scattered from pair_row (step 2 still reads the counts
+//     there).
+// One block does all three when it holds every pair.  The steps are chained
+// by programmatic launches.  No atomic decides an order, so the result is
+// the same every time.  262144 pairs over 256 experts: one cluster of 16
+// CTAs that met in distributed shared memory took 19 us, 7 of them in step
+// 1's walk on 16 SMs.
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBatch = 2;
+constexpr int kSortChunk = kSortWarps * kSortBatch * 32;  // pairs of a block, at least (no fewer than MOEQ_MAX_EXPERTS)
+// The most blocks, and the most counts (blocks x experts) that step 2 has every
+// block read: 262144 pairs over 1000 experts take 12.7 us in step 2 with 128
+// blocks, 7.9 with 64.
+constexpr int kSortBlocks = 128, kSortCounts = 32768;
+// Pairs that one block sorts alone: 2400 take it 6.8 us and 8000 12.7; the
+// three steps take 10 us or more.
+constexpr int kSortOne = 4096;
+static_assert(kSortChunk >= 2 * MOEQ_MAX_EXPERTS, "the chunks' counts fit in row_pair");
 
 __device__ __forceinline__ void load_ids(const int32_t* __restrict__ id, int64_t b, int64_t end, int E, int lane,
                                          int (&e)[kSortBatch]) {
@@ -293,116 +294,136 @@ __device__ __forceinline__ int block_scan(int v, int* scratch, int* total) {
     return __shfl_sync(0xffffffffu, w - own, warp) + inc - v;
 }
 
-template <bool kLocal>
-__global__ void __launch_bounds__(kSortThreads) expert_sort_kernel(const int32_t* __restrict__ id, int P, int E,
-                                                                   int warps, int run, int bits,
-                                                                   int32_t* __restrict__ offs,
-                                                                   int32_t* __restrict__ pair_row,
-                                                                   int32_t* __restrict__ row_pair) {
-    extern __shared__ int sm[];
-    int* bins = sm;                // [warps][E]
-    int* total = sm + warps * E;   // [E] this CTA's counts
-    int* first = total + E;        // [E] this CTA's first row of each expert
-    int* local = first + E;        // [E] its place in the CTA's sorted pairs
-    uint16_t* sorted = reinterpret_cast<uint16_t*>(local + E);  // the CTA's pairs (from its first on) by expert
-    uint16_t* sorted_e = sorted + kSortLocal;                   // and their experts
-    __shared__ int scratch[kSortWarps];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = cluster.block_rank(), ctas = cluster.num_blocks();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t cta0 = static_cast<int64_t>(rank) * warps * run, p0 = cta0 + static_cast<int64_t>(warp) * run;
-    const int64_t p1 = warp < warps ? min(p0 + run, static_cast<int64_t>(P)) : p0;
-    int* mine = bins + warp * E;
+struct SortArgs {
+    const int32_t* id;
+    int P, E, warps, run, bits;
+    int32_t *offs, *pair_row, *row_pair;
+};
 
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Step 1; with kOne the block holds every pair and does the rest too.
+template <bool kOne>
+__global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(const SortArgs a) {
+    extern __shared__ int bins[];  // [warps][E], then kOne: [E] first rows
+    __shared__ int scratch[kSortWarps];
+    pdl_launch();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
+    const int64_t p0 = (static_cast<int64_t>(blockIdx.x) * a.warps + warp) * a.run;
+    const int64_t p1 = warp < a.warps ? min(p0 + a.run, static_cast<int64_t>(a.P)) : p0;
+    int* mine = bins + warp * E;
     int e[kSortBatch], ahead[kSortBatch];
-    load_ids(id, p0, p1, E, lane, e);
-    for (int i = tid; i < warps * E; i += kSortThreads) bins[i] = 0;
+    load_ids(a.id, p0, p1, E, lane, e);
+    for (int i = tid; i < a.warps * E; i += kSortThreads) bins[i] = 0;
     __syncthreads();
     for (int64_t b = p0; b < p1;) {
+        int next[kSortBatch];
+        load_ids(a.id, b + kSortBatch * 32, p1, E, lane, next);
 #pragma unroll
         for (int i = 0; i < kSortBatch; ++i) {
-            const unsigned same = same_ids(e[i], bits);
+            const unsigned same = same_ids(e[i], a.bits);
             const int before = __popc(same & ((1u << lane) - 1u));
             const int n = e[i] >= 0 ? mine[e[i]] : 0;
             ahead[i] = n + before;
             __syncwarp();
             if (e[i] >= 0 && before == 0) mine[e[i]] = n + __popc(same);
             __syncwarp();
-        }
-        if constexpr (!kLocal) {
-#pragma unroll
-            for (int i = 0; i < kSortBatch; ++i)
-                if (b + i * 32 + lane < p1) pair_row[b + i * 32 + lane] = ahead[i];
+            const int64_t p = b + i * 32 + lane;
+            if (p < p1) a.pair_row[p] = e[i] >= 0 ? ahead[i] : -1;  // the rank in the run, for now
+            e[i] = next[i];
         }
         b += kSortBatch * 32;
-        if (b < p1) load_ids(id, b, p1, E, lane, e);
     }
     __syncthreads();
+    int count = 0;
     if (tid < E) {  // one expert a thread: E <= MOEQ_MAX_EXPERTS = kSortThreads
-        int sum = 0;
-        for (int i = 0; i < warps; ++i) {
+        for (int i = 0; i < a.warps; ++i) {
             const int c = bins[i * E + tid];
-            bins[i * E + tid] = sum;
-            sum += c;
+            bins[i * E + tid] = count;
+            count += c;
         }
-        total[tid] = sum;
+        if (!kOne) a.row_pair[static_cast<int64_t>(blockIdx.x) * E + tid] = count;
     }
-    cluster.sync();
-    int v[kSortCtas], before = 0, all = 0;
-#pragma unroll
-    for (int c = 0; c < kSortCtas; ++c) v[c] = tid < E && c < ctas ? cluster.map_shared_rank(total, c)[tid] : 0;
-#pragma unroll
-    for (int c = 0; c < kSortCtas; ++c) {
-        if (c < rank) before += v[c];
-        all += v[c];
+    int kept = 0;
+    int* first = bins + a.warps * E;
+    if constexpr (kOne) {
+        const int start = block_scan(count, scratch, &kept);
+        if (tid < E) {
+            first[tid] = start;
+            a.offs[tid] = start;
+        }
+        if (tid == 0) a.offs[E] = kept;
     }
-    int kept, in_cta;
+    __syncthreads();
+    for (int64_t p = p0 + lane; p < p1; p += 32) {
+        const int x = __ldg(a.id + p);
+        if (x < 0 || x >= E) continue;
+        const int row = a.pair_row[p] + mine[x] + (kOne ? first[x] : 0);
+        a.pair_row[p] = row;
+        if (kOne) a.row_pair[row] = static_cast<int32_t>(p);
+    }
+    if (kOne)
+        for (int r = kept + tid; r < a.P; r += kSortThreads) a.row_pair[r] = -1;
+}
+
+// Step 2.
+__global__ void __launch_bounds__(kSortThreads) sort_rows_kernel(const SortArgs a) {
+    __shared__ int before_s[kSortThreads], all_s[kSortThreads], first[MOEQ_MAX_EXPERTS], scratch[kSortWarps];
+    pdl_launch();
+    const int tid = threadIdx.x, E = a.E, blocks = gridDim.x;
+    // a power of two of threads for the experts, the rest of the block splits the chunks
+    const int log_e = a.bits, e = tid & ((1 << log_e) - 1), sub = tid >> log_e, subs = kSortThreads >> log_e;
+    int before = 0, all = 0;
+    pdl_wait();
+    if (e < E) {
+        for (int g0 = sub; g0 < blocks; g0 += 8 * subs) {
+            int c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int g = g0 + i * subs;
+                c[i] = g < blocks ? __ldcg(a.row_pair + static_cast<int64_t>(g) * E + e) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                all += c[i];
+                if (g0 + i * subs < static_cast<int>(blockIdx.x)) before += c[i];
+            }
+        }
+    }
+    before_s[tid] = before;
+    all_s[tid] = all;
+    __syncthreads();
+    before = all = 0;
+    if (tid < E)
+        for (int i = 0; i < subs; ++i) {
+            before += before_s[(i << log_e) + tid];
+            all += all_s[(i << log_e) + tid];
+        }
+    int kept;
     const int start = block_scan(all, scratch, &kept);
-    const int place = block_scan(tid < E ? total[tid] : 0, scratch, &in_cta);
     if (tid < E) {
         first[tid] = start + before;
-        local[tid] = place;
-        if (rank == 0) offs[tid] = start;
+        if (blockIdx.x == 0) a.offs[tid] = start;
     }
-    if (rank == 0 && tid == 0) offs[E] = kept;
-    cluster.sync();  // every CTA has read this one's totals; first[] is written
-    if (warp < warps) {
-        for (int64_t b = p0; b < p1; b += kSortBatch * 32) {
-            if constexpr (!kLocal) {
-                load_ids(id, b, p1, E, lane, e);
-#pragma unroll
-                for (int i = 0; i < kSortBatch; ++i) {
-                    const int64_t p = b + i * 32 + lane;
-                    ahead[i] = p < p1 ? pair_row[p] : 0;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kSortBatch; ++i) {
-                const int64_t p = b + i * 32 + lane;
-                const int in_e = e[i] >= 0 ? mine[e[i]] + ahead[i] : 0;
-                const int row = e[i] >= 0 ? first[e[i]] + in_e : -1;
-                if (p < p1) pair_row[p] = row;
-                if (row < 0) continue;
-                if constexpr (kLocal) {
-                    const int at = local[e[i]] + in_e;
-                    sorted[at] = static_cast<uint16_t>(p - cta0);
-                    sorted_e[at] = static_cast<uint16_t>(e[i]);
-                } else {
-                    row_pair[row] = static_cast<int32_t>(p);
-                }
-            }
-        }
+    if (blockIdx.x == 0 && tid == 0) a.offs[E] = kept;
+    __syncthreads();
+    const int64_t chunk = static_cast<int64_t>(a.warps) * a.run, p0 = blockIdx.x * chunk;
+    const int64_t p1 = min(p0 + chunk, static_cast<int64_t>(a.P));
+    for (int64_t p = p0 + tid; p < p1; p += kSortThreads) {
+        const int x = __ldg(a.id + p);
+        if (x >= 0 && x < E) a.pair_row[p] += first[x];
     }
-    if constexpr (kLocal) {
-        __syncthreads();
-        for (int i = tid; i < in_cta; i += kSortThreads) {
-            const int x = sorted_e[i];
-            row_pair[first[x] + i - local[x]] = static_cast<int32_t>(cta0 + sorted[i]);
-        }
-    }
-    for (int64_t r = kept + static_cast<int64_t>(rank) * kSortThreads + tid; r < P;
-         r += static_cast<int64_t>(ctas) * kSortThreads)
-        row_pair[r] = -1;
+}
+
+// Step 3.
+__global__ void __launch_bounds__(256) sort_pairs_kernel(const SortArgs a) {
+    pdl_wait();
+    const int64_t p = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (p >= a.P) return;
+    const int row = __ldcg(a.pair_row + p);
+    if (row >= 0) a.row_pair[row] = static_cast<int32_t>(p);
+    if (p >= __ldcg(a.offs + a.E)) a.row_pair[p] = -1;
 }
 
 // ------------------------------------------------------------------ gather
@@ -582,7 +603,7 @@ cudaError_t by_type(int f32, F f) {
 
 }  // namespace
 
-cudaError_t SmemOnce::raise(const void* kernel, int bytes, bool wide_cluster) {
+cudaError_t SmemOnce::raise(const void* kernel, int bytes) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -590,9 +611,6 @@ cudaError_t SmemOnce::raise(const void* kernel, int bytes, bool wide_cluster) {
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (known && (done[dev >> 6].load(std::memory_order_acquire) & bit)) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    // clusters of more than eight CTAs have to be asked for
-    if (e == cudaSuccess && wide_cluster)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess && known) done[dev >> 6].fetch_or(bit, std::memory_order_release);
     return e;
 }
@@ -618,30 +636,36 @@ cudaError_t launch_route_rows_grad(const float* dw, const int32_t* id, const flo
 
 cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* offs, int32_t* pair_row,
                                int32_t* row_pair, cudaStream_t stream) {
-    const int P = T * k;
-    const int ctas = P <= kSortOneCta ? 1 : kSortCtas;
-    const int warps = min(kSortWarps, max(1, (P + ctas * 32 - 1) / (ctas * 32)));
-    const int run = (P + ctas * warps - 1) / (ctas * warps);
-    const bool local = run <= kSortBatch * 32;
-    int bits = 0;
-    while ((1 << bits) < E) ++bits;
-    const auto kern = local ? expert_sort_kernel<true> : expert_sort_kernel<false>;
+    SortArgs a = {id, T * k, E, 0, 0, 0, offs, pair_row, row_pair};
+    // one block for few pairs; else chunks of kSortChunk, longer ones beyond the most blocks
+    const int most = min(kSortBlocks, kSortCounts / E);
+    const int blocks = a.P <= kSortOne ? 1 : min(most, (a.P + kSortChunk - 1) / kSortChunk);
+    const int chunk = (a.P + blocks - 1) / blocks;
+    a.warps = min(kSortWarps, max(1, (chunk + 31) / 32));
+    a.run = (chunk + a.warps - 1) / a.warps;
+    while ((1 << a.bits) < E) ++a.bits;
+    const auto rank = blocks == 1 ? sort_rank_kernel<true> : sort_rank_kernel<false>;
     static SmemOnce once[2];
-    cudaError_t e = once[local].raise(reinterpret_cast<const void*>(kern),
-                                      static_cast<int>(sort_smem(kSortWarps, MOEQ_MAX_EXPERTS, local)), true);
+    cudaError_t e = once[blocks == 1].raise(reinterpret_cast<const void*>(rank),
+                                            (kSortWarps + 1) * MOEQ_MAX_EXPERTS * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = sort_smem(warps, E, local);
-    cfg.stream = stream;
+    rank<<<blocks, kSortThreads, (a.warps + 1) * E * sizeof(int), stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || blocks == 1) return e;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = ctas;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, id, P, E, warps, run, bits, offs, pair_row, row_pair);
+    e = cudaLaunchKernelEx(&cfg, sort_rows_kernel, a);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((a.P + 255) / 256);
+    cfg.blockDim = dim3(256);
+    return cudaLaunchKernelEx(&cfg, sort_pairs_kernel, a);
 }
 
 cudaError_t launch_gather_rows(RowsIn x, int T, int H, int k, const int32_t* offs, int E, const int32_t* pair_row,

@@ -18,7 +18,7 @@ namespace moeq {
 // The call costs about a microsecond, a small launch's half.
 struct SmemOnce {
     std::atomic<uint64_t> done[2]{};  // devices 0 .. 127
-    cudaError_t raise(const void* kernel, int bytes, bool wide_cluster = false);
+    cudaError_t raise(const void* kernel, int bytes);
 };
 
 // A matrix of rows: base, leading dimension in elements, element type.

@@ -42,15 +42,16 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float inv) {
     return r;
 }
 
-// Four lanes hold a block of 32, eight elements each: the block's scale byte
-// (the same in all four) and this lane's codes.
-__device__ __forceinline__ uint32_t mx4_block(const float (&v)[8], uint32_t* scale) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+// Four lanes hold a block of 32: the largest of their magnitudes (as fp32
+// bits).
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t b = mx4_scale_byte(m);
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+// The block's scale byte (the same in its four lanes) and this lane's codes.
+__device__ __forceinline__ uint32_t mx4_block(const float (&v)[8], uint32_t amax, uint32_t* scale) {
+    const uint32_t b = mx4_scale_byte(amax);
     *scale = b;
     return b == kNanScale ? 0u : e2m1x8(v, mx4_inverse(b));
 }
@@ -82,6 +83,17 @@ struct Raw8 {
         }
     }
     __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+    // The largest magnitude, as fp32 bits: bf16 two at a time.
+    __device__ __forceinline__ uint32_t amax() const {
+        constexpr uint32_t kAbs = kF32 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+        if constexpr (kF32) {
+            return max(max(max(a.x & kAbs, a.y & kAbs), max(a.z & kAbs, a.w & kAbs)),
+                       max(max(b.x & kAbs, b.y & kAbs), max(b.z & kAbs, b.w & kAbs)));
+        } else {
+            const uint32_t m = __vmaxu2(__vmaxu2(a.x & kAbs, a.y & kAbs), __vmaxu2(a.z & kAbs, a.w & kAbs));
+            return max(m & 0xFFFF0000u, m << 16);
+        }
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -100,18 +112,19 @@ struct Raw8 {
 // |g|, far below the 4-bit rounding that follows.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
-// A warp's segment of a row: kSegment K blocks of 256 columns, eight of each
-// a lane (its loads all issued before the first is used).
+// A warp's segment of a row: kBlocks K blocks of 256 columns, eight of each a
+// lane (its loads all issued before the first is used): 2 KiB a warp.
 constexpr int kSegment = 4;
-__host__ __device__ constexpr int segments(int K) { return (mx4_kb(K) + kSegment - 1) / kSegment; }
+__host__ __device__ constexpr int segments(int K, int blocks) { return (mx4_kb(K) + blocks - 1) / blocks; }
 
 template <bool kF32, bool kVec, bool kSwiglu>
 struct Segment {
-    Raw8<kF32> v[kSegment], u[kSwiglu ? kSegment : 1];
+    static constexpr int kBlocks = kSegment / (kF32 ? 2 : 1) / (kSwiglu ? 2 : 1);
+    Raw8<kF32> v[kBlocks], u[kSwiglu ? kBlocks : 1];
     __device__ __forceinline__ void load(const void* x, int64_t row0, int seg, int lane, int K) {
 #pragma unroll
-        for (int i = 0; i < kSegment; ++i) {
-            const int c = (seg * kSegment + i) * kMx4TileCols + lane * 8;
+        for (int i = 0; i < kBlocks; ++i) {
+            const int c = (seg * kBlocks + i) * kMx4TileCols + lane * 8;
             v[i].zero();
             if constexpr (kSwiglu) u[i].zero();
             if (c < K) {
@@ -124,47 +137,63 @@ struct Segment {
     __device__ __forceinline__ uint32_t quant(int i, bool in, uint32_t* s) const {
         float f[8];
         v[i].get(f);
+        uint32_t m = 0;
         if constexpr (kSwiglu) {
             float g[8];
             u[i].get(g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = swiglu(f[j], g[j]);
+            for (int j = 0; j < 8; ++j) {
+                f[j] = swiglu(f[j], g[j]);
+                m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+            }
+        } else {
+            m = v[i].amax();
         }
-        const uint32_t q = mx4_block(f, s);
+        const uint32_t q = mx4_block(f, block_max(m), s);
         if (!in) *s = 0;
         return in ? q : 0u;
     }
 };
 
-// The four scale bytes of this lane's 128 columns (lanes 0..15, 16..31).
-__device__ __forceinline__ uint32_t scale_word(uint32_t s, int lane) {
-    uint32_t word = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) word |= __shfl_sync(0xffffffffu, s, (lane & 16) + 4 * j) << (8 * j);
-    return word;
-}
-
-// Rows of activations, one warp a segment.
+// Rows of activations: resident warps take a segment at a time, the next one's
+// loads in flight while this one is quantised.
 template <bool kF32, bool kVec, bool kSwiglu>
 __global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__ x, int64_t ld, int rows, int K,
                                                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-    const int lane = threadIdx.x & 31, segs = segments(K);
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t row = item / segs;
-    const int seg = static_cast<int>(item - row * segs);
+    using Seg = Segment<kF32, kVec, kSwiglu>;
+    constexpr int kBlocks = Seg::kBlocks;
+    const int lane = threadIdx.x & 31, segs = segments(K, kBlocks), pitch = mx4_scale_pitch(K);
+    const unsigned step = gridDim.x * 8, step_rows = step / segs, step_segs = step % segs;
+    const unsigned it = blockIdx.x * 8 + (threadIdx.x >> 5);
+    int64_t row = it / segs;
+    int seg = it % segs;
     if (row >= rows) return;
-    Segment<kF32, kVec, kSwiglu> g;
+    Seg g, next;
     g.load(x, row * ld, seg, lane, K);
+    for (;;) {
+        int64_t next_row = row + step_rows;
+        int next_seg = seg + step_segs;
+        if (next_seg >= segs) {
+            next_seg -= segs;
+            ++next_row;
+        }
+        const bool more = next_row < rows;
+        if (more) next.load(x, next_row * ld, next_seg, lane, K);
+        uint8_t* q_at = codes + row * (K >> 1) + seg * (kBlocks * kMx4TileCols / 2) + lane * 4;
+        uint8_t* s_at = scales + row * pitch + seg * (kBlocks * 8) + (lane >> 2);
 #pragma unroll
-    for (int i = 0; i < kSegment; ++i) {
-        const int kb = seg * kSegment + i, c = kb * kMx4TileCols + lane * 8;
-        if (kb * kMx4TileCols >= K) break;
-        uint32_t s;
-        const uint32_t q = g.quant(i, c < K, &s);
-        if (c < K) *reinterpret_cast<uint32_t*>(codes + row * (K >> 1) + (c >> 1)) = q;
-        const uint32_t word = scale_word(s, lane);
-        if ((lane & 15) == 0)
-            *reinterpret_cast<uint32_t*>(scales + row * mx4_scale_pitch(K) + kb * 8 + (lane >> 4) * 4) = word;
+        for (int i = 0; i < kBlocks; ++i) {
+            const int kb = seg * kBlocks + i, c = kb * kMx4TileCols + lane * 8;
+            if (kb * kMx4TileCols >= K) break;
+            uint32_t s;
+            const uint32_t q = g.quant(i, c < K, &s);
+            if (c < K) *reinterpret_cast<uint32_t*>(q_at + i * (kMx4TileCols / 2)) = q;
+            if ((lane & 3) == 0) s_at[i * 8] = static_cast<uint8_t>(s);
+        }
+        if (!more) return;
+        g = next;
+        row = next_row;
+        seg = next_seg;
     }
 }
 
@@ -176,7 +205,7 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) dequant_act_kernel(const uint8_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ scales, int rows, int K,
                                                           T* __restrict__ out, int64_t ld) {
-    const int lane = threadIdx.x & 31, segs = segments(K);
+    const int lane = threadIdx.x & 31, segs = segments(K, kSegment);
     const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int64_t row = item / segs;
     const int seg = static_cast<int>(item - row * segs);
@@ -234,13 +263,12 @@ __global__ void __launch_bounds__(256) dequant_act_kernel(const uint8_t* __restr
 }
 
 // Where a lane's eight elements of (row r, its 32 lanes = 256 columns) go in
-// a weight tile, and its row's scale words (lanes 0 and 16 write them).
+// a weight tile, and its block's scale byte.
 __device__ __forceinline__ void store_tile(uint8_t* tile, uint8_t* stile, int r, int lane, uint32_t q, uint32_t s) {
     const int chunk = lane >> 2;
     *reinterpret_cast<uint32_t*>(tile + r * 128 + ((chunk ^ (r & 7)) << 4) + (lane & 3) * 4) = q;
-    const uint32_t word = scale_word(s, lane);
-    if ((lane & 15) == 0)
-        *reinterpret_cast<uint32_t*>(stile + (lane >> 4) * 512 + (r & 31) * 16 + (r >> 5) * 4) = word;
+    if ((lane & 3) == 0)
+        stile[(lane >> 4) * 512 + (r & 31) * 16 + (r >> 5) * 4 + ((lane >> 2) & 3)] = static_cast<uint8_t>(s);
 }
 
 // One block of eight warps a tile, one row a warp at a time.
@@ -260,7 +288,7 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(const void* __restric
         float v[8];
         raw.get(v);
         uint32_t s;
-        const uint32_t q = mx4_block(v, &s);
+        const uint32_t q = mx4_block(v, block_max(raw.amax()), &s);
         store_tile(tiles + t * kMx4TileBytes, stiles + t * kMx4TileScaleBytes, r, lane, in ? q : 0u, in ? s : 0u);
     }
 }
@@ -308,51 +336,66 @@ __device__ __forceinline__ int act_row(const Mx4Plan& p, int r) {
     return min(p.row_pair ? max(__ldg(p.row_pair + r), 0) / p.top_k : r, p.rows - 1);
 }
 
-// From rows to quantise: a warp takes a segment of a row at a time.  The
-// first one's loads are issued before the plan is known (they need only the
-// row number).
+// From rows to quantise: a warp takes every `parts`-th segment of a row at a
+// time (parts = 1 where there are rows for all warps), and finds the row's
+// place once.  The next segment's loads are in flight while one is
+// quantised; the first one's need only the row number, not the plan.
 template <bool kF32, bool kVec, bool kSwiglu>
-__global__ void __launch_bounds__(kPlanThreads) act_tiles_kernel(RowsIn x, Mx4Plan p, int K, uint8_t* __restrict__ tiles,
+__global__ void __launch_bounds__(kPlanThreads) act_tiles_kernel(RowsIn x, Mx4Plan p, int K, int parts,
+                                                                 uint8_t* __restrict__ tiles,
                                                                  uint8_t* __restrict__ stiles) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ PlanShared plan;
-    const int lane = threadIdx.x & 31, kb_all = mx4_kb(K), segs = segments(K), sb = mx4_tile_scale_bytes(p.nt);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPlanThreads / 32);
-    int64_t it = static_cast<int64_t>(blockIdx.x) * (kPlanThreads / 32) + (threadIdx.x >> 5);
-    auto row_of = [&](int64_t i) { return static_cast<int>(i / segs); };
-    Segment<kF32, kVec, kSwiglu> g;
-    auto load = [&] {
-        const int r = row_of(it);
-        g.load(x.p, act_row(p, r) * x.ld, static_cast<int>(it - static_cast<int64_t>(r) * segs), lane, K);
-    };
-    const int64_t most = static_cast<int64_t>(p.R) * segs;
-    if (it < most) load();
+    using Seg = Segment<kF32, kVec, kSwiglu>;
+    constexpr int kBlocks = Seg::kBlocks;
+    const int lane = threadIdx.x & 31, kb_all = mx4_kb(K), segs = segments(K, kBlocks), sb = mx4_tile_scale_bytes(p.nt);
+    const unsigned it = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5);
+    const int step = gridDim.x * (kPlanThreads / 32) / parts, part = it % parts;
+    int64_t r = it / parts;  // parts divides the grid's warps, so r steps evenly
+    int seg = part;
+    Seg g, next;
+    int next_row = 0;  // the activation row after this one
+    if (r < p.R) {
+        g.load(x.p, act_row(p, static_cast<int>(r)) * x.ld, seg, lane, K);
+        if (r + step < p.R) next_row = act_row(p, static_cast<int>(r + step));
+    }
+    int64_t row = r < p.R ? act_row(p, static_cast<int>(r)) : 0;
     plan_scan(p, plan);
-    const int64_t items = static_cast<int64_t>(plan.first[p.E]) * segs;
-    while (it < items) {
-        const int r = row_of(it), seg = static_cast<int>(it - static_cast<int64_t>(r) * segs);
-        if (r >= plan.first[0]) {
-            const Place at = place_of(plan, p, r, kb_all);
-            const int c_at = at.pos * 128 + (((lane >> 2) ^ (at.pos & 7)) << 4) + (lane & 3) * 4;
+    const int r0 = plan.first[0], r1 = plan.first[p.E];
+    while (r < r1) {
+        const Place at = place_of(plan, p, max(static_cast<int>(r), r0), kb_all);
+        const int c_at = at.pos * 128 + (((lane >> 2) ^ (at.pos & 7)) << 4) + (lane & 3) * 4;
+        const int s_at = scale_at(at.pos, lane >> 4, sb) + ((lane >> 2) & 3);
+        const bool keep = r >= r0;
+        for (; seg < segs; seg += parts) {
+            // the next segment, of this row or the next
+            if (seg + parts < segs)
+                next.load(x.p, row * x.ld, seg + parts, lane, K);
+            else if (r + step < r1)
+                next.load(x.p, static_cast<int64_t>(next_row) * x.ld, part, lane, K);
+            uint8_t* t_at = tiles + (at.block0 + seg * kBlocks) * p.nt * 128 + c_at;
+            uint8_t* st_at = stiles + (at.block0 + seg * kBlocks) * sb + s_at;
 #pragma unroll
-            for (int i = 0; i < kSegment; ++i) {
-                const int kb = seg * kSegment + i;
+            for (int i = 0; i < kBlocks; ++i) {
+                const int kb = seg * kBlocks + i;
                 if (kb >= kb_all) break;
                 uint32_t s;
                 const uint32_t q = g.quant(i, kb * kMx4TileCols + lane * 8 < K, &s);
-                const uint32_t word = scale_word(s, lane);
-                *reinterpret_cast<uint32_t*>(tiles + (at.block0 + kb) * p.nt * 128 + c_at) = q;
-                if ((lane & 15) == 0)
-                    *reinterpret_cast<uint32_t*>(stiles + (at.block0 + kb) * sb + scale_at(at.pos, lane >> 4, sb)) = word;
+                if (!keep) continue;
+                *reinterpret_cast<uint32_t*>(t_at + i * (p.nt * 128)) = q;
+                if ((lane & 3) == 0) st_at[i * sb] = static_cast<uint8_t>(s);
             }
+            g = next;
         }
-        it += step;
-        if (it < items) load();
+        seg = part;
+        row = next_row;
+        r += step;
+        if (r + step < r1) next_row = act_row(p, static_cast<int>(r + step));
     }
 }
 
 // From codes: a warp moves a row, 16 bytes of codes and four scale bytes a
-// lane at a time.
+// lane at a time, up to 8192 columns' loads in flight.
 __global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ scales, Mx4Plan p, int K,
                                                                   uint8_t* __restrict__ tiles,
@@ -360,36 +403,48 @@ __global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t*
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ PlanShared plan;
     plan_scan(p, plan);
+    constexpr int kWide = 8;
     const int lane = threadIdx.x & 31, kb_all = mx4_kb(K), sb = mx4_tile_scale_bytes(p.nt), pitch = mx4_scale_pitch(K);
-    const int chunks = K >> 5, all_chunks = kb_all * 8, r_end = plan.first[p.E];
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPlanThreads / 32);
-    for (int64_t r64 = static_cast<int64_t>(blockIdx.x) * (kPlanThreads / 32) + (threadIdx.x >> 5); r64 < r_end;
-         r64 += step) {
-        const int r = static_cast<int>(r64);
-        if (r < plan.first[0]) continue;
-        const int64_t row = act_row(p, r);
+    const int chunks = K >> 5, all_chunks = kb_all * 8, r0 = plan.first[0], r1 = plan.first[p.E];
+    const int step = gridDim.x * (kPlanThreads / 32);
+    int64_t r = r0 + blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5);
+    int64_t row = r < r1 ? act_row(p, static_cast<int>(r)) : 0;
+    while (r < r1) {
+        const int64_t next_row = r + step < r1 ? act_row(p, static_cast<int>(r + step)) : 0;
         const uint4* src = reinterpret_cast<const uint4*>(codes + row * (K >> 1));
         const uint32_t* ssrc = reinterpret_cast<const uint32_t*>(scales + row * pitch);
-        const Place at = place_of(plan, p, r, kb_all);
-        for (int c0 = 0; c0 < all_chunks; c0 += 128) {
-            uint4 v[4];
+        const Place at = place_of(plan, p, static_cast<int>(r), kb_all);
+        uint8_t* t_at = tiles + (at.block0 * p.nt + at.pos) * 128;
+        uint8_t* st_at = stiles + at.block0 * sb;
+        for (int c0 = 0; c0 < all_chunks; c0 += kWide * 32) {
+            uint4 v[kWide];
+            uint32_t w[kWide / 4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kWide; ++i) {
                 const int c = c0 + i * 32 + lane;
                 v[i] = c < chunks ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
             }
-            const int word = c0 / 4 + lane;  // 32 words of 128 columns for 128 chunks of 32
-            const uint32_t w = word * 4 < pitch ? __ldg(ssrc + word) : 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kWide / 4; ++i) {  // a word for four chunks of 32 columns
+                const int word = c0 / 4 + i * 32 + lane;
+                w[i] = word * 4 < pitch ? __ldg(ssrc + word) : 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < kWide; ++i) {
                 const int c = c0 + i * 32 + lane;
                 if (c < all_chunks)
-                    *reinterpret_cast<uint4*>(tiles + ((at.block0 + (c >> 3)) * p.nt + at.pos) * 128 +
+                    *reinterpret_cast<uint4*>(t_at + static_cast<int64_t>(c >> 3) * (p.nt * 128) +
                                               (((c & 7) ^ (at.pos & 7)) << 4)) = v[i];
             }
-            if (word * 4 < pitch)
-                *reinterpret_cast<uint32_t*>(stiles + (at.block0 + (word >> 1)) * sb + scale_at(at.pos, word & 1, sb)) = w;
+#pragma unroll
+            for (int i = 0; i < kWide / 4; ++i) {
+                const int word = c0 / 4 + i * 32 + lane;
+                if (word * 4 < pitch)
+                    *reinterpret_cast<uint32_t*>(st_at + (word >> 1) * sb + scale_at(at.pos, word & 1, sb)) = w[i];
+            }
         }
+        r += step;
+        row = next_row;
     }
 }
 
@@ -400,8 +455,10 @@ bool fits(const void* p, int64_t ld, int f32) {
 }  // namespace
 
 cudaError_t launch_mx4_quant_act(RowsIn x, int rows, int K, int act, uint8_t* codes, uint8_t* scales,
-                                 cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(rows) * segments(K) + 7) / 8);
+                                 int sms, cudaStream_t stream) {
+    const int blocks = kSegment / (x.f32 ? 2 : 1) / (act ? 2 : 1);
+    const int64_t want = (static_cast<int64_t>(rows) * segments(K, blocks) + 7) / 8;
+    const unsigned grid = static_cast<unsigned>(want < sms * 4 ? want : sms * 4);
     // the second half of a SwiGLU row starts K elements on: K is a multiple of 32
     const bool vec = fits(x.p, x.ld, x.f32);
     auto go = [&](auto kern) {
@@ -418,7 +475,7 @@ cudaError_t launch_mx4_quant_act(RowsIn x, int rows, int K, int act, uint8_t* co
 
 cudaError_t launch_mx4_dequant_act(const uint8_t* codes, const uint8_t* scales, int rows, int K, RowsOut out,
                                    cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(rows) * segments(K) + 7) / 8);
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(rows) * segments(K, kSegment) + 7) / 8);
     const bool vec = fits(out.p, out.ld, out.f32);
     auto go = [&](auto* o, auto kern) {
         kern<<<grid, 256, 0, stream>>>(codes, scales, rows, K, o, out.ld);
@@ -454,18 +511,22 @@ cudaError_t launch_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, 
 cudaError_t launch_mx4_act_tiles(const Mx4Source& src, const Mx4Plan& plan, int K, uint8_t* tiles, uint8_t* stiles,
                                  int sms, cudaStream_t stream) {
     // one wave of resident blocks: each scans the plan once
-    auto grid_of = [&](int64_t warps, int per_sm) {
-        const int64_t blocks = (warps + 7) / 8;
-        return static_cast<unsigned>(blocks < static_cast<int64_t>(sms) * per_sm ? blocks : sms * per_sm);
-    };
+    const int most = sms * 4;
     if (src.codes) {
-        code_tiles_kernel<<<grid_of(plan.R, 8), kPlanThreads, 0, stream>>>(src.codes, src.scales, plan, K, tiles, stiles);
+        const int blocks = (plan.R + 7) / 8;
+        code_tiles_kernel<<<blocks < most ? blocks : most, kPlanThreads, 0, stream>>>(src.codes, src.scales, plan, K, tiles,
+                                                                                  stiles);
         return cudaGetLastError();
     }
+    // a warp a row where that fills the wave, else up to eight (a power of two: it divides a block's warps)
+    const int segs = segments(K, kSegment / (src.x.f32 ? 2 : 1) / (src.act ? 2 : 1));
+    int parts = 1;
+    while (parts < 8 && parts < segs && static_cast<int64_t>(plan.R) * parts < most * 8) parts *= 2;
+    const int64_t want = (static_cast<int64_t>(plan.R) * parts + 7) / 8;
+    const unsigned grid = static_cast<unsigned>(want < most ? want : most);
     const bool vec = fits(src.x.p, src.x.ld, src.x.f32);
     auto go = [&](auto kern) {
-        kern<<<grid_of(static_cast<int64_t>(plan.R) * segments(K), 6), kPlanThreads, 0, stream>>>(src.x, plan, K, tiles,
-                                                                                               stiles);
+        kern<<<grid, kPlanThreads, 0, stream>>>(src.x, plan, K, parts, tiles, stiles);
         return cudaGetLastError();
     };
     if (src.x.f32) {

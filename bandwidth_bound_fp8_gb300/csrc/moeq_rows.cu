@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(256) combine_rows_grad_kernel(
         d.get(df);
         // rows in flight at a time: eight 16-byte loads, or four of RawS's
         // (which would need twice the registers)
-        constexpr int kGroup = V == 8 ? 8 : 4;
+        constexpr int kGroup = V == 8 && KM >= 8 ? 8 : 4;
 #pragma unroll
         for (int j0 = 0; j0 < KM; j0 += kGroup) {
             if (j0 >= k) break;
@@ -728,6 +728,8 @@ cudaError_t launch_combine_rows_grad(RowsIn dout, RowsIn y, int T, int H, int k,
                                                dw);
                 return cudaGetLastError();
             };
+            if (k <= 4)
+                return v8 ? go(combine_rows_grad_kernel<TY, TO, 8, 4>) : go(combine_rows_grad_kernel<TY, TO, 4, 4>);
             if (k <= 8)
                 return v8 ? go(combine_rows_grad_kernel<TY, TO, 8, 8>) : go(combine_rows_grad_kernel<TY, TO, 4, 8>);
             return v8 ? go(combine_rows_grad_kernel<TY, TO, 8, kMaxK>) : go(combine_rows_grad_kernel<TY, TO, 4, kMaxK>);

@@ -65,7 +65,7 @@ __host__ __device__ constexpr int mx4_nb(int N) { return (N + kMx4TileRows - 1) 
 
 // act: x is [rows, 2K] and silu(x[:, :K]) * x[:, K:] is quantised.
 cudaError_t launch_mx4_quant_act(RowsIn x, int rows, int K, int act, uint8_t* codes, uint8_t* scales,
-                                 cudaStream_t stream);
+                                 int sms, cudaStream_t stream);
 cudaError_t launch_mx4_dequant_act(const uint8_t* codes, const uint8_t* scales, int rows, int K, RowsOut out,
                                    cudaStream_t stream);
 cudaError_t launch_mx4_quant_weight(const void* w, int w_f32, int E, int N, int K, uint8_t* tiles, uint8_t* stiles,

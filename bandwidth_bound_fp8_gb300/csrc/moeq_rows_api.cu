@@ -192,8 +192,10 @@ moeq_status moeq_mx4_quant_act(const void* x, moeq_dtype dtype, int64_t ld, int 
     if (!rows_ok(x, dtype, ld, act == MOEQ_ACT_SWIGLU ? 2 * static_cast<int64_t>(K) : K) || !al(codes, 16) ||
         !al(scales, 16))
         return MOEQ_ERR_INVALID_ARG;
-    if (!current_device().ok) return MOEQ_ERR_DEVICE;
-    return cuda_status(launch_mx4_quant_act({x, ld, dtype == MOEQ_F32}, rows, K, act, codes, scales, as_stream(stream)));
+    const Device dev = current_device();
+    if (!dev.ok) return MOEQ_ERR_DEVICE;
+    return cuda_status(launch_mx4_quant_act({x, ld, dtype == MOEQ_F32}, rows, K, act, codes, scales, dev.sms,
+                                            as_stream(stream)));
 }
 
 moeq_status moeq_mx4_dequant_act(const uint8_t* codes, const uint8_t* scales, int rows, int K, void* out,
@@ -262,7 +264,8 @@ moeq_status moeq_mx4_expert_gemm(const void* x, moeq_dtype x_dtype, int64_t ld_x
     } else if (row_pair_opt && R >= kQuantOnceRows && rows < R) {
         src.codes = u8 + l.codes;
         src.scales = u8 + l.scales;
-        if (launch_mx4_quant_act(src.x, rows, K, act, u8 + l.codes, u8 + l.scales, st) != cudaSuccess) return MOEQ_ERR_CUDA;
+        if (launch_mx4_quant_act(src.x, rows, K, act, u8 + l.codes, u8 + l.scales, dev.sms, st) != cudaSuccess)
+            return MOEQ_ERR_CUDA;
     }
     Mx4GemmArgs a = {};
     a.plan = {offs, row_pair_opt, E, R, top_k, rows, l.nt};

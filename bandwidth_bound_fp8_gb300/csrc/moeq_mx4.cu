@@ -323,7 +323,7 @@ struct Place {
 };
 __device__ __forceinline__ Place place_of(const PlanShared& plan, const Mx4Plan& p, int r, int kb_all) {
     const int e = plan_find(plan.first, p.E, r);
-    const int per = plan_rows_per_tile(plan.first[e + 1] - plan.first[e], p.nt);
+    const int per = plan_rows_per_tile(plan.first[e + 1] - plan.first[e], p.nt, p.align);
     const int in_e = r - plan.first[e], t = in_e / per;
     return {static_cast<int64_t>(plan.tile[e] + t) * kb_all, in_e - t * per};
 }

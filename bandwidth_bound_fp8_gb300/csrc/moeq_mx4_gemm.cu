@@ -7,8 +7,8 @@
 // are the MMA's 128-row operand and tokens its N operand, so a decode batch
 // (one or two rows an expert) wastes no tensor time on padding and the same
 // kernel serves one token and a prompt: N is the tile's rows, rounded to 16.
-//   warp 0      copies: a stage is a weight tile (16 KiB), a token tile's K
-//               block and both scale blocks, all contiguous (bulk copies)
+//   warps 0, 2  copies: a stage is a weight tile (16 KiB), a token tile's K
+//               block and both scale blocks, all contiguous
 //   warp 1      issues the MMAs (one thread)
 //   warps 4..7  epilogue: TMEM -> y, behind the next unit's MMAs (two
 //               accumulators)
@@ -17,6 +17,8 @@
 // between CTAs leaves fp32 partials in the workspace and the CTA that
 // arrives last sums them in the order of K, so the result does not depend on
 // which one that is.  No CTA ever waits for another.
+#include <cuda.h>
+
 #include "moeq_device.cuh"
 #include "moeq_mx4_plan.cuh"
 #include "moeq_rows.h"
@@ -26,23 +28,27 @@ namespace {
 
 constexpr int kThreads = kPlanThreads;
 constexpr int kMaxStages = 12;
+// Tiles of this many rows or more are multiplied by pairs of CTAs; their most
+// rows (a multiple of 32).
+constexpr int kPairRows = 64, kPairTileRows = 224;
 // Whole units from this many a CTA on (below, the stages are dealt evenly).
 constexpr int kWholeWaves = 4;
 // TMEM columns: accumulators at 0 and 256, the tokens' scales in between and
 // the weights' behind.
 constexpr int kTmemCols = 512, kAcc1 = 256, kColSfb = 240, kColSfa = 496;
 
-__host__ __device__ constexpr int stage_bytes_of(int nt) {
-    return (kMx4TileBytes + nt * 128 + kMx4TileScaleBytes + mx4_tile_scale_bytes(nt) + 1023) / 1024 * 1024;
+__host__ __device__ constexpr int stage_bytes_of(int nt, bool pair) {
+    return (kMx4TileBytes + nt / (pair ? 2 : 1) * 128 + kMx4TileScaleBytes + mx4_tile_scale_bytes(nt) + 1023) / 1024 * 1024;
 }
 
 struct Sched {
-    int units, kb, grid, cta;
+    int units, kb, grid, cta;  // cta, grid: of pairs where two CTAs share a unit
+    int nbu, rank;             // weight units of a tile (blocks of 128 rows, or pairs of them); this CTA of its pair
     bool whole;
     long long s0, s1;   // this CTA's stages (dealt mode)
 };
 struct Part {
-    int u, n0, r0, n, kb0, kb1, tile, tiles, e, nb;
+    int u, n0, r0, n, n_mma, kb0, kb1, tile, tiles, e, nb;
 };
 
 __device__ __forceinline__ long long deal(long long stages, int c, int grid) { return stages * c / grid; }
@@ -65,19 +71,19 @@ __device__ __forceinline__ bool part_at(const Sched& s, const Mx4GemmArgs& a, co
         p.kb0 = static_cast<int>(lo - u * s.kb);
         p.kb1 = static_cast<int>(hi - u * s.kb);
     }
-    const int nbt = mx4_nb(a.N), nt = a.plan.nt;
-    const int e = plan_find(plan.tile, a.plan.E, p.u / nbt);  // experts without tiles are never the last such
+    const int nt = a.plan.nt, align = a.plan.align;
+    const int e = plan_find(plan.tile, a.plan.E, p.u / s.nbu);  // experts without tiles are never the last such
     const int r0 = plan.first[e], cnt = plan.first[e + 1] - r0;
-    const int tiles = plan.tile[e + 1] - plan.tile[e], per = plan_rows_per_tile(cnt, nt);
-    const int local = p.u - plan.tile[e] * nbt;
+    const int tiles = plan.tile[e + 1] - plan.tile[e], per = plan_rows_per_tile(cnt, nt, align);
+    const int local = p.u - plan.tile[e] * s.nbu, nbu = local / tiles, t = local - nbu * tiles;
     p.e = e;
     p.tiles = tiles;
-    p.nb = local / tiles;
+    p.nb = align == 32 ? 2 * nbu + s.rank : nbu;
     p.n0 = p.nb * kMx4TileRows;
-    const int t = local - p.nb * tiles;
     p.tile = plan.tile[e] + t;
     p.r0 = r0 + t * per;
     p.n = min(per, cnt - t * per);
+    p.n_mma = (p.n + align - 1) & ~(align - 1);
     return true;
 }
 
@@ -90,22 +96,118 @@ __device__ __forceinline__ uint64_t sf_desc(uint32_t smem_addr) {
     d |= static_cast<uint64_t>(1) << 46;
     return d;
 }
+// With kPair the instructions act on a pair of CTAs (one cluster): issued by
+// the first, they read shared memory and write TMEM at the same offsets in
+// both.
+template <bool kPair>
 __device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    if constexpr (kPair)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
-// E2M1 operands, E8M0 scales, fp32 accumulator, 128 x N; the scale bytes of
-// the MMA's 64 columns are bytes sf and sf + 1 of each row's word.
-__device__ __forceinline__ uint32_t idesc_mx4(int n, int sf) {
+// E2M1 operands, E8M0 scales, fp32 accumulator, m x n; the scale bytes of the
+// MMA's 64 columns are bytes sf and sf + 1 of each row's word.
+__device__ __forceinline__ uint32_t idesc_mx4(int m, int n, int sf) {
     return (static_cast<uint32_t>(sf) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (1u << 23) | ((128u >> 4) << 24) | (static_cast<uint32_t>(sf) << 29);
+           (1u << 23) | (static_cast<uint32_t>(m >> 4) << 24) | (static_cast<uint32_t>(sf) << 29);
 }
+template <bool kPair>
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                         int acc) {
+    if constexpr (kPair)
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %6, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %6, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+            : "memory");
+}
+// One arrival on `bar` (in both CTAs of a pair) when everything issued so far
+// has completed.
+template <bool kPair>
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    if constexpr (kPair)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        umma_commit(bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_take(uint32_t* smem_dst) {
+    if constexpr (kPair) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_dst)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(smem_dst, kTmemCols);
+    }
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_give(uint32_t taddr) {
+    if constexpr (kPair)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
+    else
+        tmem_dealloc(taddr, kTmemCols);
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// This barrier's address in the first CTA of the pair.
+__device__ __forceinline__ uint32_t in_first(uint64_t* bar) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+    return r;
+}
+// Rows y .. of a matrix of 128-byte rows into this CTA's shared memory,
+// counted on a barrier of either CTA of the pair (which only tensor copies
+// can do; a thread that passed the news on took 1200 cycles a stage for its
+// release).
+__device__ __forceinline__ void rows_load(void* dst, const CUtensorMap* map, int y, uint32_t bar, uint64_t policy) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+        "[%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(bar), "l"(policy)
         : "memory");
+}
+// An arrival on the first CTA's barrier at this offset.
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+    asm volatile(
+        "{ .reg .b32 r; mapa.shared::cluster.u32 r, %0, 0;\nmbarrier.arrive.release.cluster.shared::cluster.b64 _, [r]; }" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+// As mbar_wait_bounded, seeing what the other CTA of the pair released.
+__device__ __forceinline__ bool cluster_try_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool cluster_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (cluster_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (cluster_try_wait(bar, parity)) return true;
+        if ((i & 63u) == 0 && (*abort || global_timer_ns() - t0 > kWaitLimitNs)) return false;
+    }
 }
 
 __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
@@ -139,17 +241,24 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 // Whether a phase is complete, without waiting.
+template <bool kPair>
 __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
     uint32_t done;
-    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(done)
-                 : "r"(smem_u32(bar)), "r"(parity)
-                 : "memory");
+    if constexpr (kPair)
+        asm volatile(
+            "{ .reg .pred p; mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(done)
+                     : "r"(smem_u32(bar)), "r"(parity)
+                     : "memory");
     return done != 0;
 }
-// Wait (bounded) for what is in flight after a give-up.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
-    const unsigned long long t0 = global_timer_ns();
+// Wait (bounded, from t0 on) for what is in flight after a give-up.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, unsigned long long t0) {
     while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs) {
     }
 }
@@ -165,8 +274,8 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
 // The sum of a unit's parts for 16 columns, all in the order of K: this CTA's
 // own (v) comes from TMEM, the others' from the workspace, two parts' loads
 // in flight at a time.  lo_second: the first CTA's part is in its second slot.
-__device__ __forceinline__ void sum_parts(const float* __restrict__ part, size_t slot_floats, int c_lo, int c_hi, int own,
-                                          int lo_second, int c0, int row, float (&v)[16]) {
+__device__ __forceinline__ void sum_parts(const float* __restrict__ part, size_t worker_floats, size_t slot_floats,
+                                          int c_lo, int c_hi, int own, int lo_second, int c0, int row, float (&v)[16]) {
     float sum[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) sum[c] = 0.f;
@@ -178,7 +287,7 @@ __device__ __forceinline__ void sum_parts(const float* __restrict__ part, size_t
             const int k = k0 + j;
             if (k > c_hi || k == own) continue;
             // only the first of a unit's CTAs can have begun in another unit
-            const float* slot = part + (static_cast<size_t>(2 * k) + (k == c_lo ? lo_second : 0)) * slot_floats + at;
+            const float* slot = part + k * worker_floats + (k == c_lo ? lo_second : 0) * slot_floats + at;
 #pragma unroll
             for (int c = 0; c < 4; ++c) f[j][c] = __ldcg(reinterpret_cast<const float4*>(slot + c * 512));
         }
@@ -251,8 +360,25 @@ __device__ __forceinline__ void store_step(const Mx4GemmArgs& a, const Part& p, 
         if (c0 + c1 + i * kRows < p.n) *reinterpret_cast<uint4*>(y + i * step) = w[i];
 }
 
-template <bool kF32>
-__global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4GemmArgs a) {
+// The operands as matrices of 128-byte rows, for a pair's copies: the box is
+// what one copy takes.
+struct PairMaps {
+    CUtensorMap w, sw, sa;                 // 128 rows, 8, and a K block's token scales
+    CUtensorMap a[kPairTileRows / 2 / 16];  // 16 rows, 32, ...
+};
+struct NoMaps {};
+template <bool kPair>
+struct MapsOf {
+    using type = NoMaps;
+};
+template <>
+struct MapsOf<true> {
+    using type = PairMaps;
+};
+
+template <bool kF32, bool kPair>
+__global__ void __maxnreg__(160)
+    mx4_gemm_kernel(const __grid_constant__ Mx4GemmArgs a, const __grid_constant__ typename MapsOf<kPair>::type maps) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_base_s;
@@ -261,8 +387,9 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nt = a.plan.nt;
     const int sfb_bytes = mx4_tile_scale_bytes(nt), sfb_chunk = sfb_bytes / 2;
-    const int off_b = kMx4TileBytes, off_sfa = off_b + nt * 128, off_sfb = off_sfa + kMx4TileScaleBytes;
-    const int stage_bytes = stage_bytes_of(nt);
+    const int off_b = kMx4TileBytes, off_sfa = off_b + nt / (kPair ? 2 : 1) * 128, off_sfb = off_sfa + kMx4TileScaleBytes;
+    const int stage_bytes = stage_bytes_of(nt, kPair);
+    const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
     volatile int* abort = &abort_s;
 
     if (tid == 0) {
@@ -273,76 +400,97 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 4);
+            mbar_init(&acc_empty[i], kPair ? 8 : 4);
         }
         mbar_init(&drained, 1);
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(&tmem_base_s, kTmemCols);
+        tmem_take<kPair>(&tmem_base_s);
         tc_fence_before();
     }
     plan_scan(a.plan, plan);  // ends in a block barrier
+    if constexpr (kPair) cluster_sync();  // the other CTA's barriers are set up
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
-    const int nbt = mx4_nb(a.N), total = plan.tile[a.plan.E] * nbt;
+    const int nbt = mx4_nb(a.N), nbu = kPair ? (nbt + 1) / 2 : nbt, total = plan.tile[a.plan.E] * nbu;
+    const int workers = gridDim.x / (kPair ? 2 : 1);
 
     Sched s;
     s.units = total;
     s.kb = mx4_kb(a.K);
-    s.cta = blockIdx.x;
+    s.cta = blockIdx.x / (kPair ? 2 : 1);
+    s.nbu = nbu;
+    s.rank = rank;
     const long long all_stages = static_cast<long long>(total) * s.kb;
-    s.grid = static_cast<int>(min(static_cast<long long>(gridDim.x), all_stages));
-    s.whole = total >= kWholeWaves * static_cast<int>(gridDim.x);
+    s.grid = static_cast<int>(min(static_cast<long long>(workers), all_stages));
+    s.whole = total >= kWholeWaves * workers;
     s.s0 = s.s1 = 0;
     if (!s.whole && s.cta < s.grid) {
         s.s0 = deal(all_stages, s.cta, s.grid);
         s.s1 = deal(all_stages, s.cta + 1, s.grid);
     }
     auto stage_at = [&](int st) { return smem + st * stage_bytes; };
+    auto slot_of = [&](int worker) { return static_cast<size_t>(kPair ? 2 * worker + rank : worker); };
     auto give_up = [&] {
         *abort = 1;
         if (a.status) atomicExch(a.status, static_cast<int>(MOEQ_ERR_TIMEOUT));
     };
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
         // -------------------------------------------------------- copies
+        // Warp 0 copies weights, warp 2 tokens: a copy takes its thread about
+        // 100 cycles, four a stage would keep the tensor cores waiting.
         if (elect_one()) {
             // weights that one token tile reads are not read again; those of
             // several, and the token tiles, come from L2 the next time
             const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
             auto weights = [&](const Part& p, int kb, int st) {
-                const int64_t tile = (static_cast<int64_t>(p.e) * nbt + p.nb) * s.kb + kb;
+                // (an odd last block has no partner: its pair reads it twice and stores it once)
+                const int64_t tile = (static_cast<int64_t>(p.e) * nbt + min(p.nb, nbt - 1)) * s.kb + kb;
                 const uint64_t policy = p.tiles > 1 ? again : once;
-                const int n16 = (p.n + 15) & ~15;
-                mbar_arrive_expect_tx(&full[st], kMx4TileBytes + kMx4TileScaleBytes + n16 * 128 + sfb_bytes);
-                bulk_load(stage_at(st), a.w + tile * kMx4TileBytes, kMx4TileBytes, &full[st], policy);
-                bulk_load(stage_at(st) + off_sfa, a.sw + tile * kMx4TileScaleBytes, kMx4TileScaleBytes, &full[st], policy);
+                uint8_t* const at = stage_at(st);
+                if constexpr (kPair) {
+                    // both CTAs' copies count on the first's barrier
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(
+                            &full[st], 2 * (kMx4TileBytes + kMx4TileScaleBytes + p.n_mma / 2 * 128 + sfb_bytes));
+                    rows_load(at, &maps.w, static_cast<int>(tile * 128), in_first(&full[st]), policy);
+                    rows_load(at + off_sfa, &maps.sw, static_cast<int>(tile * 8), in_first(&full[st]), policy);
+                } else {
+                    mbar_arrive_expect_tx(&full[st], kMx4TileBytes + kMx4TileScaleBytes + p.n_mma * 128 + sfb_bytes);
+                    bulk_load(at, a.w + tile * kMx4TileBytes, kMx4TileBytes, &full[st], policy);
+                    bulk_load(at + off_sfa, a.sw + tile * kMx4TileScaleBytes, kMx4TileScaleBytes, &full[st], policy);
+                }
             };
             auto tokens = [&](const Part& p, int kb, int st) {
                 const int64_t block = static_cast<int64_t>(p.tile) * s.kb + kb;
-                const int n16 = (p.n + 15) & ~15;
-                bulk_load(stage_at(st) + off_b, a.a + block * nt * 128, n16 * 128, &full[st], again);
-                bulk_load(stage_at(st) + off_sfb, a.sa + block * sfb_bytes, sfb_bytes, &full[st], again);
+                uint8_t* const at = stage_at(st);
+                if constexpr (kPair) {
+                    // a pair's CTAs hold half the rows each, and all the scales
+                    const int half = p.n_mma / 2;
+                    rows_load(at + off_b, &maps.a[half / 16 - 1], static_cast<int>(block * nt) + rank * half,
+                              in_first(&full[st]), again);
+                    rows_load(at + off_sfb, &maps.sa, static_cast<int>(block * (sfb_bytes / 128)), in_first(&full[st]), again);
+                } else {
+                    bulk_load(at + off_b, a.a + block * nt * 128, p.n_mma * 128, &full[st], again);
+                    bulk_load(at + off_sfb, a.sa + block * sfb_bytes, sfb_bytes, &full[st], again);
+                }
             };
-            // The first stages' weights need not wait for the kernel ahead,
-            // which writes the token tiles.
+            // The token tiles are written by the kernel ahead; the weights are not.
+            if (warp == 2) pdl_wait();
             Part p;
-            int ahead = 0;
-            for (int i = 0; ahead < a.stages && part_at(s, a, plan, i, p); ++i)
-                for (int kb = p.kb0; kb < p.kb1 && ahead < a.stages; ++kb) weights(p, kb, ahead++);
-            pdl_wait();
             int it = 0, st = 0;
             uint32_t phase = 1;  // of the ring's previous round
             bool ok = true;
             for (int i = 0; ok && part_at(s, a, plan, i, p); ++i)
                 for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
-                    if (it >= ahead) {
-                        ok = mbar_wait_bounded(&empty[st], phase, abort);
-                        if (!ok) break;
+                    if (it >= a.stages) ok = mbar_wait_bounded(&empty[st], phase, abort);
+                    if (!ok) break;
+                    if (warp == 0)
                         weights(p, kb, st);
-                    }
-                    tokens(p, kb, st);
+                    else
+                        tokens(p, kb, st);
                     if (++st == a.stages) {
                         st = 0;
                         phase ^= 1;
@@ -350,8 +498,10 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
                 }
             if (!ok) {
                 give_up();
-                // copies in flight land before the CTA may end
-                for (int j = max(0, it - a.stages); j < it; ++j) drain(&full[j % a.stages], (j / a.stages) & 1);
+                // copies in flight land before the CTA may end (a pair's are all
+                // counted in the first, and the pair ends together)
+                const unsigned long long t0 = global_timer_ns();
+                for (int j = max(0, it - a.stages); rank == 0 && j < it; ++j) drain(&full[j % a.stages], (j / a.stages) & 1, t0);
             }
         }
         __syncwarp();
@@ -359,19 +509,22 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
         // ---------------------------------------------------------- MMAs
         // The tensor core's queue holds little: the next stage's barrier is
         // asked for while this one's last MMAs go out.
-        if (elect_one()) {
+        if (rank == 0 && elect_one()) {
             int st = 0;
             uint32_t phase = 0;
             bool ok = true, ready = false;
             Part p;
             for (int i = 0; ok && part_at(s, a, plan, i, p); ++i) {
                 const int buf = i & 1;
-                if (i >= 2) ok = mbar_wait_bounded(&acc_empty[buf], ((i >> 1) - 1) & 1, abort);
-                const int n16 = (p.n + 15) & ~15;
+                if (i >= 2) {
+                    const uint32_t ph = ((i >> 1) - 1) & 1;
+                    ok = kPair ? cluster_wait_bounded(&acc_empty[buf], ph, abort) : mbar_wait_bounded(&acc_empty[buf], ph, abort);
+                }
                 const uint32_t d = tmem + buf * kAcc1;
-                const uint32_t id0 = idesc_mx4(n16, 0), id2 = idesc_mx4(n16, 2);
+                const uint32_t id0 = idesc_mx4(kPair ? 256 : 128, p.n_mma, 0), id2 = idesc_mx4(kPair ? 256 : 128, p.n_mma, 2);
                 for (int kb = p.kb0; ok && kb < p.kb1; ++kb) {
-                    if (!ready) ok = mbar_wait_bounded(&full[st], phase, abort);
+                    if (!ready)
+                        ok = kPair ? cluster_wait_bounded(&full[st], phase, abort) : mbar_wait_bounded(&full[st], phase, abort);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t sp = smem_u32(stage_at(st));
@@ -384,24 +537,25 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
                     }
 #pragma unroll
                     for (int kc = 0; kc < 2; ++kc) {
-                        sf_copy(tmem + kColSfa + kc * 4, fa + kc * (512 >> 4));
-                        sf_copy(tmem + kColSfb + kc * 8, fb + kc * (sfb_chunk >> 4));
-                        if (n16 > 128) sf_copy(tmem + kColSfb + kc * 8 + 4, fb + kc * (sfb_chunk >> 4) + (512 >> 4));
+                        sf_copy<kPair>(tmem + kColSfa + kc * 4, fa + kc * (512 >> 4));
+                        sf_copy<kPair>(tmem + kColSfb + kc * 8, fb + kc * (sfb_chunk >> 4));
+                        if (p.n_mma > 128)
+                            sf_copy<kPair>(tmem + kColSfb + kc * 8 + 4, fb + kc * (sfb_chunk >> 4) + (512 >> 4));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {  // 64 columns = 32 bytes of a row
-                        if (j == 2) ready = mbar_test_wait(&full[st], phase);
-                        mma_mx4(d, ad + j * 2, bd + j * 2, j & 1 ? id2 : id0, tmem + kColSfa + (j >> 1) * 4,
+                        if (j == 2) ready = mbar_test_wait<kPair>(&full[st], phase);
+                        mma_mx4<kPair>(d, ad + j * 2, bd + j * 2, j & 1 ? id2 : id0, tmem + kColSfa + (j >> 1) * 4,
                                 tmem + kColSfb + (j >> 1) * 8, kb > p.kb0 || j > 0);
                     }
-                    umma_commit(done);
+                    mma_commit<kPair>(done);
                 }
-                if (ok) umma_commit(&acc_full[buf]);
+                if (ok) mma_commit<kPair>(&acc_full[buf]);
             }
             if (!ok) {
                 give_up();
-                umma_commit(&drained);
-                drain(&drained, 0);
+                mma_commit<kPair>(&drained);
+                drain(&drained, 0, global_timer_ns());
             }
         }
         __syncwarp();
@@ -430,6 +584,7 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
             const uint32_t acc = tmem + buf * kAcc1 + (static_cast<uint32_t>(q * 32) << 16);
             const int n = p.n0 + q * 32 + lane;
             const size_t slot_floats = static_cast<size_t>(nt) * 128;
+            int* const ticket = a.tickets + (kPair ? 2 * p.u + rank : p.u);
             const bool cut = p.kb0 > 0 || p.kb1 < s.kb;
             // the CTAs that hold the unit's stages: c_lo .. c_hi
             int c_lo = s.cta, c_hi = s.cta;
@@ -438,12 +593,12 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
                 const long long f = static_cast<long long>(p.u) * s.kb, l = f + s.kb - 1;
                 while (deal(all_stages, c_lo, s.grid) > f) --c_lo;
                 while (deal(all_stages, c_hi + 1, s.grid) <= l) ++c_hi;
-                if (tid == 128) last_s[buf] = ld_acquire(a.tickets + p.u) == c_hi - c_lo;
+                if (tid == 128) last_s[buf] = ld_acquire(ticket) == c_hi - c_lo;
                 named_sync(1, 128);
                 join = last_s[buf];
                 if (!join) {
                     float4* slot = reinterpret_cast<float4*>(
-                                       a.part + (static_cast<size_t>(2 * s.cta) + (p.u != s.s0 / s.kb)) * slot_floats) +
+                                       a.part + (2 * slot_of(s.cta) + (p.u != s.s0 / s.kb)) * slot_floats) +
                                    q * 32 + lane;
                     for (int c0 = 0; c0 < p.n; c0 += 16) {
                         float v[16];
@@ -456,19 +611,24 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
                     }
                     __threadfence();
                     named_sync(1, 128);
-                    if (tid == 128) last_s[buf] = atom_add_acq_rel(a.tickets + p.u, 1) == c_hi - c_lo;
+                    if (tid == 128) last_s[buf] = atom_add_acq_rel(ticket, 1) == c_hi - c_lo;
                     named_sync(1, 128);
                     join = last_s[buf];
                 }
                 if (join) {
                     __threadfence();
-                    if (tid == 128) a.tickets[p.u] = 0;
+                    if (tid == 128) *ticket = 0;
                 }
             }
             auto release = [&] {  // the accumulator is read: the next unit but one may have it
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                if (lane == 0) {
+                    if (kPair && rank == 1)
+                        arrive_first(&acc_empty[buf]);
+                    else
+                        mbar_arrive(&acc_empty[buf]);
+                }
             };
             if (!cut) {
                 constexpr int kCols = Epi<kF32>::kCols;
@@ -489,7 +649,7 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
                     tmem_ld16(acc + c0, v);
                     tmem_wait_ld();
                     tmem_use16(v);
-                    sum_parts(a.part, slot_floats, c_lo, c_hi, s.cta, lo_second, c0, q * 32 + lane, v);
+                    sum_parts(a.part + 2 * rank * slot_floats, (kPair ? 2 : 1) * 2 * slot_floats, slot_floats, c_lo, c_hi, s.cta, lo_second, c0, q * 32 + lane, v);
                     store_step<kF32, 16>(a, p, c0, q, lane, n, v, stage_y, vec_y);
                 }
                 release();
@@ -502,46 +662,105 @@ __global__ void __maxnreg__(160) mx4_gemm_kernel(const __grid_constant__ Mx4Gemm
     }
     tc_fence_before();
     __syncthreads();
+    __syncwarp();
+    if constexpr (kPair) cluster_sync();  // neither CTA's shared memory or TMEM is in use any more
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_give<kPair>(tmem);
     }
 }
 
 }  // namespace
 
-// Rows of a token tile.  About twice the average of an expert, so that most
-// experts are one tile (its weights then stream once), but no wider than
-// that: a narrow tile leaves shared memory to more weight stages in flight.
-int mx4_tile_rows(int R, int E) {
-    const long long want = 2LL * R / E + 16;
-    const int r16 = (R + 15) / 16 * 16;
-    const int w16 = static_cast<int>(want > kMx4MaxTileRows ? kMx4MaxTileRows : (want + 15) / 16 * 16);
-    const int nt = E == 1 ? r16 : w16;
-    return nt < r16 ? (nt > kMx4MaxTileRows ? kMx4MaxTileRows : nt) : (r16 > kMx4MaxTileRows ? kMx4MaxTileRows : r16);
+// Rows of a token tile, and whether pairs of CTAs multiply it.  About twice
+// the average of an expert, so that most experts are one tile (its weights
+// then stream once), but no wider than that: a narrow tile leaves shared
+// memory to more weight stages in flight.
+Mx4Tiling mx4_tiling(int R, int E) {
+    const long long want = E == 1 ? R : 2LL * R / E + 16;
+    const bool pair = want >= kPairRows && R >= kPairRows;
+    const int align = pair ? 32 : 16, most = pair ? kPairTileRows : kMx4MaxTileRows;
+    auto up = [&](long long x) { return static_cast<int>(x > most ? most : (x + align - 1) / align * align); };
+    return {up(want < R ? want : R), align};
 }
 
-cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stream) {
-    const int sb = stage_bytes_of(a.plan.nt);
-    // of 227 KiB: less the static arrays, the alignment and the epilogue's buffers
-    const int budget = 216 * 1024 - kEpiBytes;
-    a.stages = budget / sb < kMaxStages ? budget / sb : kMaxStages;
-    const int smem = a.stages * sb + kEpiBytes + 1024;
-    auto kern = a.y_f32 ? mx4_gemm_kernel<true> : mx4_gemm_kernel<false>;
-    static SmemOnce once[2];
-    const cudaError_t e = once[a.y_f32 != 0].raise(reinterpret_cast<const void*>(kern), budget + kEpiBytes + 1024);
+namespace {
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder (the library links the runtime only).
+EncodeTiled encode_tiled() {
+    static const EncodeTiled f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+bool rows_map(CUtensorMap* map, const void* p, int64_t rows, int box_rows) {
+    const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)}, strides[1] = {128};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, steps[2] = {1, 1};
+    const EncodeTiled f = encode_tiled();
+    return f && f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kF32, bool kPair>
+cudaError_t launch_one(const Mx4GemmArgs& a, const typename MapsOf<kPair>::type& maps, int grid, int smem, int most_smem,
+                       bool pdl, cudaStream_t stream) {
+    const auto kern = mx4_gemm_kernel<kF32, kPair>;
+    static SmemOnce once;
+    const cudaError_t e = once.raise(reinterpret_cast<const void*>(kern), most_smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[0].val.programmaticStreamSerializationAllowed = pdl;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    cfg.numAttrs = kPair ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, maps);
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stream) {
+    const bool pair = a.plan.align == 32;
+    const int sb = stage_bytes_of(a.plan.nt, pair);
+    // of 227 KiB: less the static arrays, the alignment and the epilogue's buffers
+    const int budget = 216 * 1024 - kEpiBytes;
+    a.stages = budget / sb < kMaxStages ? budget / sb : kMaxStages;
+    const int smem = a.stages * sb + kEpiBytes + 1024, most = budget + kEpiBytes + 1024;
+    if (!pair)
+        return a.y_f32 ? launch_one<true, false>(a, NoMaps{}, grid, smem, most, pdl, stream)
+                       : launch_one<false, false>(a, NoMaps{}, grid, smem, most, pdl, stream);
+    PairMaps maps;
+    const int64_t tiles = static_cast<int64_t>(a.plan.E) * mx4_nb(a.N) * mx4_kb(a.K);
+    const int64_t blocks = mx4_max_tiles(a.plan.R, a.plan.E, a.plan.nt) * mx4_kb(a.K);
+    const int sfb_rows = mx4_tile_scale_bytes(a.plan.nt) / 128;
+    if (!rows_map(&maps.w, a.w, tiles * 128, 128) || !rows_map(&maps.sw, a.sw, tiles * 8, 8) ||
+        !rows_map(&maps.sa, a.sa, blocks * sfb_rows, sfb_rows))
+        return cudaErrorInvalidValue;
+    for (int i = 0; i < kPairTileRows / 2 / 16; ++i)
+        if (!rows_map(&maps.a[i], a.a, blocks * a.plan.nt, 16 * (i + 1))) return cudaErrorInvalidValue;
+    grid = grid / 2 * 2;
+    return a.y_f32 ? launch_one<true, true>(a, maps, grid, smem, most, pdl, stream)
+                   : launch_one<false, true>(a, maps, grid, smem, most, pdl, stream);
 }
 
 }  // namespace moeq

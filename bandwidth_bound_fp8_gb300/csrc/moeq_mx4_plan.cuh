@@ -78,10 +78,11 @@ __device__ __forceinline__ int plan_find(const int* v, int n, int x) {
     return lo;
 }
 
-// An expert's rows are shared out evenly over its tiles, 16 at a time.
-__device__ __forceinline__ int plan_rows_per_tile(int rows, int nt) {
+// An expert's rows are shared out evenly over its tiles, `align` (16 or 32) at
+// a time.
+__device__ __forceinline__ int plan_rows_per_tile(int rows, int nt, int align) {
     const int tiles = max((rows + nt - 1) / nt, 1);
-    return ((rows + tiles - 1) / tiles + 15) & ~15;
+    return ((rows + tiles - 1) / tiles + align - 1) & ~(align - 1);
 }
 
 }  // namespace moeq

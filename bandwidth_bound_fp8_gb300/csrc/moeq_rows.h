@@ -81,8 +81,12 @@ cudaError_t launch_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, 
 constexpr int kMx4MaxTileRows = 240;
 constexpr int kMx4Tickets = 4096;
 __host__ __device__ constexpr int mx4_tile_scale_bytes(int nt) { return nt > 128 ? 2048 : 1024; }
-// Most rows of one token tile for R rows over E experts (a multiple of 16).
-int mx4_tile_rows(int R, int E);
+// Most rows of one token tile for R rows over E experts, and what tiles' rows
+// are rounded to: 16, or 32 where pairs of CTAs multiply them.
+struct Mx4Tiling {
+    int nt, align;
+};
+Mx4Tiling mx4_tiling(int R, int E);
 // Most token tiles there can be.
 __host__ __device__ constexpr int64_t mx4_max_tiles(int R, int E, int nt) { return R / nt + (E < R ? E : R); }
 
@@ -91,7 +95,7 @@ struct Mx4Plan {
     const int32_t* offs;      // [E + 1]
     const int32_t* row_pair;  // [R] or NULL: row r reads activation row r
     int E, R, top_k, rows;    // rows: activation rows
-    int nt;
+    int nt, align;
 };
 
 // Source of the tiles: a matrix to quantise (act as in

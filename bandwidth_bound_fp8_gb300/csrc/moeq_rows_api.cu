@@ -67,19 +67,20 @@ bool rows_ok(const void* p, moeq_dtype t, int64_t ld, int64_t width) {
 // are gathered), the token tiles and their scales, and the parts' sums.
 struct Mx4Ws {
     size_t tickets, codes, scales, tiles, stiles, part, end;
-    int nt;
+    Mx4Tiling tiling;
 };
 Mx4Ws mx4_ws(int64_t rows, int K, int E, int R, int sms) {
     Mx4Ws l;
-    l.nt = mx4_tile_rows(R > 0 ? R : 1, E);
-    const size_t blocks = static_cast<size_t>(mx4_max_tiles(R > 0 ? R : 1, E, l.nt)) * mx4_kb(K);
+    l.tiling = mx4_tiling(R > 0 ? R : 1, E);
+    const int nt = l.tiling.nt;
+    const size_t blocks = static_cast<size_t>(mx4_max_tiles(R > 0 ? R : 1, E, nt)) * mx4_kb(K);
     l.tickets = 256;
     l.codes = l.tickets + up256(kMx4Tickets * sizeof(int));
     l.scales = l.codes + up256(static_cast<size_t>(rows) * (K / 2));
     l.tiles = l.scales + up256(static_cast<size_t>(rows) * mx4_scale_pitch(K));
-    l.stiles = l.tiles + up256(blocks * l.nt * 128);
-    l.part = l.stiles + up256(blocks * mx4_tile_scale_bytes(l.nt));
-    l.end = l.part + static_cast<size_t>(2 * sms) * l.nt * 128 * sizeof(float);
+    l.stiles = l.tiles + up256(blocks * nt * 128);
+    l.part = l.stiles + up256(blocks * mx4_tile_scale_bytes(nt));
+    l.end = l.part + static_cast<size_t>(2 * sms) * nt * 128 * sizeof(float);
     return l;
 }
 
@@ -268,7 +269,7 @@ moeq_status moeq_mx4_expert_gemm(const void* x, moeq_dtype x_dtype, int64_t ld_x
             return MOEQ_ERR_CUDA;
     }
     Mx4GemmArgs a = {};
-    a.plan = {offs, row_pair_opt, E, R, top_k, rows, l.nt};
+    a.plan = {offs, row_pair_opt, E, R, top_k, rows, l.tiling.nt, l.tiling.align};
     if (launch_mx4_act_tiles(src, a.plan, K, u8 + l.tiles, u8 + l.stiles, dev.sms, st) != cudaSuccess)
         return MOEQ_ERR_CUDA;
     a.w = w;

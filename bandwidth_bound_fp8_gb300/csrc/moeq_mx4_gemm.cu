@@ -26,7 +26,12 @@
 namespace moeq {
 namespace {
 
-constexpr int kThreads = kPlanThreads;
+// Four warps for copies and MMAs, and four of epilogue for each group: a
+// pair's short units (eight stages at K = 2048) end faster than one group
+// stores them, so there two groups take turns.
+__host__ __device__ constexpr int epi_groups(bool pair) { return pair ? 2 : 1; }
+__host__ __device__ constexpr int threads_of(bool pair) { return 128 + 128 * epi_groups(pair); }
+static_assert(threads_of(false) >= kPlanThreads, "the plan's scan needs its threads");
 constexpr int kMaxStages = 12;
 // Tiles of this many rows or more are multiplied by pairs of CTAs; their most
 // rows (a multiple of 32).
@@ -322,7 +327,7 @@ static_assert(Epi<true>::kCols * Epi<true>::kPitch <= kEpiBytes, "one buffer ser
 
 template <bool kF32, int kCols>
 __device__ __forceinline__ void store_step(const Mx4GemmArgs& a, const Part& p, int c0, int q, int lane, int n,
-                                           const float (&v)[kCols], uint8_t* buf, bool vec) {
+                                           const float (&v)[kCols], uint8_t* buf, bool vec, int bar) {
     constexpr int kPitch = Epi<kF32>::kPitch;
     if (!vec) {
 #pragma unroll
@@ -330,7 +335,7 @@ __device__ __forceinline__ void store_step(const Mx4GemmArgs& a, const Part& p, 
             if (c0 + c < p.n && n < a.N) store_y<kF32>(a.y, static_cast<int64_t>(p.r0 + c0 + c) * a.ld_y + n, v[c]);
         return;
     }
-    named_sync(1, 128);  // the step before has left the buffer
+    named_sync(bar, 128);  // the step before has left the buffer
     if constexpr (kF32) {
 #pragma unroll
         for (int c = 0; c < kCols; ++c) *reinterpret_cast<float*>(buf + c * kPitch + (q * 32 + lane) * 4) = v[c];
@@ -345,7 +350,7 @@ __device__ __forceinline__ void store_step(const Mx4GemmArgs& a, const Part& p, 
                 odd ? __floats2bfloat162_rn(got, v[c + 1]) : __floats2bfloat162_rn(v[c], got);
         }
     }
-    named_sync(1, 128);
+    named_sync(bar, 128);
     constexpr int kPer = kF32 ? 4 : 8, kPieces = 128 / kPer, kRows = 128 / kPieces;  // of a piece; of a row; at a time
     const int t = q * 32 + lane, piece = t % kPieces, c1 = t / kPieces;
     if (p.n0 + piece * kPer >= a.N) return;
@@ -382,7 +387,7 @@ __global__ void __maxnreg__(160)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_base_s;
-    __shared__ int abort_s, go_s[2], last_s[2];
+    __shared__ int abort_s, go_s[2][2], last_s[2][2];
     __shared__ PlanShared plan;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nt = a.plan.nt;
@@ -562,24 +567,24 @@ __global__ void __maxnreg__(160)
     } else if (warp >= 4) {
         // ------------------------------------------------------- epilogue
         pdl_wait();
-        const int q = warp - 4;
-        uint8_t* stage_y = smem + a.stages * stage_bytes;
+        constexpr int kGroups = epi_groups(kPair);
+        const int q = warp & 3, group = (warp >> 2) - 1, bar = 1 + group;
+        const bool chief = tid == 128 + group * 128;
+        uint8_t* stage_y = smem + a.stages * stage_bytes + group * kEpiBytes;
         // rows of y in 16-byte pieces
         const bool vec_y = a.N % (kF32 ? 4 : 8) == 0 && a.ld_y % (kF32 ? 4 : 8) == 0 &&
                            (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
         Part p;
-        for (int i = 0; part_at(s, a, plan, i, p); ++i) {
-            const int buf = i & 1;
+        for (int i = group; part_at(s, a, plan, i, p); i += kGroups) {
+            const int buf = i & 1, turn = i / kGroups & 1;
             if (lane == 0 && !mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1, abort)) give_up();
             __syncwarp();
             // One thread decides for all four warps whether to go on: they meet
-            // at barriers below.  (Two copies: a slow warp may still read the
+            // at barriers below.  (A copy a turn: a slow warp may still read the
             // last unit's.)
-            if (tid == 128) {
-                go_s[buf] = !*abort;
-            }
-            named_sync(1, 128);
-            if (!go_s[buf]) break;
+            if (chief) go_s[group][turn] = !*abort;
+            named_sync(bar, 128);
+            if (!go_s[group][turn]) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * kAcc1 + (static_cast<uint32_t>(q * 32) << 16);
             const int n = p.n0 + q * 32 + lane;
@@ -593,9 +598,9 @@ __global__ void __maxnreg__(160)
                 const long long f = static_cast<long long>(p.u) * s.kb, l = f + s.kb - 1;
                 while (deal(all_stages, c_lo, s.grid) > f) --c_lo;
                 while (deal(all_stages, c_hi + 1, s.grid) <= l) ++c_hi;
-                if (tid == 128) last_s[buf] = ld_acquire(ticket) == c_hi - c_lo;
-                named_sync(1, 128);
-                join = last_s[buf];
+                if (chief) last_s[group][turn] = ld_acquire(ticket) == c_hi - c_lo;
+                named_sync(bar, 128);
+                join = last_s[group][turn];
                 if (!join) {
                     float4* slot = reinterpret_cast<float4*>(
                                        a.part + (2 * slot_of(s.cta) + (p.u != s.s0 / s.kb)) * slot_floats) +
@@ -610,14 +615,14 @@ __global__ void __maxnreg__(160)
                             __stcg(slot + (c0 + c) / 4 * 128, make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]));
                     }
                     __threadfence();
-                    named_sync(1, 128);
-                    if (tid == 128) last_s[buf] = atom_add_acq_rel(ticket, 1) == c_hi - c_lo;
-                    named_sync(1, 128);
-                    join = last_s[buf];
+                    named_sync(bar, 128);
+                    if (chief) last_s[group][turn] = atom_add_acq_rel(ticket, 1) == c_hi - c_lo;
+                    named_sync(bar, 128);
+                    join = last_s[group][turn];
                 }
                 if (join) {
                     __threadfence();
-                    if (tid == 128) *ticket = 0;
+                    if (chief) *ticket = 0;
                 }
             }
             auto release = [&] {  // the accumulator is read: the next unit but one may have it
@@ -640,7 +645,7 @@ __global__ void __maxnreg__(160)
 #pragma unroll
                     for (int j = 0; j < kCols; j += 16) tmem_use16(v + j);
                     if (c0 + kCols >= p.n) release();
-                    store_step<kF32, kCols>(a, p, c0, q, lane, n, v, stage_y, vec_y);
+                    store_step<kF32, kCols>(a, p, c0, q, lane, n, v, stage_y, vec_y, bar);
                 }
             } else {
                 const int lo_second = deal(all_stages, c_lo, s.grid) / s.kb != p.u;
@@ -650,7 +655,7 @@ __global__ void __maxnreg__(160)
                     tmem_wait_ld();
                     tmem_use16(v);
                     sum_parts(a.part + 2 * rank * slot_floats, (kPair ? 2 : 1) * 2 * slot_floats, slot_floats, c_lo, c_hi, s.cta, lo_second, c0, q * 32 + lane, v);
-                    store_step<kF32, 16>(a, p, c0, q, lane, n, v, stage_y, vec_y);
+                    store_step<kF32, 16>(a, p, c0, q, lane, n, v, stage_y, vec_y, bar);
                 }
                 release();
             }
@@ -658,7 +663,7 @@ __global__ void __maxnreg__(160)
         // rows that belong to no expert
         const int t = tid - 128;
         for (int64_t r = static_cast<int64_t>(plan.first[a.plan.E]) + blockIdx.x; r < a.plan.R; r += gridDim.x)
-            for (int c = t; c < a.N; c += 128) store_y<kF32>(a.y, r * a.ld_y + c, 0.f);
+            for (int c = t; c < a.N; c += 128 * kGroups) store_y<kF32>(a.y, r * a.ld_y + c, 0.f);
     }
     tc_fence_before();
     __syncthreads();
@@ -723,7 +728,7 @@ cudaError_t launch_one(const Mx4GemmArgs& a, const typename MapsOf<kPair>::type&
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads_of(kPair));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
@@ -743,9 +748,9 @@ cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stre
     const bool pair = a.plan.align == 32;
     const int sb = stage_bytes_of(a.plan.nt, pair);
     // of 227 KiB: less the static arrays, the alignment and the epilogue's buffers
-    const int budget = 216 * 1024 - kEpiBytes;
+    const int epi = kEpiBytes * epi_groups(pair), budget = 216 * 1024 - epi;
     a.stages = budget / sb < kMaxStages ? budget / sb : kMaxStages;
-    const int smem = a.stages * sb + kEpiBytes + 1024, most = budget + kEpiBytes + 1024;
+    const int smem = a.stages * sb + epi + 1024, most = budget + epi + 1024;
     if (!pair)
         return a.y_f32 ? launch_one<true, false>(a, NoMaps{}, grid, smem, most, pdl, stream)
                        : launch_one<false, false>(a, NoMaps{}, grid, smem, most, pdl, stream);

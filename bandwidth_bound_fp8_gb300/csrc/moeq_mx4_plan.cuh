@@ -17,9 +17,10 @@ struct PlanShared {
 
 // Rows are given to experts by `offs`; values out of range or order are
 // clamped, so that no row, tile or buffer index leaves its range.  Called by
-// all threads of a block of kPlanThreads.
+// all threads of a block of at least kPlanThreads.
 __device__ __forceinline__ void plan_scan(const Mx4Plan& p, PlanShared& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool mine_too = tid < kPlanThreads;
     int top[4], run = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -30,14 +31,14 @@ __device__ __forceinline__ void plan_scan(const Mx4Plan& p, PlanShared& s) {
     int inc = run;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) inc = max(inc, __shfl_up_sync(0xffffffffu, inc, o));
-    if (lane == 31) s.warp[0][warp] = inc;
+    if (lane == 31 && mine_too) s.warp[0][warp] = inc;
     int before = __shfl_up_sync(0xffffffffu, inc, 1);
     if (lane == 0) before = 0;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) before = max(before, s.warp[0][w]);
+    for (int w = 0; w < warp && mine_too; ++w) before = max(before, s.warp[0][w]);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (tid * 4 + i <= p.E) s.first[tid * 4 + i] = max(before, top[i]);
+        if (mine_too && tid * 4 + i <= p.E) s.first[tid * 4 + i] = max(before, top[i]);
     if (tid == kPlanThreads - 1 && p.E == MOEQ_MAX_EXPERTS)
         s.first[p.E] = max(max(before, run), min(max(__ldg(p.offs + p.E), 0), p.R));
     __syncthreads();
@@ -46,7 +47,7 @@ __device__ __forceinline__ void plan_scan(const Mx4Plan& p, PlanShared& s) {
     for (int i = 0; i < 4; ++i) {
         const int e = tid * 4 + i;
         mine[i] = sum;
-        if (e < p.E) sum += (s.first[e + 1] - s.first[e] + p.nt - 1) / p.nt;
+        if (mine_too && e < p.E) sum += (s.first[e + 1] - s.first[e] + p.nt - 1) / p.nt;
     }
     inc = sum;
 #pragma unroll
@@ -54,13 +55,13 @@ __device__ __forceinline__ void plan_scan(const Mx4Plan& p, PlanShared& s) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
     }
-    if (lane == 31) s.warp[1][warp] = inc;
+    if (lane == 31 && mine_too) s.warp[1][warp] = inc;
     __syncthreads();
     before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += s.warp[1][w];
+    for (int w = 0; w < warp && mine_too; ++w) before += s.warp[1][w];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (tid * 4 + i < p.E) s.tile[tid * 4 + i] = before + mine[i];
+        if (mine_too && tid * 4 + i < p.E) s.tile[tid * 4 + i] = before + mine[i];
     if (tid == kPlanThreads - 1) s.tile[p.E] = before + sum;
     __syncthreads();
 }

@@ -160,6 +160,7 @@ struct Segment {
 template <bool kF32, bool kVec, bool kSwiglu>
 __global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__ x, int64_t ld, int rows, int K,
                                                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+    chain();
     using Seg = Segment<kF32, kVec, kSwiglu>;
     constexpr int kBlocks = Seg::kBlocks;
     const int lane = threadIdx.x & 31, segs = segments(K, kBlocks), pitch = mx4_scale_pitch(K);
@@ -205,6 +206,7 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) dequant_act_kernel(const uint8_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ scales, int rows, int K,
                                                           T* __restrict__ out, int64_t ld) {
+    chain();
     const int lane = threadIdx.x & 31, segs = segments(K, kSegment);
     const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int64_t row = item / segs;
@@ -344,7 +346,7 @@ template <bool kF32, bool kVec, bool kSwiglu>
 __global__ void __launch_bounds__(kPlanThreads) act_tiles_kernel(RowsIn x, Mx4Plan p, int K, int parts,
                                                                  uint8_t* __restrict__ tiles,
                                                                  uint8_t* __restrict__ stiles) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    chain();
     __shared__ PlanShared plan;
     using Seg = Segment<kF32, kVec, kSwiglu>;
     constexpr int kBlocks = Seg::kBlocks;
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t*
                                                                   const uint8_t* __restrict__ scales, Mx4Plan p, int K,
                                                                   uint8_t* __restrict__ tiles,
                                                                   uint8_t* __restrict__ stiles) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    chain();
     __shared__ PlanShared plan;
     plan_scan(p, plan);
     constexpr int kWide = 8;
@@ -448,6 +450,14 @@ __global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t*
     }
 }
 
+// The product's CTAs start while the tiles are filled, so an SM that fills
+// them keeps its shared memory as the product wants it (an SM changes the
+// split with L1 only when it is empty: 48 of 152 CTAs started 2 us late).
+template <typename K>
+cudaError_t beside_product(K kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+}
+
 bool fits(const void* p, int64_t ld, int f32) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (f32 ? 4 : 8) == 0;
 }
@@ -461,10 +471,7 @@ cudaError_t launch_mx4_quant_act(RowsIn x, int rows, int K, int act, uint8_t* co
     const unsigned grid = static_cast<unsigned>(want < sms * 4 ? want : sms * 4);
     // the second half of a SwiGLU row starts K elements on: K is a multiple of 32
     const bool vec = fits(x.p, x.ld, x.f32);
-    auto go = [&](auto kern) {
-        kern<<<grid, 256, 0, stream>>>(x.p, x.ld, rows, K, codes, scales);
-        return cudaGetLastError();
-    };
+    auto go = [&](auto kern) { return launch_chained(kern, grid, 256, 0, stream, x.p, x.ld, rows, K, codes, scales); };
     if (x.f32) {
         if (act) return vec ? go(quant_act_kernel<true, true, true>) : go(quant_act_kernel<true, false, true>);
         return vec ? go(quant_act_kernel<true, true, false>) : go(quant_act_kernel<true, false, false>);
@@ -478,8 +485,7 @@ cudaError_t launch_mx4_dequant_act(const uint8_t* codes, const uint8_t* scales, 
     const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(rows) * segments(K, kSegment) + 7) / 8);
     const bool vec = fits(out.p, out.ld, out.f32);
     auto go = [&](auto* o, auto kern) {
-        kern<<<grid, 256, 0, stream>>>(codes, scales, rows, K, o, out.ld);
-        return cudaGetLastError();
+        return launch_chained(kern, grid, 256, 0, stream, codes, scales, rows, K, o, out.ld);
     };
     if (out.f32) {
         float* o = static_cast<float*>(out.p);
@@ -514,9 +520,10 @@ cudaError_t launch_mx4_act_tiles(const Mx4Source& src, const Mx4Plan& plan, int 
     const int most = sms * 4;
     if (src.codes) {
         const int blocks = (plan.R + 7) / 8;
-        code_tiles_kernel<<<blocks < most ? blocks : most, kPlanThreads, 0, stream>>>(src.codes, src.scales, plan, K, tiles,
-                                                                                  stiles);
-        return cudaGetLastError();
+        static const cudaError_t e = beside_product(code_tiles_kernel);
+        return e != cudaSuccess ? e
+                                : launch_chained(code_tiles_kernel, blocks < most ? blocks : most, kPlanThreads, 0, stream,
+                                                 src.codes, src.scales, plan, K, tiles, stiles);
     }
     // a warp a row where that fills the wave, else up to eight (a power of two: it divides a block's warps)
     const int segs = segments(K, kSegment / (src.x.f32 ? 2 : 1) / (src.act ? 2 : 1));
@@ -526,9 +533,19 @@ cudaError_t launch_mx4_act_tiles(const Mx4Source& src, const Mx4Plan& plan, int 
     const unsigned grid = static_cast<unsigned>(want < most ? want : most);
     const bool vec = fits(src.x.p, src.x.ld, src.x.f32);
     auto go = [&](auto kern) {
-        kern<<<grid, kPlanThreads, 0, stream>>>(src.x, plan, K, parts, tiles, stiles);
-        return cudaGetLastError();
+        return launch_chained(kern, grid, kPlanThreads, 0, stream, src.x, plan, K, parts, tiles, stiles);
     };
+    static const cudaError_t e = [] {
+        for (auto k : {act_tiles_kernel<false, false, false>, act_tiles_kernel<false, true, false>,
+                       act_tiles_kernel<false, false, true>, act_tiles_kernel<false, true, true>,
+                       act_tiles_kernel<true, false, false>, act_tiles_kernel<true, true, false>,
+                       act_tiles_kernel<true, false, true>, act_tiles_kernel<true, true, true>}) {
+            const cudaError_t r = beside_product(k);
+            if (r != cudaSuccess) return r;
+        }
+        return cudaSuccess;
+    }();
+    if (e != cudaSuccess) return e;
     if (src.x.f32) {
         if (src.act) return vec ? go(act_tiles_kernel<true, true, true>) : go(act_tiles_kernel<true, false, true>);
         return vec ? go(act_tiles_kernel<true, true, false>) : go(act_tiles_kernel<true, false, false>);

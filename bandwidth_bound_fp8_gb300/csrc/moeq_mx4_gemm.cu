@@ -396,6 +396,9 @@ __global__ void __maxnreg__(160)
     const int stage_bytes = stage_bytes_of(nt, kPair);
     const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
     volatile int* abort = &abort_s;
+    // (the next kernel may be scheduled: it waits for this one before it
+    // touches memory)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (tid == 0) {
         abort_s = 0;

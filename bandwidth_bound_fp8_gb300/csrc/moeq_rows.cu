@@ -149,6 +149,7 @@ __device__ __forceinline__ void clear_key(uint32_t* key, int i, bool me) {
 template <int NPER>
 __global__ void __launch_bounds__(128) route_rows_kernel(const float* __restrict__ logits, int64_t ld, int T, int E,
                                                          int k, int32_t* __restrict__ id, float* __restrict__ w) {
+    chain();
     const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (t >= T) return;
     const float* row = logits + t * ld;
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(128) route_rows_grad_kernel(const float* __res
                                                               const int32_t* __restrict__ id,
                                                               const float* __restrict__ w, int T, int E, int k,
                                                               float* __restrict__ dl, int64_t ld, int vec) {
+    chain();
     const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (t >= T) return;
     float* row = dl + t * ld;
@@ -300,15 +302,12 @@ struct SortArgs {
     int32_t *offs, *pair_row, *row_pair;
 };
 
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Step 1; with kOne the block holds every pair and does the rest too.
 template <bool kOne>
 __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(const SortArgs a) {
     extern __shared__ int bins[];  // [warps][E], then kOne: [E] first rows
     __shared__ int scratch[kSortWarps];
-    pdl_launch();
+    chain();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
     const int64_t p0 = (static_cast<int64_t>(blockIdx.x) * a.warps + warp) * a.run;
     const int64_t p1 = warp < a.warps ? min(p0 + a.run, static_cast<int64_t>(a.P)) : p0;
@@ -370,12 +369,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(const SortArgs 
 // Step 2.
 __global__ void __launch_bounds__(kSortThreads) sort_rows_kernel(const SortArgs a) {
     __shared__ int before_s[kSortThreads], all_s[kSortThreads], first[MOEQ_MAX_EXPERTS], scratch[kSortWarps];
-    pdl_launch();
+    chain();
     const int tid = threadIdx.x, E = a.E, blocks = gridDim.x;
     // a power of two of threads for the experts, the rest of the block splits the chunks
     const int log_e = a.bits, e = tid & ((1 << log_e) - 1), sub = tid >> log_e, subs = kSortThreads >> log_e;
     int before = 0, all = 0;
-    pdl_wait();
     if (e < E) {
         for (int g0 = sub; g0 < blocks; g0 += 8 * subs) {
             int c[8];
@@ -418,7 +416,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_rows_kernel(const SortArgs 
 
 // Step 3.
 __global__ void __launch_bounds__(256) sort_pairs_kernel(const SortArgs a) {
-    pdl_wait();
+    chain();
     const int64_t p = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (p >= a.P) return;
     const int row = __ldcg(a.pair_row + p);
@@ -437,6 +435,7 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ 
                                                           const int32_t* __restrict__ offs, int E, int64_t R,
                                                           const int32_t* __restrict__ pair_row, T* __restrict__ xs,
                                                           int64_t ld_xs) {
+    chain();
     const int c = first_col<V>(blockIdx.y), left = H - c, step = blockDim.x;
     if (left <= 0) return;
     if (blockIdx.x < nt) {
@@ -469,6 +468,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const TY* __restrict_
                                                            int64_t R, const int32_t* __restrict__ pair_row,
                                                            const float* __restrict__ w, const TO* __restrict__ base,
                                                            int64_t ld_base, TO* __restrict__ out, int64_t ld_out) {
+    chain();
     const int c = first_col<V>(blockIdx.y), left = H - c, step = blockDim.x;
     if (left <= 0) return;
     const int64_t t = blockIdx.x;
@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(256) combine_rows_grad_kernel(
     const TO* __restrict__ dout, int64_t ld_do, const TY* __restrict__ y, int64_t ld_y, int nt, int H, int k,
     const int32_t* __restrict__ offs, int E, int64_t R, const int32_t* __restrict__ pair_row,
     const float* __restrict__ w, TY* __restrict__ dy, int64_t ld_dy, float* __restrict__ dw) {
+    chain();
     const int tid = threadIdx.x, step = blockDim.x;
     if (blockIdx.x >= nt) {
         Raw<TY, V> z;
@@ -617,21 +618,14 @@ cudaError_t SmemOnce::raise(const void* kernel, int bytes) {
 
 cudaError_t launch_route_rows(const float* logits, int64_t ld, int T, int E, int k, int32_t* id, float* w,
                               cudaStream_t stream) {
-    const int grid = (T + 3) / 4;
-    if (E <= 64)
-        route_rows_kernel<2><<<grid, 128, 0, stream>>>(logits, ld, T, E, k, id, w);
-    else if (E <= 256)
-        route_rows_kernel<8><<<grid, 128, 0, stream>>>(logits, ld, T, E, k, id, w);
-    else
-        route_rows_kernel<32><<<grid, 128, 0, stream>>>(logits, ld, T, E, k, id, w);
-    return cudaGetLastError();
+    const auto kern = E <= 64 ? route_rows_kernel<2> : E <= 256 ? route_rows_kernel<8> : route_rows_kernel<32>;
+    return launch_chained(kern, (T + 3) / 4, 128, 0, stream, logits, ld, T, E, k, id, w);
 }
 
 cudaError_t launch_route_rows_grad(const float* dw, const int32_t* id, const float* w, int T, int E, int k,
                                    float* dlogits, int64_t ld, cudaStream_t stream) {
     const int vec = E % 4 == 0 && fits8(dlogits, ld, 1);
-    route_rows_grad_kernel<<<(T + 3) / 4, 128, 0, stream>>>(dw, id, w, T, E, k, dlogits, ld, vec);
-    return cudaGetLastError();
+    return launch_chained(route_rows_grad_kernel, (T + 3) / 4, 128, 0, stream, dw, id, w, T, E, k, dlogits, ld, vec);
 }
 
 cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* offs, int32_t* pair_row,
@@ -649,23 +643,11 @@ cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* 
     cudaError_t e = once[blocks == 1].raise(reinterpret_cast<const void*>(rank),
                                             (kSortWarps + 1) * MOEQ_MAX_EXPERTS * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
-    rank<<<blocks, kSortThreads, (a.warps + 1) * E * sizeof(int), stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_chained(rank, blocks, kSortThreads, (a.warps + 1) * E * sizeof(int), stream, a);
     if (e != cudaSuccess || blocks == 1) return e;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.stream = stream;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, sort_rows_kernel, a);
+    e = launch_chained(sort_rows_kernel, blocks, kSortThreads, 0, stream, a);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((a.P + 255) / 256);
-    cfg.blockDim = dim3(256);
-    return cudaLaunchKernelEx(&cfg, sort_pairs_kernel, a);
+    return launch_chained(sort_pairs_kernel, (a.P + 255) / 256, 256, 0, stream, a);
 }
 
 cudaError_t launch_gather_rows(RowsIn x, int T, int H, int k, const int32_t* offs, int E, const int32_t* pair_row,
@@ -677,13 +659,8 @@ cudaError_t launch_gather_rows(RowsIn x, int T, int H, int k, const int32_t* off
         const dim3 grid(T + kTailBlocks, (nv + threads - 1) / threads);
         const Ty* xp = static_cast<const Ty*>(x.p);
         Ty* sp = static_cast<Ty*>(xs.p);
-        if (v8)
-            gather_rows_kernel<Ty, 8><<<grid, threads, 0, stream>>>(xp, x.ld, T, H, k, offs, E,
-                                                                    static_cast<int64_t>(T) * k, pair_row, sp, xs.ld);
-        else
-            gather_rows_kernel<Ty, 4><<<grid, threads, 0, stream>>>(xp, x.ld, T, H, k, offs, E,
-                                                                    static_cast<int64_t>(T) * k, pair_row, sp, xs.ld);
-        return cudaGetLastError();
+        return launch_chained(v8 ? gather_rows_kernel<Ty, 8> : gather_rows_kernel<Ty, 4>, grid, threads, 0, stream, xp, x.ld,
+                              T, H, k, offs, E, static_cast<int64_t>(T) * k, pair_row, sp, xs.ld);
     });
 }
 
@@ -702,8 +679,7 @@ cudaError_t launch_combine_rows(RowsIn y, int T, int H, int k, const int32_t* pa
             const TO* bp = static_cast<const TO*>(base.p);
             TO* op = static_cast<TO*>(out.p);
             auto go = [&](auto kern) {
-                kern<<<grid, threads, 0, stream>>>(yp, y.ld, H, k, R, pair_row, w, bp, base.ld, op, out.ld);
-                return cudaGetLastError();
+                return launch_chained(kern, grid, threads, 0, stream, yp, y.ld, H, k, R, pair_row, w, bp, base.ld, op, out.ld);
             };
             if (v8) return w ? go(combine_rows_kernel<TY, TO, 8, true>) : go(combine_rows_kernel<TY, TO, 8, false>);
             return w ? go(combine_rows_kernel<TY, TO, 4, true>) : go(combine_rows_kernel<TY, TO, 4, false>);
@@ -723,10 +699,9 @@ cudaError_t launch_combine_rows_grad(RowsIn dout, RowsIn y, int T, int H, int k,
             using TO = std::remove_pointer_t<decltype(to)>;
             const int grid = T + kTailBlocks;
             auto go = [&](auto kern) {
-                kern<<<grid, 256, 0, stream>>>(static_cast<const TO*>(dout.p), dout.ld, static_cast<const TY*>(y.p),
-                                               y.ld, T, H, k, offs, E, R, pair_row, w, static_cast<TY*>(dy.p), dy.ld,
-                                               dw);
-                return cudaGetLastError();
+                return launch_chained(kern, grid, 256, 0, stream, static_cast<const TO*>(dout.p), dout.ld,
+                                      static_cast<const TY*>(y.p), y.ld, T, H, k, offs, E, R, pair_row, w,
+                                      static_cast<TY*>(dy.p), dy.ld, dw);
             };
             if (k <= 4)
                 return v8 ? go(combine_rows_grad_kernel<TY, TO, 8, 4>) : go(combine_rows_grad_kernel<TY, TO, 4, 4>);

@@ -21,6 +21,32 @@ struct SmemOnce {
     cudaError_t raise(const void* kernel, int bytes);
 };
 
+// A launch that may be scheduled while the kernel ahead on the stream still
+// runs (programmatic dependent launch).  Kernels launched so begin with
+// chain(), which waits for everything ahead before any access to memory and
+// only then lets the next such launch be scheduled: the order of a stream,
+// without the launch latency between its kernels.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A&&... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void chain() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
+
 // A matrix of rows: base, leading dimension in elements, element type.
 struct RowsIn {
     const void* p;

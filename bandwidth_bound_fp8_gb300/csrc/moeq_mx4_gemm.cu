@@ -9,7 +9,7 @@
 // kernel serves one token and a prompt: N is the tile's rows, rounded to 16.
 //   warps 0, 2  copies: a stage is a weight tile (16 KiB), a token tile's K
 //               block and both scale blocks, all contiguous
-//   warp 1      issues the MMAs (one thread)
+//   warp 1      issues the MMAs (one thread); warp 3 tells it the parts
 //   warps 4..7  epilogue: TMEM -> y, behind the next unit's MMAs (two
 //               accumulators)
 // Work split: with many units each CTA takes whole ones, round robin.  With
@@ -386,6 +386,8 @@ __global__ void __maxnreg__(160)
     mx4_gemm_kernel(const __grid_constant__ Mx4GemmArgs a, const __grid_constant__ typename MapsOf<kPair>::type maps) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint64_t part_full[4], part_empty[4];
+    __shared__ int part_ring[4];
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s, go_s[2][2], last_s[2][2];
     __shared__ PlanShared plan;
@@ -411,6 +413,10 @@ __global__ void __maxnreg__(160)
             mbar_init(&acc_empty[i], kPair ? 8 : 4);
         }
         mbar_init(&drained, 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&part_full[i], 1);
+            mbar_init(&part_empty[i], 1);
+        }
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -515,56 +521,81 @@ __global__ void __maxnreg__(160)
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMAs
-        // The tensor core's queue holds little: the next stage's barrier is
-        // asked for while this one's last MMAs go out.
+        // The tensor core's queue holds little, so this thread does nothing but
+        // issue: the parts come ready from warp 3, and the next stage's barrier
+        // is asked for while this one's last MMAs go out.
         if (rank == 0 && elect_one()) {
+            const uint32_t base = smem_u32(smem) >> 4, pitch = static_cast<uint32_t>(stage_bytes) >> 4;
+            const uint64_t da = umma_desc_sw128(0), db = da + (off_b >> 4);
+            const uint64_t dfa = sf_desc(0) + (off_sfa >> 4), dfb = sf_desc(0) + (off_sfb >> 4);
+            const uint32_t chunk = static_cast<uint32_t>(sfb_chunk) >> 4;
             int st = 0;
-            uint32_t phase = 0;
+            uint32_t phase = 0, at = base;
             bool ok = true, ready = false;
-            Part p;
-            for (int i = 0; ok && part_at(s, a, plan, i, p); ++i) {
-                const int buf = i & 1;
+            for (int i = 0;; ++i) {
+                ok = mbar_wait_bounded(&part_full[i & 3], (i >> 2) & 1, abort);
+                if (!ok) break;
+                const int part = *reinterpret_cast<volatile int*>(&part_ring[i & 3]);
+                mbar_arrive(&part_empty[i & 3]);
+                if (!part) break;
+                const int n_mma = part & 0xFFF, stages = part >> 12, buf = i & 1;
                 if (i >= 2) {
                     const uint32_t ph = ((i >> 1) - 1) & 1;
                     ok = kPair ? cluster_wait_bounded(&acc_empty[buf], ph, abort) : mbar_wait_bounded(&acc_empty[buf], ph, abort);
                 }
                 const uint32_t d = tmem + buf * kAcc1;
-                const uint32_t id0 = idesc_mx4(kPair ? 256 : 128, p.n_mma, 0), id2 = idesc_mx4(kPair ? 256 : 128, p.n_mma, 2);
-                for (int kb = p.kb0; ok && kb < p.kb1; ++kb) {
+                const uint32_t id0 = idesc_mx4(kPair ? 256 : 128, n_mma, 0), id2 = idesc_mx4(kPair ? 256 : 128, n_mma, 2);
+                const bool wide = n_mma > 128;
+                for (int k = 0; ok && k < stages; ++k) {
                     if (!ready)
                         ok = kPair ? cluster_wait_bounded(&full[st], phase, abort) : mbar_wait_bounded(&full[st], phase, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sp = smem_u32(stage_at(st));
-                    const uint64_t fa = sf_desc(sp + off_sfa), fb = sf_desc(sp + off_sfb);
-                    const uint64_t ad = umma_desc_sw128(sp), bd = umma_desc_sw128(sp + off_b);
+                    const uint64_t ad = da + at, bd = db + at, fa = dfa + at, fb = dfb + at;
+                    sf_copy<kPair>(tmem + kColSfa, fa);
+                    sf_copy<kPair>(tmem + kColSfb, fb);
+                    if (wide) sf_copy<kPair>(tmem + kColSfb + 4, fb + (512 >> 4));
+                    sf_copy<kPair>(tmem + kColSfa + 4, fa + (512 >> 4));
+                    sf_copy<kPair>(tmem + kColSfb + 8, fb + chunk);
+                    if (wide) sf_copy<kPair>(tmem + kColSfb + 12, fb + chunk + (512 >> 4));
+                    // 64 columns = 32 bytes of a row an MMA
+                    mma_mx4<kPair>(d, ad, bd, id0, tmem + kColSfa, tmem + kColSfb, k > 0);
+                    mma_mx4<kPair>(d, ad + 2, bd + 2, id2, tmem + kColSfa, tmem + kColSfb, 1);
                     uint64_t* const done = &empty[st];
+                    at += pitch;
                     if (++st == a.stages) {
                         st = 0;
                         phase ^= 1;
+                        at = base;
                     }
-#pragma unroll
-                    for (int kc = 0; kc < 2; ++kc) {
-                        sf_copy<kPair>(tmem + kColSfa + kc * 4, fa + kc * (512 >> 4));
-                        sf_copy<kPair>(tmem + kColSfb + kc * 8, fb + kc * (sfb_chunk >> 4));
-                        if (p.n_mma > 128)
-                            sf_copy<kPair>(tmem + kColSfb + kc * 8 + 4, fb + kc * (sfb_chunk >> 4) + (512 >> 4));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // 64 columns = 32 bytes of a row
-                        if (j == 2) ready = mbar_test_wait<kPair>(&full[st], phase);
-                        mma_mx4<kPair>(d, ad + j * 2, bd + j * 2, j & 1 ? id2 : id0, tmem + kColSfa + (j >> 1) * 4,
-                                tmem + kColSfb + (j >> 1) * 8, kb > p.kb0 || j > 0);
-                    }
+                    ready = mbar_test_wait<kPair>(&full[st], phase);
+                    mma_mx4<kPair>(d, ad + 4, bd + 4, id0, tmem + kColSfa + 4, tmem + kColSfb + 8, 1);
+                    mma_mx4<kPair>(d, ad + 6, bd + 6, id2, tmem + kColSfa + 4, tmem + kColSfb + 8, 1);
                     mma_commit<kPair>(done);
                 }
-                if (ok) mma_commit<kPair>(&acc_full[buf]);
+                if (!ok) break;
+                mma_commit<kPair>(&acc_full[buf]);
             }
             if (!ok) {
                 give_up();
                 mma_commit<kPair>(&drained);
                 drain(&drained, 0, global_timer_ns());
             }
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ------------------------------------------- parts, for the MMA thread
+        if (rank == 0 && elect_one()) {
+            Part p;
+            bool more = true, ok = true;
+            for (int i = 0; ok && more; ++i) {
+                more = part_at(s, a, plan, i, p);
+                if (i >= 4) ok = mbar_wait_bounded(&part_empty[i & 3], ((i >> 2) - 1) & 1, abort);
+                if (!ok) break;
+                *reinterpret_cast<volatile int*>(&part_ring[i & 3]) = more ? p.n_mma | (p.kb1 - p.kb0) << 12 : 0;
+                mbar_arrive(&part_full[i & 3]);
+            }
+            if (!ok) give_up();
         }
         __syncwarp();
     } else if (warp >= 4) {

@@ -375,15 +375,15 @@ __global__ void __launch_bounds__(kSortThreads) sort_rows_kernel(const SortArgs 
     const int log_e = a.bits, e = tid & ((1 << log_e) - 1), sub = tid >> log_e, subs = kSortThreads >> log_e;
     int before = 0, all = 0;
     if (e < E) {
-        for (int g0 = sub; g0 < blocks; g0 += 8 * subs) {
-            int c[8];
+        for (int g0 = sub; g0 < blocks; g0 += 16 * subs) {
+            int c[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 16; ++i) {
                 const int g = g0 + i * subs;
                 c[i] = g < blocks ? __ldcg(a.row_pair + static_cast<int64_t>(g) * E + e) : 0;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 16; ++i) {
                 all += c[i];
                 if (g0 + i * subs < static_cast<int>(blockIdx.x)) before += c[i];
             }
@@ -427,36 +427,30 @@ __global__ void __launch_bounds__(256) sort_pairs_kernel(const SortArgs a) {
 // ------------------------------------------------------------------ gather
 // xs[pair_row[t, j]] = x[t].  Token-major: each of x's elements is read once
 // and written to its rows (reading row-major would read it top_k times).
-// Blocks past the tokens' zero the rows from offs[E] on.
-constexpr int kTailBlocks = 64;
-
+// The rows from offs[E] on are zeroed, shared out over the tokens' blocks.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ x, int64_t ld_x, int nt, int H, int k,
+__global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ x, int64_t ld_x, int H, int k,
                                                           const int32_t* __restrict__ offs, int E, int64_t R,
                                                           const int32_t* __restrict__ pair_row, T* __restrict__ xs,
                                                           int64_t ld_xs) {
     chain();
     const int c = first_col<V>(blockIdx.y), left = H - c, step = blockDim.x;
     if (left <= 0) return;
-    if (blockIdx.x < nt) {
-        const int64_t t = blockIdx.x;
-        Raw<T, V> v;
-        v.load(x + t * ld_x + c, left, step);
-        const int32_t* pr = pair_row + t * k;
-        for (int j0 = 0; j0 < k; j0 += 8) {
-            int r[8];
+    const int64_t t = blockIdx.x;
+    const int kept = max(__ldg(offs + E), 0);
+    Raw<T, V> v;
+    v.load(x + t * ld_x + c, left, step);
+    const int32_t* pr = pair_row + t * k;
+    for (int j0 = 0; j0 < k; j0 += 8) {
+        int r[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = j0 + j < k ? __ldg(pr + j0 + j) : -1;
+        for (int j = 0; j < 8; ++j) r[j] = j0 + j < k ? __ldg(pr + j0 + j) : -1;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (r[j] >= 0 && r[j] < R) v.store(xs + r[j] * ld_xs + c, left, step);
-        }
-    } else {
-        Raw<T, V> z;
-        z.zero();
-        for (int64_t r = max(__ldg(offs + E), 0) + (blockIdx.x - nt); r < R; r += kTailBlocks)
-            z.store(xs + r * ld_xs + c, left, step);
+        for (int j = 0; j < 8; ++j)
+            if (r[j] >= 0 && r[j] < R) v.store(xs + r[j] * ld_xs + c, left, step);
     }
+    v.zero();
+    for (int64_t r = kept + t; r < R; r += gridDim.x) v.store(xs + r * ld_xs + c, left, step);
 }
 
 // ----------------------------------------------------------------- combine
@@ -512,22 +506,16 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const TY* __restrict_
 // ---------------------------------------------------------- combine's grad
 // dy[pair_row[t, j]] = w[t, j] dout[t] and dw[t, j] = <dout[t], y[..]>: one
 // block a token, so that dout is read once for all its slots and the dot
-// products end in one block reduction (a fixed tree).  Blocks past the
-// tokens' zero the rows of dy from offs[E] on.
+// products end in one block reduction (a fixed tree).  The rows of dy from
+// offs[E] on are zeroed, shared out over the blocks.
 template <typename TY, typename TO, int V, int KM>
 __global__ void __launch_bounds__(256) combine_rows_grad_kernel(
-    const TO* __restrict__ dout, int64_t ld_do, const TY* __restrict__ y, int64_t ld_y, int nt, int H, int k,
+    const TO* __restrict__ dout, int64_t ld_do, const TY* __restrict__ y, int64_t ld_y, int H, int k,
     const int32_t* __restrict__ offs, int E, int64_t R, const int32_t* __restrict__ pair_row,
     const float* __restrict__ w, TY* __restrict__ dy, int64_t ld_dy, float* __restrict__ dw) {
     chain();
     const int tid = threadIdx.x, step = blockDim.x;
-    if (blockIdx.x >= nt) {
-        Raw<TY, V> z;
-        z.zero();
-        for (int64_t r = max(__ldg(offs + E), 0) + (blockIdx.x - nt); r < R; r += kTailBlocks)
-            for (int c = first_col<V>(0); c < H; c += step * V) z.store(dy + r * ld_dy + c, H - c, step);
-        return;
-    }
+    const int kept = max(__ldg(offs + E), 0);
     __shared__ float red[8][KM];
     const int64_t t = blockIdx.x;
     int row[KM];
@@ -590,6 +578,10 @@ __global__ void __launch_bounds__(256) combine_rows_grad_kernel(
         for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += red[i][tid];
         dw[t * k + tid] = s;
     }
+    Raw<TY, V> z;
+    z.zero();
+    for (int64_t r = kept + t; r < R; r += gridDim.x)
+        for (int c = first_col<V>(0); c < H; c += step * V) z.store(dy + r * ld_dy + c, H - c, step);
 }
 
 // Eight elements at a time fit when rows start and step on 16 bytes.
@@ -656,11 +648,11 @@ cudaError_t launch_gather_rows(RowsIn x, int T, int H, int k, const int32_t* off
     return by_type(x.f32, [&](auto* tag) {
         using Ty = std::remove_pointer_t<decltype(tag)>;
         const int nv = v8 ? H / 8 : (H + 3) / 4, threads = nv >= 256 ? 256 : (nv + 31) / 32 * 32;
-        const dim3 grid(T + kTailBlocks, (nv + threads - 1) / threads);
+        const dim3 grid(T, (nv + threads - 1) / threads);
         const Ty* xp = static_cast<const Ty*>(x.p);
         Ty* sp = static_cast<Ty*>(xs.p);
         return launch_chained(v8 ? gather_rows_kernel<Ty, 8> : gather_rows_kernel<Ty, 4>, grid, threads, 0, stream, xp, x.ld,
-                              T, H, k, offs, E, static_cast<int64_t>(T) * k, pair_row, sp, xs.ld);
+                              H, k, offs, E, static_cast<int64_t>(T) * k, pair_row, sp, xs.ld);
     });
 }
 
@@ -697,10 +689,10 @@ cudaError_t launch_combine_rows_grad(RowsIn dout, RowsIn y, int T, int H, int k,
         return by_type(dout.f32, [&](auto* to) {
             using TY = std::remove_pointer_t<decltype(ty)>;
             using TO = std::remove_pointer_t<decltype(to)>;
-            const int grid = T + kTailBlocks;
+            const int grid = T;
             auto go = [&](auto kern) {
                 return launch_chained(kern, grid, 256, 0, stream, static_cast<const TO*>(dout.p), dout.ld,
-                                      static_cast<const TY*>(y.p), y.ld, T, H, k, offs, E, R, pair_row, w,
+                                      static_cast<const TY*>(y.p), y.ld, H, k, offs, E, R, pair_row, w,
                                       static_cast<TY*>(dy.p), dy.ld, dw);
             };
             if (k <= 4)

@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(kPlanThreads) act_tiles_kernel(RowsIn x, Mx4Pl
                                                                  uint8_t* __restrict__ tiles,
                                                                  uint8_t* __restrict__ stiles) {
     chain();
-    __shared__ PlanShared plan;
+    __shared__ int plan_mem[plan_ints(MOEQ_MAX_EXPERTS)];
+    const PlanShared plan = plan_at(plan_mem, p.E);
     using Seg = Segment<kF32, kVec, kSwiglu>;
     constexpr int kBlocks = Seg::kBlocks;
     const int lane = threadIdx.x & 31, kb_all = mx4_kb(K), segs = segments(K, kBlocks), sb = mx4_tile_scale_bytes(p.nt);
@@ -403,7 +404,8 @@ __global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t*
                                                                   uint8_t* __restrict__ tiles,
                                                                   uint8_t* __restrict__ stiles) {
     chain();
-    __shared__ PlanShared plan;
+    __shared__ int plan_mem[plan_ints(MOEQ_MAX_EXPERTS)];
+    const PlanShared plan = plan_at(plan_mem, p.E);
     plan_scan(p, plan);
     constexpr int kWide = 8;
     const int lane = threadIdx.x & 31, kb_all = mx4_kb(K), sb = mx4_tile_scale_bytes(p.nt), pitch = mx4_scale_pitch(K);

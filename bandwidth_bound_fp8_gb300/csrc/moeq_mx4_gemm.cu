@@ -319,11 +319,15 @@ __device__ __forceinline__ void sum_parts(const float* __restrict__ part, size_t
 // element by element.
 template <bool kF32>
 struct Epi {
-    static constexpr int kCols = kF32 ? 32 : 64;
     static constexpr int kPitch = kF32 ? 528 : 320;  // bytes a row: neighbours in other banks
 };
-constexpr int kEpiBytes = 64 * 320;
-static_assert(Epi<true>::kCols * Epi<true>::kPitch <= kEpiBytes, "one buffer serves both types");
+// Columns a step.  A pair takes half as many: its two groups' buffers then
+// leave room for a sixth stage of the widest tiles.
+__host__ __device__ constexpr int epi_cols(bool f32, bool pair) { return (f32 ? 32 : 64) / (pair ? 2 : 1); }
+__host__ __device__ constexpr int epi_bytes(bool pair) { return epi_cols(false, pair) * Epi<false>::kPitch; }
+static_assert(epi_cols(true, false) * Epi<true>::kPitch <= epi_bytes(false) &&
+                  epi_cols(true, true) * Epi<true>::kPitch <= epi_bytes(true) && epi_bytes(true) % 16 == 0,
+              "one buffer serves both types");
 
 template <bool kF32, int kCols>
 __device__ __forceinline__ void store_step(const Mx4GemmArgs& a, const Part& p, int c0, int q, int lane, int n,
@@ -390,13 +394,15 @@ __global__ void __maxnreg__(160)
     __shared__ int part_ring[4];
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s, go_s[2][2], last_s[2][2];
-    __shared__ PlanShared plan;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nt = a.plan.nt;
     const int sfb_bytes = mx4_tile_scale_bytes(nt), sfb_chunk = sfb_bytes / 2;
     const int off_b = kMx4TileBytes, off_sfa = off_b + nt / (kPair ? 2 : 1) * 128, off_sfb = off_sfa + kMx4TileScaleBytes;
     const int stage_bytes = stage_bytes_of(nt, kPair);
     const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
+    // behind the stages: the epilogue's buffers, then the plan
+    uint8_t* const epi_mem = smem + a.stages * stage_bytes;
+    const PlanShared plan = plan_at(reinterpret_cast<int*>(epi_mem + epi_groups(kPair) * epi_bytes(kPair)), a.plan.E);
     volatile int* abort = &abort_s;
     // (the next kernel may be scheduled: it waits for this one before it
     // touches memory)
@@ -604,7 +610,7 @@ __global__ void __maxnreg__(160)
         constexpr int kGroups = epi_groups(kPair);
         const int q = warp & 3, group = (warp >> 2) - 1, bar = 1 + group;
         const bool chief = tid == 128 + group * 128;
-        uint8_t* stage_y = smem + a.stages * stage_bytes + group * kEpiBytes;
+        uint8_t* stage_y = epi_mem + group * epi_bytes(kPair);
         // rows of y in 16-byte pieces
         const bool vec_y = a.N % (kF32 ? 4 : 8) == 0 && a.ld_y % (kF32 ? 4 : 8) == 0 &&
                            (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
@@ -670,7 +676,7 @@ __global__ void __maxnreg__(160)
                 }
             };
             if (!cut) {
-                constexpr int kCols = Epi<kF32>::kCols;
+                constexpr int kCols = epi_cols(kF32, kPair);
                 for (int c0 = 0; c0 < p.n; c0 += kCols) {
                     float v[kCols];  // columns past the tile's are read and not stored
 #pragma unroll
@@ -781,10 +787,13 @@ cudaError_t launch_one(const Mx4GemmArgs& a, const typename MapsOf<kPair>::type&
 cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stream) {
     const bool pair = a.plan.align == 32;
     const int sb = stage_bytes_of(a.plan.nt, pair);
-    // of 227 KiB: less the static arrays, the alignment and the epilogue's buffers
-    const int epi = kEpiBytes * epi_groups(pair), budget = 216 * 1024 - epi;
-    a.stages = budget / sb < kMaxStages ? budget / sb : kMaxStages;
-    const int smem = a.stages * sb + epi + 1024, most = budget + epi + 1024;
+    // of 227 KiB: less the static arrays; the stages share the rest with the
+    // alignment, the epilogue's buffers and the plan
+    constexpr int kMost = 227 * 1024 - 1024;
+    const int rest = 1024 + epi_bytes(pair) * epi_groups(pair) + plan_ints(a.plan.E) * static_cast<int>(sizeof(int));
+    const int fit = (kMost - rest) / sb;
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+    const int smem = a.stages * sb + rest, most = kMost;
     if (!pair)
         return a.y_f32 ? launch_one<true, false>(a, NoMaps{}, grid, smem, most, pdl, stream)
                        : launch_one<false, false>(a, NoMaps{}, grid, smem, most, pdl, stream);

@@ -9,16 +9,21 @@ namespace moeq {
 
 constexpr int kPlanThreads = 256;  // four experts a thread: MOEQ_MAX_EXPERTS
 
+// In shared memory: plan_ints(E) ints.
 struct PlanShared {
-    int first[MOEQ_MAX_EXPERTS + 1];  // first row of each expert, clamped to [0, R] and made to rise
-    int tile[MOEQ_MAX_EXPERTS + 1];   // token tiles before each expert
-    int warp[2][kPlanThreads / 32];
+    int* first;  // [E + 1] first row of each expert, clamped to [0, R] and made to rise
+    int* tile;   // [E + 1] token tiles before each expert
+    int* warp;   // [2][kPlanThreads / 32]
 };
+__host__ __device__ constexpr int plan_ints(int E) { return 2 * (E + 1) + 2 * (kPlanThreads / 32); }
+__device__ __forceinline__ PlanShared plan_at(int* mem, int E) {
+    return {mem, mem + E + 1, mem + 2 * (E + 1)};
+}
 
 // Rows are given to experts by `offs`; values out of range or order are
 // clamped, so that no row, tile or buffer index leaves its range.  Called by
 // all threads of a block of at least kPlanThreads.
-__device__ __forceinline__ void plan_scan(const Mx4Plan& p, PlanShared& s) {
+__device__ __forceinline__ void plan_scan(const Mx4Plan& p, const PlanShared& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool mine_too = tid < kPlanThreads;
     int top[4], run = 0;
@@ -31,11 +36,11 @@ __device__ __forceinline__ void plan_scan(const Mx4Plan& p, PlanShared& s) {
     int inc = run;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) inc = max(inc, __shfl_up_sync(0xffffffffu, inc, o));
-    if (lane == 31 && mine_too) s.warp[0][warp] = inc;
+    if (lane == 31 && mine_too) s.warp[warp] = inc;
     int before = __shfl_up_sync(0xffffffffu, inc, 1);
     if (lane == 0) before = 0;
     __syncthreads();
-    for (int w = 0; w < warp && mine_too; ++w) before = max(before, s.warp[0][w]);
+    for (int w = 0; w < warp && mine_too; ++w) before = max(before, s.warp[w]);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (mine_too && tid * 4 + i <= p.E) s.first[tid * 4 + i] = max(before, top[i]);
@@ -55,10 +60,10 @@ __device__ __forceinline__ void plan_scan(const Mx4Plan& p, PlanShared& s) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
     }
-    if (lane == 31 && mine_too) s.warp[1][warp] = inc;
+    if (lane == 31 && mine_too) s.warp[kPlanThreads / 32 + warp] = inc;
     __syncthreads();
     before = inc - sum;
-    for (int w = 0; w < warp && mine_too; ++w) before += s.warp[1][w];
+    for (int w = 0; w < warp && mine_too; ++w) before += s.warp[kPlanThreads / 32 + w];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (mine_too && tid * 4 + i < p.E) s.tile[tid * 4 + i] = before + mine[i];

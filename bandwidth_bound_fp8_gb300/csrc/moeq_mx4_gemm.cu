@@ -12,11 +12,10 @@
 //   warp 1      issues the MMAs (one thread); warp 3 tells it the parts
 //   warps 4..7  epilogue: TMEM -> y, behind the next unit's MMAs (two
 //               accumulators)
-// Work split: with many units each CTA takes whole ones, round robin.  With
-// few, the stages of all units are dealt evenly over the CTAs; a unit cut
-// between CTAs leaves fp32 partials in the workspace and the CTA that
-// arrives last sums them in the order of K, so the result does not depend on
-// which one that is.  No CTA ever waits for another.
+// Work split: each CTA (or pair) takes whole units, round robin.  A few units
+// of long K are cut in four along K: the parts leave fp32 sums in the
+// workspace and the CTA that arrives last adds them in the order of K, so the
+// result does not depend on which one that is.  No CTA ever waits for another.
 #include <cuda.h>
 
 #include "moeq_device.cuh"
@@ -35,9 +34,18 @@ static_assert(threads_of(false) >= kPlanThreads, "the plan's scan needs its thre
 constexpr int kMaxStages = 12;
 // Tiles of this many rows or more are multiplied by pairs of CTAs; their most
 // rows (a multiple of 32).
-constexpr int kPairRows = 64, kPairTileRows = 224;
-// Whole units from this many a CTA on (below, the stages are dealt evenly).
-constexpr int kWholeWaves = 4;
+constexpr int kPairRows = 200, kPairTileRows = 224;
+// Units are cut in kCut parts where that many of them have a worker each and K
+// is long enough for the join to pay: a part saves about 0.2 us for every K
+// block, the join costs 2 us and 1.6 us for every 16 rows of the tile.
+// 1 x 32768 -> 128: 36 us whole; 160 x 6144 -> 1024: 15 us whole, 62 with the
+// stages dealt to all SMs; one token over eight experts (256 units): 23.4 us
+// whole, 28 with the stages dealt evenly, although half the SMs take one
+// unit and half two (the others' bandwidth goes to them).
+constexpr int kCut = 4;
+__host__ __device__ constexpr bool cut_pays(int units, int kb, int nt, int workers) {
+    return units * kCut <= workers && kb >= 8 + nt / 2;
+}
 // TMEM columns: accumulators at 0 and 256, the tokens' scales in between and
 // the weights' behind.
 constexpr int kTmemCols = 512, kAcc1 = 256, kColSfb = 240, kColSfa = 496;
@@ -49,33 +57,21 @@ __host__ __device__ constexpr int stage_bytes_of(int nt, bool pair) {
 struct Sched {
     int units, kb, grid, cta;  // cta, grid: of pairs where two CTAs share a unit
     int nbu, rank;             // weight units of a tile (blocks of 128 rows, or pairs of them); this CTA of its pair
-    bool whole;
-    long long s0, s1;   // this CTA's stages (dealt mode)
+    bool cut;
 };
 struct Part {
     int u, n0, r0, n, n_mma, kb0, kb1, tile, tiles, e, nb;
 };
 
-__device__ __forceinline__ long long deal(long long stages, int c, int grid) { return stages * c / grid; }
-
 // The i-th part of this CTA; false past its last.  A unit's number counts
 // experts, then weight blocks, then token tiles: neighbours read the same
 // weights.
 __device__ __forceinline__ bool part_at(const Sched& s, const Mx4GemmArgs& a, const PlanShared& plan, int i, Part& p) {
-    if (s.whole) {
-        p.u = s.cta + i * s.grid;
-        if (p.u >= s.units) return false;
-        p.kb0 = 0;
-        p.kb1 = s.kb;
-    } else {
-        const long long u = s.s0 / s.kb + i;
-        const long long lo = u * s.kb > s.s0 ? u * s.kb : s.s0;
-        const long long hi = (u + 1) * s.kb < s.s1 ? (u + 1) * s.kb : s.s1;
-        if (lo >= hi) return false;
-        p.u = static_cast<int>(u);
-        p.kb0 = static_cast<int>(lo - u * s.kb);
-        p.kb1 = static_cast<int>(hi - u * s.kb);
-    }
+    p.u = s.cut ? s.cta / kCut : s.cta + i * s.grid;
+    if (p.u >= s.units || (s.cut && i > 0)) return false;
+    const int c = s.cta % kCut;
+    p.kb0 = s.cut ? s.kb * c / kCut : 0;
+    p.kb1 = s.cut ? s.kb * (c + 1) / kCut : s.kb;
     const int nt = a.plan.nt, align = a.plan.align;
     const int e = plan_find(plan.tile, a.plan.E, p.u / s.nbu);  // experts without tiles are never the last such
     const int r0 = plan.first[e], cnt = plan.first[e + 1] - r0;
@@ -276,36 +272,33 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
         static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
 }
 
-// The sum of a unit's parts for 16 columns, all in the order of K: this CTA's
-// own (v) comes from TMEM, the others' from the workspace, two parts' loads
-// in flight at a time.  lo_second: the first CTA's part is in its second slot.
-__device__ __forceinline__ void sum_parts(const float* __restrict__ part, size_t worker_floats, size_t slot_floats,
-                                          int c_lo, int c_hi, int own, int lo_second, int c0, int row, float (&v)[16]) {
+// The sum of a unit's parts for 16 columns, in the order of K: this CTA's own
+// (v) comes from TMEM, the others' from the workspace, two parts' loads in
+// flight at a time.  part: the unit's first part, this thread's row.
+__device__ __forceinline__ void sum_parts(const float* __restrict__ part, size_t part_floats, int own, int c0,
+                                          float (&v)[16]) {
     float sum[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) sum[c] = 0.f;
-    const size_t at = static_cast<size_t>(c0) * 128 + row * 4;
-    for (int k0 = c_lo; k0 <= c_hi; k0 += 2) {
+#pragma unroll
+    for (int k0 = 0; k0 < kCut; k0 += 2) {
         float4 f[2][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int k = k0 + j;
-            if (k > c_hi || k == own) continue;
-            // only the first of a unit's CTAs can have begun in another unit
-            const float* slot = part + k * worker_floats + (k == c_lo ? lo_second : 0) * slot_floats + at;
+        for (int j = 0; j < 2; ++j)
+            if (k0 + j != own) {
+                const float* at = part + (k0 + j) * part_floats + static_cast<size_t>(c0) * 128;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) f[j][c] = __ldcg(reinterpret_cast<const float4*>(slot + c * 512));
-        }
+                for (int c = 0; c < 4; ++c) f[j][c] = __ldcg(reinterpret_cast<const float4*>(at + c * 512));
+            }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int k = k0 + j;
-            if (k > c_hi) continue;
+            const bool mine = k0 + j == own;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                sum[4 * c] += k == own ? v[4 * c] : f[j][c].x;
-                sum[4 * c + 1] += k == own ? v[4 * c + 1] : f[j][c].y;
-                sum[4 * c + 2] += k == own ? v[4 * c + 2] : f[j][c].z;
-                sum[4 * c + 3] += k == own ? v[4 * c + 3] : f[j][c].w;
+                sum[4 * c] += mine ? v[4 * c] : f[j][c].x;
+                sum[4 * c + 1] += mine ? v[4 * c + 1] : f[j][c].y;
+                sum[4 * c + 2] += mine ? v[4 * c + 2] : f[j][c].z;
+                sum[4 * c + 3] += mine ? v[4 * c + 3] : f[j][c].w;
             }
         }
     }
@@ -442,16 +435,9 @@ __global__ void __maxnreg__(160)
     s.cta = blockIdx.x / (kPair ? 2 : 1);
     s.nbu = nbu;
     s.rank = rank;
-    const long long all_stages = static_cast<long long>(total) * s.kb;
-    s.grid = static_cast<int>(min(static_cast<long long>(workers), all_stages));
-    s.whole = total >= kWholeWaves * workers;
-    s.s0 = s.s1 = 0;
-    if (!s.whole && s.cta < s.grid) {
-        s.s0 = deal(all_stages, s.cta, s.grid);
-        s.s1 = deal(all_stages, s.cta + 1, s.grid);
-    }
+    s.grid = workers;
+    s.cut = cut_pays(total, s.kb, nt, workers);
     auto stage_at = [&](int st) { return smem + st * stage_bytes; };
-    auto slot_of = [&](int worker) { return static_cast<size_t>(kPair ? 2 * worker + rank : worker); };
     auto give_up = [&] {
         *abort = 1;
         if (a.status) atomicExch(a.status, static_cast<int>(MOEQ_ERR_TIMEOUT));
@@ -628,23 +614,18 @@ __global__ void __maxnreg__(160)
             tc_fence_after();
             const uint32_t acc = tmem + buf * kAcc1 + (static_cast<uint32_t>(q * 32) << 16);
             const int n = p.n0 + q * 32 + lane;
-            const size_t slot_floats = static_cast<size_t>(nt) * 128;
-            int* const ticket = a.tickets + (kPair ? 2 * p.u + rank : p.u);
-            const bool cut = p.kb0 > 0 || p.kb1 < s.kb;
-            // the CTAs that hold the unit's stages: c_lo .. c_hi
-            int c_lo = s.cta, c_hi = s.cta;
-            bool join = false;  // every other part is in the workspace: this CTA sums them
-            if (cut) {
-                const long long f = static_cast<long long>(p.u) * s.kb, l = f + s.kb - 1;
-                while (deal(all_stages, c_lo, s.grid) > f) --c_lo;
-                while (deal(all_stages, c_hi + 1, s.grid) <= l) ++c_hi;
-                if (chief) last_s[group][turn] = ld_acquire(ticket) == c_hi - c_lo;
+            bool join = false;  // every other part is in the workspace: this CTA adds them up
+            // parts lie [unit][CTA of the pair][part], a row's columns in fours
+            const size_t part_floats = static_cast<size_t>(nt) * 128;
+            const int first = (kPair ? 2 * p.u + rank : p.u) * kCut, own = s.cta % kCut;
+            float* const parts = a.part + first * part_floats + (q * 32 + lane) * 4;
+            if (s.cut) {
+                int* const ticket = a.tickets + first / kCut;
+                if (chief) last_s[group][turn] = ld_acquire(ticket) == kCut - 1;
                 named_sync(bar, 128);
                 join = last_s[group][turn];
                 if (!join) {
-                    float4* slot = reinterpret_cast<float4*>(
-                                       a.part + (2 * slot_of(s.cta) + (p.u != s.s0 / s.kb)) * slot_floats) +
-                                   q * 32 + lane;
+                    float4* slot = reinterpret_cast<float4*>(parts + own * part_floats);
                     for (int c0 = 0; c0 < p.n; c0 += 16) {
                         float v[16];
                         tmem_ld16(acc + c0, v);
@@ -656,7 +637,7 @@ __global__ void __maxnreg__(160)
                     }
                     __threadfence();
                     named_sync(bar, 128);
-                    if (chief) last_s[group][turn] = atom_add_acq_rel(ticket, 1) == c_hi - c_lo;
+                    if (chief) last_s[group][turn] = atom_add_acq_rel(ticket, 1) == kCut - 1;
                     named_sync(bar, 128);
                     join = last_s[group][turn];
                 }
@@ -675,7 +656,7 @@ __global__ void __maxnreg__(160)
                         mbar_arrive(&acc_empty[buf]);
                 }
             };
-            if (!cut) {
+            if (!s.cut) {
                 constexpr int kCols = epi_cols(kF32, kPair);
                 for (int c0 = 0; c0 < p.n; c0 += kCols) {
                     float v[kCols];  // columns past the tile's are read and not stored
@@ -688,13 +669,12 @@ __global__ void __maxnreg__(160)
                     store_step<kF32, kCols>(a, p, c0, q, lane, n, v, stage_y, vec_y, bar);
                 }
             } else {
-                const int lo_second = deal(all_stages, c_lo, s.grid) / s.kb != p.u;
                 for (int c0 = 0; join && c0 < p.n; c0 += 16) {
                     float v[16];
                     tmem_ld16(acc + c0, v);
                     tmem_wait_ld();
                     tmem_use16(v);
-                    sum_parts(a.part + 2 * rank * slot_floats, (kPair ? 2 : 1) * 2 * slot_floats, slot_floats, c_lo, c_hi, s.cta, lo_second, c0, q * 32 + lane, v);
+                    sum_parts(parts, part_floats, own, c0, v);
                     store_step<kF32, 16>(a, p, c0, q, lane, n, v, stage_y, vec_y, bar);
                 }
                 release();

@@ -105,7 +105,7 @@ cudaError_t launch_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, 
 // a weight tile), its scales mx4_tile_scale_bytes(nt) at (g * KB + kb) times
 // that (a weight tile's order, one more 512 bytes for rows 128..).
 constexpr int kMx4MaxTileRows = 240;
-constexpr int kMx4Tickets = 4096;
+constexpr int kMx4Tickets = 1024;  // units that are cut (a quarter of the SMs at most)
 __host__ __device__ constexpr int mx4_tile_scale_bytes(int nt) { return nt > 128 ? 2048 : 1024; }
 // Most rows of one token tile for R rows over E experts, and what tiles' rows
 // are rounded to: 16, or 32 where pairs of CTAs multiply them.
@@ -147,7 +147,7 @@ struct Mx4GemmArgs {
     int K, N;
     int stages;
     int* tickets;           // kMx4Tickets, zero between launches
-    float* part;            // 2 * grid slots of nt * 128 floats
+    float* part;            // grid slots of nt * 128 floats
     int* status;
 };
 // pdl: start while the kernel ahead on the stream (which writes the token

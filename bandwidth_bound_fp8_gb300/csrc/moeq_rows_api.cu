@@ -80,7 +80,7 @@ Mx4Ws mx4_ws(int64_t rows, int K, int E, int R, int sms) {
     l.tiles = l.scales + up256(static_cast<size_t>(rows) * mx4_scale_pitch(K));
     l.stiles = l.tiles + up256(blocks * nt * 128);
     l.part = l.stiles + up256(blocks * mx4_tile_scale_bytes(nt));
-    l.end = l.part + static_cast<size_t>(2 * sms) * nt * 128 * sizeof(float);
+    l.end = l.part + static_cast<size_t>(sms) * nt * 128 * sizeof(float);
     return l;
 }
 

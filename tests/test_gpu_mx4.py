@@ -207,6 +207,10 @@ PRODUCTS = [  # counts per expert, N, K, x type, y type
     ([0, 0, 0], 128, 256, BF, F32),
     ([700, 3, 0, 900, 1100, 260, 17, 1500], 1280, 256, BF, F32),     # many units: whole ones
     ([1500, 700], 2048, 544, BF, BF),
+    ([3], 128, 32768, BF, F32),                                      # few units of long K: cut in four
+    ([2, 0, 40], 200, 16384, BF, BF),
+    ([240], 300, 32768, F32, BF),                                    # cut, by pairs of CTAs
+    ([300, 200], 640, 1024, BF, BF),                                 # an odd weight block of a pair
 ]
 
 

@@ -31,7 +31,11 @@ namespace {
 __host__ __device__ constexpr int epi_groups(bool pair) { return pair ? 2 : 1; }
 __host__ __device__ constexpr int threads_of(bool pair) { return 128 + 128 * epi_groups(pair); }
 static_assert(threads_of(false) >= kPlanThreads, "the plan's scan needs its threads");
-constexpr int kMaxStages = 12;
+// Stages in flight at most.  Seven of a narrow tile's (17 KiB of weights each)
+// keep HBM busy; with more, its throughput falls again: 61 tokens over 256
+// experts take 294 us with 6, 300 with 7, 313 with 9; one token 22.9, 22.4 and
+// 22.1; an LM head of 6144 x 151552 72.5, 72.5 and 75.1.
+constexpr int kMaxStages = 7;
 // Tiles of this many rows or more are multiplied by pairs of CTAs; their most
 // rows (a multiple of 32).
 constexpr int kPairRows = 200, kPairTileRows = 224;

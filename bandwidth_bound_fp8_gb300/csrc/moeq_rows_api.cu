@@ -243,6 +243,11 @@ moeq_status moeq_mx4_expert_gemm(const void* x, moeq_dtype x_dtype, int64_t ld_x
         (codes_in && act != MOEQ_ACT_NONE) || codes_in != (x_scales != nullptr))
         return MOEQ_ERR_INVALID_ARG;
     if (!mx4_shape_ok(K, N)) return MOEQ_ERR_UNSUPPORTED_SHAPE;
+    // the copies count rows of 128 bytes in 31 bits: 256 GiB of tiles
+    const int nt = mx4_tiling(R > 0 ? R : 1, E).nt;
+    if (static_cast<int64_t>(E) * mx4_nb(N) * mx4_kb(K) >= (int64_t(1) << 24) ||
+        mx4_max_tiles(R > 0 ? R : 1, E, nt) * nt * mx4_kb(K) >= (int64_t(1) << 31))
+        return MOEQ_ERR_UNSUPPORTED_SHAPE;
     // without an index row r reads activation row r; with rows to fill there has to be one to read
     if ((!row_pair_opt && rows < R) || (R > 0 && rows == 0)) return MOEQ_ERR_INVALID_ARG;
     if (R == 0) return MOEQ_OK;

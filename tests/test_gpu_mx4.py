@@ -211,6 +211,8 @@ PRODUCTS = [  # counts per expert, N, K, x type, y type
     ([2, 0, 40], 200, 16384, BF, BF),
     ([240], 300, 32768, F32, BF),                                    # cut, by pairs of CTAs
     ([300, 200], 640, 1024, BF, BF),                                 # an odd weight block of a pair
+    ([1, 0, 3, 2] * 256, 128, 96, BF, F32),                          # as many experts as there may be
+    ([0] * 1022 + [260, 1], 130, 64, BF, BF),
 ]
 
 
@@ -329,3 +331,25 @@ def test_expert_gemm_on_another_stream_and_in_a_graph(moeq):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+def test_offsets_past_32_bits(moeq):
+    """Rows 2^27 elements apart: the last start past 2^32 elements."""
+    rows, K, N, ld = 40, 512, 256, 1 << 27
+    x0 = _rand((rows, K), 3, 2).to(BF).cuda()
+    x = torch.empty(rows * ld, dtype=BF, device="cuda").as_strided((rows, K), (ld, 1))
+    x.copy_(x0)
+    for a, b in zip(_quant(moeq, x0), _quant(moeq, x)):
+        assert torch.equal(a, b)
+    W = Weights(moeq, 2, N, K, 8)
+    y0 = torch.empty((rows, N), dtype=BF, device="cuda")
+    y = torch.empty(rows * ld, dtype=BF, device="cuda").as_strided((rows, N), (ld, 1))
+    ws = moeq.Workspace(moeq.moeq_mx4_expert_gemm_workspace_size(rows, K, N, 2, rows))
+    moeq.moeq_mx4_expert_gemm(x0, W.t, W.s, _offs([33, 7]), y0, ws)
+    moeq.moeq_mx4_expert_gemm(x, W.t, W.s, _offs([33, 7]), y, ws)
+    assert torch.equal(y0, y)
+    q, s = _quant(moeq, x0)
+    v0 = torch.empty((rows, K), dtype=BF, device="cuda")
+    moeq.moeq_mx4_dequant_act(q, s, v0)
+    moeq.moeq_mx4_dequant_act(q, s, x)
+    assert torch.equal(v0, x)

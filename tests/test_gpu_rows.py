@@ -332,3 +332,33 @@ def test_bad_indices_stay_in_bounds(moeq):
     torch.cuda.synchronize()
     assert torch.equal(xs[0], x[0]) and torch.equal(xs[3], x[1]) and torch.equal(xs[1], x[2]) and (xs[4:] == 0).all()
     assert torch.equal(out[:3], x[:3]) and (out[3] == 0).all()
+
+
+def test_offsets_past_32_bits(moeq):
+    """Rows 2^27 elements apart: the last start past 2^32 elements.  Results are those of packed rows, bit for bit."""
+    T, k, H, E, ld = 20, 2, 136, 5, 1 << 27
+    ids = _ids(T, k, E, 0.1, 4)
+    offs, pr, _ = _sort(moeq, ids, E)
+    w = torch.rand((T, k), generator=_gen(1)).cuda()
+    x0, y0, do0 = (_matrix(n, H, BF, False, s) for n, s in ((T, 2), (T * k, 3), (T, 4)))
+    far = [torch.empty(T * k * ld, dtype=BF, device="cuda") for _ in range(2)]
+    rows = lambda i, n: far[i].as_strided((n, H), (ld, 1))
+
+    def run(x, y, do, new):
+        res = []
+        xs = new(T * k)
+        moeq.moeq_gather_rows(x, offs, pr, xs)
+        res.append(xs.clone())
+        dx = torch.empty((T, H), dtype=BF, device="cuda")
+        moeq.moeq_gather_rows_grad(xs, pr, dx)
+        out = torch.empty((T, H), dtype=BF, device="cuda")
+        moeq.moeq_combine_rows(y, pr, w, out, base=do)
+        dy, dw = new(T * k), torch.empty((T, k), device="cuda")
+        moeq.moeq_combine_rows_grad(do, y, offs, pr, w, dy, dw)
+        return res + [dx, out, dy.clone(), dw]
+
+    near = run(x0, y0, do0, lambda n: torch.empty((n, H), dtype=BF, device="cuda"))
+    y = rows(1, T * k)
+    y.copy_(y0)
+    for a, b in zip(near, run(x0, y, do0, lambda n: rows(0, n))):
+        assert torch.equal(a, b)

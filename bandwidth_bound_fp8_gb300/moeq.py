@@ -546,24 +546,28 @@ def moeq_mx4_quant_act(x, codes, scales, act=MOEQ_ACT_NONE, stream=None) -> None
     """x [rows, K] ([rows, 2K] with MOEQ_ACT_SWIGLU) -> codes [rows, K/2],
     scales [rows, moeq_mx4_scale_pitch(K)], uint8."""
     rows, K = x.shape[0], x.shape[1] // (2 if act == MOEQ_ACT_SWIGLU else 1)
-    L = load()
-    _check("moeq_mx4_quant_act", L.moeq_mx4_quant_act(
+    _check("moeq_mx4_quant_act", load().moeq_mx4_quant_act(
         x.data_ptr(), _dtype(x), _ld(x, "x"), rows, K, act, _packed(codes, torch.uint8, (rows, K // 2), "codes"),
-        _packed(scales, torch.uint8, (rows, L.moeq_mx4_scale_pitch(K)), "scales"), _stream(stream)))
+        _packed(scales, torch.uint8, (rows, _pitch(K)), "scales"), _stream(stream)))
 
 
 def moeq_mx4_dequant_act(codes, scales, out, stream=None) -> None:
     rows, K = out.shape
-    L = load()
-    _check("moeq_mx4_dequant_act", L.moeq_mx4_dequant_act(
+    _check("moeq_mx4_dequant_act", load().moeq_mx4_dequant_act(
         _packed(codes, torch.uint8, (rows, K // 2), "codes"),
-        _packed(scales, torch.uint8, (rows, L.moeq_mx4_scale_pitch(K)), "scales"), rows, K, out.data_ptr(),
+        _packed(scales, torch.uint8, (rows, _pitch(K)), "scales"), rows, K, out.data_ptr(),
         _dtype(out), _ld(out, "out"), _stream(stream)))
 
 
+# The sizes of include/moeq.h, for checks on every call (the library's own
+# functions are a call each).
+def _pitch(K):
+    return (K + 255) // 256 * 8
+
+
 def _tiles(tiles, scale_tiles, E, N, K):
-    return (_packed(tiles, torch.uint8, (moeq_mx4_weight_bytes(E, N, K),), "tiles"),
-            _packed(scale_tiles, torch.uint8, (moeq_mx4_weight_scale_bytes(E, N, K),), "scale_tiles"))
+    n = E * ((N + 127) // 128) * ((K + 255) // 256) * 16384
+    return (_packed(tiles, torch.uint8, (n,), "tiles"), _packed(scale_tiles, torch.uint8, (n // 16,), "scale_tiles"))
 
 
 def moeq_mx4_quant_weight(w, tiles, scale_tiles, stream=None) -> None:
@@ -595,18 +599,17 @@ def moeq_mx4_expert_gemm(x, w, w_scales, offs, y, ws: Workspace, row_pair=None, 
     E, of = _offs(offs)
     R, N = y.shape
     rows, K = x.shape
-    L = load()
     if x_scales is not None:
         K *= 2
         dt, ld = MOEQ_MX4, 0
         _packed(x, torch.uint8, (rows, K // 2), "x")
-        _packed(x_scales, torch.uint8, (rows, L.moeq_mx4_scale_pitch(K)), "x_scales")
+        _packed(x_scales, torch.uint8, (rows, _pitch(K)), "x_scales")
     else:
         if act == MOEQ_ACT_SWIGLU:
             K //= 2
         dt, ld = _dtype(x), _ld(x, "x")
     tp, sp = _tiles(w, w_scales, E, N, K)
-    _check("moeq_mx4_expert_gemm", L.moeq_mx4_expert_gemm(
+    _check("moeq_mx4_expert_gemm", load().moeq_mx4_expert_gemm(
         x.data_ptr(), dt, ld, _p(x_scales), rows, K, act, tp, sp, N, of, E, R,
         _packed(row_pair, torch.int32, (R,), "row_pair") if row_pair is not None else None, top_k, y.data_ptr(),
         _dtype(y), _ld(y, "y"), ws.ptr, ws.nbytes, _stream(stream)))

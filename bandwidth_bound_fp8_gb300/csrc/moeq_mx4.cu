@@ -115,11 +115,15 @@ __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g,
 // A warp's segment of a row: kBlocks K blocks of 256 columns, eight of each a
 // lane (its loads all issued before the first is used): 2 KiB a warp.
 constexpr int kSegment = 4;
+__host__ __device__ constexpr int segment_blocks(bool f32, bool swiglu) {
+    const int n = kSegment / (f32 ? 2 : 1) / (swiglu ? 2 : 1);
+    return n > 0 ? n : 1;
+}
 __host__ __device__ constexpr int segments(int K, int blocks) { return (mx4_kb(K) + blocks - 1) / blocks; }
 
 template <bool kF32, bool kVec, bool kSwiglu>
 struct Segment {
-    static constexpr int kBlocks = kSegment / (kF32 ? 2 : 1) / (kSwiglu ? 2 : 1);
+    static constexpr int kBlocks = segment_blocks(kF32, kSwiglu);
     Raw8<kF32> v[kBlocks], u[kSwiglu ? kBlocks : 1];
     __device__ __forceinline__ void load(const void* x, int64_t row0, int seg, int lane, int K) {
 #pragma unroll
@@ -471,8 +475,7 @@ bool fits(const void* p, int64_t ld, int f32) {
 
 cudaError_t launch_mx4_quant_act(RowsIn x, int rows, int K, int act, uint8_t* codes, uint8_t* scales,
                                  int sms, cudaStream_t stream) {
-    const int blocks = kSegment / (x.f32 ? 2 : 1) / (act ? 2 : 1);
-    const int64_t want = (static_cast<int64_t>(rows) * segments(K, blocks) + 7) / 8;
+    const int64_t want = (static_cast<int64_t>(rows) * segments(K, segment_blocks(x.f32, act)) + 7) / 8;
     const unsigned grid = static_cast<unsigned>(want < sms * 4 ? want : sms * 4);
     // the second half of a SwiGLU row starts K elements on: K is a multiple of 32
     const bool vec = fits(x.p, x.ld, x.f32);
@@ -531,7 +534,7 @@ cudaError_t launch_mx4_act_tiles(const Mx4Source& src, const Mx4Plan& plan, int 
                                                  src.codes, src.scales, plan, K, tiles, stiles);
     }
     // a warp a row where that fills the wave, else up to eight (a power of two: it divides a block's warps)
-    const int segs = segments(K, kSegment / (src.x.f32 ? 2 : 1) / (src.act ? 2 : 1));
+    const int segs = segments(K, segment_blocks(src.x.f32, src.act));
     int parts = 1;
     while (parts < 8 && parts < segs && static_cast<int64_t>(plan.R) * parts < most * 8) parts *= 2;
     const int64_t want = (static_cast<int64_t>(plan.R) * parts + 7) / 8;

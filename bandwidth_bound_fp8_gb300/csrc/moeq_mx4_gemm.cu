@@ -37,13 +37,15 @@ static_assert(threads_of(false) >= kPlanThreads, "the plan's scan needs its thre
 // 22.1; an LM head of 6144 x 151552 72.5, 72.5 and 75.1.
 constexpr int kMaxStages = 7;
 // Tiles of this many rows or more are multiplied by pairs of CTAs; their most
-// rows (a multiple of 32).
+// rows (a multiple of 32).  8192 tokens over 256 experts (K 6144, N 4096):
+// 867 us in pairs, 953 without; 64 experts of about 50 to 200 rows (K 2048,
+// N 2816): equal within 2 %.
 constexpr int kPairRows = 200, kPairTileRows = 224;
 // Units are cut in kCut parts where that many of them have a worker each and K
 // is long enough for the join to pay: a part saves about 0.2 us for every K
 // block, the join costs 2 us and 1.6 us for every 16 rows of the tile.
 // 1 x 32768 -> 128: 36 us whole; 160 x 6144 -> 1024: 15 us whole, 62 with the
-// stages dealt to all SMs; one token over eight experts (256 units): 23.4 us
+// stages dealt to all SMs; one token over eight experts (256 units): 22.4 us
 // whole, 28 with the stages dealt evenly, although half the SMs take one
 // unit and half two (the others' bandwidth goes to them).
 constexpr int kCut = 4;

@@ -6,7 +6,7 @@ or a prompt.  ``moeq.moeq_moe_layer`` is its FP8 counterpart for up to 16
 tokens in one kernel.
 
 ``route``, ``dispatch`` and ``combine`` train: the same routing and movement
-as autograd functions, around whatever experts the caller's program has.
+as autograd functions, around whatever experts the caller's program has, to any order.
 """
 from __future__ import annotations
 
@@ -28,12 +28,49 @@ class Dispatch:
 
 
 # ------------------------------------------------------------------ training
+# Every backward pass is a function of its own with a backward pass, so that a
+# second differentiation (a gradient penalty, a Hessian-vector product) sees
+# the first one's dependence on what was saved: the kernels read and write
+# through pointers, and a graph would take their results for constants.
+# (torch's once_differentiable would not refuse it: it looks at the incoming
+# gradients alone, and d_y = w d_out depends on w for a constant d_out.)
+# Indices are saved as tensors, so that autograd notices when one is
+# overwritten in place.
+def _route_grad(dw, ids, w, E):
+    dl = torch.empty((ids.shape[0], E), dtype=w.dtype, device=w.device)
+    moeq.moeq_route_rows_grad(dw, ids, w, dl)
+    return dl
+
+
+def _gather(x, offs, pair_row):
+    xs = torch.empty((pair_row.numel(), x.shape[1]), dtype=x.dtype, device=x.device)
+    moeq.moeq_gather_rows(x, offs, pair_row, xs)
+    return xs
+
+
+def _gather_grad(dxs, offs, pair_row):
+    dx = torch.empty((pair_row.shape[0], dxs.shape[1]), dtype=dxs.dtype, device=dxs.device)
+    moeq.moeq_gather_rows_grad(dxs, pair_row, dx)
+    return dx
+
+
+def _combine_grad(dout, y, w, offs, pair_row):
+    dy, dw = torch.empty_like(y), torch.empty_like(w)
+    moeq.moeq_combine_rows_grad(dout, y, offs, pair_row, w, dy, dw)
+    return dy, dw
+
+
+def _grad(function, plain):
+    """The autograd function where its result may be differentiated again, the plain call where it cannot."""
+    return function.apply if torch.is_grad_enabled() else plain
+
+
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k):
         T = logits.shape[0]
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        w = torch.empty((T, k), dtype=logits.dtype, device=logits.device)
         moeq.moeq_route_rows(logits, ids, w)
         ctx.save_for_backward(ids, w)
         ctx.E = logits.shape[1]
@@ -43,43 +80,85 @@ class _Route(torch.autograd.Function):
     @staticmethod
     def backward(ctx, _, dw):
         ids, w = ctx.saved_tensors
-        dl = torch.empty((ids.shape[0], ctx.E), dtype=torch.float32, device=w.device)
-        moeq.moeq_route_rows_grad(dw.contiguous(), ids, w, dl)
-        return dl, None
+        return _grad(_RouteGrad, _route_grad)(dw.contiguous(), ids, w, ctx.E), None
+
+
+class _RouteGrad(torch.autograd.Function):
+    """F = sum_j g_j w_j (dw_j - s), s = sum_i w_i dw_i, for a gradient g of d_logits at the picks:
+    dF/d(dw_j) = w_j (g_j - t) and dF/dw_j = g_j (dw_j - s) - dw_j t, t = sum_i w_i g_i."""
+
+    @staticmethod
+    def forward(ctx, dw, ids, w, E):
+        ctx.save_for_backward(dw, ids, w)
+        return _route_grad(dw, ids, w, E)
+
+    @staticmethod
+    def backward(ctx, g):
+        dw, ids, w = ctx.saved_tensors
+        live = ids >= 0
+        zero = torch.zeros((), dtype=w.dtype, device=w.device)
+        g = torch.where(live, g.gather(1, ids.clamp(min=0).long()), zero)
+        dw = torch.where(live, dw, zero)
+        s, t = (w * dw).sum(1, keepdim=True), (w * g).sum(1, keepdim=True)
+        return w * (g - t), None, g * (dw - s) - dw * t, None
 
 
 class _Dispatch(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, d):
-        ctx.d, ctx.T = d, x.shape[0]
-        xs = torch.empty((d.row_pair.shape[0], x.shape[1]), dtype=x.dtype, device=x.device)
-        moeq.moeq_gather_rows(x, d.offs, d.pair_row, xs)
-        return xs
+    def forward(ctx, x, offs, pair_row):
+        ctx.save_for_backward(offs, pair_row)
+        return _gather(x, offs, pair_row)
 
     @staticmethod
     def backward(ctx, dxs):
-        dxs = dxs.contiguous()
-        dx = torch.empty((ctx.T, dxs.shape[1]), dtype=dxs.dtype, device=dxs.device)
-        moeq.moeq_gather_rows_grad(dxs, ctx.d.pair_row, dx)
-        return dx, None
+        return _grad(_DispatchGrad, _gather_grad)(dxs.contiguous(), *ctx.saved_tensors), None, None
+
+
+class _DispatchGrad(torch.autograd.Function):
+    """Dispatch's adjoint, so its own is dispatch."""
+
+    @staticmethod
+    def forward(ctx, dxs, offs, pair_row):
+        ctx.save_for_backward(offs, pair_row)
+        return _gather_grad(dxs, offs, pair_row)
+
+    @staticmethod
+    def backward(ctx, g):
+        return _grad(_Dispatch, _gather)(g.contiguous(), *ctx.saved_tensors), None, None
 
 
 class _Combine(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, y, w, base, d):
-        ctx.d, ctx.has_base = d, base is not None
-        ctx.save_for_backward(y, w)
+    def forward(ctx, y, w, base, offs, pair_row):
+        ctx.has_base = base is not None
+        ctx.save_for_backward(y, w, offs, pair_row)
         out = torch.empty((w.shape[0], y.shape[1]), dtype=y.dtype if base is None else base.dtype, device=y.device)
-        moeq.moeq_combine_rows(y, d.pair_row, w, out, base=base)
+        moeq.moeq_combine_rows(y, pair_row, w, out, base=base)
         return out
 
     @staticmethod
     def backward(ctx, dout):
-        y, w = ctx.saved_tensors
         dout = dout.contiguous()
-        dy, dw = torch.empty_like(y), torch.empty_like(w)
-        moeq.moeq_combine_rows_grad(dout, y, ctx.d.offs, ctx.d.pair_row, w, dy, dw)
-        return dy, dw, dout if ctx.has_base else None, None
+        dy, dw = _grad(_CombineGrad, _combine_grad)(dout, *ctx.saved_tensors)
+        return dy, dw, dout if ctx.has_base else None, None, None
+
+
+class _CombineGrad(torch.autograd.Function):
+    """dy = w dout and dw = <dout, y> at the slots' rows.  For gradients gy and gw of them, dout gets
+    sum_j w_j gy + gw_j y, y gets gw dout, and w gets <dout, gy>: combine and this function again."""
+
+    @staticmethod
+    def forward(ctx, dout, y, w, offs, pair_row):
+        ctx.save_for_backward(dout, y, w, offs, pair_row)
+        return _combine_grad(dout, y, w, offs, pair_row)
+
+    @staticmethod
+    def backward(ctx, gy, gw):
+        dout, y, w, *plan = ctx.saved_tensors
+        gy, gw = gy.contiguous(), gw.contiguous()
+        d_dout = _Combine.apply(y, gw, _Combine.apply(gy, w, torch.zeros_like(dout), *plan), *plan)
+        dy, dw = _grad(_CombineGrad, _combine_grad)(dout, gy, gw, *plan)
+        return d_dout, dy, dw, None, None
 
 
 def route(logits: torch.Tensor, k: int):
@@ -89,12 +168,12 @@ def route(logits: torch.Tensor, k: int):
 
 def dispatch(x: torch.Tensor, d: Dispatch) -> torch.Tensor:
     """Rows of x [T, H] in expert order: [T * k, H], zero rows after the last."""
-    return _Dispatch.apply(x, d)
+    return _Dispatch.apply(x, d.offs, d.pair_row)
 
 
 def combine(y: torch.Tensor, w: torch.Tensor, d: Dispatch, base: torch.Tensor | None = None) -> torch.Tensor:
     """base[t] + sum_j w[t, j] * y[row of (t, j)]."""
-    return _Combine.apply(y.contiguous(), w.contiguous(), base, d)
+    return _Combine.apply(y.contiguous(), w.contiguous(), base, d.offs, d.pair_row)
 
 
 # ------------------------------------------------------------------- serving

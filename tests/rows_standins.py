@@ -1,0 +1,71 @@
+"""The calls that expert_layer makes, in torch operations on the CPU: for
+tests of what the Python layer itself does with them.  They write through
+.data, as the kernels write through pointers: autograd sees none of it."""
+from __future__ import annotations
+
+import torch
+
+
+def route_rows(logits, ids, w, stream=None):
+    k = ids.shape[1]
+    v, i = torch.sort(logits.data, dim=1, descending=True, stable=True)
+    v, i = v[:, :k], i[:, :k]
+    live = v > -torch.inf
+    p = torch.where(live, torch.exp(v - torch.where(live[:, :1], v[:, :1], torch.zeros_like(v[:, :1]))), torch.zeros_like(v))
+    ids.data.copy_(torch.where(live, i, torch.full_like(i, -1)))
+    w.data.copy_(p / p.sum(1, keepdim=True).clamp(min=1e-30))
+
+
+def route_rows_grad(dw, ids, w, dl, stream=None):
+    live = ids >= 0
+    d = torch.where(live, dw.data, torch.zeros_like(dw)) * w.data
+    d = d - w.data * d.sum(1, keepdim=True)
+    dl.data.zero_().scatter_add_(1, ids.clamp(min=0).long(), torch.where(live, d, torch.zeros_like(d)))
+
+
+def expert_sort(ids, E, offs, pair_row, row_pair, stream=None):
+    flat = torch.where((ids >= 0) & (ids < E), ids, torch.full_like(ids, E)).reshape(-1).long()
+    order = torch.sort(flat, stable=True).indices
+    kept = flat[order] < E
+    at = torch.arange(flat.numel())
+    offs.data[0] = 0
+    offs.data[1:] = torch.cumsum(torch.bincount(flat, minlength=E + 1)[:E], 0)
+    row_pair.data.copy_(torch.where(kept, order, -1))
+    pr = torch.empty_like(at)
+    pr[order] = torch.where(kept, at, -1)
+    pair_row.data.copy_(pr.view(ids.shape))
+
+
+def _rows(y, pair_row):
+    live = (pair_row >= 0).unsqueeze(2)
+    return torch.where(live, y.data[pair_row.clamp(min=0).long()], torch.zeros((), dtype=y.dtype))
+
+
+def _scatter(out, pair_row, rows):
+    live = pair_row >= 0
+    out.data.zero_()
+    out.data[pair_row[live].long()] = rows[live].to(out.dtype)
+
+
+def gather_rows(x, offs, pair_row, xs, stream=None):
+    _scatter(xs, pair_row, x.data.unsqueeze(1).expand(-1, pair_row.shape[1], -1))
+
+
+def gather_rows_grad(dxs, pair_row, dx, stream=None):
+    dx.data.copy_(_rows(dxs, pair_row).sum(1))
+
+
+def combine_rows(y, pair_row, w, out, base=None, stream=None):
+    v = (w.data.unsqueeze(2) * _rows(y, pair_row)).sum(1)
+    out.data.copy_(v if base is None else v + base.data)
+
+
+def combine_rows_grad(dout, y, offs, pair_row, w, dy, dw, stream=None):
+    _scatter(dy, pair_row, w.data.unsqueeze(2) * dout.data.unsqueeze(1))
+    dw.data.copy_((_rows(y, pair_row) * dout.data.unsqueeze(1)).sum(2))
+
+
+def use(monkeypatch):
+    from bandwidth_bound_fp8_gb300 import moeq
+    for f in (route_rows, route_rows_grad, expert_sort, gather_rows, gather_rows_grad, combine_rows, combine_rows_grad):
+        monkeypatch.setattr(moeq, "moeq_" + f.__name__, f)

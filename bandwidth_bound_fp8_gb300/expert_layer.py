@@ -186,13 +186,57 @@ class Mx4Weights:
         moeq.moeq_mx4_quant_weight(w, self.tiles, self.scales)
 
 
+class _Buffers:
+    """The buffers of an Mx4MoeLayer call of up to T tokens, and a workspace of ws_bytes."""
+
+    def __init__(self, layer: Mx4MoeLayer, T: int, ws_bytes: int):
+        H, I, E, k, device = layer.gu.K, layer.d.K, layer.gu.E, layer.top_k, layer.gu.tiles.device
+        new = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device=device)
+        i32 = torch.int32
+        self.T, self.captured = T, False
+        self.t = dict(ids=new(T, k, dt=i32), w=new(T, k, dt=torch.float32), offs=new(E + 1, dt=i32),
+                      pair_row=new(T, k, dt=i32), row_pair=new(T * k, dt=i32), h=new(T * k, 2 * I), y=new(T * k, H))
+        if layer.s_gu is not None:
+            # row n of s_offs is {0, n}: rows of another T are not overwritten
+            s_offs = torch.zeros((T + 1, 2), dtype=i32, device=device)
+            s_offs[:, 1] = torch.arange(T + 1, dtype=i32, device=device)
+            self.t.update(sh=new(T, 2 * layer.s_d.K), sy=new(T, H), s_offs=s_offs)
+        self.ws = moeq.Workspace(ws_bytes, device=device)   # the products run one after another
+        self.streams = {moeq.current_stream_handle()}
+
+    def views(self, T: int, k: int) -> dict:
+        n = dict(ids=T, w=T, pair_row=T, row_pair=T * k, h=T * k, y=T * k, sh=T, sy=T)
+        v = {name: t[:n[name]] if name in n else t for name, t in self.t.items()}
+        if "s_offs" in v:
+            v["s_offs"] = v["s_offs"][T]
+        return dict(v, ws=self.ws)
+
+    def used(self, capturing: bool) -> None:
+        """Notes a call's stream: memory in use there is not given to another's tensors when it is freed."""
+        if capturing:
+            self.captured = True
+            return
+        stream = moeq.current_stream_handle()
+        if stream not in self.streams:
+            for t in (*self.t.values(), self.ws.t):
+                t.record_stream(torch.cuda.current_stream())
+            self.streams.add(stream)
+
+
 class Mx4MoeLayer:
     """out = shared(x) + sum_j w_j * expert_j(x), every expert down(silu(gate x) * up x).
 
     w_gu [E, 2I, H] (gate rows, then up rows), w_d [E, H, I]; shared_gu
     [1, 2I, H] and shared_d [1, H, I], or None for a layer without a shared
-    expert.  Buffers are kept for the number of tokens last seen; one instance
-    is not to be used by two streams at once."""
+    expert.
+
+    Buffers are kept for the most tokens seen (``reserve`` makes them
+    beforehand), and those that a CUDA graph was captured with for as long as
+    the layer lives, so a graph stays valid whatever calls follow.  All calls
+    and graphs of one instance share them: they follow one another, on one
+    stream or ordered by events."""
+
+    _VIEWS = ("ids", "w", "offs", "pair_row", "row_pair", "h", "y", "sh", "sy", "s_offs", "ws")
 
     def __init__(self, w_gu, w_d, top_k: int, shared_gu=None, shared_d=None):
         self.gu, self.d = Mx4Weights(w_gu), Mx4Weights(w_d)
@@ -200,25 +244,52 @@ class Mx4MoeLayer:
         self.s_d = None if shared_d is None else Mx4Weights(shared_d)
         if (self.s_gu is None) != (self.s_d is None):
             raise ValueError("Mx4MoeLayer: shared_gu and shared_d come together")
-        self.top_k, self.T = top_k, -1
+        self.top_k, self.T = top_k, -1   # T: the tokens that the views below are for
+        self._kept, self._of_graphs = None, []
 
-    def _buffers(self, T: int, device):
-        if T == self.T:
-            return
-        H, I, E, k, R = self.gu.K, self.d.K, self.gu.E, self.top_k, T * self.top_k
-        new = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device=device)
-        self.ids, self.w = new(T, k, dt=torch.int32), new(T, k, dt=torch.float32)
-        self.offs, self.pair_row, self.row_pair = new(E + 1, dt=torch.int32), new(T, k, dt=torch.int32), new(R, dt=torch.int32)
-        self.h, self.y = new(R, 2 * I), new(R, H)
-        sizes = [moeq.moeq_mx4_expert_gemm_workspace_size(T, H, 2 * I, E, R),
-                 moeq.moeq_mx4_expert_gemm_workspace_size(R, I, H, E, R)]
+    def _ws_bytes(self, T: int) -> int:
+        H, I, E, R = self.gu.K, self.d.K, self.gu.E, T * self.top_k
+        shapes = [(T, H, 2 * I, E, R), (R, I, H, E, R)]
         if self.s_gu is not None:
-            self.sh, self.sy = new(T, 2 * self.s_d.K), new(T, H)
-            self.s_offs = torch.tensor([0, T], dtype=torch.int32, device=device)
-            sizes += [moeq.moeq_mx4_expert_gemm_workspace_size(T, H, 2 * self.s_d.K, 1, T),
-                      moeq.moeq_mx4_expert_gemm_workspace_size(T, self.s_d.K, H, 1, T)]
-        self.ws = moeq.Workspace(max(sizes), device=device)   # the products run one after another
-        self.T = T
+            shapes += [(T, H, 2 * self.s_d.K, 1, T), (T, self.s_d.K, H, 1, T)]
+        return max(moeq.moeq_mx4_expert_gemm_workspace_size(*s) for s in shapes)
+
+    def reserve(self, T: int) -> None:
+        """Makes the buffers for up to T tokens now (not inside a capture: a graph's memory is its own)."""
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("Mx4MoeLayer.reserve: a CUDA graph is being captured")
+        if self._kept is None or T > self._kept.T:
+            self._grow(T, self._ws_bytes(T))
+
+    def _grow(self, T: int, ws_bytes: int) -> None:
+        old = self._kept
+        if old is not None:
+            T, ws_bytes = max(T, old.T), max(ws_bytes, old.ws.nbytes)
+            if old.captured:
+                self._of_graphs.append(old)
+        self._kept, self.T, old = None, -1, None   # what no graph uses makes room first
+        for name in self._VIEWS:
+            self.__dict__.pop(name, None)
+        # Fewer tokens, in narrower tiles, may need a little more workspace
+        # than T; a tile's rows more than T need (240) cover them.
+        self._kept = _Buffers(self, T, max(ws_bytes, self._ws_bytes(T), self._ws_bytes(T + 240 // self.top_k + 1)))
+
+    def _buffers(self, T: int) -> None:
+        capturing = torch.cuda.is_current_stream_capturing()
+        if T != self.T:
+            need = self._ws_bytes(T)
+            fits = self._kept is not None and T <= self._kept.T and need <= self._kept.ws.nbytes
+            if not fits and not capturing:
+                self._grow(T, need)
+                fits = True
+            # Inside a capture, memory and its zeroing belong to the graph: new
+            # buffers serve this call alone.
+            b = self._kept if fits else _Buffers(self, T, need)
+            for name, v in b.views(T, self.top_k).items():
+                setattr(self, name, v)
+            self.T = T if fits else -1
+        if self.T == T:
+            self._kept.used(capturing)
 
     def __call__(self, x: torch.Tensor, logits: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
         """x [T, H] bf16, logits [T, E] fp32 -> out [T, H] bf16."""
@@ -227,7 +298,7 @@ class Mx4MoeLayer:
             out = torch.empty_like(x)
         if T == 0:
             return out
-        self._buffers(T, x.device)
+        self._buffers(T)
         base = None
         if self.s_gu is not None:
             self._ffn(x, self.s_gu, self.s_d, self.s_offs, self.sh, self.sy, None, 1)

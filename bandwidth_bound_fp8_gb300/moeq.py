@@ -174,6 +174,10 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def current_stream_handle() -> int:
+    return _stream(None)
+
+
 def _dtype(t) -> int:
     if t.dtype == torch.bfloat16:
         return MOEQ_BF16

@@ -65,7 +65,45 @@ def combine_rows_grad(dout, y, offs, pair_row, w, dy, dw, stream=None):
     dw.data.copy_((_rows(y, pair_row) * dout.data.unsqueeze(1)).sum(2))
 
 
+def expert_gemm(x, w, w_scales, offs, y, ws, row_pair=None, top_k=1, act=0, x_scales=None, stream=None):
+    R = y.shape[0]
+    assert ws.nbytes >= workspace_size(x.shape[0], w.shape[2], w.shape[1], w.shape[0], R)
+    rows = torch.arange(R) if row_pair is None else torch.div(row_pair, top_k, rounding_mode="floor")
+    a = x.float()
+    if act:
+        a = torch.nn.functional.silu(a[:, :a.shape[1] // 2]) * a[:, a.shape[1] // 2:]
+    y.data.zero_()
+    for e in range(w.shape[0]):
+        lo, hi = int(offs[e]), int(offs[e + 1])
+        y.data[lo:hi] = (a[rows[lo:hi].long()] @ w[e].t()).to(y.dtype)
+
+
+def weight_buffers(E, N, K, device=None):
+    return torch.empty((E, N, K)), torch.empty(0)
+
+
+def workspace_size(rows, K, N, E, R):
+    """Any size that does not rise with the rows, as the library's does not where tiles widen."""
+    return 4096 + 64 * (R + (16 if R % 3 else 40))
+
+
+class Workspace:
+    def __init__(self, nbytes, device=None, stream=None):
+        self.nbytes, self.t = nbytes, torch.zeros(nbytes, dtype=torch.uint8)
+
+
 def use(monkeypatch):
+    """Replaces the calls; returns what the test may set: whether a graph is being captured, and the current stream."""
+    import types
     from bandwidth_bound_fp8_gb300 import moeq
+    state = types.SimpleNamespace(capturing=False, stream=0)
     for f in (route_rows, route_rows_grad, expert_sort, gather_rows, gather_rows_grad, combine_rows, combine_rows_grad):
         monkeypatch.setattr(moeq, "moeq_" + f.__name__, f)
+    monkeypatch.setattr(moeq, "moeq_mx4_expert_gemm", expert_gemm)
+    monkeypatch.setattr(moeq, "moeq_mx4_expert_gemm_workspace_size", workspace_size)
+    monkeypatch.setattr(moeq, "mx4_weight_buffers", weight_buffers)
+    monkeypatch.setattr(moeq, "moeq_mx4_quant_weight", lambda w, tiles, scales, stream=None: tiles.copy_(w))
+    monkeypatch.setattr(moeq, "Workspace", Workspace)
+    monkeypatch.setattr(moeq, "_stream", lambda s: state.stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.capturing)
+    return state

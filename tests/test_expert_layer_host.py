@@ -1,6 +1,9 @@
 """expert_layer's own part (autograd, buffers, checks), on the CPU: the kernel
 calls are replaced by torch operations that autograd does not see, as it does
 not see the kernels."""
+import gc
+import weakref
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -82,3 +85,107 @@ def test_an_overwritten_plan_is_noticed(el):
     d.pair_row.fill_(-1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         out.sum().backward()
+
+
+# ------------------------------------------------------------------- buffers
+E, H, I, K = 5, 32, 16, 2
+
+
+def _layer(el, shared=True):
+    f = lambda s, *shape: 0.3 * _rand(s, *shape).float()
+    return el.Mx4MoeLayer(f(1, E, 2 * I, H), f(2, E, H, I), K, f(3, 1, 2 * I, H) if shared else None,
+                          f(4, 1, H, I) if shared else None)
+
+
+def _inputs(T):
+    return _rand(T, T, H).to(torch.bfloat16), _rand(T + 1, T, E).float()
+
+
+def _want(el, T, shared=True):
+    """The layer alone, with buffers of its own."""
+    return _layer(el, shared)(*_inputs(T))
+
+
+@pytest.mark.parametrize("shared", [True, False])
+def test_one_layer_for_many_token_counts(el, shared):
+    layer = _layer(el, shared)
+    for T in (3, 1, 9, 2, 9, 7, 300, 8, 1):
+        assert torch.equal(layer(*_inputs(T)), _want(el, T, shared))
+        assert layer.ids.shape == (T, K) and layer.h.shape == (T * K, 2 * I)
+        if shared:
+            assert layer.s_offs.tolist() == [0, T]
+
+
+def test_fewer_tokens_take_no_new_memory(el, monkeypatch):
+    layer = _layer(el)
+    layer(*_inputs(12))
+    made = []
+    real = el._Buffers.__init__
+    monkeypatch.setattr(el._Buffers, "__init__", lambda self, *a: (made.append(a), real(self, *a))[1])
+    for T in (6, 12, 3, 9):
+        layer(*_inputs(T))
+    assert not made
+    layer.reserve(20)
+    layer(*_inputs(18))
+    assert len(made) == 1
+
+
+def test_what_a_captured_graph_uses_stays(el, monkeypatch):
+    """A graph replays the addresses it was captured with: they must stay allocated, and the values that no replay
+    writes (the shared expert's row range) must stay as they were, whatever runs after."""
+    layer = _layer(el)
+    state = rows_standins.use(monkeypatch)
+    tensors = {}
+    for T in (3, 9, 1, 30, 2):
+        layer(*_inputs(T))                      # a warm-up, as capture asks for
+        state.capturing = True
+        layer(*_inputs(T))
+        state.capturing = False
+        for name, v in [*vars(layer).items(), ("ws", layer.ws.t)]:
+            if isinstance(v, torch.Tensor):
+                owner = v if v._base is None else v._base
+                tensors[T, name] = weakref.ref(owner), v.data_ptr() - owner.data_ptr()
+    for T in (50, 4, 30):
+        layer(*_inputs(T))
+    gc.collect()
+    assert len(tensors) == 5 * 11
+    assert not [at for at, (owner, _) in tensors.items() if owner() is None]
+    for T in (3, 9, 1, 30, 2):
+        owner, at = tensors[T, "s_offs"]
+        assert owner().reshape(-1)[at // 4:at // 4 + 2].tolist() == [0, T]
+
+
+def test_a_capture_without_a_warm_up_keeps_nothing(el, monkeypatch):
+    """Memory and zeroing inside a capture are the graph's: a later call outside must not take them for its own."""
+    layer = _layer(el)
+    state = rows_standins.use(monkeypatch)
+    state.capturing = True
+    layer(*_inputs(4))
+    with pytest.raises(RuntimeError, match="captured"):
+        layer.reserve(8)
+    state.capturing = False
+    graph_ws = layer.ws
+    layer(*_inputs(4))
+    assert layer.ws is not graph_ws
+    kept = layer.ws
+    state.capturing = True
+    layer(*_inputs(40))
+    assert layer.ws is not kept
+    state.capturing = False
+    layer(*_inputs(4))
+    assert layer.ws is kept
+
+
+def test_another_stream_is_recorded(el, monkeypatch):
+    layer = _layer(el)
+    state = rows_standins.use(monkeypatch)
+    layer(*_inputs(4))
+    seen = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.append((t.data_ptr(), s)))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: state.stream)
+    layer(*_inputs(4))
+    assert not seen
+    state.stream = 7
+    layer(*_inputs(3))
+    layer(*_inputs(4))
+    assert {s for _, s in seen} == {7} and len(seen) == len(layer._kept.t) + 1

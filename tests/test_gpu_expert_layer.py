@@ -164,3 +164,54 @@ def test_gradient_penalty_matches_autograd_in_64_bits():
     penalty(torch.stack(rows), ref)
     for a, r in zip(mine, ref):
         assert (a.grad.double() - r.grad).abs().max() <= 5e-4 * r.grad.abs().max()
+
+
+def _small_layer(shared=True):
+    from bandwidth_bound_fp8_gb300.expert_layer import Mx4MoeLayer
+    E, H, I, k = 12, 512, 256, 3
+    return Mx4MoeLayer(0.05 * _rand(1, E, 2 * I, H), 0.05 * _rand(2, E, H, I), k,
+                       0.05 * _rand(3, 1, 2 * I, H) if shared else None, 0.05 * _rand(4, 1, H, I) if shared else None)
+
+
+def _tokens(T):
+    return _rand(100 + T, T, 512).to(BF), _rand(200 + T, T, 12)
+
+
+@pytest.mark.parametrize("shared", [True, False])
+def test_one_layer_for_many_token_counts(shared):
+    """The bits of a layer that has seen no other number of tokens."""
+    layer = _small_layer(shared)
+    want = {T: _small_layer(shared)(*_tokens(T)) for T in (1, 3, 16, 250, 700)}
+    for T in (16, 1, 250, 3, 700, 16, 250, 1):
+        assert torch.equal(layer(*_tokens(T)), want[T])
+        assert layer.h.shape[0] == 3 * T
+
+
+def test_graphs_of_several_token_counts():
+    """Graphs captured from one layer, some after a warm-up and one without, replayed in any order between plain calls
+    and with other tensors taking whatever memory is free."""
+    layer = _small_layer()
+    want = {T: _small_layer()(*_tokens(T)) for T in (2, 17, 300, 400)}
+    graphs = {}
+    for T in (2, 17, 300, 400):
+        x, lg = _tokens(T)
+        out = torch.zeros_like(x)
+        if T != 400:
+            layer(x, lg, out=out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer(x, lg, out=out)
+        graphs[T] = g, x, lg, out
+    assert torch.equal(layer(*_tokens(400)), want[400])
+    fill = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in (1 << 9, 1 << 14, 1 << 18, 1 << 21, 1 << 24) * 8]
+    layer.reserve(900)
+    for T in (300, 2, 400, 17, 2, 300, 400):
+        g, x, lg, out = graphs[T]
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want[T]), T
+        other = {2: 300, 17: 2, 300: 17, 400: 2}[T]
+        assert torch.equal(layer(*_tokens(other)), want[other])
+    torch.cuda.synchronize()
+    assert all(bool((t == 0xFF).all()) for t in fill)

@@ -239,11 +239,22 @@ class Mx4MoeLayer:
     _VIEWS = ("ids", "w", "offs", "pair_row", "row_pair", "h", "y", "sh", "sy", "s_offs", "ws")
 
     def __init__(self, w_gu, w_d, top_k: int, shared_gu=None, shared_d=None):
+        if (shared_gu is None) != (shared_d is None):
+            raise ValueError("Mx4MoeLayer: shared_gu and shared_d come together")
+        # the products know their weights by the size of their tiles, which is rounded up: other widths are seen here
+        H = w_gu.shape[-1]
+        for gu, d, what in ((w_gu, w_d, "w"), (shared_gu, shared_d, "shared")):
+            if gu is None:
+                continue
+            E = w_gu.shape[0] if what == "w" else 1
+            if d.dim() != 3 or gu.shape != (E, 2 * d.shape[2], H) or d.shape != (E, H, d.shape[2]):
+                raise ValueError(f"Mx4MoeLayer: {what}_gu [{E}, 2I, {H}] and {what}_d [{E}, {H}, I] are wanted, got "
+                                 f"{tuple(gu.shape)} and {tuple(d.shape)}")
+            if gu.device != w_gu.device or d.device != w_gu.device:
+                raise ValueError("Mx4MoeLayer: the weights lie on different devices")
         self.gu, self.d = Mx4Weights(w_gu), Mx4Weights(w_d)
         self.s_gu = None if shared_gu is None else Mx4Weights(shared_gu)
         self.s_d = None if shared_d is None else Mx4Weights(shared_d)
-        if (self.s_gu is None) != (self.s_d is None):
-            raise ValueError("Mx4MoeLayer: shared_gu and shared_d come together")
         self.top_k, self.T = top_k, -1   # T: the tokens that the views below are for
         self._kept, self._of_graphs = None, []
 
@@ -294,8 +305,16 @@ class Mx4MoeLayer:
     def __call__(self, x: torch.Tensor, logits: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
         """x [T, H] bf16, logits [T, E] fp32 -> out [T, H] bf16."""
         T = x.shape[0]
+        if x.shape != (T, self.gu.K) or logits.shape != (T, self.gu.E):
+            raise ValueError(f"x [T, {self.gu.K}] and logits [T, {self.gu.E}] are wanted, got {tuple(x.shape)} and "
+                             f"{tuple(logits.shape)}")
+        if x.device != self.gu.tiles.device or logits.device != x.device:
+            raise ValueError(f"x and logits on the weights' device ({self.gu.tiles.device}) are wanted, got {x.device} "
+                             f"and {logits.device}")
         if out is None:
             out = torch.empty_like(x)
+        elif out.shape != x.shape or out.device != x.device:
+            raise ValueError(f"out: x's shape and device are wanted, got {tuple(out.shape)} on {out.device}")
         if T == 0:
             return out
         self._buffers(T)

@@ -189,3 +189,33 @@ def test_another_stream_is_recorded(el, monkeypatch):
     layer(*_inputs(3))
     layer(*_inputs(4))
     assert {s for _, s in seen} == {7} and len(seen) == len(layer._kept.t) + 1
+
+
+# -------------------------------------------------------------------- checks
+def test_layer_refuses_other_shapes(el):
+    """Logits wider than the experts named some that the sort drops; a narrower x fits the same number of tiles."""
+    layer = _layer(el)
+    x, lg = _inputs(4)
+    layer(x, lg)
+    wide = torch.cat([lg, lg + 9], 1)
+    for bad in ((x, wide), (x, lg[:, :-1]), (x, lg[:3]), (x[:, :-8], lg), (x[0], lg), (x[:0, :-8], lg[:0])):
+        with pytest.raises(ValueError):
+            layer(*bad)
+    for out in (torch.empty(4, H + 1, dtype=x.dtype), torch.empty(5, H, dtype=x.dtype)):
+        with pytest.raises(ValueError):
+            layer(x, lg, out=out)
+    assert layer(x[:0], lg[:0]).shape == (0, H)
+    with pytest.raises(ValueError):
+        layer(x, lg.to("meta"))
+
+
+def test_layer_refuses_weights_that_do_not_fit(el):
+    f = lambda *shape: torch.zeros(shape)
+    ok = dict(w_gu=f(E, 2 * I, H), w_d=f(E, H, I), top_k=K, shared_gu=f(1, 2 * I, H), shared_d=f(1, H, I))
+    el.Mx4MoeLayer(**ok)
+    for bad in (dict(w_gu=f(E, 2 * I + 2, H)), dict(w_gu=f(E + 1, 2 * I, H)), dict(w_gu=f(E, 2 * I, H - 8)),
+                dict(w_d=f(E, H, I + 1)), dict(w_d=f(H, I)), dict(shared_gu=f(2, 2 * I, H)), dict(shared_gu=None),
+                dict(shared_d=f(1, H - 8, I)), dict(shared_d=f(1, H, I).to("meta"))):
+        with pytest.raises(ValueError):
+            el.Mx4MoeLayer(**{**ok, **bad})
+    el.Mx4MoeLayer(**{**ok, "shared_gu": f(1, 6 * I, H), "shared_d": f(1, H, 3 * I)})   # a shared expert of another width

@@ -186,6 +186,19 @@ class Mx4Weights:
         moeq.moeq_mx4_quant_weight(w, self.tiles, self.scales)
 
 
+class _Serve(torch.autograd.Function):
+    """Ties the layer's output to inputs that require a gradient, so that a backward pass raises instead of leaving
+    them without one."""
+
+    @staticmethod
+    def forward(ctx, out, x, logits):
+        return out.view_as(out)   # a caller's own buffer gathers no history
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("Mx4MoeLayer has no backward pass (route, dispatch and combine train)")
+
+
 class _Buffers:
     """The buffers of an Mx4MoeLayer call of up to T tokens, and a workspace of ws_bytes."""
 
@@ -326,6 +339,8 @@ class Mx4MoeLayer:
         moeq.moeq_expert_sort(self.ids, self.gu.E, self.offs, self.pair_row, self.row_pair)
         self._ffn(x, self.gu, self.d, self.offs, self.h, self.y, self.row_pair, self.top_k)
         moeq.moeq_combine_rows(self.y, self.pair_row, self.w, out, base=base)
+        if torch.is_grad_enabled() and (x.requires_grad or logits.requires_grad):
+            return _Serve.apply(out.detach(), x, logits)
         return out
 
     def _ffn(self, x, gu, d, offs, h, y, row_pair, top_k):

@@ -219,3 +219,20 @@ def test_layer_refuses_weights_that_do_not_fit(el):
         with pytest.raises(ValueError):
             el.Mx4MoeLayer(**{**ok, **bad})
     el.Mx4MoeLayer(**{**ok, "shared_gu": f(1, 6 * I, H), "shared_d": f(1, H, 3 * I)})   # a shared expert of another width
+
+
+def test_layer_refuses_a_backward_pass(el):
+    """The forward pass is the same for inputs that require a gradient; asking for one raises."""
+    layer = _layer(el)
+    x, lg = _inputs(4)
+    want = layer(x, lg)
+    for xr, lr in ((True, False), (False, True)):
+        a, b = x.clone().requires_grad_(xr), lg.clone().requires_grad_(lr)
+        given = torch.empty_like(x)
+        for out in (layer(a, b), layer(a, b, out=given)):
+            assert torch.equal(out, want)
+            with pytest.raises(RuntimeError, match="no backward pass"):
+                out.sum().backward()
+        assert torch.equal(given, want) and not given.requires_grad and out.data_ptr() == given.data_ptr()
+        with torch.no_grad():
+            assert torch.equal(layer(a, b), want) and not layer(a, b).requires_grad

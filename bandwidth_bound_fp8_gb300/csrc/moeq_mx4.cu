@@ -65,17 +65,17 @@ struct Raw8 {
     __device__ __forceinline__ void load(const void* p, int64_t at) {
         if constexpr (kVec) {
             const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * (kF32 ? 4 : 2));
-            a = __ldg(q);
-            if constexpr (kF32) b = __ldg(q + 1);
+            a = q[0];
+            if constexpr (kF32) b = q[1];
         } else {
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < (kF32 ? 8 : 4); ++i) {
                 if constexpr (kF32) {
-                    w[i] = __ldg(static_cast<const uint32_t*>(p) + at + i);
+                    w[i] = static_cast<const uint32_t*>(p)[at + i];
                 } else {
                     const uint16_t* h = static_cast<const uint16_t*>(p) + at + 2 * i;
-                    w[i] = __ldg(h) | static_cast<uint32_t>(__ldg(h + 1)) << 16;
+                    w[i] = h[0] | static_cast<uint32_t>(h[1]) << 16;
                 }
             }
             a = make_uint4(w[0], w[1], w[2], w[3]);
@@ -162,7 +162,7 @@ struct Segment {
 // Rows of activations: resident warps take a segment at a time, the next one's
 // loads in flight while this one is quantised.
 template <bool kF32, bool kVec, bool kSwiglu>
-__global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__ x, int64_t ld, int rows, int K,
+__global__ void __launch_bounds__(256) quant_act_kernel(const void* x, int64_t ld, int rows, int K,
                                                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
     chain();
     using Seg = Segment<kF32, kVec, kSwiglu>;
@@ -207,8 +207,7 @@ __global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__
 // subnormal of at least 2^-128 fits both).  The scale is applied in two
 // halves, because 2^-127 is no normal number.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(256) dequant_act_kernel(const uint8_t* __restrict__ codes,
-                                                          const uint8_t* __restrict__ scales, int rows, int K,
+__global__ void __launch_bounds__(256) dequant_act_kernel(const uint8_t* codes, const uint8_t* scales, int rows, int K,
                                                           T* __restrict__ out, int64_t ld) {
     chain();
     const int lane = threadIdx.x & 31, segs = segments(K, kSegment);
@@ -222,8 +221,8 @@ __global__ void __launch_bounds__(256) dequant_act_kernel(const uint8_t* __restr
         const int c = (seg * kSegment + i) * kMx4TileCols + lane * 8;
         q[i] = sc[i] = 0;
         if (c < K) {
-            q[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (K >> 1) + (c >> 1)));
-            sc[i] = __ldg(scales + row * mx4_scale_pitch(K) + (c >> 5));
+            q[i] = *reinterpret_cast<const uint32_t*>(codes + row * (K >> 1) + (c >> 1));
+            sc[i] = scales[row * mx4_scale_pitch(K) + (c >> 5)];
         }
     }
 #pragma unroll
@@ -339,7 +338,7 @@ __device__ __forceinline__ int scale_at(int pos, int kc, int sb) {
     return kc * (sb >> 1) + (pos >> 7) * 512 + (pos & 31) * 16 + ((pos >> 5) & 3) * 4;
 }
 __device__ __forceinline__ int act_row(const Mx4Plan& p, int r) {
-    return min(p.row_pair ? max(__ldg(p.row_pair + r), 0) / p.top_k : r, p.rows - 1);
+    return min(p.row_pair ? max(p.row_pair[r], 0) / p.top_k : r, p.rows - 1);
 }
 
 // From rows to quantise: a warp takes every `parts`-th segment of a row at a
@@ -406,8 +405,8 @@ __global__ void __launch_bounds__(kPlanThreads) act_tiles_kernel(RowsIn x, Mx4Pl
 // order of the tile's words, so that a warp writes 128 bytes in one piece
 // (row by row, a third of the kernel's 57 us for 65536 rows of 6144 went into
 // their scattered words).
-__global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t* __restrict__ codes,
-                                                                  const uint8_t* __restrict__ scales, Mx4Plan p, int K,
+__global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t* codes, const uint8_t* scales, Mx4Plan p,
+                                                                  int K,
                                                                   uint8_t* __restrict__ tiles,
                                                                   uint8_t* __restrict__ stiles) {
     chain();
@@ -430,7 +429,7 @@ __global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t*
 #pragma unroll
             for (int i = 0; i < kWide; ++i) {
                 const int c = c0 + i * 32 + lane;
-                v[i] = c < chunks ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                v[i] = c < chunks ? src[c] : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < kWide; ++i) {
@@ -452,7 +451,7 @@ __global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t*
         uint8_t* to = stiles + static_cast<int64_t>(g) * kb_all * sb + scale_at(pos, 0, sb);
 #pragma unroll 8
         for (int kb = 0; kb < kb_all; ++kb) {
-            const uint2 w = __ldg(from + kb);
+            const uint2 w = from[kb];
             *reinterpret_cast<uint32_t*>(to + static_cast<int64_t>(kb) * sb) = w.x;
             *reinterpret_cast<uint32_t*>(to + static_cast<int64_t>(kb) * sb + (sb >> 1)) = w.y;
         }

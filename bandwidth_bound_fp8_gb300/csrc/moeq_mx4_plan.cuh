@@ -22,7 +22,10 @@ __device__ __forceinline__ PlanShared plan_at(int* mem, int E) {
 
 // Rows are given to experts by `offs`; values out of range or order are
 // clamped, so that no row, tile or buffer index leaves its range.  Called by
-// all threads of a block of at least kPlanThreads.
+// all threads of a block of at least kPlanThreads.  `offs` is read from L2,
+// where its writer left it: the product scans the plan ahead of its own
+// griddepcontrol.wait (the kernel between it and that writer let it start only
+// once that writer had ended).
 __device__ __forceinline__ void plan_scan(const Mx4Plan& p, const PlanShared& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool mine_too = tid < kPlanThreads;
@@ -30,7 +33,7 @@ __device__ __forceinline__ void plan_scan(const Mx4Plan& p, const PlanShared& s)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int e = tid * 4 + i;
-        if (e <= p.E) run = max(run, min(max(__ldg(p.offs + e), 0), p.R));
+        if (e <= p.E) run = max(run, min(max(__ldcg(p.offs + e), 0), p.R));
         top[i] = run;
     }
     int inc = run;
@@ -45,7 +48,7 @@ __device__ __forceinline__ void plan_scan(const Mx4Plan& p, const PlanShared& s)
     for (int i = 0; i < 4; ++i)
         if (mine_too && tid * 4 + i <= p.E) s.first[tid * 4 + i] = max(before, top[i]);
     if (tid == kPlanThreads - 1 && p.E == MOEQ_MAX_EXPERTS)
-        s.first[p.E] = max(max(before, run), min(max(__ldg(p.offs + p.E), 0), p.R));
+        s.first[p.E] = max(max(before, run), min(max(__ldcg(p.offs + p.E), 0), p.R));
     __syncthreads();
     int sum = 0, mine[4];
 #pragma unroll

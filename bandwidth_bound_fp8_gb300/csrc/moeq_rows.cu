@@ -23,7 +23,7 @@ struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
     uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p, int, int) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int, int) { a = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void store(__nv_bfloat16* p, int, int) const { *reinterpret_cast<uint4*>(p) = a; }
     __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -48,8 +48,8 @@ template <>
 struct Raw8<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float* p, int, int) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ __forceinline__ void store(float* p, int, int) const {
         reinterpret_cast<float4*>(p)[0] = a;
@@ -77,7 +77,7 @@ struct RawS {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (i * step < left)
-                a[i] = __ldg(p + i * step);
+                a[i] = p[i * step];
             else
                 st1(&a[i], 0.f);
     }
@@ -147,7 +147,7 @@ __device__ __forceinline__ void clear_key(uint32_t* key, int i, bool me) {
 // takes the largest key and the lowest id that holds it (two warp
 // reductions), and lane j keeps round j's pick for the softmax.
 template <int NPER>
-__global__ void __launch_bounds__(128) route_rows_kernel(const float* __restrict__ logits, int64_t ld, int T, int E,
+__global__ void __launch_bounds__(128) route_rows_kernel(const float* logits, int64_t ld, int T, int E,
                                                          int k, int32_t* __restrict__ id, float* __restrict__ w) {
     chain();
     const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(128) route_rows_kernel(const float* __restrict
 #pragma unroll
     for (int i = 0; i < NPER; ++i) {
         const int e = lane + 32 * i;
-        key[i] = e < E ? logit_key(__ldg(row + e)) : 0u;
+        key[i] = e < E ? logit_key(row[e]) : 0u;
     }
     int my_id = -1;
     float my_v = 0.f;
@@ -192,9 +192,9 @@ __global__ void __launch_bounds__(128) route_rows_kernel(const float* __restrict
 
 // dl[id_j] = w_j (dw_j - sum_i w_i dw_i), zero elsewhere.  One warp a row:
 // zeros first, then the picks (ordered by the warp barrier).
-__global__ void __launch_bounds__(128) route_rows_grad_kernel(const float* __restrict__ dw,
-                                                              const int32_t* __restrict__ id,
-                                                              const float* __restrict__ w, int T, int E, int k,
+__global__ void __launch_bounds__(128) route_rows_grad_kernel(const float* dw,
+                                                              const int32_t* id,
+                                                              const float* w, int T, int E, int k,
                                                               float* __restrict__ dl, int64_t ld, int vec) {
     chain();
     const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -253,12 +253,12 @@ constexpr int kSortBlocks = 128, kSortCounts = 32768;
 constexpr int kSortOne = 4096;
 static_assert(kSortChunk >= 2 * MOEQ_MAX_EXPERTS, "the chunks' counts fit in row_pair");
 
-__device__ __forceinline__ void load_ids(const int32_t* __restrict__ id, int64_t b, int64_t end, int E, int lane,
+__device__ __forceinline__ void load_ids(const int32_t* id, int64_t b, int64_t end, int E, int lane,
                                          int (&e)[kSortBatch]) {
 #pragma unroll
     for (int i = 0; i < kSortBatch; ++i) {
         const int64_t p = b + i * 32 + lane;
-        e[i] = p < end ? __ldg(id + p) : -1;
+        e[i] = p < end ? id[p] : -1;
     }
 #pragma unroll
     for (int i = 0; i < kSortBatch; ++i)
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(const SortArgs 
     }
     __syncthreads();
     for (int64_t p = p0 + lane; p < p1; p += 32) {
-        const int x = __ldg(a.id + p);
+        const int x = a.id[p];
         if (x < 0 || x >= E) continue;
         const int row = a.pair_row[p] + mine[x] + (kOne ? first[x] : 0);
         a.pair_row[p] = row;
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_rows_kernel(const SortArgs 
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int g = g0 + i * subs;
-                c[i] = g < blocks ? __ldcg(a.row_pair + static_cast<int64_t>(g) * E + e) : 0;
+                c[i] = g < blocks ? a.row_pair[static_cast<int64_t>(g) * E + e] : 0;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_rows_kernel(const SortArgs 
     const int64_t chunk = static_cast<int64_t>(a.warps) * a.run, p0 = blockIdx.x * chunk;
     const int64_t p1 = min(p0 + chunk, static_cast<int64_t>(a.P));
     for (int64_t p = p0 + tid; p < p1; p += kSortThreads) {
-        const int x = __ldg(a.id + p);
+        const int x = a.id[p];
         if (x >= 0 && x < E) a.pair_row[p] += first[x];
     }
 }
@@ -421,9 +421,9 @@ __global__ void __launch_bounds__(256) sort_pairs_kernel(const SortArgs a) {
     chain();
     const int64_t p = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (p >= a.P) return;
-    const int row = __ldcg(a.pair_row + p);
+    const int row = a.pair_row[p], kept = a.offs[a.E];
     if (row >= 0) a.row_pair[row] = static_cast<int32_t>(p);
-    if (p >= __ldcg(a.offs + a.E)) a.row_pair[p] = -1;
+    if (p >= kept) a.row_pair[p] = -1;
 }
 
 // ------------------------------------------------------------------ gather
@@ -431,22 +431,22 @@ __global__ void __launch_bounds__(256) sort_pairs_kernel(const SortArgs a) {
 // and written to its rows (reading row-major would read it top_k times).
 // The rows from offs[E] on are zeroed, shared out over the tokens' blocks.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ x, int64_t ld_x, int H, int k,
-                                                          const int32_t* __restrict__ offs, int E, int64_t R,
-                                                          const int32_t* __restrict__ pair_row, T* __restrict__ xs,
+__global__ void __launch_bounds__(256) gather_rows_kernel(const T* x, int64_t ld_x, int H, int k,
+                                                          const int32_t* offs, int E, int64_t R,
+                                                          const int32_t* pair_row, T* __restrict__ xs,
                                                           int64_t ld_xs) {
     chain();
     const int c = first_col<V>(blockIdx.y), left = H - c, step = blockDim.x;
     if (left <= 0) return;
     const int64_t t = blockIdx.x;
-    const int kept = max(__ldg(offs + E), 0);
+    const int kept = max(offs[E], 0);
     Raw<T, V> v;
     v.load(x + t * ld_x + c, left, step);
     const int32_t* pr = pair_row + t * k;
     for (int j0 = 0; j0 < k; j0 += 8) {
         int r[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = j0 + j < k ? __ldg(pr + j0 + j) : -1;
+        for (int j = 0; j < 8; ++j) r[j] = j0 + j < k ? pr[j0 + j] : -1;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (r[j] >= 0 && r[j] < R) v.store(xs + r[j] * ld_xs + c, left, step);
@@ -460,9 +460,9 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ 
 // (the base first), rounded once.  Each thread holds the loads of up to
 // eight rows in flight; slots without a row add nothing.
 template <typename TY, typename TO, int V, bool kWeighted>
-__global__ void __launch_bounds__(256) combine_rows_kernel(const TY* __restrict__ y, int64_t ld_y, int H, int k,
-                                                           int64_t R, const int32_t* __restrict__ pair_row,
-                                                           const float* __restrict__ w, const TO* __restrict__ base,
+__global__ void __launch_bounds__(256) combine_rows_kernel(const TY* y, int64_t ld_y, int H, int k,
+                                                           int64_t R, const int32_t* pair_row,
+                                                           const float* w, const TO* base,
                                                            int64_t ld_base, TO* __restrict__ out, int64_t ld_out) {
     chain();
     const int c = first_col<V>(blockIdx.y), left = H - c, step = blockDim.x;
@@ -485,10 +485,10 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const TY* __restrict_
             ww[j] = 0.f;
             v[j].zero();
             if (j0 + j < k) {
-                const int r = __ldg(pr + j0 + j);
+                const int r = pr[j0 + j];
                 if (r >= 0 && r < R) {
                     v[j].load(y + r * ld_y + c, left, step);
-                    ww[j] = kWeighted ? __ldg(w + t * k + j0 + j) : 1.f;
+                    ww[j] = kWeighted ? w[t * k + j0 + j] : 1.f;
                 }
             }
         }
@@ -512,12 +512,12 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const TY* __restrict_
 // offs[E] on are zeroed, shared out over the blocks.
 template <typename TY, typename TO, int V, int KM>
 __global__ void __launch_bounds__(256) combine_rows_grad_kernel(
-    const TO* __restrict__ dout, int64_t ld_do, const TY* __restrict__ y, int64_t ld_y, int H, int k,
-    const int32_t* __restrict__ offs, int E, int64_t R, const int32_t* __restrict__ pair_row,
-    const float* __restrict__ w, TY* __restrict__ dy, int64_t ld_dy, float* __restrict__ dw) {
+    const TO* dout, int64_t ld_do, const TY* y, int64_t ld_y, int H, int k,
+    const int32_t* offs, int E, int64_t R, const int32_t* pair_row,
+    const float* w, TY* __restrict__ dy, int64_t ld_dy, float* __restrict__ dw) {
     chain();
     const int tid = threadIdx.x, step = blockDim.x;
-    const int kept = max(__ldg(offs + E), 0);
+    const int kept = max(offs[E], 0);
     __shared__ float red[8][KM];
     const int64_t t = blockIdx.x;
     int row[KM];
@@ -527,10 +527,10 @@ __global__ void __launch_bounds__(256) combine_rows_grad_kernel(
         row[j] = -1;
         ww[j] = dot[j] = 0.f;
         if (j < k) {
-            const int r = __ldg(pair_row + t * k + j);
+            const int r = pair_row[t * k + j];
             if (r >= 0 && r < R) {
                 row[j] = r;
-                ww[j] = __ldg(w + t * k + j);
+                ww[j] = w[t * k + j];
             }
         }
     }

@@ -26,6 +26,12 @@ struct SmemOnce {
 // chain(), which waits for everything ahead before any access to memory and
 // only then lets the next such launch be scheduled: the order of a stream,
 // without the launch latency between its kernels.
+//
+// Such a kernel is resident while its inputs are still being written, so it
+// reads them with plain loads.  A non-coherent one (__ldg, or what the
+// compiler makes of a load through a `const T* __restrict__` parameter) is
+// for memory that nobody writes while the kernel runs, and the compiler may
+// move it ahead of chain().
 template <typename... P, typename... A>
 cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A&&... args) {
     cudaLaunchAttribute at[1];

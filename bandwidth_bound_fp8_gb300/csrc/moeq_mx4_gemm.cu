@@ -41,6 +41,8 @@ constexpr int kMaxStages = 7;
 // 867 us in pairs, 953 without; 64 experts of about 50 to 200 rows (K 2048,
 // N 2816): equal within 2 %.
 constexpr int kPairRows = 200, kPairTileRows = 224;
+// Most rows of one CTA's tile.
+constexpr int kSingleTileRows = (kPairRows + 14) / 16 * 16;
 // Units are cut in kCut parts where that many of them have a worker each and K
 // is long enough for the join to pay: a part saves about 0.2 us for every K
 // block, the join costs 2 us and 1.6 us for every 16 rows of the tile.
@@ -55,6 +57,9 @@ __host__ __device__ constexpr bool cut_pays(int units, int kb, int nt, int worke
 // TMEM columns: accumulators at 0 and 256, the tokens' scales in between and
 // the weights' behind.
 constexpr int kTmemCols = 512, kAcc1 = 256, kColSfb = 240, kColSfa = 496;
+static_assert(kSingleTileRows == 208 && kSingleTileRows <= kColSfb && kPairTileRows <= kColSfb &&
+                  kAcc1 + kPairTileRows <= kColSfa && kAcc1 + kSingleTileRows <= kColSfa,
+              "accumulators end before the scales");
 
 __host__ __device__ constexpr int stage_bytes_of(int nt, bool pair) {
     return (kMx4TileBytes + nt / (pair ? 2 : 1) * 128 + kMx4TileScaleBytes + mx4_tile_scale_bytes(nt) + 1023) / 1024 * 1024;
@@ -710,7 +715,7 @@ __global__ void __maxnreg__(160)
 Mx4Tiling mx4_tiling(int R, int E) {
     const long long want = E == 1 ? R : 2LL * R / E + 16;
     const bool pair = want >= kPairRows && R >= kPairRows;
-    const int align = pair ? 32 : 16, most = pair ? kPairTileRows : kMx4MaxTileRows;
+    const int align = pair ? 32 : 16, most = pair ? kPairTileRows : kSingleTileRows;
     auto up = [&](long long x) { return static_cast<int>(x > most ? most : (x + align - 1) / align * align); };
     return {up(want < R ? want : R), align};
 }

@@ -110,7 +110,6 @@ cudaError_t launch_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, 
 // is nt rows of 128 bytes at ((g * KB + kb) * nt) * 128 (chunks rotated as in
 // a weight tile), its scales mx4_tile_scale_bytes(nt) at (g * KB + kb) times
 // that (a weight tile's order, one more 512 bytes for rows 128..).
-constexpr int kMx4MaxTileRows = 240;
 constexpr int kMx4Tickets = 1024;  // units that are cut (a quarter of the SMs at most)
 __host__ __device__ constexpr int mx4_tile_scale_bytes(int nt) { return nt > 128 ? 2048 : 1024; }
 // Most rows of one token tile for R rows over E experts, and what tiles' rows

@@ -295,8 +295,8 @@ class Mx4MoeLayer:
         for name in self._VIEWS:
             self.__dict__.pop(name, None)
         # Fewer tokens, in narrower tiles, may need a little more workspace
-        # than T; a tile's rows more than T need (240) cover them.
-        self._kept = _Buffers(self, T, max(ws_bytes, self._ws_bytes(T), self._ws_bytes(T + 240 // self.top_k + 1)))
+        # than T; what a tile's rows (224) more need covers them.
+        self._kept = _Buffers(self, T, max(ws_bytes, self._ws_bytes(T), self._ws_bytes(T + 224 // self.top_k + 1)))
 
     def _buffers(self, T: int) -> None:
         capturing = torch.cuda.is_current_stream_capturing()

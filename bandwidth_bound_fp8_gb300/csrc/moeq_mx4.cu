@@ -460,10 +460,15 @@ __global__ void __launch_bounds__(kPlanThreads) code_tiles_kernel(const uint8_t*
 
 // The product's CTAs start while the tiles are filled, so an SM that fills
 // them keeps its shared memory as the product wants it (an SM changes the
-// split with L1 only when it is empty: 48 of 152 CTAs started 2 us late).
+// split with L1 only when it is empty: 48 of 152 CTAs started 2 us late).  A
+// preference: a failure costs time, not the product.
 template <typename K>
-cudaError_t beside_product(K kernel) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+void beside_product(OncePerDevice& once, K kernel) {
+    int dev = 0;
+    const auto set = [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    };
+    if (cudaGetDevice(&dev) != cudaSuccess || once.on(dev, set) != cudaSuccess) cudaGetLastError();
 }
 
 bool fits(const void* p, int64_t ld, int f32) {
@@ -527,10 +532,10 @@ cudaError_t launch_mx4_act_tiles(const Mx4Source& src, const Mx4Plan& plan, int 
     const int most = sms * 4;
     if (src.codes) {
         const int blocks = (plan.R + 7) / 8;
-        static const cudaError_t e = beside_product(code_tiles_kernel);
-        return e != cudaSuccess ? e
-                                : launch_chained(code_tiles_kernel, blocks < most ? blocks : most, kPlanThreads, 0, stream,
-                                                 src.codes, src.scales, plan, K, tiles, stiles);
+        static OncePerDevice once;
+        beside_product(once, code_tiles_kernel);
+        return launch_chained(code_tiles_kernel, blocks < most ? blocks : most, kPlanThreads, 0, stream, src.codes,
+                              src.scales, plan, K, tiles, stiles);
     }
     // a warp a row where that fills the wave, else up to eight (a power of two: it divides a block's warps)
     const int segs = segments(K, segment_blocks(src.x.f32, src.act));
@@ -539,20 +544,11 @@ cudaError_t launch_mx4_act_tiles(const Mx4Source& src, const Mx4Plan& plan, int 
     const int64_t want = (static_cast<int64_t>(plan.R) * parts + 7) / 8;
     const unsigned grid = static_cast<unsigned>(want < most ? want : most);
     const bool vec = fits(src.x.p, src.x.ld, src.x.f32);
+    static OncePerDevice once[2][2][2];
     auto go = [&](auto kern) {
+        beside_product(once[src.x.f32 != 0][vec][src.act != 0], kern);
         return launch_chained(kern, grid, kPlanThreads, 0, stream, src.x, plan, K, parts, tiles, stiles);
     };
-    static const cudaError_t e = [] {
-        for (auto k : {act_tiles_kernel<false, false, false>, act_tiles_kernel<false, true, false>,
-                       act_tiles_kernel<false, false, true>, act_tiles_kernel<false, true, true>,
-                       act_tiles_kernel<true, false, false>, act_tiles_kernel<true, true, false>,
-                       act_tiles_kernel<true, false, true>, act_tiles_kernel<true, true, true>}) {
-            const cudaError_t r = beside_product(k);
-            if (r != cudaSuccess) return r;
-        }
-        return cudaSuccess;
-    }();
-    if (e != cudaSuccess) return e;
     if (src.x.f32) {
         if (src.act) return vec ? go(act_tiles_kernel<true, true, true>) : go(act_tiles_kernel<true, false, true>);
         return vec ? go(act_tiles_kernel<true, true, false>) : go(act_tiles_kernel<true, false, false>);

@@ -754,8 +754,8 @@ template <bool kF32, bool kPair>
 cudaError_t launch_one(const Mx4GemmArgs& a, const typename MapsOf<kPair>::type& maps, int grid, int smem, int most_smem,
                        bool pdl, cudaStream_t stream) {
     const auto kern = mx4_gemm_kernel<kF32, kPair>;
-    static SmemOnce once;
-    const cudaError_t e = once.raise(reinterpret_cast<const void*>(kern), most_smem);
+    static OncePerDevice once;
+    const cudaError_t e = raise_smem(once, reinterpret_cast<const void*>(kern), most_smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);

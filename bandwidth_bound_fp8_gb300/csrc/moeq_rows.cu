@@ -598,16 +598,11 @@ cudaError_t by_type(int f32, F f) {
 
 }  // namespace
 
-cudaError_t SmemOnce::raise(const void* kernel, int bytes) {
+cudaError_t raise_smem(OncePerDevice& once, const void* kernel, int bytes) {
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const bool known = dev < 128;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (known && (done[dev >> 6].load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && known) done[dev >> 6].fetch_or(bit, std::memory_order_release);
-    return e;
+    return once.on(dev, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
 }
 
 cudaError_t launch_route_rows(const float* logits, int64_t ld, int T, int E, int k, int32_t* id, float* w,
@@ -633,9 +628,9 @@ cudaError_t launch_expert_sort(const int32_t* id, int T, int k, int E, int32_t* 
     a.run = (chunk + a.warps - 1) / a.warps;
     while ((1 << a.bits) < E) ++a.bits;
     const auto rank = blocks == 1 ? sort_rank_kernel<true> : sort_rank_kernel<false>;
-    static SmemOnce once[2];
-    cudaError_t e = once[blocks == 1].raise(reinterpret_cast<const void*>(rank),
-                                            (kSortWarps + 1) * MOEQ_MAX_EXPERTS * static_cast<int>(sizeof(int)));
+    static OncePerDevice once[2];
+    cudaError_t e = raise_smem(once[blocks == 1], reinterpret_cast<const void*>(rank),
+                               (kSortWarps + 1) * MOEQ_MAX_EXPERTS * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
     e = launch_chained(rank, blocks, kSortThreads, (a.warps + 1) * E * sizeof(int), stream, a);
     if (e != cudaSuccess || blocks == 1) return e;

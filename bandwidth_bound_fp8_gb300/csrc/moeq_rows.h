@@ -7,19 +7,15 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "../../include/moeq.h"
+#include "moeq_once.h"
 
 namespace moeq {
 
 // Raises a kernel's dynamic shared memory limit to `bytes` on the current
-// device, once a device and kernel (`done`: the kernel's own static, zero).
-// The call costs about a microsecond, a small launch's half.
-struct SmemOnce {
-    std::atomic<uint64_t> done[2]{};  // devices 0 .. 127
-    cudaError_t raise(const void* kernel, int bytes);
-};
+// device (`once`: the kernel's own static).  The call costs about a
+// microsecond, a small launch's half.
+cudaError_t raise_smem(OncePerDevice& once, const void* kernel, int bytes);
 
 // A launch that may be scheduled while the kernel ahead on the stream still
 // runs (programmatic dependent launch).  Kernels launched so begin with

@@ -62,6 +62,7 @@ class moeq_route_plan(ctypes.Structure):
 
 
 _lib = None
+_many_gpus = False   # this process sees more than one: a CUDA tensor may lie on another
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
@@ -70,7 +71,7 @@ _ll = ctypes.c_int64
 
 def load(path: str = LIB_PATH):
     """Load libmoeq.so (raises if it is not built)."""
-    global _lib
+    global _lib, _many_gpus
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -136,6 +137,7 @@ def load(path: str = LIB_PATH):
         f = getattr(L, name)
         f.restype = res
         f.argtypes = args
+    _many_gpus = torch.cuda.device_count() > 1
     _lib = L
     return L
 
@@ -178,12 +180,14 @@ def current_stream_handle() -> int:
     return _stream(None)
 
 
+_DTYPES = {torch.bfloat16: MOEQ_BF16, torch.float32: MOEQ_F32}
+
+
 def _dtype(t) -> int:
-    if t.dtype == torch.bfloat16:
-        return MOEQ_BF16
-    if t.dtype == torch.float32:
-        return MOEQ_F32
-    raise TypeError(f"unsupported activation dtype {t.dtype}")
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"unsupported activation dtype {t.dtype}")
+    return d
 
 
 # ----------------------------------------------------------------- sizes
@@ -415,8 +419,27 @@ def moeq_gemm_ws_count_offset(rows_out, K, rows_in, max_uniq, is_gate_up, which)
 
 
 # ------------------------------------------------- any number of tokens
+# The kernels follow pointers: a tensor elsewhere than on the current device
+# would be a fault of the GPU.  (These checks and the launch are most of a
+# small call's time.)
+def _elsewhere(t, name: str):
+    raise ValueError(f"{name}: a tensor on the current CUDA device is wanted, got one on {t.device}")
+
+
+_device = _raw_device if _raw_device is not None else torch.cuda.current_device
+
+
+def _queue(stream):
+    """The stream's handle; tensors checked by now lie on the current device, so CUDA is initialised."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(_device())
+    return _stream(stream)
+
+
 def _ld(t, name: str = "matrix") -> int:
-    """Leading dimension, in elements, of a 2-D tensor whose rows are contiguous."""
+    """Leading dimension, in elements, of a 2-D tensor on the device whose rows are contiguous."""
+    if not t.is_cuda or _many_gpus and t.get_device() != _device():
+        _elsewhere(t, name)
     sh, st = t.shape, t.stride()
     if len(sh) != 2 or (st[1] != 1 and sh[1] > 1):
         raise ValueError(f"{name}: a 2-D tensor with contiguous rows is wanted, got shape {tuple(sh)}, strides {st}")
@@ -424,7 +447,9 @@ def _ld(t, name: str = "matrix") -> int:
 
 
 def _packed(t, dtype, shape, name: str):
-    """A contiguous tensor of this dtype and shape, or an error that says which is not."""
+    """The address of a contiguous tensor of this dtype and shape, or an error that says which is not."""
+    if not t.is_cuda or _many_gpus and t.get_device() != _device():
+        _elsewhere(t, name)
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} is wanted, got {t.dtype} "
                          f"{tuple(t.shape)}, strides {t.stride()}")
@@ -438,9 +463,9 @@ def moeq_route_rows(logits, topk_id, topk_w, stream=None) -> None:
     k = topk_id.shape[1]
     if logits.dtype is not torch.float32:
         raise TypeError(f"unsupported logits dtype {logits.dtype}")
-    _check("moeq_route_rows", load().moeq_route_rows(
+    _check("moeq_route_rows", (_lib or load()).moeq_route_rows(
         logits.data_ptr(), _ld(logits, "logits"), T, E, k, _packed(topk_id, torch.int32, (T, k), "topk_id"),
-        _packed(topk_w, torch.float32, (T, k), "topk_w"), _stream(stream)))
+        _packed(topk_w, torch.float32, (T, k), "topk_w"), _queue(stream)))
 
 
 def moeq_route_rows_grad(d_topk_w, topk_id, topk_w, d_logits, stream=None) -> None:
@@ -448,20 +473,20 @@ def moeq_route_rows_grad(d_topk_w, topk_id, topk_w, d_logits, stream=None) -> No
     k = topk_id.shape[1]
     if d_logits.dtype is not torch.float32:
         raise TypeError(f"unsupported d_logits dtype {d_logits.dtype}")
-    _check("moeq_route_rows_grad", load().moeq_route_rows_grad(
+    _check("moeq_route_rows_grad", (_lib or load()).moeq_route_rows_grad(
         _packed(d_topk_w, torch.float32, (T, k), "d_topk_w"), _packed(topk_id, torch.int32, (T, k), "topk_id"),
         _packed(topk_w, torch.float32, (T, k), "topk_w"), T, E, k, d_logits.data_ptr(), _ld(d_logits, "d_logits"),
-        _stream(stream)))
+        _queue(stream)))
 
 
 def moeq_expert_sort(topk_id, E, offs, pair_row, row_pair, stream=None) -> None:
     """Stable sort of the (token, slot) pairs of topk_id [T, k] by expert:
     offs [E + 1], pair_row [T, k], row_pair [T * k], all int32."""
     T, k = topk_id.shape
-    _check("moeq_expert_sort", load().moeq_expert_sort(
+    _check("moeq_expert_sort", (_lib or load()).moeq_expert_sort(
         _packed(topk_id, torch.int32, (T, k), "topk_id"), T, k, E, _packed(offs, torch.int32, (E + 1,), "offs"),
         _packed(pair_row, torch.int32, (T, k), "pair_row"), _packed(row_pair, torch.int32, (T * k,), "row_pair"),
-        _stream(stream)))
+        _queue(stream)))
 
 
 def _pairs(pair_row):
@@ -481,8 +506,8 @@ def moeq_gather_rows(x, offs, pair_row, xs, stream=None) -> None:
     if x.shape != (T, H) or xs.shape != (T * k, H) or x.dtype is not xs.dtype:
         raise ValueError(f"x [{T}, H] and xs [{T * k}, H] of one type are wanted, got {tuple(x.shape)} and "
                          f"{tuple(xs.shape)}")
-    _check("moeq_gather_rows", load().moeq_gather_rows(
-        x.data_ptr(), _dtype(x), _ld(x, "x"), T, H, k, of, E, pr, xs.data_ptr(), _ld(xs, "xs"), _stream(stream)))
+    _check("moeq_gather_rows", (_lib or load()).moeq_gather_rows(
+        x.data_ptr(), _dtype(x), _ld(x, "x"), T, H, k, of, E, pr, xs.data_ptr(), _ld(xs, "xs"), _queue(stream)))
 
 
 def moeq_gather_rows_grad(d_xs, pair_row, d_x, stream=None) -> None:
@@ -492,9 +517,9 @@ def moeq_gather_rows_grad(d_xs, pair_row, d_x, stream=None) -> None:
     if d_x.shape != (T, H) or d_xs.shape != (T * k, H) or d_x.dtype is not d_xs.dtype:
         raise ValueError(f"d_x [{T}, H] and d_xs [{T * k}, H] of one type are wanted, got {tuple(d_x.shape)} and "
                          f"{tuple(d_xs.shape)}")
-    _check("moeq_gather_rows_grad", load().moeq_gather_rows_grad(
+    _check("moeq_gather_rows_grad", (_lib or load()).moeq_gather_rows_grad(
         d_xs.data_ptr(), _dtype(d_xs), _ld(d_xs, "d_xs"), T, H, k, pr, d_x.data_ptr(), _ld(d_x, "d_x"),
-        _stream(stream)))
+        _queue(stream)))
 
 
 def moeq_combine_rows(y, pair_row, topk_w, out, base=None, stream=None) -> None:
@@ -505,9 +530,9 @@ def moeq_combine_rows(y, pair_row, topk_w, out, base=None, stream=None) -> None:
         raise ValueError(f"out [{T}, H] and y [{T * k}, H] are wanted, got {tuple(out.shape)} and {tuple(y.shape)}")
     if base is not None and (base.shape != (T, H) or base.dtype is not out.dtype):
         raise ValueError("base: out's shape and type are wanted")
-    _check("moeq_combine_rows", load().moeq_combine_rows(
+    _check("moeq_combine_rows", (_lib or load()).moeq_combine_rows(
         y.data_ptr(), _dtype(y), _ld(y, "y"), T, H, k, pr, _packed(topk_w, torch.float32, (T, k), "topk_w"), _p(base),
-        _ld(base, "base") if base is not None else 0, out.data_ptr(), _dtype(out), _ld(out, "out"), _stream(stream)))
+        _ld(base, "base") if base is not None else 0, out.data_ptr(), _dtype(out), _ld(out, "out"), _queue(stream)))
 
 
 def moeq_combine_rows_grad(d_out, y, offs, pair_row, topk_w, d_y, d_topk_w, stream=None) -> None:
@@ -519,10 +544,10 @@ def moeq_combine_rows_grad(d_out, y, offs, pair_row, topk_w, d_y, d_topk_w, stre
     if d_out.shape != (T, H) or y.shape != (T * k, H) or d_y.shape != (T * k, H) or d_y.dtype is not y.dtype:
         raise ValueError(f"d_out [{T}, H], y and d_y [{T * k}, H] are wanted, got {tuple(d_out.shape)}, "
                          f"{tuple(y.shape)} and {tuple(d_y.shape)}")
-    _check("moeq_combine_rows_grad", load().moeq_combine_rows_grad(
+    _check("moeq_combine_rows_grad", (_lib or load()).moeq_combine_rows_grad(
         d_out.data_ptr(), _dtype(d_out), _ld(d_out, "d_out"), y.data_ptr(), _dtype(y), _ld(y, "y"), T, H, k, of, E, pr,
         _packed(topk_w, torch.float32, (T, k), "topk_w"), d_y.data_ptr(), _ld(d_y, "d_y"),
-        _packed(d_topk_w, torch.float32, (T, k), "d_topk_w"), _stream(stream)))
+        _packed(d_topk_w, torch.float32, (T, k), "d_topk_w"), _queue(stream)))
 
 
 def moeq_mx4_scale_pitch(K) -> int:
@@ -550,17 +575,17 @@ def moeq_mx4_quant_act(x, codes, scales, act=MOEQ_ACT_NONE, stream=None) -> None
     """x [rows, K] ([rows, 2K] with MOEQ_ACT_SWIGLU) -> codes [rows, K/2],
     scales [rows, moeq_mx4_scale_pitch(K)], uint8."""
     rows, K = x.shape[0], x.shape[1] // (2 if act == MOEQ_ACT_SWIGLU else 1)
-    _check("moeq_mx4_quant_act", load().moeq_mx4_quant_act(
+    _check("moeq_mx4_quant_act", (_lib or load()).moeq_mx4_quant_act(
         x.data_ptr(), _dtype(x), _ld(x, "x"), rows, K, act, _packed(codes, torch.uint8, (rows, K // 2), "codes"),
-        _packed(scales, torch.uint8, (rows, _pitch(K)), "scales"), _stream(stream)))
+        _packed(scales, torch.uint8, (rows, _pitch(K)), "scales"), _queue(stream)))
 
 
 def moeq_mx4_dequant_act(codes, scales, out, stream=None) -> None:
     rows, K = out.shape
-    _check("moeq_mx4_dequant_act", load().moeq_mx4_dequant_act(
+    _check("moeq_mx4_dequant_act", (_lib or load()).moeq_mx4_dequant_act(
         _packed(codes, torch.uint8, (rows, K // 2), "codes"),
         _packed(scales, torch.uint8, (rows, _pitch(K)), "scales"), rows, K, out.data_ptr(),
-        _dtype(out), _ld(out, "out"), _stream(stream)))
+        _dtype(out), _ld(out, "out"), _queue(stream)))
 
 
 # The sizes of include/moeq.h, for checks on every call (the library's own
@@ -577,18 +602,17 @@ def _tiles(tiles, scale_tiles, E, N, K):
 def moeq_mx4_quant_weight(w, tiles, scale_tiles, stream=None) -> None:
     """w [E, N, K] bf16 or fp32 -> tiles and scale tiles (mx4_weight_buffers)."""
     E, N, K = w.shape
-    if not w.is_contiguous():
-        raise ValueError("w: a contiguous tensor is wanted")
-    _check("moeq_mx4_quant_weight", load().moeq_mx4_quant_weight(
-        w.data_ptr(), _dtype(w), E, N, K, *_tiles(tiles, scale_tiles, E, N, K), _stream(stream)))
+    dt = _dtype(w)
+    _check("moeq_mx4_quant_weight", (_lib or load()).moeq_mx4_quant_weight(
+        _packed(w, w.dtype, (E, N, K), "w"), dt, E, N, K, *_tiles(tiles, scale_tiles, E, N, K), _queue(stream)))
 
 
 def moeq_mx4_pack_weight(codes, scales, tiles, scale_tiles, stream=None) -> None:
     """Row-major MXFP4 codes [E, N, K/2] and scales [E, N, K/32] -> tiles."""
     E, N, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
-    _check("moeq_mx4_pack_weight", load().moeq_mx4_pack_weight(
+    _check("moeq_mx4_pack_weight", (_lib or load()).moeq_mx4_pack_weight(
         _packed(codes, torch.uint8, (E, N, K // 2), "codes"), _packed(scales, torch.uint8, (E, N, K // 32), "scales"),
-        E, N, K, *_tiles(tiles, scale_tiles, E, N, K), _stream(stream)))
+        E, N, K, *_tiles(tiles, scale_tiles, E, N, K), _queue(stream)))
 
 
 def moeq_mx4_expert_gemm_workspace_size(rows, K, N, E, R) -> int:
@@ -613,7 +637,7 @@ def moeq_mx4_expert_gemm(x, w, w_scales, offs, y, ws: Workspace, row_pair=None, 
             K //= 2
         dt, ld = _dtype(x), _ld(x, "x")
     tp, sp = _tiles(w, w_scales, E, N, K)
-    _check("moeq_mx4_expert_gemm", load().moeq_mx4_expert_gemm(
+    _check("moeq_mx4_expert_gemm", (_lib or load()).moeq_mx4_expert_gemm(
         x.data_ptr(), dt, ld, _p(x_scales), rows, K, act, tp, sp, N, of, E, R,
         _packed(row_pair, torch.int32, (R,), "row_pair") if row_pair is not None else None, top_k, y.data_ptr(),
-        _dtype(y), _ld(y, "y"), ws.ptr, ws.nbytes, _stream(stream)))
+        _dtype(y), _ld(y, "y"), ws.ptr, ws.nbytes, _queue(stream)))

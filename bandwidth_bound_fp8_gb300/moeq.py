@@ -571,10 +571,18 @@ def mx4_weight_buffers(E, N, K, device="cuda"):
             torch.empty(moeq_mx4_weight_scale_bytes(E, N, K), dtype=torch.uint8, device=device))
 
 
+def _half(width: int) -> int:
+    if width % 2:
+        raise ValueError(f"x: rows of gate and up are wanted, got {width} columns")
+    return width // 2
+
+
 def moeq_mx4_quant_act(x, codes, scales, act=MOEQ_ACT_NONE, stream=None) -> None:
     """x [rows, K] ([rows, 2K] with MOEQ_ACT_SWIGLU) -> codes [rows, K/2],
     scales [rows, moeq_mx4_scale_pitch(K)], uint8."""
-    rows, K = x.shape[0], x.shape[1] // (2 if act == MOEQ_ACT_SWIGLU else 1)
+    rows, K = x.shape
+    if act == MOEQ_ACT_SWIGLU:
+        K = _half(K)
     _check("moeq_mx4_quant_act", (_lib or load()).moeq_mx4_quant_act(
         x.data_ptr(), _dtype(x), _ld(x, "x"), rows, K, act, _packed(codes, torch.uint8, (rows, K // 2), "codes"),
         _packed(scales, torch.uint8, (rows, _pitch(K)), "scales"), _queue(stream)))
@@ -624,7 +632,6 @@ def moeq_mx4_expert_gemm(x, w, w_scales, offs, y, ws: Workspace, row_pair=None, 
     """y[r] = W[e(r)] . q(x[row(r)]) for rows sorted by expert (offs [E + 1]).
     x [rows, K] bf16 or fp32, or uint8 codes [rows, K/2] with x_scales; row r
     reads x[row_pair[r] // top_k], or x[r] without row_pair.  y [R, N]."""
-    E, of = _offs(offs)
     R, N = y.shape
     rows, K = x.shape
     if x_scales is not None:
@@ -634,8 +641,9 @@ def moeq_mx4_expert_gemm(x, w, w_scales, offs, y, ws: Workspace, row_pair=None, 
         _packed(x_scales, torch.uint8, (rows, _pitch(K)), "x_scales")
     else:
         if act == MOEQ_ACT_SWIGLU:
-            K //= 2
+            K = _half(K)
         dt, ld = _dtype(x), _ld(x, "x")
+    E, of = _offs(offs)
     tp, sp = _tiles(w, w_scales, E, N, K)
     _check("moeq_mx4_expert_gemm", (_lib or load()).moeq_mx4_expert_gemm(
         x.data_ptr(), dt, ld, _p(x_scales), rows, K, act, tp, sp, N, of, E, R,

@@ -44,3 +44,13 @@ def test_tensors_elsewhere_are_refused(name, dev):
     MoeqError after the pointer checks.)"""
     with pytest.raises(ValueError, match="on the current CUDA device"):
         _calls(dev)[name]()
+
+
+def test_swiglu_rows_have_two_halves():
+    """65 columns were read as a gate of 32 and an up of 32."""
+    z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt)
+    with pytest.raises(ValueError, match="gate and up"):
+        moeq.moeq_mx4_quant_act(z(4, 65), z(4, 16, dt=U8), z(4, 8, dt=U8), act=moeq.MOEQ_ACT_SWIGLU, stream=0)
+    with pytest.raises(ValueError, match="gate and up"):
+        moeq.moeq_mx4_expert_gemm(z(4, 65), z(16384, dt=U8), z(1024, dt=U8), z(2, dt=I32), z(4, 16),
+                                  type("Ws", (), dict(ptr=0, nbytes=0))(), act=moeq.MOEQ_ACT_SWIGLU, stream=0)

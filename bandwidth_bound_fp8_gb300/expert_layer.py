@@ -161,19 +161,25 @@ class _CombineGrad(torch.autograd.Function):
         return d_dout, dy, dw, None, None
 
 
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy where its rows are not contiguous or lie over each other (a transpose, an expanded bias)."""
+    fits = t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1) and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1)
+    return t if fits else t.contiguous()
+
+
 def route(logits: torch.Tensor, k: int):
     """topk_id [T, k] int32 and topk_w [T, k] fp32 of logits [T, E] fp32; the weights carry the gradient."""
-    return _Route.apply(logits, k)
+    return _Route.apply(_rows(logits), k)
 
 
 def dispatch(x: torch.Tensor, d: Dispatch) -> torch.Tensor:
     """Rows of x [T, H] in expert order: [T * k, H], zero rows after the last."""
-    return _Dispatch.apply(x, d.offs, d.pair_row)
+    return _Dispatch.apply(_rows(x), d.offs, d.pair_row)
 
 
 def combine(y: torch.Tensor, w: torch.Tensor, d: Dispatch, base: torch.Tensor | None = None) -> torch.Tensor:
     """base[t] + sum_j w[t, j] * y[row of (t, j)]."""
-    return _Combine.apply(y.contiguous(), w.contiguous(), base, d.offs, d.pair_row)
+    return _Combine.apply(y.contiguous(), w.contiguous(), None if base is None else _rows(base), d.offs, d.pair_row)
 
 
 # ------------------------------------------------------------------- serving

@@ -6,7 +6,15 @@ from __future__ import annotations
 import torch
 
 
+def _matrix(*tensors):
+    """The rows that the binding accepts."""
+    for t in tensors:
+        if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"shape {tuple(t.shape)}, strides {t.stride()}")
+
+
 def route_rows(logits, ids, w, stream=None):
+    _matrix(logits)
     k = ids.shape[1]
     v, i = torch.sort(logits.data, dim=1, descending=True, stable=True)
     v, i = v[:, :k], i[:, :k]
@@ -48,19 +56,23 @@ def _scatter(out, pair_row, rows):
 
 
 def gather_rows(x, offs, pair_row, xs, stream=None):
+    _matrix(x, xs)
     _scatter(xs, pair_row, x.data.unsqueeze(1).expand(-1, pair_row.shape[1], -1))
 
 
 def gather_rows_grad(dxs, pair_row, dx, stream=None):
+    _matrix(dxs, dx)
     dx.data.copy_(_rows(dxs, pair_row).sum(1))
 
 
 def combine_rows(y, pair_row, w, out, base=None, stream=None):
+    _matrix(y, out, *([] if base is None else [base]))
     v = (w.data.unsqueeze(2) * _rows(y, pair_row)).sum(1)
     out.data.copy_(v if base is None else v + base.data)
 
 
 def combine_rows_grad(dout, y, offs, pair_row, w, dy, dw, stream=None):
+    _matrix(dout, y, dy)
     _scatter(dy, pair_row, w.data.unsqueeze(2) * dout.data.unsqueeze(1))
     dw.data.copy_((_rows(y, pair_row) * dout.data.unsqueeze(1)).sum(2))
 

@@ -78,6 +78,26 @@ def test_gradient_penalty_with_a_constant_incoming_gradient(el):
         assert (a - b).abs().max() <= 1e-12 * (1 + b.abs().max())
 
 
+def test_any_strides_and_broadcast_inputs(el):
+    """Transposes, every second row or column, one row for all: values and gradients of the plain copies, each input's
+    gradient in its own shape."""
+    lg, x, b, y = (_rand(s, *shape).requires_grad_() for s, shape in
+                   ((1, (4, 6)), (2, (3, 6)), (3, (3,)), (4, (3, 18))))
+
+    def loss(view):
+        ids, w = el.route(view(lg.t()), 2)
+        d = el.Dispatch(ids, 4)
+        xs = el.dispatch(view(x.t()), d)
+        a = el.combine(view(y.t()[:12]), w, d, base=view(b.expand(6, 3)))
+        c = el.combine(xs, w, d, base=view(torch.stack([x.t()] * 2, 2)[:, :, 1]))
+        return (a * xs[:6].detach()).sum() + (c ** 2).sum() + (w ** 3).sum()
+
+    got = torch.autograd.grad(loss(lambda t: t), (lg, x, b, y))
+    want = torch.autograd.grad(loss(lambda t: t.contiguous()), (lg, x, b, y))
+    for g, r in zip(got, want):
+        assert torch.equal(g, r) and r.abs().max() > 0
+
+
 def test_an_overwritten_plan_is_noticed(el):
     d = el.Dispatch(_ids(), 3)
     x = _rand(1, 5, 3).requires_grad_()

@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(256) quant_act_kernel(const void* x, int64_t l
 
 // Codes and scales back to values.  A value is a code (at most two
 // significant bits) times a power of two: exact in bf16 and in fp32 (a
-// subnormal of at least 2^-128 fits both).  The scale is applied in two
-// halves, because 2^-127 is no normal number.
+// subnormal of at least 2^-128 fits both; past 2^128 it is an infinity).  The
+// scale is applied in two halves, because 2^-127 is no normal number.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) dequant_act_kernel(const uint8_t* codes, const uint8_t* scales, int rows, int K,
                                                           T* __restrict__ out, int64_t ld) {

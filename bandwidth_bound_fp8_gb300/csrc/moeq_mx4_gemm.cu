@@ -243,10 +243,9 @@ __device__ __forceinline__ void tmem_use16(float* v) {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// One lane of a converged warp, the same each time.  tcgen05 instructions take
-// their operands from uniform registers: under an elected predicate the
-// compiler keeps them there, under `lane == 0` it moves them over one by one
-// (a stage of 6 scale copies and 4 MMAs of N = 240: 549 cycles against 717).
+// One lane of a converged warp, the same each time.  Issued under it, a stage
+// of 6 scale copies and 4 MMAs takes 510 cycles at N = 208 by one CTA and 449
+// at N = 224 by a pair; under `lane == 0` both take 718.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(p));

@@ -145,7 +145,9 @@ __device__ __forceinline__ void clear_key(uint32_t* key, int i, bool me) {
 
 // One warp a row: lane l holds the keys of experts l, l + 32, ...; a round
 // takes the largest key and the lowest id that holds it (two warp
-// reductions), and lane j keeps round j's pick for the softmax.
+// reductions), and lane j keeps round j's pick for the softmax.  8191 rows of
+// 256 take 8.0 us for eight picks, 5.7 for four and 3.9 for one: the rounds
+// bound it, not the 1.3 us of bytes.
 template <int NPER>
 __global__ void __launch_bounds__(128) route_rows_kernel(const float* logits, int64_t ld, int T, int E,
                                                          int k, int32_t* __restrict__ id, float* __restrict__ w) {
@@ -191,7 +193,8 @@ __global__ void __launch_bounds__(128) route_rows_kernel(const float* logits, in
 }
 
 // dl[id_j] = w_j (dw_j - sum_i w_i dw_i), zero elsewhere.  One warp a row:
-// zeros first, then the picks (ordered by the warp barrier).
+// zeros first, then the picks (ordered by the warp barrier).  8191 rows of 256:
+// 2.7 us.
 __global__ void __launch_bounds__(128) route_rows_grad_kernel(const float* dw,
                                                               const int32_t* id,
                                                               const float* w, int T, int E, int k,
@@ -241,15 +244,17 @@ __global__ void __launch_bounds__(128) route_rows_grad_kernel(const float* dw,
 // CTAs that met in distributed shared memory took 19 us, 7 of them in step
 // 1's walk on 16 SMs.
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBatch = 2;
-// Pairs of a block, at least: with 2048, 262144 pairs took 18.6 us against 16.4
-// (step 2 reads twice the counts).
+// Pairs of a block, at least: with 2048, 262144 pairs over 256 experts take 15.9
+// us against 15.7 (step 2 reads twice the counts).
 constexpr int kSortChunk = 4096;
-// The most blocks, and the most counts (blocks x experts) that step 2 has every
-// block read: 262144 pairs over 1000 experts take 12.7 us in step 2 with 128
-// blocks, 7.9 with 64.
+// The most blocks: 524288 pairs over 256 experts take 21.1 us with 128, 24.6 with
+// 64 (longer runs in step 1).  The most counts (blocks x experts) that step 2
+// has every block read: 262144 pairs over 1000 experts take 20.4 us with the 32
+// blocks that this leaves and 18.3 with 64, so a higher limit is open; with 256
+// experts it does not bind.
 constexpr int kSortBlocks = 128, kSortCounts = 32768;
-// Pairs that one block sorts alone: 2400 take it 6.8 us and 8000 12.7; the
-// three steps take 10 us or more.
+// Pairs that one block sorts alone: 2400 take it 6.2 us, 4096 7.1 and 8000 12.0;
+// the three steps take 9.7 us for 4104.
 constexpr int kSortOne = 4096;
 static_assert(kSortChunk >= 2 * MOEQ_MAX_EXPERTS, "the chunks' counts fit in row_pair");
 

@@ -42,7 +42,11 @@ constexpr int64_t kMaxPairs = int64_t(1) << 30;  // T * top_k and R: row numbers
 constexpr int kMaxWidth = 1 << 20;               // H and N
 // Rows of a gathered product from which the activations are quantised once,
 // in token order, and their codes gathered; below, each row is quantised as
-// it is gathered (one launch less, top_k times the arithmetic).
+// it is gathered (one launch less, top_k times the arithmetic).  With a product
+// narrow enough to show it (N = 128, 8 experts), K = 6144 and top-8: 2048 rows
+// take 21.5 us once and 21.0 as they are gathered, 4096 rows 24.0 and 27.2,
+// 65536 rows 137 and 243; K = 2048 and top-2: 4096 rows 16.9 and 16.0, 8192
+// rows 20.5 and 22.4.
 constexpr int kQuantOnceRows = 4096;
 
 inline bool al(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }

@@ -562,7 +562,9 @@ size_t moeq_mx4_weight_scale_bytes(int E, int N, int K);
 /* gate then up, and silu(gate) * up is quantised.                          */
 moeq_status moeq_mx4_quant_act(const void* x, moeq_dtype dtype, int64_t ld, int rows, int K, moeq_act act,
                                uint8_t* codes, uint8_t* scales, void* stream);
-/* The values that codes and scales stand for (exact in both types).        */
+/* The values that codes and scales stand for: exact in both types, and an  */
+/* infinity past their largest number (scales 253 and 254, which the        */
+/* quantiser does not make).                                                */
 moeq_status moeq_mx4_dequant_act(const uint8_t* codes, const uint8_t* scales, int rows, int K,
                                  void* out, moeq_dtype dtype, int64_t ld, void* stream);
 /* w [E, N, K] -> tiles.                                                    */
@@ -583,7 +585,11 @@ moeq_status moeq_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, in
 /*   y       [R, N] bf16 or fp32; rows from offs[E] on are zeroed           */
 /*   ws      moeq_mx4_expert_gemm_workspace_size(rows, K, N, E, R) bytes,   */
 /*           zeroed once (moeq_workspace_init); the status word is as for   */
-/*           the other calls.  The size depends on the device's SM count.   */
+/*           the other calls.  The size depends on the device's SM count    */
+/*           and need not rise with R (fewer rows may take narrower tiles). */
+/*           Products may share one that is large enough for each; it is    */
+/*           not to be shared with the FP8 calls, which keep counts         */
+/*           elsewhere in theirs.                                           */
 size_t moeq_mx4_expert_gemm_workspace_size(int rows, int K, int N, int E, int R);
 moeq_status moeq_mx4_expert_gemm(const void* x, moeq_dtype x_dtype, int64_t ld_x, const uint8_t* x_scales,
                                  int rows, int K, moeq_act act,

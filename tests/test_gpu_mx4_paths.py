@@ -110,3 +110,17 @@ def test_down_product_with_swiglu(moeq, R, K, N, xt):  # noqa: F811
     moeq.moeq_mx4_expert_gemm(x, W.t, W.s, _offs(counts), y, ws, act=moeq.MOEQ_ACT_SWIGLU)
     _close(y, ref, terms, K)
     assert moeq.moeq_read_device_status(ws.t, ws.nbytes) == 0
+
+
+def test_dequant_of_the_largest_scales(moeq):  # noqa: F811
+    """Scales 2^126 and 2^127, which the quantiser does not make: values past the type's largest are infinities."""
+    scale = np.array([[253], [254]], np.uint8)
+    code = np.tile(np.arange(16, dtype=np.uint8), (2, 2))
+    q, s = torch.from_numpy(rp.pack_codes(code)).cuda(), torch.from_numpy(rp.pad_scales(scale, 8)).cuda()
+    ref = rp.mx4_values(code, scale)
+    for dt in (BF, F32):
+        v = torch.empty((2, 32), dtype=dt, device="cuda")
+        moeq.moeq_mx4_dequant_act(q, s, v)
+        with np.errstate(over="ignore"):
+            want = np.where(np.abs(ref) > np.finfo(np.float32).max, np.copysign(np.inf, ref), ref)
+        assert np.array_equal(to64(v), want)

@@ -1,7 +1,6 @@
 // C ABI entry points of the operators that take any number of tokens
 // (include/moeq.h): argument checks on the host, then the launches.
-#include <mutex>
-#include <vector>
+#include <atomic>
 
 #include "moeq_rows.h"
 
@@ -14,28 +13,28 @@ struct Device {
     int sms = 0;
 };
 
+// (No lock and no container: nothing here may throw through a C entry.)
 Device current_device() {
-    static std::mutex mu;
-    static std::vector<Device> cache;
+    static std::atomic<int> known[128];  // the SM count of a device that runs this, -1 of another; 0: not asked yet
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
         return Device{};
     }
-    std::lock_guard<std::mutex> lock(mu);
-    if (static_cast<int>(cache.size()) <= dev) cache.resize(dev + 1);
-    if (!cache[dev].sms) {
-        int major = 0, minor = 0, sms = 0;
+    const bool keep = dev >= 0 && dev < 128;
+    int sms = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (!sms) {
+        int major = 0, minor = 0;
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
             cudaGetLastError();
             return Device{};
         }
-        cache[dev].sms = sms;
-        cache[dev].ok = major == 10 && minor == 3;
+        if (major != 10 || minor != 3) sms = -1;
+        if (keep) known[dev].store(sms, std::memory_order_relaxed);
     }
-    return cache[dev];
+    return sms > 0 ? Device{true, sms} : Device{};
 }
 
 constexpr int64_t kMaxPairs = int64_t(1) << 30;  // T * top_k and R: row numbers stay in 31 bits

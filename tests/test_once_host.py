@@ -50,3 +50,10 @@ def test_no_result_of_a_cuda_call_is_kept_for_the_process():
         if f.endswith((".cu", ".cuh", ".h")):
             with open(os.path.join(CSRC, f)) as h:
                 assert not re.search(r"static\s+(const\s+)?cudaError_t\s+\w+\s*=", h.read()), f
+
+
+def test_no_exception_can_leave_the_c_entries():
+    """The C entries of the operators on any number of tokens use nothing of C++ that throws."""
+    with open(os.path.join(CSRC, "moeq_rows_api.cu")) as h:
+        src = re.sub(r"//[^\n]*", "", h.read())
+    assert not re.search(r"std::(vector|string|map|mutex|lock_guard|unique_lock|call_once|function)|\bnew\b|\bthrow\b", src)

@@ -187,9 +187,22 @@ class Mx4Weights:
     """Expert matrices w [E, N, K] (bf16 or fp32, on the device) quantised to MXFP4 tiles."""
 
     def __init__(self, w: torch.Tensor):
-        self.E, self.N, self.K = w.shape
-        self.tiles, self.scales = moeq.mx4_weight_buffers(self.E, self.N, self.K, device=w.device)
+        self._make(w.shape, w.device)
         moeq.moeq_mx4_quant_weight(w, self.tiles, self.scales)
+
+    @classmethod
+    def from_codes(cls, codes: torch.Tensor, scales: torch.Tensor) -> Mx4Weights:
+        """From row-major MXFP4 codes [E, N, K/2] and scales [E, N, K/32] (uint8), as a checkpoint holds them."""
+        self = cls.__new__(cls)
+        E, N, half = codes.shape
+        self._make((E, N, 2 * half), codes.device)
+        moeq.moeq_mx4_pack_weight(codes, scales, self.tiles, self.scales)
+        return self
+
+    def _make(self, shape, device):
+        self.E, self.N, self.K = self.shape = tuple(shape)
+        self.device = device
+        self.tiles, self.scales = moeq.mx4_weight_buffers(self.E, self.N, self.K, device=device)
 
 
 class _Serve(torch.autograd.Function):
@@ -247,7 +260,7 @@ class Mx4MoeLayer:
 
     w_gu [E, 2I, H] (gate rows, then up rows), w_d [E, H, I]; shared_gu
     [1, 2I, H] and shared_d [1, H, I], or None for a layer without a shared
-    expert.
+    expert.  Each is a tensor or Mx4Weights.
 
     Buffers are kept for the most tokens seen (``reserve`` makes them
     beforehand), and those that a CUDA graph was captured with for as long as
@@ -266,14 +279,13 @@ class Mx4MoeLayer:
             if gu is None:
                 continue
             E = w_gu.shape[0] if what == "w" else 1
-            if d.dim() != 3 or gu.shape != (E, 2 * d.shape[2], H) or d.shape != (E, H, d.shape[2]):
+            if len(d.shape) != 3 or gu.shape != (E, 2 * d.shape[2], H) or d.shape != (E, H, d.shape[2]):
                 raise ValueError(f"Mx4MoeLayer: {what}_gu [{E}, 2I, {H}] and {what}_d [{E}, {H}, I] are wanted, got "
                                  f"{tuple(gu.shape)} and {tuple(d.shape)}")
             if gu.device != w_gu.device or d.device != w_gu.device:
                 raise ValueError("Mx4MoeLayer: the weights lie on different devices")
-        self.gu, self.d = Mx4Weights(w_gu), Mx4Weights(w_d)
-        self.s_gu = None if shared_gu is None else Mx4Weights(shared_gu)
-        self.s_d = None if shared_d is None else Mx4Weights(shared_d)
+        tiled = lambda w: w if w is None or isinstance(w, Mx4Weights) else Mx4Weights(w)
+        self.gu, self.d, self.s_gu, self.s_d = (tiled(w) for w in (w_gu, w_d, shared_gu, shared_d))
         self.top_k, self.T = top_k, -1   # T: the tokens that the views below are for
         self._kept, self._of_graphs = None, []
 

@@ -94,6 +94,13 @@ def weight_buffers(E, N, K, device=None):
     return torch.empty((E, N, K)), torch.empty(0)
 
 
+def pack_weight(codes, scales, tiles, stiles, stream=None):
+    import rows_plain as rp
+    E, N, K = tiles.shape
+    code = torch.stack((codes & 15, codes >> 4), -1).reshape(E * N, K)
+    tiles.copy_(torch.from_numpy(rp.mx4_values(code.numpy(), scales.reshape(E * N, -1).numpy())).reshape(E, N, K))
+
+
 def workspace_size(rows, K, N, E, R):
     """Any size that does not rise with the rows, as the library's does not where tiles widen."""
     return 4096 + 64 * (R + (16 if R % 3 else 40))
@@ -115,6 +122,7 @@ def use(monkeypatch):
     monkeypatch.setattr(moeq, "moeq_mx4_expert_gemm_workspace_size", workspace_size)
     monkeypatch.setattr(moeq, "mx4_weight_buffers", weight_buffers)
     monkeypatch.setattr(moeq, "moeq_mx4_quant_weight", lambda w, tiles, scales, stream=None: tiles.copy_(w))
+    monkeypatch.setattr(moeq, "moeq_mx4_pack_weight", pack_weight)
     monkeypatch.setattr(moeq, "Workspace", Workspace)
     monkeypatch.setattr(moeq, "_stream", lambda s: state.stream)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.capturing)

@@ -256,3 +256,21 @@ def test_layer_refuses_a_backward_pass(el):
         assert torch.equal(given, want) and not given.requires_grad and out.data_ptr() == given.data_ptr()
         with torch.no_grad():
             assert torch.equal(layer(a, b), want) and not layer(a, b).requires_grad
+
+
+def test_layer_takes_weights_that_are_mxfp4_already(el):
+    import rows_plain as rp
+    ws = [0.3 * _rand(s, *shape).float() for s, shape in
+          ((1, (E, 64, H)), (2, (E, H, 32)), (3, (1, 64, H)), (4, (1, H, 32)))]   # I = 32: a block of scales
+    packed, values = [], []
+    for w in ws:
+        code, scale = rp.mx4_codes(w.reshape(-1, w.shape[2]).numpy())
+        packed.append(el.Mx4Weights.from_codes(torch.from_numpy(rp.pack_codes(code)).reshape(*w.shape[:2], -1),
+                                               torch.from_numpy(scale).reshape(*w.shape[:2], -1)))
+        values.append(torch.from_numpy(rp.mx4_values(code, scale)).float().reshape(w.shape))
+        assert packed[-1].shape == tuple(w.shape)
+    x, lg = _inputs(4)
+    assert torch.equal(el.Mx4MoeLayer(packed[0], packed[1], K, packed[2], packed[3])(x, lg),
+                       el.Mx4MoeLayer(values[0], values[1], K, values[2], values[3])(x, lg))
+    with pytest.raises(ValueError):
+        el.Mx4MoeLayer(packed[0], packed[0], K)

@@ -215,3 +215,17 @@ def test_graphs_of_several_token_counts():
         assert torch.equal(layer(*_tokens(other)), want[other])
     torch.cuda.synchronize()
     assert all(bool((t == 0xFF).all()) for t in fill)
+
+
+def test_layer_of_packed_weights():
+    """Weights given as MXFP4 codes and scales: the bits of the layer that quantised them itself."""
+    from bandwidth_bound_fp8_gb300.expert_layer import Mx4MoeLayer, Mx4Weights
+    E, H, I, k = 12, 512, 256, 3
+    packed = []
+    for s, shape in ((1, (E, 2 * I, H)), (2, (E, H, I)), (3, (1, 2 * I, H)), (4, (1, H, I))):
+        code, scale = rp.mx4_codes(rp.to64(0.05 * _rand(s, *shape)).reshape(-1, shape[2]))
+        packed.append(Mx4Weights.from_codes(torch.from_numpy(rp.pack_codes(code)).reshape(*shape[:2], -1).cuda(),
+                                            torch.from_numpy(scale).reshape(*shape[:2], -1).cuda()))
+    layer = Mx4MoeLayer(packed[0], packed[1], k, packed[2], packed[3])
+    for T in (1, 250):
+        assert torch.equal(layer(*_tokens(T)), _small_layer()(*_tokens(T)))

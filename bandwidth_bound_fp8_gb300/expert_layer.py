@@ -211,7 +211,8 @@ class _Serve(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, out, x, logits):
-        return out.view_as(out)   # a caller's own buffer gathers no history
+        # a caller's own buffer gathers no history, and the result may be added to in place (a view might not)
+        return out.detach()
 
     @staticmethod
     def backward(ctx, _):

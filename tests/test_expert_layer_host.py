@@ -274,3 +274,14 @@ def test_layer_takes_weights_that_are_mxfp4_already(el):
                        el.Mx4MoeLayer(values[0], values[1], K, values[2], values[3])(x, lg))
     with pytest.raises(ValueError):
         el.Mx4MoeLayer(packed[0], packed[0], K)
+
+
+def test_layer_output_may_be_added_to_in_place(el):
+    layer = _layer(el)
+    x, lg = _inputs(4)
+    want = layer(x, lg) + x
+    out = layer(x.clone().requires_grad_(), lg)
+    out += x
+    assert torch.equal(out, want)
+    with pytest.raises(RuntimeError, match="no backward pass"):
+        out.sum().backward()

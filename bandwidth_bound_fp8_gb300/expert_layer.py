@@ -336,17 +336,16 @@ class Mx4MoeLayer:
 
     def __call__(self, x: torch.Tensor, logits: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
         """x [T, H] bf16, logits [T, E] fp32 -> out [T, H] bf16."""
-        T = x.shape[0]
-        if x.shape != (T, self.gu.K) or logits.shape != (T, self.gu.E):
-            raise ValueError(f"x [T, {self.gu.K}] and logits [T, {self.gu.E}] are wanted, got {tuple(x.shape)} and "
+        # (that all tensors lie on the weights' device, the current one, the calls check)
+        shape = x.shape
+        T = shape[0]
+        if shape != (T, self.gu.K) or logits.shape != (T, self.gu.E):
+            raise ValueError(f"x [T, {self.gu.K}] and logits [T, {self.gu.E}] are wanted, got {tuple(shape)} and "
                              f"{tuple(logits.shape)}")
-        if x.device != self.gu.tiles.device or logits.device != x.device:
-            raise ValueError(f"x and logits on the weights' device ({self.gu.tiles.device}) are wanted, got {x.device} "
-                             f"and {logits.device}")
         if out is None:
             out = torch.empty_like(x)
-        elif out.shape != x.shape or out.device != x.device:
-            raise ValueError(f"out: x's shape and device are wanted, got {tuple(out.shape)} on {out.device}")
+        elif out.shape != shape:
+            raise ValueError(f"out: x's shape is wanted, got {tuple(out.shape)}")
         if T == 0:
             return out
         self._buffers(T)

@@ -176,10 +176,6 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def current_stream_handle() -> int:
-    return _stream(None)
-
-
 _DTYPES = {torch.bfloat16: MOEQ_BF16, torch.float32: MOEQ_F32}
 
 
@@ -436,6 +432,11 @@ def _queue(stream):
     return _stream(stream)
 
 
+def current_stream_handle() -> int:
+    """torch's current stream, where CUDA is known to be initialised."""
+    return _queue(None)
+
+
 def _ld(t, name: str = "matrix") -> int:
     """Leading dimension, in elements, of a 2-D tensor on the device whose rows are contiguous."""
     if not t.is_cuda or _many_gpus and t.get_device() != _device():
@@ -490,12 +491,13 @@ def moeq_expert_sort(topk_id, E, offs, pair_row, row_pair, stream=None) -> None:
 
 
 def _pairs(pair_row):
-    T, k = pair_row.shape
-    return T, k, _packed(pair_row, torch.int32, (T, k), "pair_row")
+    T, k = shape = pair_row.shape
+    return T, k, _packed(pair_row, torch.int32, shape, "pair_row")
 
 
 def _offs(offs):
-    return offs.shape[0] - 1, _packed(offs, torch.int32, offs.shape[:1], "offs")
+    shape = offs.shape
+    return shape[0] - 1, _packed(offs, torch.int32, shape[:1], "offs")
 
 
 def moeq_gather_rows(x, offs, pair_row, xs, stream=None) -> None:

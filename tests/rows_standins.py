@@ -124,6 +124,6 @@ def use(monkeypatch):
     monkeypatch.setattr(moeq, "moeq_mx4_quant_weight", lambda w, tiles, scales, stream=None: tiles.copy_(w))
     monkeypatch.setattr(moeq, "moeq_mx4_pack_weight", pack_weight)
     monkeypatch.setattr(moeq, "Workspace", Workspace)
-    monkeypatch.setattr(moeq, "_stream", lambda s: state.stream)
+    monkeypatch.setattr(moeq, "current_stream_handle", lambda: state.stream)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.capturing)
     return state

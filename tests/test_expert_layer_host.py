@@ -225,8 +225,6 @@ def test_layer_refuses_other_shapes(el):
         with pytest.raises(ValueError):
             layer(x, lg, out=out)
     assert layer(x[:0], lg[:0]).shape == (0, H)
-    with pytest.raises(ValueError):
-        layer(x, lg.to("meta"))
 
 
 def test_layer_refuses_weights_that_do_not_fit(el):

@@ -229,3 +229,13 @@ def test_layer_of_packed_weights():
     layer = Mx4MoeLayer(packed[0], packed[1], k, packed[2], packed[3])
     for T in (1, 250):
         assert torch.equal(layer(*_tokens(T)), _small_layer()(*_tokens(T)))
+
+
+def test_layer_refuses_tensors_elsewhere():
+    layer = _small_layer()
+    x, lg = _tokens(4)
+    want = layer(x, lg)
+    for bad in (dict(x=x.cpu(), logits=lg), dict(x=x, logits=lg.cpu()), dict(x=x, logits=lg, out=x.cpu())):
+        with pytest.raises(ValueError, match="on the current CUDA device"):
+            layer(**bad)
+    assert torch.equal(layer(x, lg), want)

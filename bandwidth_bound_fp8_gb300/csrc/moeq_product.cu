@@ -1,0 +1,750 @@
+// The experts' products with bf16 weights, for rows sorted by expert, on the
+// tcgen05 tensor cores (kind::f16, fp32 accumulation), in three directions:
+//   y[r]  = W[e] x[r]                 product_rows_kernel, contraction over K
+//   dx[r] = W[e]^T dy[r]              product_rows_kernel, contraction over N
+//   dW[e] = sum_r dy[r] x[r]^T        product_weights_kernel, over e's rows
+// No operand is transposed in memory: the shared-memory tiles are what lies
+// there, and the MMA takes either major order.
+//
+// Rows out (y, dx): the weights' side is the MMA's 128-row operand (256 for a
+// pair of CTAs) and the rows are its N operand, so one row an expert wastes no
+// tensor time on padding.  A unit is (expert, features of a CTA or a pair, a
+// tile of the expert's rows); its contraction runs in stages of 64 columns.
+//   warps 0, 2  tensor copies: weights; rows
+//   warp 1      issues the MMAs (one thread); warp 3 tells it the parts
+//   warps 4..   epilogue: TMEM -> rows, behind the next unit's MMAs (two
+//               accumulators)
+// Whole units, round robin over the CTAs (pairs); none waits for another.
+//
+// Weights out (dW): a unit is (expert, 256 x 256 of dW) for a pair, the
+// contraction over the expert's rows in stages of 64.  Rows are sorted, so a
+// stage may reach past the expert's last row: what follows are another
+// expert's rows (or a NaN in a masked place), and 0 * NaN is not 0.  So the
+// last stage is copied row-exactly, in boxes of 32, 16, .. 1 rows, and filled
+// up to the MMA's 16 rows from beyond the matrix, where a tensor copy reads
+// zeros.
+#include "moeq_mx4_plan.cuh"
+#include "moeq_pair.cuh"
+#include "moeq_rows.h"
+
+namespace moeq {
+namespace {
+
+constexpr int kBlock = 64;                      // contraction a stage: 128 bytes of bf16, the swizzle's span
+constexpr int kTileBytes = 128 * kBlock * 2;    // 128 features (or dW rows / columns) of a stage
+constexpr int kAcc1 = 256;                      // TMEM columns of the second accumulator
+constexpr int kMaxStages = 7;
+// Most rows of a tile, for one CTA and for a pair.
+constexpr int kSingleTileRows = 128, kPairTileRows = 256;
+constexpr int kPairRows = 128;  // tiles of this many are a pair's
+constexpr int kBand = 8;                        // row tiles that take turns on the same weights
+
+__host__ __device__ constexpr int stage_bytes_of(int nt, bool pair) { return kTileBytes + nt / (pair ? 2 : 1) * 128; }
+
+// ------------------------------------------------------------- instructions
+// A and B bf16, D fp32, m x n; a_mn, b_mn: the operand's M (N) index is the
+// one that runs along memory.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+template <bool kPair>
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc) {
+    if constexpr (kPair)
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+// An operand whose M (N) index runs along memory, 128-byte swizzle: columns of
+// 64 of it, kBlock rows of 128 bytes each (one a contraction index), one after
+// the other.  The next 16 contraction indices are 2048 bytes on.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t smem_addr) {
+    uint64_t d = static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(kBlock * 128 >> 4) << 16;  // to the next 64
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;          // to the next 8 contraction indices
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+// A box into this CTA's shared memory, counted on `bar` (an address in the
+// cluster: a pair's copies count on the first CTA's).
+template <bool kPair>
+__device__ __forceinline__ void copy2(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
+    if constexpr (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+            : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void copy3(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
+                                      uint64_t policy) {
+    if constexpr (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+            : "memory");
+}
+__device__ __forceinline__ void store3(const CUtensorMap* map, const void* src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// What this thread wrote to shared memory, for copies that it or (behind a
+// barrier) another starts.
+__device__ __forceinline__ void fence_smem_for_copies() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t part_of(int n, int steps) {
+    return static_cast<uint32_t>(steps) << 5 | static_cast<uint32_t>(n >> 4);
+}
+// Barriers and the queue of parts that both kernels have.
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+    uint64_t part_full[4], part_empty[4];
+    uint32_t part_ring[4], tmem_base;
+    int abort, go[2][2];
+};
+
+// Set-up up to the point where memory may be read; ends in a block barrier
+// (plan_scan's) and, for a pair, one of the cluster.
+template <bool kPair>
+__device__ __forceinline__ uint32_t set_up(Shared& s, int stages, const Mx4Plan& p, const PlanShared& plan) {
+    const int tid = threadIdx.x, warp = tid >> 5;
+    if (tid == 0) {
+        s.abort = 0;
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.acc_full[i], 1);
+            mbar_init(&s.acc_empty[i], kPair ? 8 : 4);
+        }
+        mbar_init(&s.drained, 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s.part_full[i], 1);
+            mbar_init(&s.part_empty[i], 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_take<kPair>(&s.tmem_base);
+        tc_fence_before();
+    }
+    chain();
+    plan_scan(p, plan);
+    if constexpr (kPair) cluster_sync();  // the other CTA's barriers are set up
+    tc_fence_after();
+    return s.tmem_base;
+}
+
+// The ring of stages as its users walk it.
+struct Ring {
+    int stages, at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == stages) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// The thread that issues the MMAs: for each part of the queue, its stages.
+// A part is part_of(N of the MMAs, how many of 16 contraction indices there
+// are); 0 ends the queue.
+template <bool kPair, int kStepA, int kStepB, typename Desc>
+__device__ __forceinline__ void issue_parts(Shared& s, int stages, int stage_bytes, uint32_t tmem, uint64_t da, uint64_t db,
+                                            Desc idesc_of, volatile int* abort, int* status) {
+    const uint32_t pitch = static_cast<uint32_t>(stage_bytes) >> 4;
+    Ring ring{stages};
+    uint32_t at = 0;
+    bool ok = true, ready = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return kPair ? cluster_wait_bounded(bar, parity, abort) : mbar_wait_bounded(bar, parity, abort);
+    };
+    for (int i = 0;; ++i) {
+        ok = mbar_wait_bounded(&s.part_full[i & 3], (i >> 2) & 1, abort);
+        if (!ok) break;
+        const uint32_t part = *reinterpret_cast<volatile uint32_t*>(&s.part_ring[i & 3]);
+        mbar_arrive(&s.part_empty[i & 3]);
+        if (!part) break;
+        const int buf = i & 1;
+        int steps = static_cast<int>(part >> 5);
+        if (i >= 2) ok = wait(&s.acc_empty[buf], ((i >> 1) - 1) & 1);
+        const uint32_t d = tmem + buf * kAcc1, id = idesc_of(static_cast<int>(part & 31) << 4);
+        for (int k = 0; ok && steps > 0; ++k, steps -= 4) {
+            if (!ready) ok = wait(&s.full[ring.at], ring.phase);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t a = da + at, b = db + at;
+            mma_bf16<kPair>(d, a, b, id, k > 0);
+            if (steps > 1) mma_bf16<kPair>(d, a + kStepA, b + kStepB, id, 1);
+            uint64_t* const done = &s.empty[ring.at];
+            ring.next();
+            at = ring.at * pitch;
+            ready = mbar_test_wait<kPair>(&s.full[ring.at], ring.phase);
+            if (steps > 2) mma_bf16<kPair>(d, a + 2 * kStepA, b + 2 * kStepB, id, 1);
+            if (steps > 3) mma_bf16<kPair>(d, a + 3 * kStepA, b + 3 * kStepB, id, 1);
+            mma_commit<kPair>(done);
+        }
+        if (!ok) break;
+        mma_commit<kPair>(&s.acc_full[buf]);
+    }
+    if (!ok) {
+        *abort = 1;
+        if (status) atomicExch(status, static_cast<int>(MOEQ_ERR_TIMEOUT));
+        mma_commit<kPair>(&s.drained);
+        drain(&s.drained, 0, global_timer_ns());
+    }
+}
+
+// Puts a part into the queue; false where the wait for room gave up.
+__device__ __forceinline__ bool push_part(Shared& s, int i, uint32_t part, volatile int* abort) {
+    if (i >= 4 && !mbar_wait_bounded(&s.part_empty[i & 3], ((i >> 2) - 1) & 1, abort)) return false;
+    *reinterpret_cast<volatile uint32_t*>(&s.part_ring[i & 3]) = part;
+    mbar_arrive(&s.part_full[i & 3]);
+    return true;
+}
+
+// Whether the four warps of an epilogue group go on to a part whose
+// accumulator they wait for: one thread decides for all, because they meet at
+// barriers.  (A copy a turn: a slow warp may still read the last unit's.)
+template <typename GiveUp>
+__device__ __forceinline__ bool part_done(Shared& s, int i, int group, int groups, int lane, bool chief,
+                                          volatile int* abort, GiveUp give_up) {
+    const int turn = i / groups & 1;
+    if (lane == 0 && !mbar_wait_bounded(&s.acc_full[i & 1], (i >> 1) & 1, abort)) give_up();
+    __syncwarp();
+    if (chief) s.go[group][turn] = !*abort;
+    named_sync(1 + group, 128);
+    if (!s.go[group][turn]) return false;
+    tc_fence_after();
+    return true;
+}
+// The accumulator is read: the next unit but one may have it.
+template <bool kPair>
+__device__ __forceinline__ void release_acc(Shared& s, int buf, int rank, int lane) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+        if (kPair && rank == 1)
+            arrive_first(&s.acc_empty[buf]);
+        else
+            mbar_arrive(&s.acc_empty[buf]);
+    }
+}
+
+// ----------------------------------------------------------------- rows out
+struct RowsArgs {
+    Mx4Plan plan;
+    void* y;
+    int64_t ld_y;
+    int N, C;  // features of a row of y, contraction
+    int stages;
+    int* status;
+};
+struct RowsMaps {
+    CUtensorMap w;
+    CUtensorMap x[kSingleTileRows / 16];  // 16 rows, 32, ... (a pair's CTA copies half a tile)
+};
+
+struct Part {
+    int n0, r0, n, n_mma, tiles, e;
+};
+// The i-th part of this CTA (pair); false past its last.  Units count experts,
+// then bands of kBand row tiles, then blocks of features, then the band's
+// tiles: CTAs at work together share both operands in L2, whatever the
+// expert's size.
+template <bool kPair>
+__device__ __forceinline__ bool part_at(const RowsArgs& a, const PlanShared& plan, int i, int worker, int workers,
+                                        int nbu, int rank, Part& p) {
+    const int u = worker + i * workers;
+    if (u >= plan.tile[a.plan.E] * nbu) return false;
+    const int e = plan_find(plan.tile, a.plan.E, u / nbu);  // experts without tiles are never the last such
+    const int r0 = plan.first[e], cnt = plan.first[e + 1] - r0;
+    const int tiles = plan.tile[e + 1] - plan.tile[e], per = plan_rows_per_tile(cnt, a.plan.nt, a.plan.align);
+    const int local = u - plan.tile[e] * nbu, band = local / (nbu * kBand), in = local - band * nbu * kBand;
+    const int width = min(kBand, tiles - band * kBand), nb = in / width, t = band * kBand + in - nb * width;
+    p.e = e;
+    p.tiles = tiles;
+    p.n0 = (kPair ? 2 * nb + rank : nb) * 128;
+    p.r0 = r0 + t * per;
+    p.n = min(per, cnt - t * per);
+    p.n_mma = (p.n + a.plan.align - 1) & ~(a.plan.align - 1);
+    return true;
+}
+
+template <bool kF32, bool kPair, bool kTrans>
+__global__ void __maxnreg__(160)
+    product_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ RowsMaps maps) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared s;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int stage_bytes = stage_bytes_of(a.plan.nt, kPair);
+    const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
+    // behind the stages: the epilogue's buffers, then the plan
+    uint8_t* const epi_mem = smem + a.stages * stage_bytes;
+    const PlanShared plan = plan_at(reinterpret_cast<int*>(epi_mem + epi_groups(kPair) * epi_bytes(kPair)), a.plan.E);
+    const uint32_t tmem = set_up<kPair>(s, a.stages, a.plan, plan);
+    volatile int* abort = &s.abort;
+    const int workers = gridDim.x / (kPair ? 2 : 1), worker = blockIdx.x / (kPair ? 2 : 1);
+    const int nbu = kPair ? (a.N + 255) / 256 : (a.N + 127) / 128, kb_n = (a.C + kBlock - 1) / kBlock;
+    auto part = [&](int i, Part& p) { return part_at<kPair>(a, plan, i, worker, workers, nbu, rank, p); };
+    auto give_up = [&] {
+        *abort = 1;
+        if (a.status) atomicExch(a.status, static_cast<int>(MOEQ_ERR_TIMEOUT));
+    };
+
+    if (warp == 0 || warp == 2) {
+        // -------------------------------------------------------- copies
+        if (elect_one()) {
+            // weights that one tile reads are not read again; those of several,
+            // and the rows, come from L2 the next time
+            const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
+            Part p;
+            Ring ring{a.stages};
+            int it = 0;
+            bool ok = true;
+            for (int i = 0; ok && part(i, p); ++i)
+                for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                    if (it >= a.stages) ok = mbar_wait_bounded(&s.empty[ring.at], ring.phase ^ 1, abort);
+                    if (!ok) break;
+                    uint8_t* const at = smem + ring.at * stage_bytes;
+                    const uint32_t bar = kPair ? in_first(&s.full[ring.at]) : smem_u32(&s.full[ring.at]);
+                    const int rows = p.n_mma / (kPair ? 2 : 1);
+                    if (warp == 0) {
+                        // both CTAs' copies of a pair count on the first's barrier
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(&s.full[ring.at], (kPair ? 2 : 1) * (kTileBytes + rows * 128));
+                        const uint64_t policy = p.tiles > 1 ? again : once;
+                        if constexpr (kTrans) {
+                            copy3<kPair>(at, &maps.w, p.n0, kb * kBlock, p.e, bar, policy);
+                            copy3<kPair>(at + kTileBytes / 2, &maps.w, p.n0 + 64, kb * kBlock, p.e, bar, policy);
+                        } else {
+                            copy3<kPair>(at, &maps.w, kb * kBlock, p.n0, p.e, bar, policy);
+                        }
+                    } else {
+                        copy2<kPair>(at + kTileBytes, &maps.x[rows / 16 - 1], kb * kBlock, p.r0 + rank * rows, bar, again);
+                    }
+                    ring.next();
+                }
+            if (!ok) {
+                give_up();
+                // copies in flight land before the CTA may end (a pair's are all
+                // counted in the first, and the pair ends together)
+                const unsigned long long t0 = global_timer_ns();
+                for (int j = max(0, it - a.stages); rank == 0 && j < it; ++j)
+                    drain(&s.full[j % a.stages], (j / a.stages) & 1, t0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- MMAs
+        if (rank == 0 && elect_one()) {
+            const uint32_t base = smem_u32(smem);
+            const uint64_t da = kTrans ? desc_mn(base) : umma_desc_sw128(base), db = umma_desc_sw128(base + kTileBytes);
+            // 16 contraction indices on: 32 bytes of a row, or 16 rows
+            issue_parts<kPair, kTrans ? 128 : 2, 2>(
+                s, a.stages, stage_bytes, tmem, da, db,
+                [](int n) { return idesc_bf16(kPair ? 256 : 128, n, kTrans, false); }, abort, a.status);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ------------------------------------------- parts, for the MMA thread
+        if (rank == 0 && elect_one()) {
+            Part p;
+            bool more = true, ok = true;
+            for (int i = 0; ok && more; ++i) {
+                more = part(i, p);
+                ok = push_part(s, i, more ? part_of(p.n_mma, 4 * kb_n) : 0, abort);
+            }
+            if (!ok) give_up();
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------- epilogue
+        constexpr int kGroups = epi_groups(kPair);
+        const int q = warp & 3, group = (warp >> 2) - 1, bar = 1 + group;
+        const bool chief = tid == 128 + group * 128;
+        uint8_t* stage_y = epi_mem + group * epi_bytes(kPair);
+        // rows of y in 16-byte pieces
+        const bool vec_y = a.N % (kF32 ? 4 : 8) == 0 && a.ld_y % (kF32 ? 4 : 8) == 0 &&
+                           (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+        Part p;
+        for (int i = group; part(i, p); i += kGroups) {
+            const int buf = i & 1;
+            if (!part_done(s, i, group, kGroups, lane, chief, abort, give_up)) break;
+            const uint32_t acc = tmem + buf * kAcc1 + (static_cast<uint32_t>(q * 32) << 16);
+            const int n = p.n0 + q * 32 + lane;
+            constexpr int kCols = epi_cols(kF32, kPair);
+            for (int c0 = 0; c0 < p.n; c0 += kCols) {
+                float v[kCols];  // columns past the tile's are read and not stored
+#pragma unroll
+                for (int j = 0; j < kCols; j += 16) tmem_ld16(acc + c0 + j, v + j);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < kCols; j += 16) tmem_use16(v + j);
+                if (c0 + kCols >= p.n) release_acc<kPair>(s, buf, rank, lane);
+                store_step<kF32, kCols>(a, p, c0, q, lane, n, v, stage_y, vec_y, bar);
+            }
+        }
+        // rows that belong to no expert
+        const int t = tid - 128, per = vec_y ? (kF32 ? 4 : 8) : 1;
+        for (int64_t r = static_cast<int64_t>(plan.first[a.plan.E]) + blockIdx.x; r < a.plan.R; r += gridDim.x)
+            for (int c = t * per; c < a.N; c += 128 * kGroups * per) {
+                if (vec_y)
+                    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.y) + (r * a.ld_y + c) * (kF32 ? 4 : 2)) =
+                        make_uint4(0, 0, 0, 0);
+                else
+                    store_y<kF32>(a.y, r * a.ld_y + c, 0.f);
+            }
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    if constexpr (kPair) cluster_sync();  // neither CTA's shared memory or TMEM is in use any more
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_give<kPair>(tmem);
+    }
+}
+
+// -------------------------------------------------------------- weights out
+struct WeightsArgs {
+    Mx4Plan plan;
+    int N, K;
+    int stages;
+    int* status;
+};
+struct WeightsMaps {
+    CUtensorMap dy[7], x[7];  // 64 rows, 32, .. 1
+    CUtensorMap dw;
+};
+constexpr int kWStageBytes = 2 * kTileBytes;  // a CTA's 128 rows of dW, and half of the 256 columns
+constexpr int kWStages = 5;
+constexpr int kWEpiBytes = 4096;              // a warp's 32 rows of 128 bytes
+
+struct WPart {
+    int e, n0, k0, r0, cnt;
+};
+__device__ __forceinline__ bool wpart_at(const WeightsArgs& a, const PlanShared& plan, int i, int worker, int workers,
+                                         WPart& p) {
+    const int nbu = (a.N + 255) / 256, kbu = (a.K + 255) / 256, u = worker + i * workers;
+    if (u >= a.plan.E * nbu * kbu) return false;
+    p.e = u / (nbu * kbu);
+    const int in = u - p.e * nbu * kbu, nb = in / kbu;
+    p.n0 = nb * 256;
+    p.k0 = (in - nb * kbu) * 256;
+    p.r0 = plan.first[p.e];
+    p.cnt = plan.first[p.e + 1] - p.r0;
+    return true;
+}
+
+// Up to 64 rows of 128 columns, r0 on, into a stage; the rows past the
+// expert's last up to the next multiple of 16 are zeros (R: past the matrix).
+__device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, int col, int r0, int rows, int R,
+                                          uint32_t bar, uint64_t policy) {
+    if (rows >= kBlock) {
+        copy2<true>(at, &maps[0], col, r0, bar, policy);
+        copy2<true>(at + kTileBytes / 2, &maps[0], col + 64, r0, bar, policy);
+        return;
+    }
+    int done = 0;
+    for (int z = 0; z < 2; ++z) {
+        const int want = z ? (-rows) & 15 : rows;
+        for (int m = 1; m < 7; ++m) {
+            const int box = kBlock >> m;
+            if (!(want & box)) continue;
+            copy2<true>(at + done * 128, &maps[m], col, z ? R : r0 + done, bar, policy);
+            copy2<true>(at + kTileBytes / 2 + done * 128, &maps[m], col + 64, z ? R : r0 + done, bar, policy);
+            done += box;
+        }
+    }
+}
+
+template <bool kF32>
+__global__ void __maxnreg__(160)
+    product_weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ WeightsMaps maps) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared s;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_rank());
+    constexpr int kGroups = epi_groups(true);
+    uint8_t* const epi_mem = smem + a.stages * kWStageBytes;
+    const PlanShared plan = plan_at(reinterpret_cast<int*>(epi_mem + kGroups * 4 * kWEpiBytes), a.plan.E);
+    const uint32_t tmem = set_up<true>(s, a.stages, a.plan, plan);
+    volatile int* abort = &s.abort;
+    const int workers = gridDim.x / 2, worker = blockIdx.x / 2;
+    auto part = [&](int i, WPart& p) { return wpart_at(a, plan, i, worker, workers, p); };
+    auto give_up = [&] {
+        *abort = 1;
+        if (a.status) atomicExch(a.status, static_cast<int>(MOEQ_ERR_TIMEOUT));
+    };
+
+    if (warp == 0 || warp == 2) {
+        // -------------------------------------------------------- copies
+        // Warp 0 copies dy, warp 2 x: both come from L2 for every block of dW.
+        if (elect_one()) {
+            const uint64_t again = l2_evict_normal_policy();
+            WPart p;
+            Ring ring{a.stages};
+            int it = 0;
+            bool ok = true;
+            for (int i = 0; ok && part(i, p); ++i)
+                for (int r = 0; r < p.cnt; r += kBlock, ++it) {
+                    if (it >= a.stages) ok = mbar_wait_bounded(&s.empty[ring.at], ring.phase ^ 1, abort);
+                    if (!ok) break;
+                    uint8_t* const at = smem + ring.at * kWStageBytes;
+                    const uint32_t bar = in_first(&s.full[ring.at]);
+                    const int rows = min(p.cnt - r, kBlock), rows16 = (rows + 15) & ~15;
+                    if (warp == 0) {
+                        if (rank == 0) mbar_arrive_expect_tx(&s.full[ring.at], 2 * 4 * rows16 * 128);
+                        copy_rows(at, maps.dy, p.n0 + rank * 128, p.r0 + r, rows, a.plan.R, bar, again);
+                    } else {
+                        copy_rows(at + kTileBytes, maps.x, p.k0 + rank * 128, p.r0 + r, rows, a.plan.R, bar, again);
+                    }
+                    ring.next();
+                }
+            if (!ok) {
+                give_up();
+                const unsigned long long t0 = global_timer_ns();
+                for (int j = max(0, it - a.stages); rank == 0 && j < it; ++j)
+                    drain(&s.full[j % a.stages], (j / a.stages) & 1, t0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- MMAs
+        if (rank == 0 && elect_one()) {
+            const uint32_t base = smem_u32(smem);
+            issue_parts<true, 128, 128>(
+                s, a.stages, kWStageBytes, tmem, desc_mn(base), desc_mn(base + kTileBytes),
+                [](int n) { return idesc_bf16(256, n, true, true); }, abort, a.status);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ------------------------------------------- parts, for the MMA thread
+        if (rank == 0 && elect_one()) {
+            WPart p;
+            bool more = true, ok = true;
+            for (int i = 0; ok && more; ++i) {
+                more = part(i, p);
+                ok = push_part(s, i, more ? part_of(256, (p.cnt + 15) / 16) : 0, abort);
+            }
+            if (!ok) give_up();
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------- epilogue
+        // Lane = row of dW.  A warp's 32 rows leave through shared memory, 128
+        // bytes of each at a time, as tensor copies (which clip at N and K); an
+        // expert without rows gets zeros.
+        const int q = warp & 3, group = (warp >> 2) - 1;
+        const bool chief = tid == 128 + group * 128;
+        uint8_t* const buf_y = epi_mem + (group * 4 + q) * kWEpiBytes;
+        constexpr int kCols = kF32 ? 32 : 64;
+        WPart p;
+        for (int i = group; part(i, p); i += kGroups) {
+            const int buf = i & 1, n0 = p.n0 + rank * 128 + q * 32;
+            if (!part_done(s, i, group, kGroups, lane, chief, abort, give_up)) break;
+            const uint32_t acc = tmem + buf * kAcc1 + (static_cast<uint32_t>(q * 32) << 16);
+            for (int c0 = 0; c0 < 256; c0 += kCols) {
+                float v[kCols];
+#pragma unroll
+                for (int j = 0; j < kCols; j += 16) tmem_ld16(acc + c0 + j, v + j);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < kCols; j += 16) tmem_use16(v + j);
+                if (c0 + kCols == 256) release_acc<true>(s, buf, rank, lane);
+                if (n0 >= a.N || p.k0 + c0 >= a.K) continue;
+                if (p.cnt == 0) {
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) v[j] = 0.f;
+                }
+                if (lane == 0) stores_read();  // the copy before has left the buffer
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint4 w;
+                    if constexpr (kF32) {
+                        w = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                                       __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+                    } else {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * c + 2 * j], v[8 * c + 2 * j + 1]);
+                            u[j] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        w = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                    *reinterpret_cast<uint4*>(buf_y + lane * 128 + ((c ^ (lane & 7)) << 4)) = w;
+                }
+                fence_smem_for_copies();
+                __syncwarp();
+                if (lane == 0) store3(&maps.dw, buf_y, p.k0 + c0, n0, p.e);
+            }
+        }
+        if (lane == 0) stores_done();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();  // neither CTA's shared memory or TMEM is in use any more
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_give<true>(tmem);
+    }
+}
+
+// --------------------------------------------------------------------- host
+bool map2(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(box_rows)}, steps[2] = {1, 1};
+    const EncodeTiled f = encode_tiled();
+    return f && f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// [E, N, K], contiguous; the box is one expert's.
+bool map3(CUtensorMap* map, const void* p, int f32, int64_t K, int64_t N, int64_t E, int box_k, int box_n) {
+    const cuuint64_t size = f32 ? 4 : 2;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(E)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K) * size, static_cast<cuuint64_t>(K * N) * size};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_k), static_cast<cuuint32_t>(box_n), 1}, steps[3] = {1, 1, 1};
+    const EncodeTiled f = encode_tiled();
+    return f && f(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p),
+                  dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Args, typename Maps>
+cudaError_t launch(void (*kern)(Args, Maps), OncePerDevice& once, const Args& a, const Maps& maps, bool pair, int grid,
+                   int smem, int most_smem, cudaStream_t stream) {
+    const cudaError_t e = raise_smem(once, reinterpret_cast<const void*>(kern), most_smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads_of(pair));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = pair ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, maps);
+}
+
+// Of 227 KiB, less the static arrays.
+constexpr int kMostSmem = 227 * 1024 - 1024;
+
+template <bool kF32, bool kPair, bool kTrans>
+cudaError_t launch_rows(const RowsArgs& a, const RowsMaps& maps, int grid, int smem, cudaStream_t stream) {
+    static OncePerDevice once;
+    return launch(product_rows_kernel<kF32, kPair, kTrans>, once, a, maps, kPair, grid, smem, kMostSmem, stream);
+}
+
+// Rows of a tile, and whether pairs of CTAs multiply it: about twice an
+// expert's average, so that most experts are one tile and their weights are
+// read once.
+Mx4Tiling tiling_of(int R, int E) {
+    const long long want = E == 1 ? R : 2LL * R / E + 16;
+    const bool pair = want >= kPairRows && R >= kPairRows;
+    const int align = pair ? 32 : 16, most = pair ? kPairTileRows : kSingleTileRows;
+    const long long rows = want < R ? want : R;
+    return {static_cast<int>(rows > most ? most : (rows + align - 1) / align * align), align};
+}
+
+}  // namespace
+
+cudaError_t launch_expert_product(const void* x, int64_t ld_x, int R, const void* w, int E, int N, int K, bool trans,
+                                  const int32_t* offs, RowsOut y, int* status, int sms, cudaStream_t stream) {
+    const Mx4Tiling t = tiling_of(R, E);
+    const bool pair = t.align == 32;
+    RowsArgs a = {};
+    a.plan = {offs, nullptr, E, R, 1, R, t.nt, t.align};
+    a.y = y.p;
+    a.ld_y = y.ld;
+    a.N = trans ? K : N;
+    a.C = trans ? N : K;
+    a.status = status;
+    RowsMaps maps;
+    if (!map3(&maps.w, w, 0, K, N, E, kBlock, trans ? kBlock : 128)) return cudaErrorInvalidValue;
+    const int boxes = t.nt / (pair ? 2 : 1) / 16;
+    for (int i = 0; i < boxes; ++i)
+        if (!map2(&maps.x[i], x, a.C, R, ld_x, 16 * (i + 1))) return cudaErrorInvalidValue;
+    const int sb = stage_bytes_of(t.nt, pair);
+    const int rest = 1024 + epi_bytes(pair) * epi_groups(pair) + plan_ints(E) * static_cast<int>(sizeof(int));
+    const int fit = (kMostSmem - rest) / sb;
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+    const int smem = a.stages * sb + rest, grid = pair ? sms / 2 * 2 : sms;
+    auto go = [&](auto f32, auto two, auto tr) {
+        return launch_rows<decltype(f32)::value, decltype(two)::value, decltype(tr)::value>(a, maps, grid, smem, stream);
+    };
+    using T = std::true_type;
+    using F = std::false_type;
+    if (pair) {
+        if (y.f32) return trans ? go(T{}, T{}, T{}) : go(T{}, T{}, F{});
+        return trans ? go(F{}, T{}, T{}) : go(F{}, T{}, F{});
+    }
+    if (y.f32) return trans ? go(T{}, F{}, T{}) : go(T{}, F{}, F{});
+    return trans ? go(F{}, F{}, T{}) : go(F{}, F{}, F{});
+}
+
+cudaError_t launch_expert_product_grad_w(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int R, int E, int N,
+                                         int K, const int32_t* offs, void* dw, int dw_f32, int* status, int sms,
+                                         cudaStream_t stream) {
+    WeightsArgs a = {};
+    a.plan = {offs, nullptr, E, R, 1, R, kBlock, 16};
+    a.N = N;
+    a.K = K;
+    a.status = status;
+    a.stages = kWStages;
+    WeightsMaps maps;
+    for (int i = 0; i < 7; ++i)
+        if (!map2(&maps.dy[i], dy, N, R, ld_dy, kBlock >> i) || !map2(&maps.x[i], x, K, R, ld_x, kBlock >> i))
+            return cudaErrorInvalidValue;
+    if (!map3(&maps.dw, dw, dw_f32, K, N, E, dw_f32 ? 32 : 64, 32)) return cudaErrorInvalidValue;
+    const int smem = 1024 + kWStages * kWStageBytes + epi_groups(true) * 4 * kWEpiBytes +
+                     plan_ints(E) * static_cast<int>(sizeof(int));
+    static OncePerDevice once[2];
+    return dw_f32 ? launch(product_weights_kernel<true>, once[1], a, maps, true, sms / 2 * 2, smem, kMostSmem, stream)
+                  : launch(product_weights_kernel<false>, once[0], a, maps, true, sms / 2 * 2, smem, kMostSmem, stream);
+}
+
+}  // namespace moeq

@@ -155,4 +155,12 @@ struct Mx4GemmArgs {
 // tiles, and nothing else of the arguments) runs.
 cudaError_t launch_mx4_gemm(Mx4GemmArgs a, int grid, bool pdl, cudaStream_t stream);
 
+// ---------------------------------------------------------- bf16 products
+// trans: y[r] = w[e]^T x[r], x's rows N wide and y's K; else y[r] = w[e] x[r].
+cudaError_t launch_expert_product(const void* x, int64_t ld_x, int R, const void* w, int E, int N, int K, bool trans,
+                                  const int32_t* offs, RowsOut y, int* status, int sms, cudaStream_t stream);
+cudaError_t launch_expert_product_grad_w(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int R, int E, int N,
+                                         int K, const int32_t* offs, void* dw, int dw_f32, int* status, int sms,
+                                         cudaStream_t stream);
+
 }  // namespace moeq

@@ -87,6 +87,26 @@ Mx4Ws mx4_ws(int64_t rows, int K, int E, int R, int sms) {
     return l;
 }
 
+// Rows that tensor copies read: bf16, rows and base on 16 bytes.
+bool copy_rows_ok(const void* p, int64_t ld, int64_t width) { return al(p, 16) && ld % 8 == 0 && ld >= width; }
+bool product_shape_ok(int K, int N) {
+    return K >= 8 && K % 8 == 0 && K <= kMaxWidth && N >= 8 && N % 8 == 0 && N <= kMaxWidth;
+}
+// y = product of x (rows x_width wide) and w, either way round.
+moeq_status expert_product(const void* x, int64_t ld_x, const void* w, int K, int N, bool trans, const int32_t* offs,
+                           int E, int R, void* y, moeq_dtype y_dtype, int64_t ld_y, int32_t* status_opt, void* stream) {
+    if (R < 0 || R > kMaxPairs || E < 1 || E > MOEQ_MAX_EXPERTS || !type_ok(y_dtype)) return MOEQ_ERR_INVALID_ARG;
+    if (!product_shape_ok(K, N)) return MOEQ_ERR_UNSUPPORTED_SHAPE;
+    if (R == 0) return MOEQ_OK;
+    if (!copy_rows_ok(x, ld_x, trans ? N : K) || !al(w, 16) || !al(offs, 4) ||
+        !rows_ok(y, y_dtype, ld_y, trans ? K : N) || (status_opt && !al(status_opt, 4)))
+        return MOEQ_ERR_INVALID_ARG;
+    const Device dev = current_device();
+    if (!dev.ok) return MOEQ_ERR_DEVICE;
+    return cuda_status(launch_expert_product(x, ld_x, R, w, E, N, K, trans, offs, {y, ld_y, y_dtype == MOEQ_F32},
+                                             status_opt, dev.sms, as_stream(stream)));
+}
+
 bool mx4_shape_ok(int K, int N) { return K >= 32 && K % 32 == 0 && K <= MOEQ_MAX_K && N >= 1 && N <= kMaxWidth; }
 
 }  // namespace
@@ -296,6 +316,33 @@ moeq_status moeq_mx4_expert_gemm(const void* x, moeq_dtype x_dtype, int64_t ld_x
     // the token tiles, runs: it waits for it before it reads one, and
     // everything before that kernel has ended by then.
     return cuda_status(launch_mx4_gemm(a, dev.sms, true, st));
+}
+
+moeq_status moeq_expert_product(const void* x, int64_t ld_x, const void* w, int K, int N, const int32_t* offs, int E,
+                                int R, void* y, moeq_dtype y_dtype, int64_t ld_y, int32_t* status_opt, void* stream) {
+    return expert_product(x, ld_x, w, K, N, false, offs, E, R, y, y_dtype, ld_y, status_opt, stream);
+}
+
+moeq_status moeq_expert_product_grad_x(const void* d_y, int64_t ld_dy, const void* w, int K, int N, const int32_t* offs,
+                                       int E, int R, void* d_x, moeq_dtype dx_dtype, int64_t ld_dx, int32_t* status_opt,
+                                       void* stream) {
+    return expert_product(d_y, ld_dy, w, K, N, true, offs, E, R, d_x, dx_dtype, ld_dx, status_opt, stream);
+}
+
+moeq_status moeq_expert_product_grad_w(const void* d_y, int64_t ld_dy, const void* x, int64_t ld_x, int K, int N,
+                                       const int32_t* offs, int E, int R, void* d_w, moeq_dtype dw_dtype,
+                                       int32_t* status_opt, void* stream) {
+    if (R < 0 || R > kMaxPairs || E < 1 || E > MOEQ_MAX_EXPERTS || !type_ok(dw_dtype)) return MOEQ_ERR_INVALID_ARG;
+    if (!product_shape_ok(K, N)) return MOEQ_ERR_UNSUPPORTED_SHAPE;
+    if (!al(d_w, 16) || (status_opt && !al(status_opt, 4)) ||
+        (R > 0 && (!copy_rows_ok(d_y, ld_dy, N) || !copy_rows_ok(x, ld_x, K) || !al(offs, 4))))
+        return MOEQ_ERR_INVALID_ARG;
+    const Device dev = current_device();
+    if (!dev.ok) return MOEQ_ERR_DEVICE;
+    if (R == 0)
+        return cuda_status(cudaMemsetAsync(d_w, 0, static_cast<size_t>(E) * N * K * size_of(dw_dtype), as_stream(stream)));
+    return cuda_status(launch_expert_product_grad_w(d_y, ld_dy, x, ld_x, R, E, N, K, offs, d_w, dw_dtype == MOEQ_F32,
+                                                    status_opt, dev.sms, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -47,6 +47,7 @@ EXPORTS = [
     "moeq_combine_rows", "moeq_combine_rows_grad", "moeq_mx4_scale_pitch", "moeq_mx4_weight_bytes",
     "moeq_mx4_weight_scale_bytes", "moeq_mx4_quant_act", "moeq_mx4_dequant_act", "moeq_mx4_quant_weight",
     "moeq_mx4_pack_weight", "moeq_mx4_expert_gemm_workspace_size", "moeq_mx4_expert_gemm",
+    "moeq_expert_product", "moeq_expert_product_grad_x", "moeq_expert_product_grad_w",
 ]
 
 
@@ -132,6 +133,9 @@ def load(path: str = LIB_PATH):
         "moeq_mx4_expert_gemm_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
         "moeq_mx4_expert_gemm": (_i, [_vp, _i, _ll, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _i,
                                       _ll, _vp, _sz, _vp]),
+        "moeq_expert_product": (_i, [_vp, _ll, _vp, _i, _i, _vp, _i, _i, _vp, _i, _ll, _vp, _vp]),
+        "moeq_expert_product_grad_x": (_i, [_vp, _ll, _vp, _i, _i, _vp, _i, _i, _vp, _i, _ll, _vp, _vp]),
+        "moeq_expert_product_grad_w": (_i, [_vp, _ll, _vp, _ll, _i, _i, _vp, _i, _i, _vp, _i, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -651,3 +655,50 @@ def moeq_mx4_expert_gemm(x, w, w_scales, offs, y, ws: Workspace, row_pair=None, 
         x.data_ptr(), dt, ld, _p(x_scales), rows, K, act, tp, sp, N, of, E, R,
         _packed(row_pair, torch.int32, (R,), "row_pair") if row_pair is not None else None, top_k, y.data_ptr(),
         _dtype(y), _ld(y, "y"), ws.ptr, ws.nbytes, _queue(stream)))
+
+
+# ------------------------------------------------------- bf16 products
+def _bf16_rows(t, name: str, R: int, width: int):
+    """Address and leading dimension of bf16 rows [R, width] that tensor copies can read."""
+    if t.dtype is not torch.bfloat16 or t.shape != (R, width):
+        raise ValueError(f"{name}: bf16 rows [{R}, {width}] are wanted, got {t.dtype} {tuple(t.shape)}")
+    ld = _ld(t, name)
+    return t.data_ptr(), ld if R > 1 else (ld + 7) // 8 * 8   # (one row is never stepped over)
+
+
+def _word(status):
+    return None if status is None else _packed(status, torch.int32, (1,), "status")
+
+
+def moeq_expert_product(x, w, offs, y, status=None, stream=None) -> None:
+    """y[r] = w[e(r)] x[r] for rows sorted by expert (offs [E + 1]): x [R, K]
+    bf16, w [E, N, K] bf16, y [R, N] bf16 or fp32.  Rows of y from offs[E] on
+    are zeroed.  status: optional int32 [1] that receives the status word."""
+    R, N = y.shape
+    E, K = offs.shape[0] - 1, x.shape[1]
+    xp, ld = _bf16_rows(x, "x", R, K)
+    _check("moeq_expert_product", (_lib or load()).moeq_expert_product(
+        xp, ld, _packed(w, torch.bfloat16, (E, N, K), "w"), K, N, _offs(offs)[1], E, R, y.data_ptr(), _dtype(y),
+        _ld(y, "y"), _word(status), _queue(stream)))
+
+
+def moeq_expert_product_grad_x(d_y, w, offs, d_x, status=None, stream=None) -> None:
+    """d_x[r] = w[e(r)]^T d_y[r]: d_y [R, N] bf16, d_x [R, K] bf16 or fp32."""
+    R, K = d_x.shape
+    E, N = offs.shape[0] - 1, d_y.shape[1]
+    yp, ld = _bf16_rows(d_y, "d_y", R, N)
+    _check("moeq_expert_product_grad_x", (_lib or load()).moeq_expert_product_grad_x(
+        yp, ld, _packed(w, torch.bfloat16, (E, N, K), "w"), K, N, _offs(offs)[1], E, R, d_x.data_ptr(), _dtype(d_x),
+        _ld(d_x, "d_x"), _word(status), _queue(stream)))
+
+
+def moeq_expert_product_grad_w(d_y, x, offs, d_w, status=None, stream=None) -> None:
+    """d_w[e] = sum of d_y[r] x[r]^T over e's rows: d_y [R, N] and x [R, K]
+    bf16, d_w [E, N, K] bf16 or fp32 (zeros for an expert without rows)."""
+    R, N = d_y.shape
+    E, K = offs.shape[0] - 1, x.shape[1]
+    yp, ld_y = _bf16_rows(d_y, "d_y", R, N)
+    xp, ld_x = _bf16_rows(x, "x", R, K)
+    _check("moeq_expert_product_grad_w", (_lib or load()).moeq_expert_product_grad_w(
+        yp, ld_y, xp, ld_x, K, N, _offs(offs)[1], E, R, _packed(d_w, d_w.dtype, (E, N, K), "d_w"), _dtype(d_w),
+        _word(status), _queue(stream)))

@@ -599,6 +599,38 @@ moeq_status moeq_mx4_expert_gemm(const void* x, moeq_dtype x_dtype, int64_t ld_x
                                  void* y, moeq_dtype y_dtype, int64_t ld_y,
                                  void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The experts' products with bf16 weights, for training (and for serving   */
+/* them unquantised): rows sorted by expert, fp32 accumulation on the       */
+/* tensor cores, rounded once.  K and N are multiples of 8 up to 2^20; the  */
+/* bf16 inputs x and d_y have rows and base on 16 bytes (a leading dimension */
+/* that is a multiple of 8); w and d_w are [E, N, K], contiguous, 16-byte   */
+/* aligned.  offs [E + 1] on the device as moeq_expert_sort leaves it; a     */
+/* dense product is E = 1, offs = {0, R}.  An output overlaps no input.     */
+/* A NaN or an infinity reaches its own row of y or d_x, and its own        */
+/* expert's d_w, alone.  No workspace.  status_opt: NULL, or a device word   */
+/* that receives MOEQ_ERR_TIMEOUT where a wait inside the kernel gave up    */
+/* (the results are not valid then); it is not written otherwise.           */
+/*   moeq_expert_product         y[r] = w[e] x[r]; x [R, K] -> y [R, N]     */
+/*   moeq_expert_product_grad_x  d_x[r] = w[e]^T d_y[r]; d_x [R, K]         */
+/*   moeq_expert_product_grad_w  d_w[e] = sum over e's rows r of            */
+/*           d_y[r] x[r]^T, summed in the order of the rows; every element  */
+/*           is written, zeros for an expert without rows                  */
+/* Rows of y and d_x from offs[E] on are zeroed.  Outputs are bf16 or fp32. */
+/* ------------------------------------------------------------------------ */
+moeq_status moeq_expert_product(const void* x, int64_t ld_x, const void* w, int K, int N,
+                                const int32_t* offs, int E, int R,
+                                void* y, moeq_dtype y_dtype, int64_t ld_y,
+                                int32_t* status_opt, void* stream);
+moeq_status moeq_expert_product_grad_x(const void* d_y, int64_t ld_dy, const void* w, int K, int N,
+                                       const int32_t* offs, int E, int R,
+                                       void* d_x, moeq_dtype dx_dtype, int64_t ld_dx,
+                                       int32_t* status_opt, void* stream);
+moeq_status moeq_expert_product_grad_w(const void* d_y, int64_t ld_dy, const void* x, int64_t ld_x, int K, int N,
+                                       const int32_t* offs, int E, int R,
+                                       void* d_w, moeq_dtype dw_dtype,
+                                       int32_t* status_opt, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -345,4 +345,75 @@ moeq_status moeq_expert_product_grad_w(const void* d_y, int64_t ld_dy, const voi
                                                     status_opt, dev.sms, as_stream(stream)));
 }
 
+moeq_status moeq_fp8_quant_rows(const void* x, moeq_dtype dtype, int64_t ld, int rows, int K, uint8_t* codes,
+                                float* scales, void* stream) {
+    if (rows < 0 || rows > kMaxPairs || !type_ok(dtype)) return MOEQ_ERR_INVALID_ARG;
+    if (K < 1 || K > kMaxWidth) return MOEQ_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0) return MOEQ_OK;
+    if (!rows_ok(x, dtype, ld, K) || !al(codes, 16) || !al(scales, 4)) return MOEQ_ERR_INVALID_ARG;
+    if (!current_device().ok) return MOEQ_ERR_DEVICE;
+    return cuda_status(launch_fp8_quant_rows({x, ld, dtype == MOEQ_F32}, rows, K, codes, scales, as_stream(stream)));
+}
+
+moeq_status moeq_fp8_dequant_rows(const uint8_t* codes, const float* scales, int rows, int K, void* out, moeq_dtype dtype,
+                                  int64_t ld, void* stream) {
+    if (rows < 0 || rows > kMaxPairs || !type_ok(dtype)) return MOEQ_ERR_INVALID_ARG;
+    if (K < 1 || K > kMaxWidth) return MOEQ_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0) return MOEQ_OK;
+    if (!rows_ok(out, dtype, ld, K) || !al(codes, 16) || !al(scales, 4)) return MOEQ_ERR_INVALID_ARG;
+    if (!current_device().ok) return MOEQ_ERR_DEVICE;
+    return cuda_status(launch_fp8_gather_rows(codes, scales, rows, K, 1, nullptr, 0, nullptr, {out, ld, dtype == MOEQ_F32},
+                                              as_stream(stream)));
+}
+
+moeq_status moeq_fp8_gather_rows(const uint8_t* codes, const float* scales, int T, int H, int top_k, const int32_t* offs,
+                                 int E, const int32_t* pair_row, void* xs, moeq_dtype dtype, int64_t ld_xs, void* stream) {
+    if (!slots_ok(T, top_k, E) || !type_ok(dtype)) return MOEQ_ERR_INVALID_ARG;
+    if (H < 1 || H > kMaxWidth) return MOEQ_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MOEQ_OK;
+    if (!rows_ok(xs, dtype, ld_xs, H) || !al(codes, 16) || !al(scales, 4) || !al(offs, 4) || !al(pair_row, 4))
+        return MOEQ_ERR_INVALID_ARG;
+    if (!current_device().ok) return MOEQ_ERR_DEVICE;
+    return cuda_status(launch_fp8_gather_rows(codes, scales, T, H, top_k, offs, E, pair_row,
+                                              {xs, ld_xs, dtype == MOEQ_F32}, as_stream(stream)));
+}
+
+moeq_status moeq_swiglu_rows(const void* gu, moeq_dtype dtype, int64_t ld_gu, int R, int I, const int32_t* row_pair_opt,
+                             const float* topk_w_opt, void* h, int64_t ld_h, uint8_t* codes_opt, float* scales_opt,
+                             void* stream) {
+    if (R < 0 || R > kMaxPairs || !type_ok(dtype) || !codes_opt != !scales_opt || (topk_w_opt && !row_pair_opt))
+        return MOEQ_ERR_INVALID_ARG;
+    if (I < 1 || I > kMaxWidth) return MOEQ_ERR_UNSUPPORTED_SHAPE;
+    if (R == 0) return MOEQ_OK;
+    if (!rows_ok(gu, dtype, ld_gu, 2 * static_cast<int64_t>(I)) || !rows_ok(h, dtype, ld_h, I) ||
+        (codes_opt && (!al(codes_opt, 16) || !al(scales_opt, 4))) || (row_pair_opt && !al(row_pair_opt, 4)) ||
+        (topk_w_opt && !al(topk_w_opt, 4)))
+        return MOEQ_ERR_INVALID_ARG;
+    if (!current_device().ok) return MOEQ_ERR_DEVICE;
+    const int f32 = dtype == MOEQ_F32;
+    return cuda_status(launch_swiglu_rows({gu, ld_gu, f32}, R, I, row_pair_opt, topk_w_opt, {h, ld_h, f32}, codes_opt,
+                                          scales_opt, as_stream(stream)));
+}
+
+moeq_status moeq_swiglu_rows_grad(const void* d_h, moeq_dtype dtype, int64_t ld_dh, const uint8_t* codes,
+                                  const float* scales, int R, int I, const int32_t* row_pair_opt, const float* topk_w_opt,
+                                  const int32_t* pair_row_opt, void* d_gu, int64_t ld_dgu, void* h_opt, int64_t ld_h,
+                                  float* d_topk_w_opt, void* stream) {
+    if (R < 0 || R > kMaxPairs || !type_ok(dtype) || (topk_w_opt && !row_pair_opt) ||
+        (d_topk_w_opt && (!topk_w_opt || !pair_row_opt)))
+        return MOEQ_ERR_INVALID_ARG;
+    if (I < 1 || I > kMaxWidth) return MOEQ_ERR_UNSUPPORTED_SHAPE;
+    if (R == 0) return MOEQ_OK;
+    if (!rows_ok(d_h, dtype, ld_dh, I) || !rows_ok(d_gu, dtype, ld_dgu, 2 * static_cast<int64_t>(I)) || !al(codes, 16) ||
+        !al(scales, 4) || (h_opt && !rows_ok(h_opt, dtype, ld_h, I)) || (row_pair_opt && !al(row_pair_opt, 4)) ||
+        (topk_w_opt && !al(topk_w_opt, 4)) || (pair_row_opt && !al(pair_row_opt, 4)) ||
+        (d_topk_w_opt && !al(d_topk_w_opt, 4)))
+        return MOEQ_ERR_INVALID_ARG;
+    if (!current_device().ok) return MOEQ_ERR_DEVICE;
+    const int f32 = dtype == MOEQ_F32;
+    return cuda_status(launch_swiglu_rows_grad({d_h, ld_dh, f32}, codes, scales, R, I, row_pair_opt, topk_w_opt,
+                                               pair_row_opt, {d_gu, ld_dgu, f32}, {h_opt, ld_h, f32}, d_topk_w_opt,
+                                               as_stream(stream)));
+}
+
 }  // extern "C"

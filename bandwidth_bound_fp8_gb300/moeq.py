@@ -48,6 +48,7 @@ EXPORTS = [
     "moeq_mx4_weight_scale_bytes", "moeq_mx4_quant_act", "moeq_mx4_dequant_act", "moeq_mx4_quant_weight",
     "moeq_mx4_pack_weight", "moeq_mx4_expert_gemm_workspace_size", "moeq_mx4_expert_gemm",
     "moeq_expert_product", "moeq_expert_product_grad_x", "moeq_expert_product_grad_w",
+    "moeq_fp8_quant_rows", "moeq_fp8_dequant_rows", "moeq_fp8_gather_rows", "moeq_swiglu_rows", "moeq_swiglu_rows_grad",
 ]
 
 
@@ -136,6 +137,11 @@ def load(path: str = LIB_PATH):
         "moeq_expert_product": (_i, [_vp, _ll, _vp, _i, _i, _vp, _i, _i, _vp, _i, _ll, _vp, _vp]),
         "moeq_expert_product_grad_x": (_i, [_vp, _ll, _vp, _i, _i, _vp, _i, _i, _vp, _i, _ll, _vp, _vp]),
         "moeq_expert_product_grad_w": (_i, [_vp, _ll, _vp, _ll, _i, _i, _vp, _i, _i, _vp, _i, _vp, _vp]),
+        "moeq_fp8_quant_rows": (_i, [_vp, _i, _ll, _i, _i, _vp, _vp, _vp]),
+        "moeq_fp8_dequant_rows": (_i, [_vp, _vp, _i, _i, _vp, _i, _ll, _vp]),
+        "moeq_fp8_gather_rows": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _i, _ll, _vp]),
+        "moeq_swiglu_rows": (_i, [_vp, _i, _ll, _i, _i, _vp, _vp, _vp, _ll, _vp, _vp, _vp]),
+        "moeq_swiglu_rows_grad": (_i, [_vp, _i, _ll, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _ll, _vp, _ll, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -702,3 +708,79 @@ def moeq_expert_product_grad_w(d_y, x, offs, d_w, status=None, stream=None) -> N
     _check("moeq_expert_product_grad_w", (_lib or load()).moeq_expert_product_grad_w(
         yp, ld_y, xp, ld_x, K, N, _offs(offs)[1], E, R, _packed(d_w, d_w.dtype, (E, N, K), "d_w"), _dtype(d_w),
         _word(status), _queue(stream)))
+
+
+# ------------------------------------------------- activations in 8 bits
+def fp8_groups(K: int) -> int:
+    """Scales of a row of K columns."""
+    return (K + MOEQ_GROUP - 1) // MOEQ_GROUP
+
+
+def _codes8(codes, scales, rows, K, halves=1):
+    return (_packed(codes, torch.uint8, (rows, halves * K), "codes"),
+            _packed(scales, torch.float32, (rows, halves * fp8_groups(K)), "scales"))
+
+
+def moeq_fp8_quant_rows(x, codes, scales, stream=None) -> None:
+    """x [rows, K] bf16 or fp32 -> codes [rows, K] uint8, scales [rows, fp8_groups(K)] fp32."""
+    rows, K = x.shape
+    _check("moeq_fp8_quant_rows", (_lib or load()).moeq_fp8_quant_rows(
+        x.data_ptr(), _dtype(x), _ld(x, "x"), rows, K, *_codes8(codes, scales, rows, K), _queue(stream)))
+
+
+def moeq_fp8_dequant_rows(codes, scales, out, stream=None) -> None:
+    """The values that codes and scales stand for: out [rows, K] bf16 or fp32."""
+    rows, K = out.shape
+    _check("moeq_fp8_dequant_rows", (_lib or load()).moeq_fp8_dequant_rows(
+        *_codes8(codes, scales, rows, K), rows, K, out.data_ptr(), _dtype(out), _ld(out, "out"), _queue(stream)))
+
+
+def moeq_fp8_gather_rows(codes, scales, offs, pair_row, xs, stream=None) -> None:
+    """xs[pair_row[t, j]] = the values of row t; rows of xs from offs[E] on are zeroed."""
+    T, k, pr = _pairs(pair_row)
+    E, of = _offs(offs)
+    H = xs.shape[1]
+    if xs.shape != (T * k, H):
+        raise ValueError(f"xs [{T * k}, H] is wanted, got {tuple(xs.shape)}")
+    _check("moeq_fp8_gather_rows", (_lib or load()).moeq_fp8_gather_rows(
+        *_codes8(codes, scales, T, H), T, H, k, of, E, pr, xs.data_ptr(), _dtype(xs), _ld(xs, "xs"), _queue(stream)))
+
+
+def _row_weights(row_pair, topk_w, R):
+    """row_pair and topk_w, with as many elements as there are rows."""
+    if topk_w is not None and (row_pair is None or topk_w.numel() != R):
+        raise ValueError(f"topk_w: the weights of {R} pairs and their row_pair are wanted")
+    return (None if row_pair is None else _packed(row_pair, torch.int32, (R,), "row_pair"),
+            None if topk_w is None else _packed(topk_w, torch.float32, topk_w.shape, "topk_w"))
+
+
+def moeq_swiglu_rows(gu, h, row_pair=None, topk_w=None, codes=None, scales=None, stream=None) -> None:
+    """h[r] = w_r silu(gate) up for rows gu [R, 2I] (gate, then up), bf16 or fp32, w_r = topk_w[row_pair[r]] or 1; rows
+    without a pair are zeros.  With codes [R, 2I] and scales [R, 2 fp8_groups(I)], gate and up are kept in 8 bits."""
+    R, I = h.shape
+    if gu.shape != (R, 2 * I) or gu.dtype is not h.dtype:
+        raise ValueError(f"gu [{R}, {2 * I}] of h's type is wanted, got {gu.dtype} {tuple(gu.shape)}")
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales come together")
+    kept = (None, None) if codes is None else _codes8(codes, scales, R, I, 2)
+    _check("moeq_swiglu_rows", (_lib or load()).moeq_swiglu_rows(
+        gu.data_ptr(), _dtype(gu), _ld(gu, "gu"), R, I, *_row_weights(row_pair, topk_w, R), h.data_ptr(), _ld(h, "h"),
+        *kept, _queue(stream)))
+
+
+def moeq_swiglu_rows_grad(d_h, codes, scales, d_gu, h=None, row_pair=None, topk_w=None, pair_row=None, d_topk_w=None,
+                          stream=None) -> None:
+    """From what moeq_swiglu_rows kept: d_gu [R, 2I] of d_h [R, I], h again, and d_topk_w of topk_w."""
+    R, I = d_h.shape
+    if d_gu.shape != (R, 2 * I) or d_gu.dtype is not d_h.dtype:
+        raise ValueError(f"d_gu [{R}, {2 * I}] of d_h's type is wanted, got {d_gu.dtype} {tuple(d_gu.shape)}")
+    if h is not None and (h.shape != d_h.shape or h.dtype is not d_h.dtype):
+        raise ValueError("h: d_h's shape and type are wanted")
+    if d_topk_w is not None and (topk_w is None or pair_row is None or pair_row.numel() != R):
+        raise ValueError("d_topk_w: topk_w and the sort's pair_row are wanted")
+    rp, w = _row_weights(row_pair, topk_w, R)
+    _check("moeq_swiglu_rows_grad", (_lib or load()).moeq_swiglu_rows_grad(
+        d_h.data_ptr(), _dtype(d_h), _ld(d_h, "d_h"), *_codes8(codes, scales, R, I, 2), R, I, rp, w,
+        None if d_topk_w is None else _packed(pair_row, torch.int32, pair_row.shape, "pair_row"), d_gu.data_ptr(),
+        _ld(d_gu, "d_gu"), _p(h), 0 if h is None else _ld(h, "h"),
+        None if d_topk_w is None else _packed(d_topk_w, torch.float32, topk_w.shape, "d_topk_w"), _queue(stream)))

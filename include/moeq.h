@@ -631,6 +631,55 @@ moeq_status moeq_expert_product_grad_w(const void* d_y, int64_t ld_dy, const voi
                                        void* d_w, moeq_dtype dw_dtype,
                                        int32_t* status_opt, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Activations kept in 8 bits between the passes of a training step: the    */
+/* library's activation quantisation (numeric contract, above) for rows of  */
+/* any number, width and stride.                                            */
+/*   codes  [rows, K] u8, 16-byte aligned; scales [rows, ceil(K / 128)] fp32 */
+/*          (the last group of a row is shorter); contiguous                */
+/* A code stands for fl32(code * s), rounded once more to bf16 where that   */
+/* is the type asked for.  Unlike moeq_quant_act, a group with a NaN or an  */
+/* infinity gets the scale NaN and codes 0: it comes back as NaN.           */
+/*   moeq_fp8_quant_rows    x [rows, K] bf16 or fp32 -> codes, scales       */
+/*   moeq_fp8_dequant_rows  and back                                        */
+/*   moeq_fp8_gather_rows   xs[pair_row[t, j]] = the values of row t, as    */
+/*           moeq_gather_rows of them (rows from offs[E] on are zeroed)     */
+/* ------------------------------------------------------------------------ */
+moeq_status moeq_fp8_quant_rows(const void* x, moeq_dtype dtype, int64_t ld, int rows, int K,
+                                uint8_t* codes, float* scales, void* stream);
+moeq_status moeq_fp8_dequant_rows(const uint8_t* codes, const float* scales, int rows, int K,
+                                  void* out, moeq_dtype dtype, int64_t ld, void* stream);
+moeq_status moeq_fp8_gather_rows(const uint8_t* codes, const float* scales, int T, int H, int top_k,
+                                 const int32_t* offs, int E, const int32_t* pair_row,
+                                 void* xs, moeq_dtype dtype, int64_t ld_xs, void* stream);
+
+/* moeq_swiglu_rows -- h[r] = w_r silu(gate) up for rows gu [R, 2I], gate    */
+/* then up (bf16 or fp32, h of the same type), and with codes_opt and        */
+/* scales_opt (both or neither) gate and up in 8 bits, groups of their own:  */
+/* codes [R, 2I], scales [R, 2 ceil(I / 128)], gate's then up's.            */
+/*   row_pair_opt [R]: rows of a sort by expert (R = T * top_k). A row whose */
+/*           pair is not in [0, R) is not read; its h, codes and scales are  */
+/*           zeros.  NULL: every row is live                                */
+/*   topk_w_opt [R]: w_r = topk_w[row_pair[r]] (with row_pair_opt); NULL: 1.  */
+/*           With the routing weight in h, down's products add up to the    */
+/*           layer's output (moeq_gather_rows_grad), and its gradient needs  */
+/*           no product kept.                                               */
+/* moeq_swiglu_rows_grad -- from d_h and what was kept (x = gate's values,  */
+/* u = up's):  d_gu = (w_r d_h u silu'(x), w_r d_h silu(x)); h_opt = w_r    */
+/* silu(x) u again, for down's weight gradient; d_topk_w_opt [R] (with       */
+/* topk_w_opt and pair_row_opt [R], the sort's): <d_h, silu(x) u> at the     */
+/* pair's place, fp32 sums in a fixed order, 0 for a pair without a row.    */
+/* Rows that are not live get zeros.                                        */
+moeq_status moeq_swiglu_rows(const void* gu, moeq_dtype dtype, int64_t ld_gu, int R, int I,
+                             const int32_t* row_pair_opt, const float* topk_w_opt,
+                             void* h, int64_t ld_h, uint8_t* codes_opt, float* scales_opt, void* stream);
+moeq_status moeq_swiglu_rows_grad(const void* d_h, moeq_dtype dtype, int64_t ld_dh,
+                                  const uint8_t* codes, const float* scales, int R, int I,
+                                  const int32_t* row_pair_opt, const float* topk_w_opt,
+                                  const int32_t* pair_row_opt,
+                                  void* d_gu, int64_t ld_dgu, void* h_opt, int64_t ld_h,
+                                  float* d_topk_w_opt, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,6 +7,9 @@ tokens in one kernel.
 
 ``route``, ``dispatch`` and ``combine`` train: the same routing and movement
 as autograd functions, around whatever experts the caller's program has, to any order.
+``expert_product`` is the product of bf16 experts for it, to any order too;
+``swiglu`` and ``expert_mlp`` (the experts between dispatch and combine as one
+function) keep what their backward pass needs in 8 bits.
 """
 from __future__ import annotations
 
@@ -180,6 +183,215 @@ def dispatch(x: torch.Tensor, d: Dispatch) -> torch.Tensor:
 def combine(y: torch.Tensor, w: torch.Tensor, d: Dispatch, base: torch.Tensor | None = None) -> torch.Tensor:
     """base[t] + sum_j w[t, j] * y[row of (t, j)]."""
     return _Combine.apply(y.contiguous(), w.contiguous(), None if base is None else _rows(base), d.offs, d.pair_row)
+
+
+# ------------------------------------------------------- training: experts
+def _product(x, w, offs):
+    y = torch.empty((x.shape[0], w.shape[1]), dtype=x.dtype, device=x.device)
+    moeq.moeq_expert_product(x, w, offs, y)
+    return y
+
+
+def _product_grad_x(dy, w, offs):
+    dx = torch.empty((dy.shape[0], w.shape[2]), dtype=dy.dtype, device=dy.device)
+    moeq.moeq_expert_product_grad_x(dy, w, offs, dx)
+    return dx
+
+
+def _product_grad_w(dy, x, offs):
+    dw = torch.empty((offs.shape[0] - 1, dy.shape[1], x.shape[1]), dtype=x.dtype, device=x.device)
+    moeq.moeq_expert_product_grad_w(dy, x, offs, dw)
+    return dw
+
+
+def _copied(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy where tensor copies cannot read its rows: they start and step on 16 bytes."""
+    t = _rows(t)
+    fits = t.data_ptr() % 16 == 0 and (t.stride(0) % 8 == 0 or t.shape[0] <= 1)
+    return t if fits else t.clone(memory_format=torch.contiguous_format)
+
+
+# y = W x, dx = W^T dy and dW = dy x^T are linear in either argument, and each
+# one's derivatives are the other two.
+class _Product(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offs):
+        ctx.save_for_backward(x, w, offs)
+        return _product(x, w, offs)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, offs = ctx.saved_tensors
+        dy, need = _copied(dy), ctx.needs_input_grad
+        return (_grad(_ProductGradX, _product_grad_x)(dy, w, offs) if need[0] else None,
+                _grad(_ProductGradW, _product_grad_w)(dy, x, offs) if need[1] else None, None)
+
+
+class _ProductGradX(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, dy, w, offs):
+        ctx.save_for_backward(dy, w, offs)
+        return _product_grad_x(dy, w, offs)
+
+    @staticmethod
+    def backward(ctx, g):
+        dy, w, offs = ctx.saved_tensors
+        g, need = _copied(g), ctx.needs_input_grad
+        return (_grad(_Product, _product)(g, w, offs) if need[0] else None,
+                _grad(_ProductGradW, _product_grad_w)(dy, g, offs) if need[1] else None, None)
+
+
+class _ProductGradW(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, dy, x, offs):
+        ctx.save_for_backward(dy, x, offs)
+        return _product_grad_w(dy, x, offs)
+
+    @staticmethod
+    def backward(ctx, g):
+        dy, x, offs = ctx.saved_tensors
+        g, need = g.contiguous(), ctx.needs_input_grad
+        return (_grad(_Product, _product)(x, g, offs) if need[0] else None,
+                _grad(_ProductGradX, _product_grad_x)(dy, g, offs) if need[1] else None, None)
+
+
+class _Once(torch.autograd.Function):
+    """Ties gradients to what they depend on, so that a second differentiation raises instead of taking them for
+    constants."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(None if t is None else t.detach() for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("swiglu and expert_mlp keep their inputs in 8 bits: they are differentiable once")
+
+
+def _once(grads, *of):
+    """Gradients as a backward pass returns them; `of`: the tensors they depend on."""
+    return _Once.apply(len(grads), *grads, *of) if torch.is_grad_enabled() else grads
+
+
+def _keep8(x):
+    codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    scales = torch.empty((x.shape[0], moeq.fp8_groups(x.shape[1])), dtype=torch.float32, device=x.device)
+    moeq.moeq_fp8_quant_rows(x, codes, scales)
+    return codes, scales
+
+
+def _swiglu(gu, w, row_pair, keep):
+    """h, and gate and up in 8 bits where they are kept."""
+    R, I = gu.shape[0], gu.shape[1] // 2
+    h = torch.empty((R, I), dtype=gu.dtype, device=gu.device)
+    if not keep:
+        moeq.moeq_swiglu_rows(gu, h, row_pair=row_pair, topk_w=w)
+        return h, None, None
+    codes = torch.empty(gu.shape, dtype=torch.uint8, device=gu.device)
+    scales = torch.empty((R, 2 * moeq.fp8_groups(I)), dtype=torch.float32, device=gu.device)
+    moeq.moeq_swiglu_rows(gu, h, row_pair=row_pair, topk_w=w, codes=codes, scales=scales)
+    return h, codes, scales
+
+
+def _swiglu_grad(dh, codes, scales, w, pair_row, row_pair, need_w, again):
+    """d_gu, d_w where it is needed, and h where it is asked for again."""
+    dgu = torch.empty(codes.shape, dtype=dh.dtype, device=dh.device)
+    dw = torch.empty_like(w) if need_w else None
+    h = torch.empty_like(dh, memory_format=torch.contiguous_format) if again else None
+    moeq.moeq_swiglu_rows_grad(dh, codes, scales, dgu, h=h, row_pair=row_pair, topk_w=w, pair_row=pair_row, d_topk_w=dw)
+    return dgu, dw, h
+
+
+class _Swiglu(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gu, w, pair_row, row_pair, keep):
+        h, codes, scales = _swiglu(gu, w, row_pair, keep)
+        ctx.save_for_backward(codes, scales, w, pair_row, row_pair)
+        return h
+
+    @staticmethod
+    def backward(ctx, dh):
+        codes, scales, w, pair_row, row_pair = ctx.saved_tensors
+        dgu, dw, _ = _swiglu_grad(_rows(dh), codes, scales, w, pair_row, row_pair, ctx.needs_input_grad[1], False)
+        return (*_once((dgu, dw), dh, w), None, None, None)
+
+
+class _ExpertMlp(torch.autograd.Function):
+    """The routing weight is part of h, so that the rows of y add up to out, and its gradient is <d_h, h / w>: neither y
+    nor h is kept, and x and its gate and up rows are in 8 bits."""
+
+    @staticmethod
+    def forward(ctx, x, w, w_gu, w_d, offs, pair_row, row_pair, keep):
+        gu = _product(_gather(x, offs, pair_row), w_gu, offs)
+        h, codes, scales = _swiglu(gu, w, row_pair, keep)
+        del gu
+        x8 = _keep8(x) if keep and ctx.needs_input_grad[2] else (None, None)
+        ctx.save_for_backward(*x8, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair)
+        return _gather_grad(_product(h, w_d, offs), offs, pair_row)
+
+    @staticmethod
+    def backward(ctx, dout):
+        x_codes, x_scales, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair = ctx.saved_tensors
+        need_x, need_w, need_gu, need_d = ctx.needs_input_grad[:4]
+        with torch.no_grad():
+            dy = _gather(_rows(dout), offs, pair_row)
+            dgu, dw, h = _swiglu_grad(_product_grad_x(dy, w_d, offs), codes, scales, w, pair_row, row_pair, need_w, need_d)
+            dw_d = _product_grad_w(dy, h, offs) if need_d else None
+            del dy, h
+            dx = _gather_grad(_product_grad_x(dgu, w_gu, offs), offs, pair_row) if need_x else None
+            dw_gu = None
+            if need_gu:
+                xs = torch.empty((dgu.shape[0], w_gu.shape[2]), dtype=dgu.dtype, device=dgu.device)
+                moeq.moeq_fp8_gather_rows(x_codes, x_scales, offs, pair_row, xs)
+                dw_gu = _product_grad_w(dgu, xs, offs)
+        return (*_once((dx, dw, dw_gu, dw_d), dout, w, w_gu, w_d), None, None, None, None)
+
+
+def _experts_fit(what: str, w: torch.Tensor, d: Dispatch, width: int, name: str = "w") -> None:
+    if w.dim() != 3 or w.shape[0] != d.E or w.shape[2] != width:
+        raise ValueError(f"{what}: {name} [{d.E}, N, {width}] is wanted, got {tuple(w.shape)}")
+
+
+def _weights_fit(what: str, w: torch.Tensor, d: Dispatch) -> None:
+    if w.shape != d.pair_row.shape or w.dtype is not torch.float32:
+        raise ValueError(f"{what}: weights {tuple(d.pair_row.shape)} fp32 are wanted, got {w.dtype} {tuple(w.shape)}")
+
+
+def expert_product(x: torch.Tensor, w: torch.Tensor, d: Dispatch) -> torch.Tensor:
+    """w[e] x[r] for the rows [T * k, K] of dispatch, bf16, and w [E, N, K] bf16: [T * k, N], zero rows after the last.
+    K and N are multiples of 8."""
+    _experts_fit("expert_product", w, d, x.shape[-1])
+    return _Product.apply(_copied(x), w.contiguous(), d.offs)
+
+
+def swiglu(gu: torch.Tensor, d: Dispatch, w: torch.Tensor | None = None) -> torch.Tensor:
+    """w silu(gate) up for the rows gu [T * k, 2I] (gate, then up; bf16 or fp32), w [T, k] a pair's weight (None: 1).
+    The backward pass sees gate and up in 8 bits (groups of 128, moeq_fp8_quant_rows): half to a quarter of the bytes."""
+    if gu.dim() != 2 or gu.shape[0] != d.row_pair.shape[0] or gu.shape[1] % 2:
+        raise ValueError(f"swiglu: gu [{d.row_pair.shape[0]}, 2I] is wanted, got {tuple(gu.shape)}")
+    if w is not None:
+        _weights_fit("swiglu", w, d)
+        w = w.contiguous()
+    keep = torch.is_grad_enabled() and (gu.requires_grad or w is not None and w.requires_grad)
+    return _Swiglu.apply(_rows(gu), w, d.pair_row, d.row_pair, keep)
+
+
+def expert_mlp(x: torch.Tensor, w: torch.Tensor, w_gu: torch.Tensor, w_d: torch.Tensor, d: Dispatch) -> torch.Tensor:
+    """out[t] = sum_j w[t, j] expert_j(x[t]), expert = down(silu(gate x) * up x): x [T, H] bf16, w [T, k] fp32 as route
+    gives it, w_gu [E, 2I, H] (gate rows, then up rows) and w_d [E, H, I] bf16, H and I multiples of 8.  As
+    combine(expert_product(swiglu(expert_product(dispatch(x)))), w), with less kept for the backward pass: x [T, H] and
+    the gate and up rows [T * k, 2I] in 8 bits, and nothing else of its size."""
+    if x.dim() != 2 or x.shape[0] != d.pair_row.shape[0] or x.dtype is not torch.bfloat16:
+        raise ValueError(f"expert_mlp: x [{d.pair_row.shape[0]}, H] bf16 is wanted, got {x.dtype} {tuple(x.shape)}")
+    _weights_fit("expert_mlp", w, d)
+    H = x.shape[1]
+    _experts_fit("expert_mlp", w_gu, d, H, "w_gu")
+    if w_gu.shape[1] % 2 or w_d.shape != (d.E, H, w_gu.shape[1] // 2):
+        raise ValueError(f"expert_mlp: w_gu [{d.E}, 2I, {H}] and w_d [{d.E}, {H}, I] are wanted, got {tuple(w_gu.shape)} "
+                         f"and {tuple(w_d.shape)}")
+    keep = torch.is_grad_enabled() and any(t.requires_grad for t in (x, w, w_gu, w_d))
+    return _ExpertMlp.apply(_rows(x), w.contiguous(), w_gu.contiguous(), w_d.contiguous(), d.offs, d.pair_row, d.row_pair,
+                            keep)
 
 
 # ------------------------------------------------------------------- serving

@@ -1,0 +1,176 @@
+"""What expert_layer makes of its training calls, on the CPU: the calls are
+replaced by plain forms that write through .data, as the kernels write through
+pointers."""
+import pytest
+import torch
+
+import keep_plain as kp
+import rows_standins
+
+F = torch.nn.functional
+
+
+def _each(offs, E):
+    return [(e, slice(int(offs[e]), int(offs[e + 1]))) for e in range(E)]
+
+
+def _fits(t):
+    """Rows that tensor copies can read."""
+    assert t.dim() == 2 and t.stride(1) == 1 and t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or t.stride(0) % 8 == 0)
+
+
+def product(x, w, offs, y, status=None, stream=None):
+    _fits(x)
+    assert w.is_contiguous()
+    y.data.zero_()
+    for e, at in _each(offs, w.shape[0]):
+        y.data[at] = x.data[at] @ w.data[e].t()
+
+
+def product_grad_x(dy, w, offs, dx, status=None, stream=None):
+    _fits(dy)
+    dx.data.zero_()
+    for e, at in _each(offs, w.shape[0]):
+        dx.data[at] = dy.data[at] @ w.data[e]
+
+
+def product_grad_w(dy, x, offs, dw, status=None, stream=None):
+    _fits(dy), _fits(x)
+    for e, at in _each(offs, dw.shape[0]):
+        dw.data[e] = dy.data[at].t() @ x.data[at]
+
+
+def quant(x, codes, scales, stream=None):
+    c, s = kp.keep(x.detach().float().numpy())
+    codes.copy_(torch.from_numpy(c))
+    scales.copy_(torch.from_numpy(s))
+
+
+def gather8(codes, scales, offs, pair_row, xs, stream=None):
+    v = torch.from_numpy(kp.values(codes.numpy(), scales.numpy())).to(xs.dtype)
+    rows_standins.gather_rows(v, offs, pair_row, xs)
+
+
+def _w(row_pair, w):
+    live = row_pair >= 0
+    v = torch.ones(row_pair.shape[0], dtype=torch.float64) if w is None else w.data.reshape(-1)[row_pair.clamp(min=0).long()].double()
+    return torch.where(live, v, torch.zeros((), dtype=torch.float64)).numpy(), live
+
+
+def swiglu(gu, h, row_pair=None, topk_w=None, codes=None, scales=None, stream=None):
+    w, live = _w(row_pair, topk_w)
+    z = torch.where(live[:, None], gu.data, torch.zeros((), dtype=gu.dtype)).double().numpy()
+    I = z.shape[1] // 2
+    h.data.copy_(torch.from_numpy(kp.swiglu(z[:, :I], z[:, I:], w)))
+    if codes is not None:
+        c, s = kp.keep_gate_up(z.astype("float32"))
+        codes.copy_(torch.from_numpy(c))
+        scales.copy_(torch.from_numpy(s))
+
+
+def swiglu_grad(d_h, codes, scales, d_gu, h=None, row_pair=None, topk_w=None, pair_row=None, d_topk_w=None, stream=None):
+    w, live = _w(row_pair, topk_w)
+    gate, up = (v.astype("float64") for v in kp.values_gate_up(codes.numpy(), scales.numpy()))
+    dg, du, hh, dw = kp.swiglu_grad(d_h.data.double().numpy(), gate, up, w)
+    d_gu.data.copy_(torch.cat((torch.from_numpy(dg), torch.from_numpy(du)), 1))
+    if h is not None:
+        h.data.copy_(torch.from_numpy(hh))
+    if d_topk_w is not None:
+        d_topk_w.data.zero_()
+        d_topk_w.data.view(-1)[row_pair[live].long()] = torch.from_numpy(dw).float()[live]
+
+
+@pytest.fixture()
+def el(monkeypatch):
+    from bandwidth_bound_fp8_gb300 import expert_layer, moeq
+    rows_standins.use(monkeypatch)
+    for name, f in (("expert_product", product), ("expert_product_grad_x", product_grad_x),
+                    ("expert_product_grad_w", product_grad_w), ("fp8_quant_rows", quant), ("fp8_gather_rows", gather8),
+                    ("swiglu_rows", swiglu), ("swiglu_rows_grad", swiglu_grad)):
+        monkeypatch.setattr(moeq, "moeq_" + name, f)
+    return expert_layer
+
+
+def _plan(el, T=9, E=4, k=2, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32)
+    ids[0, 1] = -1
+    ids[2] = -1
+    return el.Dispatch(ids, E), ids
+
+
+def _leaf(g, *s, dt=torch.float64, scale=1.0):
+    return (scale * torch.randn(s, generator=g, dtype=torch.float64)).to(dt).requires_grad_()
+
+
+def test_product_gradients_to_second_order(el):
+    """In 64 bits, against differences."""
+    d, _ = _plan(el)
+    g = torch.Generator().manual_seed(1)
+    R, K, N = d.row_pair.numel(), 8, 16
+    x, w = _leaf(g, R, K), _leaf(g, 4, N, K)
+    f = lambda x, w: el.expert_product(x, w, d)
+    assert torch.autograd.gradcheck(f, (x, w))
+    assert torch.autograd.gradgradcheck(f, (x, w))
+
+
+def test_product_takes_any_layout(el):
+    """Rows that tensor copies cannot read are copied; an expanded gradient too."""
+    d, _ = _plan(el)
+    g = torch.Generator().manual_seed(2)
+    R, K, N = d.row_pair.numel(), 8, 16
+    x, w = _leaf(g, R, K), _leaf(g, 4, N, K)
+    want = torch.autograd.grad(el.expert_product(x, w, d).sum(), (x, w))
+    odd = torch.zeros((R, K + 3), dtype=torch.float64)
+    odd[:, 1:K + 1] = x.detach()
+    odd.requires_grad_()
+    wt = w.detach().transpose(1, 2).contiguous().requires_grad_()
+    gx, gw = torch.autograd.grad(el.expert_product(odd[:, 1:K + 1], wt.transpose(1, 2), d).sum(), (odd, wt))
+    assert torch.equal(gx[:, 1:K + 1], want[0]) and torch.equal(gw.transpose(1, 2), want[1])
+
+
+def _values(t):
+    return torch.from_numpy(kp.values(*kp.keep(t.detach().float().numpy()))).to(t.dtype)
+
+
+def test_swiglu_sees_eight_bits(el):
+    """Its gradient is the formula's at the 8-bit values; without a gradient nothing is kept."""
+    d, _ = _plan(el)
+    g = torch.Generator().manual_seed(3)
+    R, I = d.row_pair.numel(), 24
+    gu, w = _leaf(g, R, 2 * I, dt=torch.float32), _leaf(g, 9, 2, dt=torch.float32)
+    dh = torch.randn(R, I, generator=g)
+    h = el.swiglu(gu, d, w)
+    got = torch.autograd.grad(h, (gu, w), dh)
+    at = torch.cat((_values(gu[:, :I]), _values(gu[:, I:])), 1).double().requires_grad_()
+    w64 = w.detach().double().requires_grad_()
+    live = d.row_pair >= 0
+    wr = torch.where(live, w64.reshape(-1)[d.row_pair.clamp(min=0).long()], torch.zeros((), dtype=torch.float64))
+    want = torch.autograd.grad(wr[:, None] * F.silu(at[:, :I]) * at[:, I:], (at, w64), dh.double())
+    for a, b in zip(got, want):
+        assert torch.allclose(a.double(), b, rtol=1e-5, atol=1e-6)
+    with torch.no_grad():
+        assert torch.equal(el.swiglu(gu, d, w), h)
+    (once,) = torch.autograd.grad(el.swiglu(gu, d, w), gu, dh, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        once.sum().backward()
+
+
+def test_expert_mlp_refuses_what_does_not_fit(el):
+    d, _ = _plan(el)
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)
+    ok = dict(x=z(9, 16), w=z(9, 2, dt=torch.float32), w_gu=z(4, 48, 16), w_d=z(4, 16, 24))
+    call = lambda **kw: el.expert_mlp(*{**ok, **kw}.values(), d)
+    for bad in (dict(x=z(8, 16)), dict(x=z(9, 16, dt=torch.float32)), dict(w=z(9, 3, dt=torch.float32)), dict(w=z(9, 2)),
+                dict(w_gu=z(5, 48, 16)), dict(w_gu=z(4, 48, 8)), dict(w_gu=z(4, 47, 16)), dict(w_d=z(4, 16, 23)),
+                dict(w_d=z(4, 24, 16)), dict(w_d=z(3, 16, 24))):
+        with pytest.raises(ValueError, match="expert_mlp"):
+            call(**bad)
+    with pytest.raises(ValueError, match="expert_product"):
+        el.expert_product(z(18, 16), z(4, 48, 8), d)
+    with pytest.raises(ValueError, match="swiglu"):
+        el.swiglu(z(18, 15), d)
+    with pytest.raises(ValueError, match="swiglu"):
+        el.swiglu(z(17, 16), d)
+    with pytest.raises(ValueError, match="swiglu"):
+        el.swiglu(z(18, 16), d, z(9, 2))

@@ -381,3 +381,30 @@ def test_offsets_past_32_bits():
     out = torch.empty((R, 2 * I), dtype=BF, device="cuda")
     moeq.moeq_fp8_dequant_rows(codes, scales, out)
     assert torch.equal(out[-1].cpu(), torch.from_numpy(kp.values(c, scales[-1:].cpu().numpy())[0]).to(BF))
+
+
+def test_refusals():
+    """On the device: shapes and types that do not fit each other, and nothing is written."""
+    from bandwidth_bound_fp8_gb300 import moeq
+    z = lambda *s, dt=F32: torch.zeros(s, dtype=dt, device="cuda")
+    u8, i32 = torch.uint8, torch.int32
+    offs, pr, rp_ = z(4, dt=i32), z(4, 2, dt=i32), z(8, dt=i32)
+    with pytest.raises(ValueError, match="xs"):
+        moeq.moeq_fp8_gather_rows(z(4, 64, dt=u8), z(4, 1), offs, pr, z(7, 64))
+    with pytest.raises(ValueError, match="codes"):
+        moeq.moeq_fp8_gather_rows(z(5, 64, dt=u8), z(4, 1), offs, pr, z(8, 64))
+    with pytest.raises(ValueError, match="scales"):
+        moeq.moeq_fp8_quant_rows(z(4, 129), z(4, 129, dt=u8), z(4, 1))
+    with pytest.raises(TypeError):
+        moeq.moeq_fp8_quant_rows(z(4, 64, dt=torch.float16), z(4, 64, dt=u8), z(4, 1))
+    with pytest.raises(ValueError, match="row_pair"):
+        moeq.moeq_swiglu_rows(z(8, 64), z(8, 32), row_pair=rp_[:7], topk_w=z(4, 2))
+    with pytest.raises(ValueError, match="topk_w"):
+        moeq.moeq_swiglu_rows(z(8, 64), z(8, 32), row_pair=rp_, topk_w=z(4, 3))
+    with pytest.raises(ValueError, match="d_topk_w"):
+        moeq.moeq_swiglu_rows_grad(z(8, 32), z(8, 64, dt=u8), z(8, 2), z(8, 64), row_pair=rp_, topk_w=z(4, 2), pair_row=pr,
+                                   d_topk_w=z(2, 4))
+    with pytest.raises(moeq.MoeqError):
+        moeq.moeq_expert_product(z(8, 60, dt=BF), z(3, 64, 60, dt=BF), offs, z(8, 64))
+    with pytest.raises(ValueError, match="x:"):
+        moeq.moeq_expert_product_grad_w(z(8, 64, dt=BF), z(7, 64, dt=BF), offs, z(3, 64, 64))

@@ -20,9 +20,9 @@
 // contraction over the expert's rows in stages of 64.  Rows are sorted, so a
 // stage may reach past the expert's last row: what follows are another
 // expert's rows (or a NaN in a masked place), and 0 * NaN is not 0.  So the
-// last stage is copied row-exactly, in boxes of 32, 16, .. 1 rows, and filled
-// up to the MMA's 16 rows from beyond the matrix, where a tensor copy reads
-// zeros.
+// last stage is copied row-exactly, in boxes of a power of two of rows, and
+// filled up to the MMA's 16 rows from beyond the matrix, where a tensor copy
+// reads zeros.
 #include "moeq_mx4_plan.cuh"
 #include "moeq_pair.cuh"
 #include "moeq_rows.h"
@@ -37,6 +37,10 @@ constexpr int kMaxStages = 7;
 // Most rows of a tile, for one CTA and for a pair.
 constexpr int kSingleTileRows = 128, kPairTileRows = 256;
 constexpr int kPairRows = 128;  // tiles of this many are a pair's
+// Steps of 16 contraction indices that one accumulator takes where the output
+// is fp32: the tensor core truncates as it accumulates, so parts of 512 are
+// summed in registers.
+constexpr int kRun = 32;
 constexpr int kBand = 8;                        // row tiles that take turns on the same weights
 
 __host__ __device__ constexpr int stage_bytes_of(int nt, bool pair) { return kTileBytes + nt / (pair ? 2 : 1) * 128; }
@@ -107,6 +111,7 @@ __device__ __forceinline__ void copy3(void* dst, const CUtensorMap* map, int x, 
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
             : "memory");
 }
+// A box out of shared memory.
 __device__ __forceinline__ void store3(const CUtensorMap* map, const void* src, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
@@ -144,7 +149,7 @@ __device__ __forceinline__ uint32_t set_up(Shared& s, int stages, const Mx4Plan&
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.acc_full[i], 1);
-            mbar_init(&s.acc_empty[i], kPair ? 8 : 4);
+            mbar_init(&s.acc_empty[i], kPair ? 16 : 4);  // every epilogue warp of both CTAs
         }
         mbar_init(&s.drained, 1);
         for (int i = 0; i < 4; ++i) {
@@ -235,30 +240,75 @@ __device__ __forceinline__ bool push_part(Shared& s, int i, uint32_t part, volat
 
 // Whether the four warps of an epilogue group go on to a part whose
 // accumulator they wait for: one thread decides for all, because they meet at
-// barriers.  (A copy a turn: a slow warp may still read the last unit's.)
+// barriers.  (A copy a turn: a slow warp may still read the last part's.)
 template <typename GiveUp>
-__device__ __forceinline__ bool part_done(Shared& s, int i, int group, int groups, int lane, bool chief,
-                                          volatile int* abort, GiveUp give_up) {
-    const int turn = i / groups & 1;
+__device__ __forceinline__ bool part_done(Shared& s, int i, int group, int lane, bool chief, volatile int* abort,
+                                          GiveUp give_up) {
     if (lane == 0 && !mbar_wait_bounded(&s.acc_full[i & 1], (i >> 1) & 1, abort)) give_up();
     __syncwarp();
-    if (chief) s.go[group][turn] = !*abort;
+    if (chief) s.go[group][i & 1] = !*abort;
     named_sync(1 + group, 128);
-    if (!s.go[group][turn]) return false;
+    if (!s.go[group][i & 1]) return false;
     tc_fence_after();
     return true;
 }
-// The accumulator is read: the next unit but one may have it.
+// The accumulator is read: the next part but one may have it.  The arrival at
+// the other CTA's barrier is relaxed: the fence orders the accumulator, and a
+// release to the cluster would wait for this thread's stores of the part
+// before (1.2 us: 954 us where dW's stores alone take 554).
 template <bool kPair>
 __device__ __forceinline__ void release_acc(Shared& s, int buf, int rank, int lane) {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
         if (kPair && rank == 1)
-            arrive_first(&s.acc_empty[buf]);
+            asm volatile(
+                "{ .reg .b32 r; mapa.shared::cluster.u32 r, %0, 0;\n"
+                "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [r]; }" ::"r"(smem_u32(&s.acc_empty[buf]))
+                : "memory");
         else
             mbar_arrive(&s.acc_empty[buf]);
     }
+}
+// A part's `cols` columns (at most 128) of this thread's lane into registers,
+// or added to what is there; then the accumulator is free.  All loads of a
+// first part are in flight at once: the MMAs of the part after next wait for
+// them.
+template <bool kPair, int kA, int kB>
+__device__ __forceinline__ void take_acc(Shared& s, int buf, uint32_t acc, int cols, bool first, int rank, int lane,
+                                         float (&v)[kA][kB]) {
+    static_assert(kA * kB == 128 && kB % 16 == 0, "128 columns");
+    if (first) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 16)
+            if (c < cols) tmem_ld16(acc + c, v[c / kB] + c % kB);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) tmem_use16(v[c / kB] + c % kB);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 128; c += 16)
+            if (c < cols) {
+                float t[16];
+                tmem_ld16(acc + c, t);
+                tmem_wait_ld();
+                tmem_use16(t);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[c / kB][c % kB + k] += t[k];
+            }
+    }
+    release_acc<kPair>(s, buf, rank, lane);
+}
+
+// A pair's 384 threads start with 168 registers each; the epilogue's 256 take
+// 40 more from the 128 that copy and issue: 128 * 88 + 256 * 208 = 384 * 168.
+template <bool kPair>
+__device__ __forceinline__ void give_registers() {
+    if constexpr (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+}
+template <bool kPair>
+__device__ __forceinline__ void take_registers() {
+    if constexpr (kPair) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
 }
 
 // ----------------------------------------------------------------- rows out
@@ -302,7 +352,7 @@ __device__ __forceinline__ bool part_at(const RowsArgs& a, const PlanShared& pla
 }
 
 template <bool kF32, bool kPair, bool kTrans>
-__global__ void __maxnreg__(160)
+__global__ void __launch_bounds__(threads_of(kPair), 1)
     product_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ RowsMaps maps) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Shared s;
@@ -317,12 +367,14 @@ __global__ void __maxnreg__(160)
     volatile int* abort = &s.abort;
     const int workers = gridDim.x / (kPair ? 2 : 1), worker = blockIdx.x / (kPair ? 2 : 1);
     const int nbu = kPair ? (a.N + 255) / 256 : (a.N + 127) / 128, kb_n = (a.C + kBlock - 1) / kBlock;
+    const int steps_n = 4 * kb_n, run = kF32 ? kRun : steps_n;  // of 16; a part's
     auto part = [&](int i, Part& p) { return part_at<kPair>(a, plan, i, worker, workers, nbu, rank, p); };
     auto give_up = [&] {
         *abort = 1;
         if (a.status) atomicExch(a.status, static_cast<int>(MOEQ_ERR_TIMEOUT));
     };
 
+    if (warp < 4) give_registers<kPair>();
     if (warp == 0 || warp == 2) {
         // -------------------------------------------------------- copies
         if (elect_one()) {
@@ -382,16 +434,20 @@ __global__ void __maxnreg__(160)
         if (rank == 0 && elect_one()) {
             Part p;
             bool more = true, ok = true;
-            for (int i = 0; ok && more; ++i) {
-                more = part(i, p);
-                ok = push_part(s, i, more ? part_of(p.n_mma, 4 * kb_n) : 0, abort);
+            for (int u = 0, i = 0; ok && more;) {
+                more = part(u++, p);
+                if (!more) ok = push_part(s, i, 0, abort);
+                for (int k0 = 0; ok && more && k0 < steps_n; k0 += run)
+                    ok = push_part(s, i++, part_of(p.n_mma, min(run, steps_n - k0)), abort);
             }
             if (!ok) give_up();
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------- epilogue
-        constexpr int kGroups = epi_groups(kPair);
+        take_registers<kPair>();
+        // Lane = feature.  A pair's two groups share a tile's columns.
+        constexpr int kGroups = epi_groups(kPair), kCols = epi_cols(kF32, kPair);
         const int q = warp & 3, group = (warp >> 2) - 1, bar = 1 + group;
         const bool chief = tid == 128 + group * 128;
         uint8_t* stage_y = epi_mem + group * epi_bytes(kPair);
@@ -399,22 +455,22 @@ __global__ void __maxnreg__(160)
         const bool vec_y = a.N % (kF32 ? 4 : 8) == 0 && a.ld_y % (kF32 ? 4 : 8) == 0 &&
                            (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
         Part p;
-        for (int i = group; part(i, p); i += kGroups) {
-            const int buf = i & 1;
-            if (!part_done(s, i, group, kGroups, lane, chief, abort, give_up)) break;
-            const uint32_t acc = tmem + buf * kAcc1 + (static_cast<uint32_t>(q * 32) << 16);
-            const int n = p.n0 + q * 32 + lane;
-            constexpr int kCols = epi_cols(kF32, kPair);
-            for (int c0 = 0; c0 < p.n; c0 += kCols) {
-                float v[kCols];  // columns past the tile's are read and not stored
-#pragma unroll
-                for (int j = 0; j < kCols; j += 16) tmem_ld16(acc + c0 + j, v + j);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < kCols; j += 16) tmem_use16(v + j);
-                if (c0 + kCols >= p.n) release_acc<kPair>(s, buf, rank, lane);
-                store_step<kF32, kCols>(a, p, c0, q, lane, n, v, stage_y, vec_y, bar);
+        bool ok = true;
+        for (int u = 0, i = 0; part(u, p); ++u) {
+            const int share = kPair ? p.n_mma / 2 : p.n_mma, base = group * share, cols = min(share, p.n - base);
+            float v[128 / kCols][kCols];
+            for (int k0 = 0; ok && k0 < steps_n; k0 += run, ++i) {
+                ok = part_done(s, i, group, lane, chief, abort, give_up);
+                if (!ok) break;
+                const uint32_t acc = tmem + (i & 1) * kAcc1 + base + (static_cast<uint32_t>(q * 32) << 16);
+                take_acc<kPair>(s, i & 1, acc, cols, k0 == 0, rank, lane, v);
             }
+            if (!ok) break;
+            const int n = p.n0 + q * 32 + lane;
+            p.n = base + cols;
+#pragma unroll
+            for (int c = 0; c < 128; c += kCols)
+                if (c < cols) store_step<kF32, kCols>(a, p, base + c, q, lane, n, v[c / kCols], stage_y, vec_y, bar);
         }
         // rows that belong to no expert
         const int t = tid - 128, per = vec_y ? (kF32 ? 4 : 8) : 1;
@@ -449,8 +505,7 @@ struct WeightsMaps {
     CUtensorMap dw;
 };
 constexpr int kWStageBytes = 2 * kTileBytes;  // a CTA's 128 rows of dW, and half of the 256 columns
-constexpr int kWStages = 5;
-constexpr int kWEpiBytes = 4096;              // a warp's 32 rows of 128 bytes
+constexpr int kWEpiBytes = 8 * 4096;          // 128 bytes of 32 rows for each epilogue warp
 
 struct WPart {
     int e, n0, k0, r0, cnt;
@@ -468,39 +523,61 @@ __device__ __forceinline__ bool wpart_at(const WeightsArgs& a, const PlanShared&
     return true;
 }
 
-// Up to 64 rows of 128 columns, r0 on, into a stage; the rows past the
-// expert's last up to the next multiple of 16 are zeros (R: past the matrix).
+// 64 rows of 128 columns, or fewer at the end of an expert's, into a stage.
+// Then the rows up to the next multiple of 16 are zeros, read from beyond the
+// matrix (R).  Two boxes of the largest power of two cover any count, one from
+// each end (what both write is the same); zeros may also run on into rows that
+// no MMA reads.  (A box for each bit of the count: 64 experts of 383 rows, K
+// 6144, N 4096, took 1030 us where 384 take 868.)
+struct Boxes {
+    int m, n;      // maps[m]: 64 >> m rows; how many boxes
+    int at, last;  // rows of the stage where they start
+};
+__device__ __forceinline__ Boxes boxes_of(int at, int rows, bool may_pass) {
+    Boxes b{0, 0, at, at};
+    if (rows == 0) return b;
+    b.m = __clz(rows) - 25;  // the largest box of at most `rows` rows
+    int box = kBlock >> b.m;
+    b.n = box == rows ? 1 : 2;
+    if (may_pass && b.n == 2 && at + 2 * box <= kBlock) {
+        --b.m;
+        b.n = 1;
+        return b;
+    }
+    b.last = at + rows - box;
+    return b;
+}
+// The rows that copy_rows writes, those written twice twice.
+__device__ __forceinline__ int copied_rows(int rows) {
+    const Boxes v = boxes_of(0, rows, false), z = boxes_of(rows, (-rows) & 15, true);
+    return v.n * (kBlock >> v.m) + z.n * (kBlock >> z.m);
+}
 __device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, int col, int r0, int rows, int R,
                                           uint32_t bar, uint64_t policy) {
-    if (rows >= kBlock) {
-        copy2<true>(at, &maps[0], col, r0, bar, policy);
-        copy2<true>(at + kTileBytes / 2, &maps[0], col + 64, r0, bar, policy);
-        return;
+    const Boxes v = boxes_of(0, rows, false), z = boxes_of(rows, (-rows) & 15, true);
+    for (int i = 0; i < v.n; ++i) {
+        const int to = i ? v.last : v.at;
+        copy2<true>(at + to * 128, &maps[v.m], col, r0 + to, bar, policy);
+        copy2<true>(at + kTileBytes / 2 + to * 128, &maps[v.m], col + 64, r0 + to, bar, policy);
     }
-    int done = 0;
-    for (int z = 0; z < 2; ++z) {
-        const int want = z ? (-rows) & 15 : rows;
-        for (int m = 1; m < 7; ++m) {
-            const int box = kBlock >> m;
-            if (!(want & box)) continue;
-            copy2<true>(at + done * 128, &maps[m], col, z ? R : r0 + done, bar, policy);
-            copy2<true>(at + kTileBytes / 2 + done * 128, &maps[m], col + 64, z ? R : r0 + done, bar, policy);
-            done += box;
-        }
+    for (int i = 0; i < z.n; ++i) {
+        const int to = i ? z.last : z.at;
+        copy2<true>(at + to * 128, &maps[z.m], col, R, bar, policy);
+        copy2<true>(at + kTileBytes / 2 + to * 128, &maps[z.m], col + 64, R, bar, policy);
     }
 }
 
 template <bool kF32>
-__global__ void __maxnreg__(160)
+__global__ void __launch_bounds__(threads_of(true), 1)
     product_weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ WeightsMaps maps) {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ Shared s;
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // (everything is dynamic, and starts where the swizzle's pattern does: six
+    // stages then fit beside the epilogue's buffers)
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cluster_rank());
-    constexpr int kGroups = epi_groups(true);
     uint8_t* const epi_mem = smem + a.stages * kWStageBytes;
-    const PlanShared plan = plan_at(reinterpret_cast<int*>(epi_mem + kGroups * 4 * kWEpiBytes), a.plan.E);
+    Shared& s = *reinterpret_cast<Shared*>(epi_mem + kWEpiBytes);
+    const PlanShared plan = plan_at(reinterpret_cast<int*>(&s + 1), a.plan.E);
     const uint32_t tmem = set_up<true>(s, a.stages, a.plan, plan);
     volatile int* abort = &s.abort;
     const int workers = gridDim.x / 2, worker = blockIdx.x / 2;
@@ -510,6 +587,7 @@ __global__ void __maxnreg__(160)
         if (a.status) atomicExch(a.status, static_cast<int>(MOEQ_ERR_TIMEOUT));
     };
 
+    if (warp < 4) give_registers<true>();
     if (warp == 0 || warp == 2) {
         // -------------------------------------------------------- copies
         // Warp 0 copies dy, warp 2 x: both come from L2 for every block of dW.
@@ -525,9 +603,10 @@ __global__ void __maxnreg__(160)
                     if (!ok) break;
                     uint8_t* const at = smem + ring.at * kWStageBytes;
                     const uint32_t bar = in_first(&s.full[ring.at]);
-                    const int rows = min(p.cnt - r, kBlock), rows16 = (rows + 15) & ~15;
+                    const int rows = min(p.cnt - r, kBlock);
                     if (warp == 0) {
-                        if (rank == 0) mbar_arrive_expect_tx(&s.full[ring.at], 2 * 4 * rows16 * 128);
+                        // two CTAs, two operands, two columns of 64
+                        if (rank == 0) mbar_arrive_expect_tx(&s.full[ring.at], 8 * 128 * copied_rows(rows));
                         copy_rows(at, maps.dy, p.n0 + rank * 128, p.r0 + r, rows, a.plan.R, bar, again);
                     } else {
                         copy_rows(at + kTileBytes, maps.x, p.k0 + rank * 128, p.r0 + r, rows, a.plan.R, bar, again);
@@ -556,62 +635,68 @@ __global__ void __maxnreg__(160)
         if (rank == 0 && elect_one()) {
             WPart p;
             bool more = true, ok = true;
-            for (int i = 0; ok && more; ++i) {
-                more = part(i, p);
-                ok = push_part(s, i, more ? part_of(256, (p.cnt + 15) / 16) : 0, abort);
+            for (int u = 0, i = 0; ok && more;) {
+                more = part(u++, p);
+                if (!more) ok = push_part(s, i, 0, abort);
+                const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : steps_n;
+                for (int k0 = 0; ok && more && k0 < steps_n; k0 += run)
+                    ok = push_part(s, i++, part_of(256, min(run, steps_n - k0)), abort);
             }
             if (!ok) give_up();
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------- epilogue
-        // Lane = row of dW.  A warp's 32 rows leave through shared memory, 128
-        // bytes of each at a time, as tensor copies (which clip at N and K); an
-        // expert without rows gets zeros.
+        take_registers<true>();
+        // Lane = row of dW; the two groups share the columns, which leave
+        // registers through shared memory, 128 bytes of a warp's 32 rows at a time,
+        // as tensor copies (they clip at N and K).  (Stored by the lanes, 32 bytes
+        // each, dW goes out at 4.1 TB/s; so at 6.8.)  An expert without rows has
+        // no part: it gets zeros.
         const int q = warp & 3, group = (warp >> 2) - 1;
         const bool chief = tid == 128 + group * 128;
-        uint8_t* const buf_y = epi_mem + (group * 4 + q) * kWEpiBytes;
+        uint8_t* const buf_y = epi_mem + (group * 4 + q) * (kWEpiBytes / 8);
         constexpr int kCols = kF32 ? 32 : 64;
         WPart p;
-        for (int i = group; part(i, p); i += kGroups) {
-            const int buf = i & 1, n0 = p.n0 + rank * 128 + q * 32;
-            if (!part_done(s, i, group, kGroups, lane, chief, abort, give_up)) break;
-            const uint32_t acc = tmem + buf * kAcc1 + (static_cast<uint32_t>(q * 32) << 16);
-            for (int c0 = 0; c0 < 256; c0 += kCols) {
-                float v[kCols];
+        bool ok = true;
+        for (int u = 0, i = 0; part(u, p); ++u) {
+            const int n0 = p.n0 + rank * 128 + q * 32, k0 = p.k0 + group * 128;
+            const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : steps_n;
+            float v[128 / kCols][kCols];
+            if (p.cnt == 0) {
 #pragma unroll
-                for (int j = 0; j < kCols; j += 16) tmem_ld16(acc + c0 + j, v + j);
-                tmem_wait_ld();
+                for (int c = 0; c < 128; ++c) v[c / kCols][c % kCols] = 0.f;
+            }
+            for (int st = 0; ok && st < steps_n; st += run, ++i) {
+                ok = part_done(s, i, group, lane, chief, abort, give_up);
+                if (!ok) break;
+                const uint32_t acc = tmem + (i & 1) * kAcc1 + group * 128 + (static_cast<uint32_t>(q * 32) << 16);
+                take_acc<true>(s, i & 1, acc, 128, st == 0, rank, lane, v);
+            }
+            if (!ok) break;
 #pragma unroll
-                for (int j = 0; j < kCols; j += 16) tmem_use16(v + j);
-                if (c0 + kCols == 256) release_acc<true>(s, buf, rank, lane);
-                if (n0 >= a.N || p.k0 + c0 >= a.K) continue;
-                if (p.cnt == 0) {
-#pragma unroll
-                    for (int j = 0; j < kCols; ++j) v[j] = 0.f;
-                }
+            for (int c0 = 0; c0 < 128; c0 += kCols) {
+                if (n0 >= a.N || k0 + c0 >= a.K) continue;
+                const float(&w)[kCols] = v[c0 / kCols];
                 if (lane == 0) stores_read();  // the copy before has left the buffer
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    uint4 w;
-                    if constexpr (kF32) {
-                        w = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                                       __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-                    } else {
-                        uint32_t u[4];
+                    uint32_t x[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * c + 2 * j], v[8 * c + 2 * j + 1]);
-                            u[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (kF32) {
+                            x[k] = __float_as_uint(w[4 * c + k]);
+                        } else {
+                            const __nv_bfloat162 t = __floats2bfloat162_rn(w[8 * c + 2 * k], w[8 * c + 2 * k + 1]);
+                            x[k] = *reinterpret_cast<const uint32_t*>(&t);
                         }
-                        w = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                    *reinterpret_cast<uint4*>(buf_y + lane * 128 + ((c ^ (lane & 7)) << 4)) = w;
+                    *reinterpret_cast<uint4*>(buf_y + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
                 }
                 fence_smem_for_copies();
                 __syncwarp();
-                if (lane == 0) store3(&maps.dw, buf_y, p.k0 + c0, n0, p.e);
+                if (lane == 0) store3(&maps.dw, buf_y, k0 + c0, n0, p.e);
             }
         }
         if (lane == 0) stores_done();
@@ -639,9 +724,8 @@ bool map2(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t l
 }
 // [E, N, K], contiguous; the box is one expert's.
 bool map3(CUtensorMap* map, const void* p, int f32, int64_t K, int64_t N, int64_t E, int box_k, int box_n) {
-    const cuuint64_t size = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(E)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K) * size, static_cast<cuuint64_t>(K * N) * size};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K) * (f32 ? 4 : 2), static_cast<cuuint64_t>(K * N) * (f32 ? 4 : 2)};
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_k), static_cast<cuuint32_t>(box_n), 1}, steps[3] = {1, 1, 1};
     const EncodeTiled f = encode_tiled();
     return f && f(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p),
@@ -734,17 +818,20 @@ cudaError_t launch_expert_product_grad_w(const void* dy, int64_t ld_dy, const vo
     a.N = N;
     a.K = K;
     a.status = status;
-    a.stages = kWStages;
     WeightsMaps maps;
     for (int i = 0; i < 7; ++i)
         if (!map2(&maps.dy[i], dy, N, R, ld_dy, kBlock >> i) || !map2(&maps.x[i], x, K, R, ld_x, kBlock >> i))
             return cudaErrorInvalidValue;
     if (!map3(&maps.dw, dw, dw_f32, K, N, E, dw_f32 ? 32 : 64, 32)) return cudaErrorInvalidValue;
-    const int smem = 1024 + kWStages * kWStageBytes + epi_groups(true) * 4 * kWEpiBytes +
-                     plan_ints(E) * static_cast<int>(sizeof(int));
+    // six stages up to 340 experts, five beyond: 64 experts of 384 rows (K 6144,
+    // N 4096) take 846 us with six and 915 with five
+    const int rest = kWEpiBytes + static_cast<int>(sizeof(Shared)) + plan_ints(E) * static_cast<int>(sizeof(int));
+    const int fit = (227 * 1024 - rest) / kWStageBytes;
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+    const int smem = a.stages * kWStageBytes + rest;
     static OncePerDevice once[2];
-    return dw_f32 ? launch(product_weights_kernel<true>, once[1], a, maps, true, sms / 2 * 2, smem, kMostSmem, stream)
-                  : launch(product_weights_kernel<false>, once[0], a, maps, true, sms / 2 * 2, smem, kMostSmem, stream);
+    return dw_f32 ? launch(product_weights_kernel<true>, once[1], a, maps, true, sms / 2 * 2, smem, 227 * 1024, stream)
+                  : launch(product_weights_kernel<false>, once[0], a, maps, true, sms / 2 * 2, smem, 227 * 1024, stream);
 }
 
 }  // namespace moeq

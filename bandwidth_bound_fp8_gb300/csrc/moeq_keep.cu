@@ -9,7 +9,7 @@
 // is the type.  A group with a NaN or an infinity comes back as NaN.
 //
 // Each byte moves once: HBM bounds all of them, and the arithmetic of the
-// quantisation comes close (see codes8).  Half a warp has a group: eight
+// quantisation comes close.  Half a warp has a group: eight
 // elements a lane, neighbours where rows allow 16-byte accesses (kVec), else
 // 16 apart, so that neighbouring lanes still touch neighbouring elements.
 #include "moeq_device.cuh"
@@ -21,71 +21,138 @@ namespace {
 constexpr int kThreads = 256, kHalves = kThreads / 16;  // half warps of a block
 constexpr float kNaN = __builtin_nanf("");
 
+// Two fp32 in a register pair: half the issue slots of their arithmetic, which
+// is what these kernels are short of beside HBM.
+struct F2 {
+    uint64_t b;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.b) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 both(float v) { return f2(v, v); }
+__device__ __forceinline__ float lo(F2 a) { return __uint_as_float(static_cast<uint32_t>(a.b)); }
+__device__ __forceinline__ float hi(F2 a) { return __uint_as_float(static_cast<uint32_t>(a.b >> 32)); }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
+    return r;
+}
+
 // ---------------------------------------------------------- eight elements
 // `left`: columns from this lane's first on.
 template <bool kVec>
 __device__ __forceinline__ int col_of(int lane16) {
     return kVec ? lane16 * 8 : lane16;
 }
+// As they were read, until they are used.
+template <typename T, bool kVec>
+struct Eight;
 template <bool kVec>
-__device__ __forceinline__ void load8(const float* p, int left, float (&v)[8]) {
-    if constexpr (kVec) {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        if (left > 0) {
-            a = reinterpret_cast<const float4*>(p)[0];
-            b = reinterpret_cast<const float4*>(p)[1];
-        }
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 16 * i < left ? p[16 * i] : 0.f;
-    }
-}
-template <bool kVec>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int left, float (&v)[8]) {
-    if constexpr (kVec) {
-        const uint4 a = left > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 16 * i < left ? __bfloat162float(p[16 * i]) : 0.f;
-    }
-}
-template <bool kVec>
-__device__ __forceinline__ void store8(float* p, int left, const float (&v)[8]) {
-    if constexpr (kVec) {
-        if (left > 0) {
-            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (16 * i < left) p[16 * i] = v[i];
-    }
-}
-template <bool kVec>
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int left, const float (&v)[8]) {
-    if constexpr (kVec) {
-        if (left > 0) {
-            uint32_t u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                u[i] = *reinterpret_cast<const uint32_t*>(&h);
+struct Eight<float, kVec> {
+    float v[8];
+    __device__ __forceinline__ void load(const float* p, int left) {
+        if constexpr (kVec) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            if (left > 0) {
+                a = reinterpret_cast<const float4*>(p)[0];
+                b = reinterpret_cast<const float4*>(p)[1];
             }
-            *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 16 * i < left ? p[16 * i] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void keep_if(bool live) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = live ? v[i] : 0.f;
+    }
+    __device__ __forceinline__ void get(F2 (&o)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = f2(v[2 * i], v[2 * i + 1]);
+    }
+    // The bits of the largest magnitude (a NaN is the largest).
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        return t;
+    }
+    // The bytes that start with the signs of elements 4 i .. 4 i + 3.
+    __device__ __forceinline__ uint32_t signs(int i) const {
+        const uint32_t a = __byte_perm(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), 0x0073);
+        return __byte_perm(a, __byte_perm(__float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]), 0x0073), 0x5410);
+    }
+};
+template <bool kVec>
+struct Eight<__nv_bfloat16, kVec> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int left) {
+        if constexpr (kVec) {
+            const uint4 a = left > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        } else {
+            const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 16 * i < left ? q[16 * i] : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = v[2 * i] | v[2 * i + 1] << 16;
+        }
+    }
+    __device__ __forceinline__ void keep_if(bool live) {
+        const uint32_t mask = live ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] &= mask;
+    }
+    __device__ __forceinline__ void get(F2 (&o)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+    // The same of bf16's 16 bits: two magnitudes a comparison.
+    __device__ __forceinline__ uint32_t top() const {
+        const uint32_t a = 0x7FFF7FFFu;
+        const uint32_t m = __vimax3_u16x2(__vimax3_u16x2(w[0] & a, w[1] & a, w[2] & a), w[3] & a, 0u);
+        return max(m & 0xFFFFu, m >> 16);
+    }
+    __device__ __forceinline__ uint32_t signs(int i) const { return __byte_perm(w[2 * i], w[2 * i + 1], 0x7531); }
+};
+template <bool kVec>
+__device__ __forceinline__ void store8(float* p, int left, const F2 (&v)[4]) {
+    if constexpr (kVec) {
+        if (left > 0) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(lo(v[0]), hi(v[0]), lo(v[1]), hi(v[1]));
+            reinterpret_cast<float4*>(p)[1] = make_float4(lo(v[2]), hi(v[2]), lo(v[3]), hi(v[3]));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (16 * i < left) p[16 * i] = __float2bfloat16_rn(v[i]);
+            if (16 * i < left) p[16 * i] = i & 1 ? hi(v[i / 2]) : lo(v[i / 2]);
+    }
+}
+template <bool kVec>
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int left, const F2 (&v)[4]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo(v[i]), hi(v[i]));
+        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if constexpr (kVec) {
+        if (left > 0) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+        unsigned short* q = reinterpret_cast<unsigned short*>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (16 * i < left) q[16 * i] = static_cast<unsigned short>(u[i / 2] >> (16 * (i & 1)));
     }
 }
 // Eight codes, the first in the lowest byte.
@@ -117,60 +184,96 @@ __device__ __forceinline__ void store8(uint8_t* p, int left, uint2 c) {
 }
 
 // ------------------------------------------------------------ quantisation
-__device__ __forceinline__ uint2 pack8(const float (&q)[8]) {
-    const auto four = [&](int i) {
-        return static_cast<uint32_t>(e4m3x2_from_f32(q[i], q[i + 1])) |
-               (static_cast<uint32_t>(e4m3x2_from_f32(q[i + 2], q[i + 3])) << 16);
-    };
-    return make_uint2(four(0), four(4));
+// A group's scale, and 1 / scale in two parts (the first is rounded to
+// nearest).  A group that is not finite gets the scale NaN.
+struct Scale {
+    float s, inv, low;
+};
+__device__ __forceinline__ Scale scale_of(uint32_t top) {
+    const float s = __fdiv_rn(__uint_as_float(top), 448.0f), inv = __frcp_rn(s);
+    return {top >= 0x7F800000u ? kNaN : s, inv, fmaf(-s, inv, 1.f) * inv};
 }
-// The codes of this lane's eight elements of a group, and its scale.
-// Quotients are taken as products with 1 / s, which may be two steps of fp32
-// off fl32(x / s): the same code, unless a border between two codes lies that
-// near.  Then (8 in 2^20 quotients) the lane divides.  A border is where the
-// 20 bits below E4M3's three are 2^19; below 2^-6 the codes are 2^-9 apart, as
-// they are in [2^-6, 2^-5), so 2^-6 is added first.
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float* scale) {
-    uint32_t top = 0;  // as integers, so that a NaN is the largest
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+// Of one group, or of two at once (gate and up), of which each half of the
+// half warp's lanes computes one.
+template <typename T, bool kVec>
+__device__ __forceinline__ Scale scale_one(const Eight<T, kVec>& v) {
+    uint32_t top = v.top();
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float s = __fdiv_rn(__uint_as_float(top), 448.0f);
-    *scale = s;
-    if (top >= 0x7F800000u) {
-        *scale = kNaN;
-        return make_uint2(0, 0);
-    }
-    float q[8];
-    bool near = s < 1e-30f;  // 1 / s may be out of range
-    const float inv = __frcp_rn(s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        q[i] = v[i] * inv;
-        const float a = fabsf(q[i]) + (fabsf(q[i]) < 0.015625f ? 0.015625f : 0.f);
-        near |= ((__float_as_uint(a) + 0x80004u) & 0xFFFFFu) <= 8u;
-    }
-    if (near) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = s == 0.f ? copysignf(0.f, v[i]) : __fdiv_rn(v[i], s);
-    }
-    return pack8(q);
+    return scale_of(sizeof(T) == 2 ? top << 16 : top);
 }
-__device__ __forceinline__ void values8(uint2 c, float s, float (&v)[8]) {
-    float2 f[4];
-    e4m3x4_to_f32(c.x, f[0], f[1]);
-    e4m3x4_to_f32(c.y, f[2], f[3]);
+template <typename T, bool kVec>
+__device__ __forceinline__ void scale_two(const Eight<T, kVec>& a, const Eight<T, kVec>& b, Scale& sa, Scale& sb) {
+    const int lane = threadIdx.x & 31, first = lane & 16;
+    uint32_t ta = a.top(), tb = b.top();
+    if constexpr (sizeof(T) == 2) {
+        uint32_t t = ta | tb << 16;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) t = __vimax3_u16x2(t, __shfl_xor_sync(0xffffffffu, t, o), 0u);
+        ta = t << 16;
+        tb = t & 0xFFFF0000u;
+    } else {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            ta = max(ta, __shfl_xor_sync(0xffffffffu, ta, o));
+            tb = max(tb, __shfl_xor_sync(0xffffffffu, tb, o));
+        }
+    }
+    const Scale m = scale_of(lane & 8 ? tb : ta);
+    const auto from = [&](int src) {
+        return Scale{__shfl_sync(0xffffffffu, m.s, src), __shfl_sync(0xffffffffu, m.inv, src),
+                     __shfl_sync(0xffffffffu, m.low, src)};
+    };
+    sa = from(first);
+    sb = from(first | 8);
+}
+// The codes of eight elements (v: their values).  A quotient fl32(x / s) is
+// x / s from the two parts of 1 / s, at most one step off, corrected by the
+// remainder x - q s, which is exact then (P. Markstein, IBM J. Res. Dev. 34,
+// 1990, on division by fused multiply-adds).  Ties between codes are common
+// where both numbers are bf16 (whenever seven divides amax's significand), so
+// an approximate quotient will not do.  A code has its element's sign, zeros
+// too.
+template <typename T, bool kVec>
+__device__ __forceinline__ uint2 codes8(const Eight<T, kVec>& e, const F2 (&v)[4], Scale sc) {
+    uint32_t c[4];
+    if (sc.s < 1e-30f) {  // remainders could be out of range
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[i] = sc.s == 0.f ? 0u : e4m3x2_from_f32(__fdiv_rn(lo(v[i]), sc.s), __fdiv_rn(hi(v[i]), sc.s));
+    } else {
+        const F2 inv = both(sc.inv), low = both(sc.low), neg = both(-sc.s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            F2 q = fma2(v[i], inv, v[i] * low);
+            q = fma2(fma2(q, neg, v[i]), inv, q);
+            c[i] = e4m3x2_from_f32(lo(q), hi(q));
+        }
+    }
+    if (sc.s != sc.s) return make_uint2(0, 0);
+    return make_uint2(__byte_perm(c[0], c[1], 0x5410) | (e.signs(0) & 0x80808080u),
+                      __byte_perm(c[2], c[3], 0x5410) | (e.signs(1) & 0x80808080u));
+}
+__device__ __forceinline__ void values8(uint2 c, float s, F2 (&v)[4]) {
+    const F2 ss = both(s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[2 * i] = f[i].x * s;
-        v[2 * i + 1] = f[i].y * s;
+        const uint32_t w = i < 2 ? c.x : c.y;
+        const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(i & 1 ? w >> 16 : w & 0xFFFFu)));
+        v[i] = f2(f.x, f.y) * ss;
     }
 }
 
 // A block's half warps over rows and groups: rows of few groups share a block.
+// Blocks walk down the rows, with the next rows' loads in flight behind this
+// one's arithmetic (a block for each row: 120 us where this takes KEEP1, for
+// 32760 rows of 2 x 2048 bf16).
 struct Split {
     int log_groups;  // half warps of a row: a power of two, at most kHalves
+    __device__ __forceinline__ int half() const { return threadIdx.x >> 4; }
+    __host__ __device__ int rows() const { return kHalves >> log_groups; }          // of a block at a time
+    __device__ __forceinline__ int row() const { return half() >> log_groups; }     // of them, this half warp's
+    __device__ __forceinline__ int group() const { return half() & ((1 << log_groups) - 1); }
 };
 __host__ __device__ constexpr int groups_of(int K) { return (K + kGroup - 1) / kGroup; }
 Split split_of(int groups) {
@@ -178,32 +281,38 @@ Split split_of(int groups) {
     while ((1 << s.log_groups) < groups && (1 << s.log_groups) < kHalves) ++s.log_groups;
     return s;
 }
-unsigned blocks_of(int rows, Split s) {
-    const int per = kHalves >> s.log_groups;
-    return static_cast<unsigned>((static_cast<int64_t>(rows) + per - 1) / per);
+// Blocks for all rows, at most 16 an SM (four of which run at once) over `wide`
+// columns of blocks.  Only accesses of 16 bytes leave registers for loads
+// ahead: the others take a block for every few rows.
+unsigned blocks_of(int rows, Split s, int wide, bool vec, int sms) {
+    const int64_t all = (static_cast<int64_t>(rows) + s.rows() - 1) / s.rows(), most = (16 * sms + wide - 1) / wide;
+    return static_cast<unsigned>(all < most || !vec ? all : most);
 }
-__device__ __forceinline__ int64_t row_of(Split s) {
-    const int half = threadIdx.x >> 4;
-    return static_cast<int64_t>(blockIdx.x) * (kHalves >> s.log_groups) + (half >> s.log_groups);
-}
-__device__ __forceinline__ int group_of(Split s) { return (threadIdx.x >> 4) & ((1 << s.log_groups) - 1); }
 
 // ------------------------------------------------------------- rows to codes
-// (The shuffles of codes8 want whole warps: rows and groups out of range run
+// (The shuffles of the scale want whole warps: rows and groups out of range run
 // along with nothing to load or store.)
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) quant_rows_kernel(const T* x, int64_t ld, int rows, int K, Split sp,
+__global__ void __launch_bounds__(kThreads, kVec ? 4 : 5) quant_rows_kernel(const T* x, int64_t ld, int rows, int K, Split sp,
                                                               uint8_t* __restrict__ codes, float* __restrict__ scales) {
     chain();
-    const int64_t r = row_of(sp);
-    const int G = groups_of(K), g = (blockIdx.y << sp.log_groups) + group_of(sp), lane16 = threadIdx.x & 15;
-    const bool live = r < rows && g < G;
-    const int c = g * kGroup + col_of<kVec>(lane16), left = live ? min(K, (g + 1) * kGroup) - c : 0;
-    float v[8], s;
-    load8<kVec>(x + r * ld + c, left, v);
-    const uint2 q = codes8(v, &s);
-    store8<kVec>(codes + r * K + c, left, q);
-    if (live && lane16 == 0) scales[r * G + g] = s;
+    const int G = groups_of(K), g = (blockIdx.y << sp.log_groups) + sp.group(), lane16 = threadIdx.x & 15;
+    const int c = g * kGroup + col_of<kVec>(lane16), width = min(K, (g + 1) * kGroup) - c;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * sp.rows();
+    int64_t base = static_cast<int64_t>(blockIdx.x) * sp.rows(), r = base + sp.row();
+    Eight<T, kVec> next;
+    if (kVec) next.load(x + r * ld + c, r < rows ? width : 0);
+    for (; base < rows; base += step, r += step) {
+        if (!kVec) next.load(x + r * ld + c, r < rows ? width : 0);
+        const Eight<T, kVec> e = next;
+        if (kVec) next.load(x + (r + step) * ld + c, r + step < rows ? width : 0);
+        F2 v[4];
+        e.get(v);
+        const Scale s = scale_one(e);
+        const bool in = r < rows && g < G;
+        store8<kVec>(codes + r * K + c, in ? width : 0, codes8(e, v, s));
+        if (in && lane16 == 0) scales[r * G + g] = s.s;
+    }
 }
 
 // ------------------------------------------------------------- codes to rows
@@ -219,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) gather_codes_kernel(const uint8_t* c
     const int lane16 = threadIdx.x & 15, g = blockIdx.y * (blockDim.x >> 4) + (threadIdx.x >> 4);
     const int c = g * kGroup + col_of<kVec>(lane16), left = min(H, (g + 1) * kGroup) - c;
     if (left <= 0) return;
-    float v[8];
+    F2 v[4];
     values8(load8<kVec>(codes + t * H + c, left), scales[t * groups_of(H) + g], v);
     if (!pair_row) {
         store8<kVec>(xs + t * ld + c, left, v);
@@ -234,16 +343,28 @@ __global__ void __launch_bounds__(kThreads) gather_codes_kernel(const uint8_t* c
             if (r[j] >= 0 && r[j] < R) store8<kVec>(xs + r[j] * ld + c, left, v);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    for (int i = 0; i < 4; ++i) v[i] = both(0.f);
     for (int64_t r = max(offs[E], 0) + t; r < R; r += gridDim.x) store8<kVec>(xs + r * ld + c, left, v);
 }
 
 // ------------------------------------------------------------------- SwiGLU
-// 1 / (1 + exp(-g)): at most three steps of fp32 off.
-__device__ __forceinline__ float sigmoid(float g) {
-    float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + expf(-g)));
-    return r;
+// 1 / (1 + exp(-g)).  For fp32 rows at most four steps off.  For bf16 rows
+// exp(-g) is 2^(-g log2 e) of the rounded product: |g| steps more, which half
+// a step of bf16 (2^15 of fp32's) does not show.
+template <typename T>
+__device__ __forceinline__ F2 sigmoid(F2 g) {
+    float e[2], r[2];
+    if constexpr (sizeof(T) == 2) {
+        const F2 t = g * both(-1.44269504f);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[0]) : "f"(lo(t)));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[1]) : "f"(hi(t)));
+    } else {
+        e[0] = expf(-lo(g));
+        e[1] = expf(-hi(g));
+    }
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[0]) : "f"(1.f + e[0]));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[1]) : "f"(1.f + e[1]));
+    return f2(r[0], r[1]);
 }
 
 struct SwigluArgs {
@@ -252,51 +373,62 @@ struct SwigluArgs {
     const int32_t* row_pair;  // [R] or NULL: every row is live
     const float* w;           // [R], a pair's weight, or NULL: 1
 };
-// Whether a row belongs to an expert, and its pair and weight.
-struct RowOf {
-    bool live;
-    int pair;
-    float w;
-};
-__device__ __forceinline__ RowOf row_info(const SwigluArgs& a, int64_t r) {
-    RowOf o{r < a.R, 0, 1.f};
-    if (o.live && a.row_pair) {
-        o.pair = a.row_pair[r];
-        o.live = o.pair >= 0 && o.pair < a.R;
-        if (o.live && a.w) o.w = a.w[o.pair];
-    }
-    return o;
+// A row's pair; -1 where it belongs to no expert (or is none).
+__device__ __forceinline__ int pair_of(const SwigluArgs& a, int64_t r) {
+    if (r >= a.R) return -1;
+    if (!a.row_pair) return 0;
+    const int pair = a.row_pair[r];
+    return pair < a.R ? pair : -1;
 }
+__device__ __forceinline__ float weight_of(const SwigluArgs& a, int pair) { return a.w && pair >= 0 ? a.w[pair] : 1.f; }
 
-// h[r] = w_r silu(gate) up, and gate and up in 8 bits.  A row that belongs to
-// no expert is not read; its h, codes and scales are zeros.
+// h[r] = w_r silu(gate) up, and gate and up in 8 bits.  The h, codes and scales
+// of a row that belongs to no expert are zeros, whatever it holds.
 template <typename T, bool kVec, bool kKeep>
-__global__ void __launch_bounds__(kThreads) swiglu_rows_kernel(const SwigluArgs a, const T* gu, int64_t ld, T* __restrict__ h,
+__global__ void __launch_bounds__(kThreads, kVec ? 4 : 5) swiglu_rows_kernel(const SwigluArgs a, const T* gu, int64_t ld, T* __restrict__ h,
                                                                int64_t ld_h, uint8_t* __restrict__ codes,
                                                                float* __restrict__ scales) {
     chain();
-    const int64_t r = row_of(a.sp);
-    const int G = groups_of(a.I), g = (blockIdx.y << a.sp.log_groups) + group_of(a.sp), lane16 = threadIdx.x & 15;
-    const bool in = r < a.R && g < G;
-    const int c = g * kGroup + col_of<kVec>(lane16), left = in ? min(a.I, (g + 1) * kGroup) - c : 0;
-    const RowOf row = row_info(a, r);
-    const int read = row.live ? left : 0;
-    float x[8], u[8], y[8];
-    load8<kVec>(gu + r * ld + c, read, x);
-    load8<kVec>(gu + r * ld + a.I + c, read, u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = row.w * (x[i] * sigmoid(x[i])) * u[i];
-    store8<kVec>(h + r * ld_h + c, left, y);
-    if constexpr (kKeep) {
-        float sx, su;
-        const uint2 qx = codes8(x, &sx), qu = codes8(u, &su);
-        uint8_t* const at = codes + r * 2 * a.I + c;
-        store8<kVec>(at, left, qx);
-        store8<kVec>(at + a.I, left, qu);
-        if (in && lane16 == 0) {
-            scales[r * 2 * G + g] = sx;
-            scales[r * 2 * G + G + g] = su;
+    const int G = groups_of(a.I), g = (blockIdx.y << a.sp.log_groups) + a.sp.group(), lane16 = threadIdx.x & 15;
+    const int c = g * kGroup + col_of<kVec>(lane16), width = min(a.I, (g + 1) * kGroup) - c;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * a.sp.rows();
+    int64_t base = static_cast<int64_t>(blockIdx.x) * a.sp.rows(), r = base + a.sp.row();
+    Eight<T, kVec> next_x, next_u;
+    int next_pair;
+    auto fetch = [&](int64_t row) {
+        const int left = row < a.R ? width : 0;
+        next_x.load(gu + row * ld + c, left);
+        next_u.load(gu + row * ld + a.I + c, left);
+        next_pair = pair_of(a, row);
+    };
+    if (kVec) fetch(r);
+    for (; base < a.R; base += step, r += step) {
+        if (!kVec) fetch(r);
+        Eight<T, kVec> ex = next_x, eu = next_u;
+        const int pair = next_pair;
+        const float w = weight_of(a, pair);
+        if (kVec) fetch(r + step);
+        ex.keep_if(pair >= 0);
+        eu.keep_if(pair >= 0);
+        F2 x[4], u[4], y[4];
+        ex.get(x);
+        eu.get(u);
+        const bool in = r < a.R && g < G;
+        const int left = in ? width : 0;
+        if constexpr (kKeep) {
+            Scale sx, su;
+            scale_two(ex, eu, sx, su);
+            uint8_t* const at = codes + r * 2 * a.I + c;
+            store8<kVec>(at, left, codes8(ex, x, sx));
+            store8<kVec>(at + a.I, left, codes8(eu, u, su));
+            if (in && lane16 == 0) {
+                scales[r * 2 * G + g] = sx.s;
+                scales[r * 2 * G + G + g] = su.s;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = both(w) * (x[i] * sigmoid<T>(x[i])) * u[i];
+        store8<kVec>(h + r * ld_h + c, left, y);
     }
 }
 
@@ -304,47 +436,87 @@ __global__ void __launch_bounds__(kThreads) swiglu_rows_kernel(const SwigluArgs 
 // h again, and d_w[pair] = <dh, silu(gate) up>.  A row's half warps add their
 // parts up in a fixed order.  A pair without a row gets d_w 0.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) swiglu_rows_grad_kernel(const SwigluArgs a, const T* dh, int64_t ld_dh,
+__global__ void __launch_bounds__(kThreads, kVec ? 4 : 5) swiglu_rows_grad_kernel(const SwigluArgs a, const T* dh, int64_t ld_dh,
                                                                     const uint8_t* codes, const float* scales,
                                                                     T* __restrict__ dgu, int64_t ld_dgu, T* __restrict__ h,
                                                                     int64_t ld_h, const int32_t* pair_row,
                                                                     float* __restrict__ dw) {
     chain();
-    __shared__ float part[kHalves];
-    const int64_t r = row_of(a.sp);
-    const int G = groups_of(a.I), lane16 = threadIdx.x & 15;
-    const RowOf row = row_info(a, r);
-    float dot = 0.f;
-    for (int g = group_of(a.sp); g < G && r < a.R; g += 1 << a.sp.log_groups) {
-        const int c = g * kGroup + col_of<kVec>(lane16), left = min(a.I, (g + 1) * kGroup) - c;
-        const int read = row.live ? left : 0;
-        const uint8_t* const at = codes + r * 2 * a.I + c;
-        float d[8], x[8], u[8], dx[8], du[8], y[8];
-        load8<kVec>(dh + r * ld_dh + c, read, d);
-        values8(load8<kVec>(at, read), row.live ? scales[r * 2 * G + g] : 0.f, x);
-        values8(load8<kVec>(at + a.I, read), row.live ? scales[r * 2 * G + G + g] : 0.f, u);
+    __shared__ float part[2][kHalves];
+    const int G = groups_of(a.I), g0 = a.sp.group(), lane16 = threadIdx.x & 15;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * a.sp.rows();
+    int64_t base = static_cast<int64_t>(blockIdx.x) * a.sp.rows(), r = base + a.sp.row();
+    Eight<T, kVec> next_d;
+    uint2 next_x, next_u;
+    float next_sx, next_su;
+    int next_pair;
+    auto width_of = [&](int g) { return min(a.I, (g + 1) * kGroup) - g * kGroup - col_of<kVec>(lane16); };
+    auto fetch = [&](int64_t row, int g) {
+        const int c = g * kGroup + col_of<kVec>(lane16);
+        const bool in = row < a.R && g < G;
+        const int left = in ? width_of(g) : 0;
+        const uint8_t* const at = codes + row * 2 * a.I + c;
+        next_d.load(dh + row * ld_dh + c, left);
+        next_x = load8<kVec>(at, left);
+        next_u = load8<kVec>(at + a.I, left);
+        next_sx = in ? scales[row * 2 * G + g] : 0.f;
+        next_su = in ? scales[row * 2 * G + G + g] : 0.f;
+        next_pair = pair_of(a, row);
+    };
+    if (kVec) fetch(r, g0);
+    for (int turn = 0; base < a.R; base += step, r += step, turn ^= 1) {
+        const int pair = kVec ? next_pair : pair_of(a, r);
+        const float w = weight_of(a, pair);
+        F2 dot = both(0.f);
+        for (int gb = 0; gb < G; gb += 1 << a.sp.log_groups) {
+            const int g = gb + g0, c = g * kGroup + col_of<kVec>(lane16);
+            const int left = r < a.R && g < G ? width_of(g) : 0;
+            if (!kVec) fetch(r, g);
+            Eight<T, kVec> ed = next_d;
+            uint2 cx = next_x, cu = next_u;
+            float sx = next_sx, su = next_su;
+            const bool last = gb + (1 << a.sp.log_groups) >= G;
+            if (kVec) fetch(last ? r + step : r, last ? g0 : g + (1 << a.sp.log_groups));
+            if (pair < 0) {
+                cx = cu = make_uint2(0, 0);
+                sx = su = 0.f;
+            }
+            ed.keep_if(pair >= 0);
+            F2 d[4], x[4], u[4], dx[4], du[4], y[4];
+            ed.get(d);
+            values8(cx, sx, x);
+            values8(cu, su, u);
+            const F2 one = both(1.f), minus = both(-1.f), ww = both(w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float sig = sigmoid(x[i]), act = x[i] * sig, wd = row.w * d[i];
-            dx[i] = wd * u[i] * (sig * (1.f + x[i] * (1.f - sig)));
-            du[i] = wd * act;
-            y[i] = row.w * act * u[i];
-            dot = fmaf(d[i], act * u[i], dot);
+            for (int i = 0; i < 4; ++i) {
+                const F2 sig = sigmoid<T>(x[i]), act = x[i] * sig, da = d[i] * act, wu = ww * u[i];
+                dot = fma2(da, u[i], dot);
+                du[i] = da * ww;
+                y[i] = act * wu;
+                dx[i] = d[i] * wu * (sig * fma2(x[i], fma2(sig, minus, one), one));
+            }
+            store8<kVec>(dgu + r * ld_dgu + c, left, dx);
+            store8<kVec>(dgu + r * ld_dgu + a.I + c, left, du);
+            if (h) store8<kVec>(h + r * ld_h + c, left, y);
         }
-        store8<kVec>(dgu + r * ld_dgu + c, left, dx);
-        store8<kVec>(dgu + r * ld_dgu + a.I + c, left, du);
-        if (h) store8<kVec>(h + r * ld_h + c, left, y);
-    }
-    if (!dw) return;
+        if (!dw) continue;
+        float all = lo(dot) + hi(dot);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (lane16 == 0) part[threadIdx.x >> 4] = dot;
-    __syncthreads();
-    if (lane16 == 0 && group_of(a.sp) == 0 && r < a.R) {
-        float sum = 0.f;
-        for (int i = 0; i < 1 << a.sp.log_groups; ++i) sum += part[(threadIdx.x >> 4) + i];
-        if (row.live) dw[row.pair] = sum;
-        if (pair_row[r] < 0) dw[r] = 0.f;
+        for (int o = 8; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        if (a.sp.log_groups == 1) {
+            all += __shfl_xor_sync(0xffffffffu, all, 16);
+        } else if (a.sp.log_groups > 1) {
+            if (lane16 == 0) part[turn][a.sp.half()] = all;
+            __syncthreads();  // (one a row: the other turn's parts are read before the next)
+            if (g0 == 0) {
+                all = 0.f;
+                for (int i = 0; i < 1 << a.sp.log_groups; ++i) all += part[turn][a.sp.half() + i];
+            }
+        }
+        if (lane16 == 0 && g0 == 0 && r < a.R) {
+            if (pair >= 0) dw[pair] = all;
+            if (pair_row[r] < 0) dw[r] = 0.f;
+        }
     }
 }
 
@@ -359,11 +531,12 @@ cudaError_t by_type(int f32, F f) {
 
 }  // namespace
 
-cudaError_t launch_fp8_quant_rows(RowsIn x, int rows, int K, uint8_t* codes, float* scales, cudaStream_t stream) {
+cudaError_t launch_fp8_quant_rows(RowsIn x, int rows, int K, uint8_t* codes, float* scales, int sms, cudaStream_t stream) {
     const int G = groups_of(K);
     const Split sp = split_of(G);
-    const dim3 grid(blocks_of(rows, sp), (G + (1 << sp.log_groups) - 1) >> sp.log_groups);
+    const int wide = (G + (1 << sp.log_groups) - 1) >> sp.log_groups;
     const bool vec = K % 8 == 0 && fits8(x.p, x.ld, x.f32);
+    const dim3 grid(blocks_of(rows, sp, wide, vec, sms), wide);
     return by_type(x.f32, [&](auto* tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
         const T* p = static_cast<const T*>(x.p);
@@ -386,11 +559,12 @@ cudaError_t launch_fp8_gather_rows(const uint8_t* codes, const float* scales, in
 }
 
 cudaError_t launch_swiglu_rows(RowsIn gu, int R, int I, const int32_t* row_pair, const float* w, RowsOut h, uint8_t* codes,
-                               float* scales, cudaStream_t stream) {
+                               float* scales, int sms, cudaStream_t stream) {
     const int G = groups_of(I);
     const SwigluArgs a = {R, I, split_of(G), row_pair, w};
-    const dim3 grid(blocks_of(R, a.sp), (G + (1 << a.sp.log_groups) - 1) >> a.sp.log_groups);
+    const int wide = (G + (1 << a.sp.log_groups) - 1) >> a.sp.log_groups;
     const bool vec = I % 8 == 0 && fits8(gu.p, gu.ld, gu.f32) && fits8(h.p, h.ld, gu.f32);
+    const dim3 grid(blocks_of(R, a.sp, wide, vec, sms), wide);
     return by_type(gu.f32, [&](auto* tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
         auto go = [&](auto kern) {
@@ -404,14 +578,16 @@ cudaError_t launch_swiglu_rows(RowsIn gu, int R, int I, const int32_t* row_pair,
 
 cudaError_t launch_swiglu_rows_grad(RowsIn dh, const uint8_t* codes, const float* scales, int R, int I,
                                     const int32_t* row_pair, const float* w, const int32_t* pair_row, RowsOut dgu, RowsOut h,
-                                    float* dw, cudaStream_t stream) {
-    const SwigluArgs a = {R, I, split_of(groups_of(I)), row_pair, w};
+                                    float* dw, int sms, cudaStream_t stream) {
+    SwigluArgs a = {R, I, split_of(groups_of(I)), row_pair, w};
     const bool vec = I % 8 == 0 && fits8(dh.p, dh.ld, dh.f32) && fits8(dgu.p, dgu.ld, dh.f32) &&
                      (!h.p || fits8(h.p, h.ld, dh.f32));
+    // A warp a row where there are rows enough: its part of d_w then needs no barrier.
+    if (vec && R >= 96 * sms && a.sp.log_groups > 1) a.sp.log_groups = 1;
     return by_type(dh.f32, [&](auto* tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
         return launch_chained(vec ? swiglu_rows_grad_kernel<T, true> : swiglu_rows_grad_kernel<T, false>,
-                              dim3(blocks_of(R, a.sp)), kThreads, 0, stream, a, static_cast<const T*>(dh.p), dh.ld, codes,
+                              dim3(blocks_of(R, a.sp, 1, vec, sms)), kThreads, 0, stream, a, static_cast<const T*>(dh.p), dh.ld, codes,
                               scales, static_cast<T*>(dgu.p), dgu.ld, static_cast<T*>(h.p), h.ld, pair_row, dw);
     });
 }

@@ -166,15 +166,16 @@ cudaError_t launch_expert_product_grad_w(const void* dy, int64_t ld_dy, const vo
 // --------------------------------------------------- activations in 8 bits
 // codes [rows, K], scales [rows, ceil(K / 128)]; of gate and up rows [R, 2I]
 // and [R, 2 ceil(I / 128)].
-cudaError_t launch_fp8_quant_rows(RowsIn x, int rows, int K, uint8_t* codes, float* scales, cudaStream_t stream);
+cudaError_t launch_fp8_quant_rows(RowsIn x, int rows, int K, uint8_t* codes, float* scales, int sms,
+                                  cudaStream_t stream);
 // pair_row NULL: xs[t] is row t (k = 1).
 cudaError_t launch_fp8_gather_rows(const uint8_t* codes, const float* scales, int T, int H, int k, const int32_t* offs,
                                    int E, const int32_t* pair_row, RowsOut xs, cudaStream_t stream);
 // row_pair NULL: every row is live; w NULL: weights 1; codes NULL: nothing is kept.
 cudaError_t launch_swiglu_rows(RowsIn gu, int R, int I, const int32_t* row_pair, const float* w, RowsOut h, uint8_t* codes,
-                               float* scales, cudaStream_t stream);
+                               float* scales, int sms, cudaStream_t stream);
 cudaError_t launch_swiglu_rows_grad(RowsIn dh, const uint8_t* codes, const float* scales, int R, int I,
                                     const int32_t* row_pair, const float* w, const int32_t* pair_row, RowsOut dgu, RowsOut h,
-                                    float* dw, cudaStream_t stream);
+                                    float* dw, int sms, cudaStream_t stream);
 
 }  // namespace moeq

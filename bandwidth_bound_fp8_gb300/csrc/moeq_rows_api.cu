@@ -351,8 +351,10 @@ moeq_status moeq_fp8_quant_rows(const void* x, moeq_dtype dtype, int64_t ld, int
     if (K < 1 || K > kMaxWidth) return MOEQ_ERR_UNSUPPORTED_SHAPE;
     if (rows == 0) return MOEQ_OK;
     if (!rows_ok(x, dtype, ld, K) || !al(codes, 16) || !al(scales, 4)) return MOEQ_ERR_INVALID_ARG;
-    if (!current_device().ok) return MOEQ_ERR_DEVICE;
-    return cuda_status(launch_fp8_quant_rows({x, ld, dtype == MOEQ_F32}, rows, K, codes, scales, as_stream(stream)));
+    const Device dev = current_device();
+    if (!dev.ok) return MOEQ_ERR_DEVICE;
+    return cuda_status(launch_fp8_quant_rows({x, ld, dtype == MOEQ_F32}, rows, K, codes, scales, dev.sms,
+                                             as_stream(stream)));
 }
 
 moeq_status moeq_fp8_dequant_rows(const uint8_t* codes, const float* scales, int rows, int K, void* out, moeq_dtype dtype,
@@ -389,10 +391,11 @@ moeq_status moeq_swiglu_rows(const void* gu, moeq_dtype dtype, int64_t ld_gu, in
         (codes_opt && (!al(codes_opt, 16) || !al(scales_opt, 4))) || (row_pair_opt && !al(row_pair_opt, 4)) ||
         (topk_w_opt && !al(topk_w_opt, 4)))
         return MOEQ_ERR_INVALID_ARG;
-    if (!current_device().ok) return MOEQ_ERR_DEVICE;
+    const Device dev = current_device();
+    if (!dev.ok) return MOEQ_ERR_DEVICE;
     const int f32 = dtype == MOEQ_F32;
     return cuda_status(launch_swiglu_rows({gu, ld_gu, f32}, R, I, row_pair_opt, topk_w_opt, {h, ld_h, f32}, codes_opt,
-                                          scales_opt, as_stream(stream)));
+                                          scales_opt, dev.sms, as_stream(stream)));
 }
 
 moeq_status moeq_swiglu_rows_grad(const void* d_h, moeq_dtype dtype, int64_t ld_dh, const uint8_t* codes,
@@ -409,11 +412,12 @@ moeq_status moeq_swiglu_rows_grad(const void* d_h, moeq_dtype dtype, int64_t ld_
         (topk_w_opt && !al(topk_w_opt, 4)) || (pair_row_opt && !al(pair_row_opt, 4)) ||
         (d_topk_w_opt && !al(d_topk_w_opt, 4)))
         return MOEQ_ERR_INVALID_ARG;
-    if (!current_device().ok) return MOEQ_ERR_DEVICE;
+    const Device dev = current_device();
+    if (!dev.ok) return MOEQ_ERR_DEVICE;
     const int f32 = dtype == MOEQ_F32;
     return cuda_status(launch_swiglu_rows_grad({d_h, ld_dh, f32}, codes, scales, R, I, row_pair_opt, topk_w_opt,
                                                pair_row_opt, {d_gu, ld_dgu, f32}, {h_opt, ld_h, f32}, d_topk_w_opt,
-                                               as_stream(stream)));
+                                               dev.sms, as_stream(stream)));
 }
 
 }  // extern "C"

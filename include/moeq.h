@@ -658,8 +658,8 @@ moeq_status moeq_fp8_gather_rows(const uint8_t* codes, const float* scales, int 
 /* scales_opt (both or neither) gate and up in 8 bits, groups of their own:  */
 /* codes [R, 2I], scales [R, 2 ceil(I / 128)], gate's then up's.            */
 /*   row_pair_opt [R]: rows of a sort by expert (R = T * top_k). A row whose */
-/*           pair is not in [0, R) is not read; its h, codes and scales are  */
-/*           zeros.  NULL: every row is live                                */
+/*           pair is not in [0, R) counts for nothing, whatever it holds:   */
+/*           its h, codes and scales are zeros.  NULL: every row is live    */
 /*   topk_w_opt [R]: w_r = topk_w[row_pair[r]] (with row_pair_opt); NULL: 1.  */
 /*           With the routing weight in h, down's products add up to the    */
 /*           layer's output (moeq_gather_rows_grad), and its gradient needs  */

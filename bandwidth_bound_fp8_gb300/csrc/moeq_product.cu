@@ -14,7 +14,8 @@
 //   warp 1      issues the MMAs (one thread); warp 3 tells it the parts
 //   warps 4..   epilogue: TMEM -> rows, behind the next unit's MMAs (two
 //               accumulators)
-// Whole units, round robin over the CTAs (pairs); none waits for another.
+// Whole units, round robin over the CTAs (pairs); none waits for another.  A
+// few units are split along their contraction instead (see how_of).
 //
 // Weights out (dW): a unit is (expert, 256 x 256 of dW) for a pair, the
 // contraction over the expert's rows in stages of 64.  Rows are sorted, so a
@@ -128,18 +129,24 @@ __device__ __forceinline__ void fence_smem_for_copies() { asm volatile("fence.pr
 __device__ __forceinline__ uint32_t part_of(int n, int steps) {
     return static_cast<uint32_t>(steps) << 5 | static_cast<uint32_t>(n >> 4);
 }
+// A map's fetch from memory is then behind its first copy.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Barriers and the queue of parts that both kernels have.
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
     uint64_t part_full[4], part_empty[4];
+    uint64_t joined;  // the other CTAs' sums of a unit whose contraction is split
     uint32_t part_ring[4], tmem_base;
     int abort, go[2][2];
 };
 
 // Set-up up to the point where memory may be read; ends in a block barrier
-// (plan_scan's) and, for a pair, one of the cluster.
-template <bool kPair>
-__device__ __forceinline__ uint32_t set_up(Shared& s, int stages, const Mx4Plan& p, const PlanShared& plan) {
+// (plan_scan's) and, for a pair or a split, one of the cluster.
+template <bool kPair, bool kSplit>
+__device__ __forceinline__ uint32_t set_up(Shared& s, int stages, int split, const Mx4Plan& p, const PlanShared& plan) {
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         s.abort = 0;
@@ -152,6 +159,7 @@ __device__ __forceinline__ uint32_t set_up(Shared& s, int stages, const Mx4Plan&
             mbar_init(&s.acc_empty[i], kPair ? 16 : 4);  // every epilogue warp of both CTAs
         }
         mbar_init(&s.drained, 1);
+        if (kSplit) mbar_init(&s.joined, 4 * (split - 1));
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s.part_full[i], 1);
             mbar_init(&s.part_empty[i], 1);
@@ -164,7 +172,7 @@ __device__ __forceinline__ uint32_t set_up(Shared& s, int stages, const Mx4Plan&
     }
     chain();
     plan_scan(p, plan);
-    if constexpr (kPair) cluster_sync();  // the other CTA's barriers are set up
+    if constexpr (kPair || kSplit) cluster_sync();  // the other CTAs' barriers are set up
     tc_fence_after();
     return s.tmem_base;
 }
@@ -300,6 +308,39 @@ __device__ __forceinline__ void take_acc(Shared& s, int buf, uint32_t acc, int c
     release_acc<kPair>(s, buf, rank, lane);
 }
 
+// A unit whose contraction is split over a cluster: every CTA but the first
+// leaves its sums in the first's shared memory ([CTA][column][lane]), and the
+// first adds them to its own in the order of the contraction.
+template <int kA, int kB>
+__device__ __forceinline__ void send_sums(Shared& s, const float* join, int part_floats, int rank, int q, int cols,
+                                          int lane, const float (&v)[kA][kB]) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+                 : "=r"(at)
+                 : "r"(smem_u32(join + (rank - 1) * part_floats + q * 32 + lane)));
+#pragma unroll
+    for (int c = 0; c < 128; ++c)
+        if (c < cols) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + c * 512), "f"(v[c / kB][c % kB]) : "memory");
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) arrive_first(&s.joined);
+}
+template <int kA, int kB, typename GiveUp>
+__device__ __forceinline__ bool add_sums(Shared& s, const float* join, int part_floats, int split, int q, int cols, int lane,
+                                         bool chief, volatile int* abort, GiveUp give_up, float (&v)[kA][kB]) {
+    if (lane == 0 && !cluster_wait_bounded(&s.joined, 0, abort)) give_up();
+    __syncwarp();
+    if (chief) s.go[1][0] = !*abort;
+    named_sync(1, 128);
+    if (!s.go[1][0]) return false;
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    for (int r = 1; r < split; ++r, join += part_floats)
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+            if (c < cols) v[c / kB][c % kB] += join[c * 128 + q * 32 + lane];
+    return true;
+}
+
 // A pair's 384 threads start with 168 registers each; the epilogue's 256 take
 // 40 more from the 128 that copy and issue: 128 * 88 + 256 * 208 = 384 * 168.
 template <bool kPair>
@@ -318,6 +359,7 @@ struct RowsArgs {
     int64_t ld_y;
     int N, C;  // features of a row of y, contraction
     int stages;
+    int split;  // CTAs (a cluster) that share a unit's contraction
     int* status;
 };
 struct RowsMaps {
@@ -351,7 +393,9 @@ __device__ __forceinline__ bool part_at(const RowsArgs& a, const PlanShared& pla
     return true;
 }
 
-template <bool kF32, bool kPair, bool kTrans>
+// kSplit (of single CTAs): a cluster has one unit, and each of its CTAs a share
+// of the contraction.
+template <bool kF32, bool kPair, bool kTrans, bool kSplit>
 __global__ void __launch_bounds__(threads_of(kPair), 1)
     product_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ RowsMaps maps) {
     extern __shared__ uint8_t smem_raw[];
@@ -360,15 +404,23 @@ __global__ void __launch_bounds__(threads_of(kPair), 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int stage_bytes = stage_bytes_of(a.plan.nt, kPair);
     const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
-    // behind the stages: the epilogue's buffers, then the plan
-    uint8_t* const epi_mem = smem + a.stages * stage_bytes;
+    const int split = kSplit ? a.split : 1, srank = kSplit ? static_cast<int>(cluster_rank()) : 0;
+    // behind the stages: the others' sums, the epilogue's buffers, the plan
+    float* const join = reinterpret_cast<float*>(smem + a.stages * stage_bytes);
+    const int part_floats = a.plan.nt * 128;
+    uint8_t* const epi_mem = reinterpret_cast<uint8_t*>(join + (split - 1) * part_floats);
     const PlanShared plan = plan_at(reinterpret_cast<int*>(epi_mem + epi_groups(kPair) * epi_bytes(kPair)), a.plan.E);
-    const uint32_t tmem = set_up<kPair>(s, a.stages, a.plan, plan);
+    if (tid == 0) prefetch_map(&maps.w);
+    if (tid == 64) prefetch_map(&maps.x[a.plan.nt / (kPair ? 32 : 16) - 1]);
+    const uint32_t tmem = set_up<kPair, kSplit>(s, a.stages, split, a.plan, plan);
     volatile int* abort = &s.abort;
-    const int workers = gridDim.x / (kPair ? 2 : 1), worker = blockIdx.x / (kPair ? 2 : 1);
+    const int each = kPair ? 2 : split, workers = gridDim.x / each, worker = blockIdx.x / each;
     const int nbu = kPair ? (a.N + 255) / 256 : (a.N + 127) / 128, kb_n = (a.C + kBlock - 1) / kBlock;
-    const int steps_n = 4 * kb_n, run = kF32 ? kRun : steps_n;  // of 16; a part's
-    auto part = [&](int i, Part& p) { return part_at<kPair>(a, plan, i, worker, workers, nbu, rank, p); };
+    const int kb0 = kb_n * srank / split, kb1 = kb_n * (srank + 1) / split;  // (kb_n * 8 < 2^18)
+    const int steps_n = 4 * (kb1 - kb0), run = kF32 ? kRun : steps_n;        // of 16; a part's
+    auto part = [&](int i, Part& p) {
+        return (!kSplit || i == 0) && part_at<kPair>(a, plan, i, worker, workers, nbu, rank, p);
+    };
     auto give_up = [&] {
         *abort = 1;
         if (a.status) atomicExch(a.status, static_cast<int>(MOEQ_ERR_TIMEOUT));
@@ -386,7 +438,7 @@ __global__ void __launch_bounds__(threads_of(kPair), 1)
             int it = 0;
             bool ok = true;
             for (int i = 0; ok && part(i, p); ++i)
-                for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     if (it >= a.stages) ok = mbar_wait_bounded(&s.empty[ring.at], ring.phase ^ 1, abort);
                     if (!ok) break;
                     uint8_t* const at = smem + ring.at * stage_bytes;
@@ -466,6 +518,14 @@ __global__ void __launch_bounds__(threads_of(kPair), 1)
                 take_acc<kPair>(s, i & 1, acc, cols, k0 == 0, rank, lane, v);
             }
             if (!ok) break;
+            if constexpr (kSplit) {
+                if (srank > 0) {
+                    send_sums(s, join, part_floats, srank, q, cols, lane, v);
+                    continue;
+                }
+                ok = add_sums(s, join, part_floats, split, q, cols, lane, chief, abort, give_up, v);
+                if (!ok) break;
+            }
             const int n = p.n0 + q * 32 + lane;
             p.n = base + cols;
 #pragma unroll
@@ -486,7 +546,7 @@ __global__ void __launch_bounds__(threads_of(kPair), 1)
     tc_fence_before();
     __syncthreads();
     __syncwarp();
-    if constexpr (kPair) cluster_sync();  // neither CTA's shared memory or TMEM is in use any more
+    if constexpr (kPair || kSplit) cluster_sync();  // no CTA's shared memory or TMEM is in use any more
     if (warp == 1) {
         tc_fence_after();
         tmem_give<kPair>(tmem);
@@ -578,7 +638,10 @@ __global__ void __launch_bounds__(threads_of(true), 1)
     uint8_t* const epi_mem = smem + a.stages * kWStageBytes;
     Shared& s = *reinterpret_cast<Shared*>(epi_mem + kWEpiBytes);
     const PlanShared plan = plan_at(reinterpret_cast<int*>(&s + 1), a.plan.E);
-    const uint32_t tmem = set_up<true>(s, a.stages, a.plan, plan);
+    if (tid == 0) prefetch_map(&maps.dy[0]);
+    if (tid == 64) prefetch_map(&maps.x[0]);
+    if (tid == 128) prefetch_map(&maps.dw);
+    const uint32_t tmem = set_up<true, false>(s, a.stages, 1, a.plan, plan);
     volatile int* abort = &s.abort;
     const int workers = gridDim.x / 2, worker = blockIdx.x / 2;
     auto part = [&](int i, WPart& p) { return wpart_at(a, plan, i, worker, workers, p); };
@@ -734,8 +797,8 @@ bool map3(CUtensorMap* map, const void* p, int f32, int64_t K, int64_t N, int64_
 }
 
 template <typename Args, typename Maps>
-cudaError_t launch(void (*kern)(Args, Maps), OncePerDevice& once, const Args& a, const Maps& maps, bool pair, int grid,
-                   int smem, int most_smem, cudaStream_t stream) {
+cudaError_t launch(void (*kern)(Args, Maps), OncePerDevice& once, const Args& a, const Maps& maps, bool pair, int cluster,
+                   int grid, int smem, int most_smem, cudaStream_t stream) {
     const cudaError_t e = raise_smem(once, reinterpret_cast<const void*>(kern), most_smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -747,38 +810,57 @@ cudaError_t launch(void (*kern)(Args, Maps), OncePerDevice& once, const Args& a,
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.x = cluster;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = pair ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, a, maps);
 }
 
 // Of 227 KiB, less the static arrays.
 constexpr int kMostSmem = 227 * 1024 - 1024;
 
-template <bool kF32, bool kPair, bool kTrans>
+template <bool kF32, bool kPair, bool kTrans, bool kSplit>
 cudaError_t launch_rows(const RowsArgs& a, const RowsMaps& maps, int grid, int smem, cudaStream_t stream) {
     static OncePerDevice once;
-    return launch(product_rows_kernel<kF32, kPair, kTrans>, once, a, maps, kPair, grid, smem, kMostSmem, stream);
+    return launch(product_rows_kernel<kF32, kPair, kTrans, kSplit>, once, a, maps, kPair, kPair ? 2 : a.split, grid, smem,
+                  kMostSmem, stream);
 }
 
-// Rows of a tile, and whether pairs of CTAs multiply it: about twice an
-// expert's average, so that most experts are one tile and their weights are
-// read once.
-Mx4Tiling tiling_of(int R, int E) {
-    const long long want = E == 1 ? R : 2LL * R / E + 16;
-    const bool pair = want >= kPairRows && R >= kPairRows;
-    const int align = pair ? 32 : 16, most = pair ? kPairTileRows : kSingleTileRows;
-    const long long rows = want < R ? want : R;
-    return {static_cast<int>(rows > most ? most : (rows + align - 1) / align * align), align};
+// How rows are multiplied: about twice an expert's average of rows a tile, so
+// that most experts are one tile and their weights are read once; from kPairRows
+// on by pairs of CTAs.  Units so few that SMs would be idle are split along
+// their contraction over a cluster instead, eight stages or more a CTA: 16 rows
+// of a dense product (6144 -> 4096, 32 units) take SPLIT1 us by four CTAs a
+// unit and 23 whole, 256 rows SPLIT2 by two and 34 by pairs.  (Clusters of
+// eight and four leave some SMs out; `clusters` is how many run at once.)
+int64_t most_tiles(int R, int E, int nt) { return E == 1 ? (R + nt - 1) / nt : mx4_max_tiles(R, E, nt); }
+struct How {
+    Mx4Tiling t;
+    int split;
+};
+How how_of(int R, int E, int features, int contraction, int sms) {
+    const long long want = E == 1 ? R : 2LL * R / E + 16, rows = want < R ? want : R;
+    const auto up = [](long long x, int align, int most) {
+        return static_cast<int>(x > most ? most : (x + align - 1) / align * align);
+    };
+    How h{{up(rows, 16, kSingleTileRows), 16}, 1};
+    const long long units = most_tiles(R, E, h.t.nt) * ((features + 127) / 128);
+    for (int split = 2; split <= 8; split *= 2) {
+        const int clusters = split == 8 ? sms * 3 / 32 : split == 4 ? sms * 15 / 64 : sms / 2;
+        if (units <= clusters && (contraction + kBlock - 1) / kBlock >= 8 * split && (split - 1) * h.t.nt * 512 <= 96 * 1024)
+            h.split = split;
+    }
+    if (h.split == 1 && want >= kPairRows && R >= kPairRows) h.t = {up(rows, 32, kPairTileRows), 32};
+    return h;
 }
 
 }  // namespace
 
 cudaError_t launch_expert_product(const void* x, int64_t ld_x, int R, const void* w, int E, int N, int K, bool trans,
                                   const int32_t* offs, RowsOut y, int* status, int sms, cudaStream_t stream) {
-    const Mx4Tiling t = tiling_of(R, E);
+    const How h = how_of(R, E, trans ? K : N, trans ? N : K, sms);
+    const Mx4Tiling t = h.t;
     const bool pair = t.align == 32;
     RowsArgs a = {};
     a.plan = {offs, nullptr, E, R, 1, R, t.nt, t.align};
@@ -786,6 +868,7 @@ cudaError_t launch_expert_product(const void* x, int64_t ld_x, int R, const void
     a.ld_y = y.ld;
     a.N = trans ? K : N;
     a.C = trans ? N : K;
+    a.split = h.split;
     a.status = status;
     RowsMaps maps;
     if (!map3(&maps.w, w, 0, K, N, E, kBlock, trans ? kBlock : 128)) return cudaErrorInvalidValue;
@@ -793,21 +876,23 @@ cudaError_t launch_expert_product(const void* x, int64_t ld_x, int R, const void
     for (int i = 0; i < boxes; ++i)
         if (!map2(&maps.x[i], x, a.C, R, ld_x, 16 * (i + 1))) return cudaErrorInvalidValue;
     const int sb = stage_bytes_of(t.nt, pair);
-    const int rest = 1024 + epi_bytes(pair) * epi_groups(pair) + plan_ints(E) * static_cast<int>(sizeof(int));
+    const int rest = 1024 + (h.split - 1) * t.nt * 512 + epi_bytes(pair) * epi_groups(pair) +
+                     plan_ints(E) * static_cast<int>(sizeof(int));
     const int fit = (kMostSmem - rest) / sb;
     a.stages = fit < kMaxStages ? fit : kMaxStages;
-    const int smem = a.stages * sb + rest, grid = pair ? sms / 2 * 2 : sms;
-    auto go = [&](auto f32, auto two, auto tr) {
-        return launch_rows<decltype(f32)::value, decltype(two)::value, decltype(tr)::value>(a, maps, grid, smem, stream);
+    const int smem = a.stages * sb + rest;
+    const int grid = pair ? sms / 2 * 2 : h.split > 1 ? static_cast<int>(most_tiles(R, E, t.nt)) * ((a.N + 127) / 128) * h.split : sms;
+    const auto by_way = [&](auto f32, auto two, auto cut) {
+        constexpr bool kF = decltype(f32)::value, kP = decltype(two)::value, kS = decltype(cut)::value;
+        return trans ? launch_rows<kF, kP, true, kS>(a, maps, grid, smem, stream)
+                     : launch_rows<kF, kP, false, kS>(a, maps, grid, smem, stream);
     };
-    using T = std::true_type;
-    using F = std::false_type;
-    if (pair) {
-        if (y.f32) return trans ? go(T{}, T{}, T{}) : go(T{}, T{}, F{});
-        return trans ? go(F{}, T{}, T{}) : go(F{}, T{}, F{});
-    }
-    if (y.f32) return trans ? go(T{}, F{}, T{}) : go(T{}, F{}, F{});
-    return trans ? go(F{}, F{}, T{}) : go(F{}, F{}, F{});
+    const auto by_kind = [&](auto f32) {
+        using T = std::true_type;
+        using F = std::false_type;
+        return pair ? by_way(f32, T{}, F{}) : h.split > 1 ? by_way(f32, F{}, T{}) : by_way(f32, F{}, F{});
+    };
+    return y.f32 ? by_kind(std::true_type{}) : by_kind(std::false_type{});
 }
 
 cudaError_t launch_expert_product_grad_w(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int R, int E, int N,
@@ -830,8 +915,8 @@ cudaError_t launch_expert_product_grad_w(const void* dy, int64_t ld_dy, const vo
     a.stages = fit < kMaxStages ? fit : kMaxStages;
     const int smem = a.stages * kWStageBytes + rest;
     static OncePerDevice once[2];
-    return dw_f32 ? launch(product_weights_kernel<true>, once[1], a, maps, true, sms / 2 * 2, smem, 227 * 1024, stream)
-                  : launch(product_weights_kernel<false>, once[0], a, maps, true, sms / 2 * 2, smem, 227 * 1024, stream);
+    return dw_f32 ? launch(product_weights_kernel<true>, once[1], a, maps, true, 2, sms / 2 * 2, smem, 227 * 1024, stream)
+                  : launch(product_weights_kernel<false>, once[0], a, maps, true, 2, sms / 2 * 2, smem, 227 * 1024, stream);
 }
 
 }  // namespace moeq

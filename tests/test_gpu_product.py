@@ -104,6 +104,18 @@ def test_dense(way, rows):
 
 
 @pytest.mark.parametrize("way", ["y", "dx"])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("counts,C,features", [([1], 4096, 200), ([16], 1024, 136), ([40], 4104, 136), ([100], 2048, 264),
+                                               ([128], 4096, 72), ([200], 1032, 520), ([0, 3, 0], 4096, 128), ([1, 0, 2, 5], 2056, 264),
+                                               ([0, 0], 4096, 64)])
+def test_few_units_of_long_contraction(way, counts, C, features, dt):
+    """Units split over clusters of two, four and eight CTAs; the same result every time."""
+    K, N = (C, features) if way == "y" else (features, C)
+    out = _run(way, counts, K, N, dt, extra=2)
+    assert torch.equal(out, _run(way, counts, K, N, dt, extra=2))
+
+
+@pytest.mark.parametrize("way", ["y", "dx"])
 def test_many_tiles_of_one_expert(way):
     """More row tiles than a band of them, the last band narrower."""
     _run(way, [2304 + 100, 0, 2048], 128, 520, BF)
@@ -194,10 +206,10 @@ def test_offsets_out_of_range_stay_inside(way):
 
 
 @pytest.mark.parametrize("way", WAYS)
-@pytest.mark.parametrize("counts", [[2, 0, 5], [300, 0, 150]])
-def test_captured_and_replayed(way, counts):
+@pytest.mark.parametrize("counts,K,N", [([2, 0, 5], 136, 72), ([300, 0, 150], 136, 72), ([2, 0, 5], 4096, 2048)])
+def test_captured_and_replayed(way, counts, K, N):
     """A graph follows new inputs and new offsets, on another stream, and the status word stays as it was."""
-    E, R, K, N = len(counts), sum(counts), 136, 72
+    E, R = len(counts), sum(counts)
     x, dy, w, offs = _rand(1, R, K), _rand(2, R, N), _rand(3, E, N, K), _offs(counts)
     a, b = {"y": (x, w), "dx": (dy, w), "dw": (dy, x)}[way]
     shape = {"y": (R, N), "dx": (R, K), "dw": (E, N, K)}[way]

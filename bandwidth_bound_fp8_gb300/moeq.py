@@ -711,47 +711,60 @@ def moeq_expert_product_grad_w(d_y, x, offs, d_w, status=None, stream=None) -> N
 
 
 # ------------------------------------------------- activations in 8 bits
+# (A small call's time is the host's, and most of that these checks: each
+# property of a tensor is asked for once.)
+def _flat(t, dtype, n: int, name: str):
+    """The address of a contiguous tensor of this dtype and number of elements."""
+    if t.is_cuda and t.dtype is dtype and t.numel() == n and t.is_contiguous() and not (
+            _many_gpus and t.get_device() != _device()):
+        return t.data_ptr()
+    if not t.is_cuda or _many_gpus and t.get_device() != _device():
+        _elsewhere(t, name)
+    raise ValueError(f"{name}: a contiguous {dtype} tensor of {n} elements is wanted, got {t.dtype} {tuple(t.shape)}, "
+                     f"strides {t.stride()}")
+
+
 def fp8_groups(K: int) -> int:
     """Scales of a row of K columns."""
-    return (K + MOEQ_GROUP - 1) // MOEQ_GROUP
+    return (K + 127) >> 7
 
 
-def _codes8(codes, scales, rows, K, halves=1):
-    return (_packed(codes, torch.uint8, (rows, halves * K), "codes"),
-            _packed(scales, torch.float32, (rows, halves * fp8_groups(K)), "scales"))
+_U8, _F32, _I32 = torch.uint8, torch.float32, torch.int32
 
 
 def moeq_fp8_quant_rows(x, codes, scales, stream=None) -> None:
     """x [rows, K] bf16 or fp32 -> codes [rows, K] uint8, scales [rows, fp8_groups(K)] fp32."""
     rows, K = x.shape
-    _check("moeq_fp8_quant_rows", (_lib or load()).moeq_fp8_quant_rows(
-        x.data_ptr(), _dtype(x), _ld(x, "x"), rows, K, *_codes8(codes, scales, rows, K), _queue(stream)))
+    st = (_lib or load()).moeq_fp8_quant_rows(
+        x.data_ptr(), _dtype(x), _ld(x, "x"), rows, K, _flat(codes, _U8, rows * K, "codes"),
+        _flat(scales, _F32, rows * fp8_groups(K), "scales"), _queue(stream))
+    if st:
+        raise MoeqError("moeq_fp8_quant_rows", st)
 
 
 def moeq_fp8_dequant_rows(codes, scales, out, stream=None) -> None:
     """The values that codes and scales stand for: out [rows, K] bf16 or fp32."""
     rows, K = out.shape
-    _check("moeq_fp8_dequant_rows", (_lib or load()).moeq_fp8_dequant_rows(
-        *_codes8(codes, scales, rows, K), rows, K, out.data_ptr(), _dtype(out), _ld(out, "out"), _queue(stream)))
+    st = (_lib or load()).moeq_fp8_dequant_rows(
+        _flat(codes, _U8, rows * K, "codes"), _flat(scales, _F32, rows * fp8_groups(K), "scales"), rows, K, out.data_ptr(),
+        _dtype(out), _ld(out, "out"), _queue(stream))
+    if st:
+        raise MoeqError("moeq_fp8_dequant_rows", st)
 
 
 def moeq_fp8_gather_rows(codes, scales, offs, pair_row, xs, stream=None) -> None:
     """xs[pair_row[t, j]] = the values of row t; rows of xs from offs[E] on are zeroed."""
-    T, k, pr = _pairs(pair_row)
-    E, of = _offs(offs)
-    H = xs.shape[1]
-    if xs.shape != (T * k, H):
+    T, k = pair_row.shape
+    R, H = xs.shape
+    E = offs.shape[0] - 1
+    if R != T * k:
         raise ValueError(f"xs [{T * k}, H] is wanted, got {tuple(xs.shape)}")
-    _check("moeq_fp8_gather_rows", (_lib or load()).moeq_fp8_gather_rows(
-        *_codes8(codes, scales, T, H), T, H, k, of, E, pr, xs.data_ptr(), _dtype(xs), _ld(xs, "xs"), _queue(stream)))
-
-
-def _row_weights(row_pair, topk_w, R):
-    """row_pair and topk_w, with as many elements as there are rows."""
-    if topk_w is not None and (row_pair is None or topk_w.numel() != R):
-        raise ValueError(f"topk_w: the weights of {R} pairs and their row_pair are wanted")
-    return (None if row_pair is None else _packed(row_pair, torch.int32, (R,), "row_pair"),
-            None if topk_w is None else _packed(topk_w, torch.float32, topk_w.shape, "topk_w"))
+    st = (_lib or load()).moeq_fp8_gather_rows(
+        _flat(codes, _U8, T * H, "codes"), _flat(scales, _F32, T * fp8_groups(H), "scales"), T, H, k,
+        _flat(offs, _I32, E + 1, "offs"), E, _flat(pair_row, _I32, R, "pair_row"), xs.data_ptr(), _dtype(xs), _ld(xs, "xs"),
+        _queue(stream))
+    if st:
+        raise MoeqError("moeq_fp8_gather_rows", st)
 
 
 def moeq_swiglu_rows(gu, h, row_pair=None, topk_w=None, codes=None, scales=None, stream=None) -> None:
@@ -762,25 +775,38 @@ def moeq_swiglu_rows(gu, h, row_pair=None, topk_w=None, codes=None, scales=None,
         raise ValueError(f"gu [{R}, {2 * I}] of h's type is wanted, got {gu.dtype} {tuple(gu.shape)}")
     if (codes is None) != (scales is None):
         raise ValueError("codes and scales come together")
-    kept = (None, None) if codes is None else _codes8(codes, scales, R, I, 2)
-    _check("moeq_swiglu_rows", (_lib or load()).moeq_swiglu_rows(
-        gu.data_ptr(), _dtype(gu), _ld(gu, "gu"), R, I, *_row_weights(row_pair, topk_w, R), h.data_ptr(), _ld(h, "h"),
-        *kept, _queue(stream)))
+    if topk_w is not None and row_pair is None:
+        raise ValueError("topk_w: the rows' row_pair is wanted beside it")
+    st = (_lib or load()).moeq_swiglu_rows(
+        gu.data_ptr(), _dtype(gu), _ld(gu, "gu"), R, I, None if row_pair is None else _flat(row_pair, _I32, R, "row_pair"),
+        None if topk_w is None else _flat(topk_w, _F32, R, "topk_w"), h.data_ptr(), _ld(h, "h"),
+        None if codes is None else _flat(codes, _U8, R * 2 * I, "codes"),
+        None if codes is None else _flat(scales, _F32, R * 2 * fp8_groups(I), "scales"), _queue(stream))
+    if st:
+        raise MoeqError("moeq_swiglu_rows", st)
 
 
 def moeq_swiglu_rows_grad(d_h, codes, scales, d_gu, h=None, row_pair=None, topk_w=None, pair_row=None, d_topk_w=None,
                           stream=None) -> None:
     """From what moeq_swiglu_rows kept: d_gu [R, 2I] of d_h [R, I], h again, and d_topk_w of topk_w."""
-    R, I = d_h.shape
-    if d_gu.shape != (R, 2 * I) or d_gu.dtype is not d_h.dtype:
+    shape, dt = d_h.shape, d_h.dtype
+    R, I = shape
+    if d_gu.shape != (R, 2 * I) or d_gu.dtype is not dt:
         raise ValueError(f"d_gu [{R}, {2 * I}] of d_h's type is wanted, got {d_gu.dtype} {tuple(d_gu.shape)}")
-    if h is not None and (h.shape != d_h.shape or h.dtype is not d_h.dtype):
+    if h is not None and (h.shape != shape or h.dtype is not dt):
         raise ValueError("h: d_h's shape and type are wanted")
-    if d_topk_w is not None and (topk_w is None or pair_row is None or pair_row.numel() != R):
-        raise ValueError("d_topk_w: topk_w and the sort's pair_row are wanted")
-    rp, w = _row_weights(row_pair, topk_w, R)
-    _check("moeq_swiglu_rows_grad", (_lib or load()).moeq_swiglu_rows_grad(
-        d_h.data_ptr(), _dtype(d_h), _ld(d_h, "d_h"), *_codes8(codes, scales, R, I, 2), R, I, rp, w,
-        None if d_topk_w is None else _packed(pair_row, torch.int32, pair_row.shape, "pair_row"), d_gu.data_ptr(),
-        _ld(d_gu, "d_gu"), _p(h), 0 if h is None else _ld(h, "h"),
-        None if d_topk_w is None else _packed(d_topk_w, torch.float32, topk_w.shape, "d_topk_w"), _queue(stream)))
+    if topk_w is not None and row_pair is None:
+        raise ValueError("topk_w: the rows' row_pair is wanted beside it")
+    pr = dw = None
+    if d_topk_w is not None:
+        if topk_w is None or pair_row is None or d_topk_w.shape != topk_w.shape:
+            raise ValueError("d_topk_w: topk_w, of the same shape, and the sort's pair_row are wanted")
+        pr, dw = _flat(pair_row, _I32, R, "pair_row"), _flat(d_topk_w, _F32, R, "d_topk_w")
+    st = (_lib or load()).moeq_swiglu_rows_grad(
+        d_h.data_ptr(), _dtype(d_h), _ld(d_h, "d_h"), _flat(codes, _U8, R * 2 * I, "codes"),
+        _flat(scales, _F32, R * 2 * fp8_groups(I), "scales"), R, I,
+        None if row_pair is None else _flat(row_pair, _I32, R, "row_pair"),
+        None if topk_w is None else _flat(topk_w, _F32, R, "topk_w"), pr, d_gu.data_ptr(), _ld(d_gu, "d_gu"),
+        None if h is None else h.data_ptr(), 0 if h is None else _ld(h, "h"), dw, _queue(stream))
+    if st:
+        raise MoeqError("moeq_swiglu_rows_grad", st)

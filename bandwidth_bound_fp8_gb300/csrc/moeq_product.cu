@@ -112,6 +112,15 @@ __device__ __forceinline__ void copy3(void* dst, const CUtensorMap* map, int x, 
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
             : "memory");
 }
+// Two neighbouring columns of 64 at once, of a matrix whose rows are whole
+// columns; they lie one after the other in shared memory.
+__device__ __forceinline__ void copy_columns(void* dst, const CUtensorMap* map, int col, int row, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(col / kBlock), "r"(bar), "l"(policy)
+        : "memory");
+}
 // A box out of shared memory.
 __device__ __forceinline__ void store3(const CUtensorMap* map, const void* src, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
@@ -558,10 +567,12 @@ struct WeightsArgs {
     Mx4Plan plan;
     int N, K;
     int stages;
+    bool whole;  // N and K are whole columns of 64
     int* status;
 };
 struct WeightsMaps {
     CUtensorMap dy[7], x[7];  // 64 rows, 32, .. 1
+    CUtensorMap dy2, x2;      // 64 rows of two columns of 64
     CUtensorMap dw;
 };
 constexpr int kWStageBytes = 2 * kTileBytes;  // a CTA's 128 rows of dW, and half of the 256 columns
@@ -609,11 +620,25 @@ __device__ __forceinline__ Boxes boxes_of(int at, int rows, bool may_pass) {
 }
 // The rows that copy_rows writes, those written twice twice.
 __device__ __forceinline__ int copied_rows(int rows) {
+    if (rows == kBlock) return kBlock;
     const Boxes v = boxes_of(0, rows, false), z = boxes_of(rows, (-rows) & 15, true);
     return v.n * (kBlock >> v.m) + z.n * (kBlock >> z.m);
 }
-__device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, int col, int r0, int rows, int R,
-                                          uint32_t bar, uint64_t policy) {
+// The copying threads have little time, so whole stages take one copy where
+// they can (maps2) and none of the arithmetic: a dense dW of 16384 rows (K 6144,
+// N 4096) takes 566 us so and 612 without, 64 experts of 384 rows (K 2048, N
+// 2816) 232 and 251.
+__device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, const CUtensorMap* maps2, bool whole, int col,
+                                          int r0, int rows, int R, uint32_t bar, uint64_t policy) {
+    if (rows == kBlock) {
+        if (whole) {
+            copy_columns(at, maps2, col, r0, bar, policy);
+        } else {
+            copy2<true>(at, &maps[0], col, r0, bar, policy);
+            copy2<true>(at + kTileBytes / 2, &maps[0], col + 64, r0, bar, policy);
+        }
+        return;
+    }
     const Boxes v = boxes_of(0, rows, false), z = boxes_of(rows, (-rows) & 15, true);
     for (int i = 0; i < v.n; ++i) {
         const int to = i ? v.last : v.at;
@@ -638,8 +663,8 @@ __global__ void __launch_bounds__(threads_of(true), 1)
     uint8_t* const epi_mem = smem + a.stages * kWStageBytes;
     Shared& s = *reinterpret_cast<Shared*>(epi_mem + kWEpiBytes);
     const PlanShared plan = plan_at(reinterpret_cast<int*>(&s + 1), a.plan.E);
-    if (tid == 0) prefetch_map(&maps.dy[0]);
-    if (tid == 64) prefetch_map(&maps.x[0]);
+    if (tid == 0) prefetch_map(a.whole ? &maps.dy2 : &maps.dy[0]);
+    if (tid == 64) prefetch_map(a.whole ? &maps.x2 : &maps.x[0]);
     if (tid == 128) prefetch_map(&maps.dw);
     const uint32_t tmem = set_up<true, false>(s, a.stages, 1, a.plan, plan);
     volatile int* abort = &s.abort;
@@ -670,9 +695,10 @@ __global__ void __launch_bounds__(threads_of(true), 1)
                     if (warp == 0) {
                         // two CTAs, two operands, two columns of 64
                         if (rank == 0) mbar_arrive_expect_tx(&s.full[ring.at], 8 * 128 * copied_rows(rows));
-                        copy_rows(at, maps.dy, p.n0 + rank * 128, p.r0 + r, rows, a.plan.R, bar, again);
+                        copy_rows(at, maps.dy, &maps.dy2, a.whole, p.n0 + rank * 128, p.r0 + r, rows, a.plan.R, bar, again);
                     } else {
-                        copy_rows(at + kTileBytes, maps.x, p.k0 + rank * 128, p.r0 + r, rows, a.plan.R, bar, again);
+                        copy_rows(at + kTileBytes, maps.x, &maps.x2, a.whole, p.k0 + rank * 128, p.r0 + r, rows, a.plan.R, bar,
+                                  again);
                     }
                     ring.next();
                 }
@@ -776,14 +802,26 @@ __global__ void __launch_bounds__(threads_of(true), 1)
 }
 
 // --------------------------------------------------------------------- host
+bool encode(CUtensorMap* map, const void* p, int dims_n, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    const EncodeTiled f = encode_tiled();
+    return f && f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims_n, const_cast<void*>(p), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool map2(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(box_rows)}, steps[2] = {1, 1};
-    const EncodeTiled f = encode_tiled();
-    return f && f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(box_rows)};
+    return encode(map, p, 2, dims, strides, box);
+}
+// For copy_columns: 64 rows of two columns of 64; cols is a multiple of 64.
+bool columns_map(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld) {
+    const cuuint64_t dims[3] = {kBlock, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / kBlock)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, kBlock * 2};
+    const cuuint32_t box[3] = {kBlock, kBlock, 2};
+    return encode(map, p, 3, dims, strides, box);
 }
 // [E, N, K], contiguous; the box is one expert's.
 bool map3(CUtensorMap* map, const void* p, int f32, int64_t K, int64_t N, int64_t E, int box_k, int box_n) {
@@ -907,6 +945,8 @@ cudaError_t launch_expert_product_grad_w(const void* dy, int64_t ld_dy, const vo
     for (int i = 0; i < 7; ++i)
         if (!map2(&maps.dy[i], dy, N, R, ld_dy, kBlock >> i) || !map2(&maps.x[i], x, K, R, ld_x, kBlock >> i))
             return cudaErrorInvalidValue;
+    a.whole = N % kBlock == 0 && K % kBlock == 0;
+    if (a.whole && (!columns_map(&maps.dy2, dy, N, R, ld_dy) || !columns_map(&maps.x2, x, K, R, ld_x))) return cudaErrorInvalidValue;
     if (!map3(&maps.dw, dw, dw_f32, K, N, E, dw_f32 ? 32 : 64, 32)) return cudaErrorInvalidValue;
     // six stages up to 340 experts, five beyond: 64 experts of 384 rows (K 6144,
     // N 4096) take 846 us with six and 915 with five

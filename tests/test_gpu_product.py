@@ -115,6 +115,14 @@ def test_few_units_of_long_contraction(way, counts, C, features, dt):
     assert torch.equal(out, _run(way, counts, K, N, dt, extra=2))
 
 
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("K,N", [(576, 320), (192, 1088)])
+@pytest.mark.parametrize("counts", [[257, 256, 300, 0, 511, 512, 513, 1025], [64, 128, 640, 1]])
+def test_whole_columns(way, K, N, counts):
+    """Widths that are multiples of 64 and not of 128: one copy a stage."""
+    _run(way, counts, K, N, BF, extra=7)
+
+
 @pytest.mark.parametrize("way", ["y", "dx"])
 def test_many_tiles_of_one_expert(way):
     """More row tiles than a band of them, the last band narrower."""

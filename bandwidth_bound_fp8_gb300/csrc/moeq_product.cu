@@ -122,10 +122,10 @@ __device__ __forceinline__ void copy_columns(void* dst, const CUtensorMap* map, 
         : "memory");
 }
 // A box out of shared memory.
-__device__ __forceinline__ void store3(const CUtensorMap* map, const void* src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+__device__ __forceinline__ void store3(const CUtensorMap* map, const void* src, int x, int y, int z, uint64_t policy) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "l"(policy)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -746,6 +746,9 @@ __global__ void __launch_bounds__(threads_of(true), 1)
         const bool chief = tid == 128 + group * 128;
         uint8_t* const buf_y = epi_mem + (group * 4 + q) * (kWEpiBytes / 8);
         constexpr int kCols = kF32 ? 32 : 64;
+        // dW is not read again here: left to stay in L2 it drives out dy and x (256
+        // experts of 128 rows, K 6144, N 4096: 2550 us so, 2385 with this)
+        const uint64_t once = l2_evict_first_policy();
         WPart p;
         bool ok = true;
         for (int u = 0, i = 0; part(u, p); ++u) {
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(threads_of(true), 1)
                 }
                 fence_smem_for_copies();
                 __syncwarp();
-                if (lane == 0) store3(&maps.dw, buf_y, k0 + c0, n0, p.e);
+                if (lane == 0) store3(&maps.dw, buf_y, k0 + c0, n0, p.e, once);
             }
         }
         if (lane == 0) stores_done();

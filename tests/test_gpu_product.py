@@ -123,6 +123,13 @@ def test_whole_columns(way, K, N, counts):
     _run(way, counts, K, N, BF, extra=7)
 
 
+@pytest.mark.parametrize("N,K", [(1032, 2064), (264, 9000), (1288, 1800), (1024, 2304)])
+@pytest.mark.parametrize("counts", [[257, 256, 300, 0, 511, 512, 513, 1025], [1, 16, 17, 0, 63, 64, 65, 129]])
+def test_weight_gradient_in_wide_units(N, K, counts):
+    """Two blocks of dW share their dy; odd numbers of blocks, an expert without rows, ragged last stages."""
+    _run("dw", counts, K, N, BF, extra=7)
+
+
 @pytest.mark.parametrize("way", ["y", "dx"])
 def test_many_tiles_of_one_expert(way):
     """More row tiles than a band of them, the last band narrower."""

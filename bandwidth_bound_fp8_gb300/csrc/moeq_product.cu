@@ -872,8 +872,8 @@ cudaError_t launch_rows(const RowsArgs& a, const RowsMaps& maps, int grid, int s
 // that most experts are one tile and their weights are read once; from kPairRows
 // on by pairs of CTAs.  Units so few that SMs would be idle are split along
 // their contraction over a cluster instead, eight stages or more a CTA: 16 rows
-// of a dense product (6144 -> 4096, 32 units) take SPLIT1 us by four CTAs a
-// unit and 23 whole, 256 rows SPLIT2 by two and 34 by pairs.  (Clusters of
+// of a dense product (6144 -> 4096, 32 units) take 16.8 us by four CTAs a unit
+// and 23.3 whole, 256 rows 24.6 by two and 34 by pairs.  (Clusters of
 // eight and four leave some SMs out; `clusters` is how many run at once.)
 int64_t most_tiles(int R, int E, int nt) { return E == 1 ? (R + nt - 1) / nt : mx4_max_tiles(R, E, nt); }
 struct How {

@@ -34,15 +34,25 @@ namespace {
 constexpr int kBlock = 64;                      // contraction a stage: 128 bytes of bf16, the swizzle's span
 constexpr int kTileBytes = 128 * kBlock * 2;    // 128 features (or dW rows / columns) of a stage
 constexpr int kAcc1 = 256;                      // TMEM columns of the second accumulator
+// Stages in flight at most: one token over 8 of 256 experts (K 6144, N 4096)
+// takes 70 us with 5, 67 with 7, 66 with 9 and 12; 64 experts of about 6 rows (K
+// 2048, N 2816) 119, 115, 114 and 114.
 constexpr int kMaxStages = 7;
 // Most rows of a tile, for one CTA and for a pair.
 constexpr int kSingleTileRows = 128, kPairTileRows = 256;
-constexpr int kPairRows = 128;  // tiles of this many are a pair's
+// Tiles of this many rows are a pair's.  An average of 72 or 100 rows an expert
+// (64 of them, sizes spread by a fifth) takes pairs 1 to 2 % longer than single
+// CTAs, 128 rows 4 to 8 % less, 256 rows a quarter less.
+constexpr int kPairRows = 128;
 // Steps of 16 contraction indices that one accumulator takes where the output
 // is fp32: the tensor core truncates as it accumulates, so parts of 512 are
-// summed in registers.
+// summed in registers (over K = 2048 the error against 64 bits is 5.1e-7 of the
+// result, with one accumulator 2.6e-6; a plain fp32 product's is 5e-7).
 constexpr int kRun = 32;
-constexpr int kBand = 8;                        // row tiles that take turns on the same weights
+// Row tiles that take turns on the same weights, so that a wave of CTAs covers
+// a block of both operands: a dense product of 16384 rows (6144 -> 4096) takes
+// 437 us so, and 503 with all 64 tiles in a row.
+constexpr int kBand = 8;
 
 __host__ __device__ constexpr int stage_bytes_of(int nt, bool pair) { return kTileBytes + nt / (pair ? 2 : 1) * 128; }
 
@@ -114,7 +124,8 @@ __device__ __forceinline__ void copy3(void* dst, const CUtensorMap* map, int x, 
 }
 // Two neighbouring columns of 64 at once, of a matrix whose rows are whole
 // columns; they lie one after the other in shared memory.
-__device__ __forceinline__ void copy_columns(void* dst, const CUtensorMap* map, int col, int row, uint32_t bar, uint64_t policy) {
+__device__ __forceinline__ void copy_columns(void* dst, const CUtensorMap* map, int col, int row, uint32_t bar,
+                                             uint64_t policy) {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
         "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
@@ -123,10 +134,11 @@ __device__ __forceinline__ void copy_columns(void* dst, const CUtensorMap* map, 
 }
 // A box out of shared memory.
 __device__ __forceinline__ void store3(const CUtensorMap* map, const void* src, int x, int y, int z, uint64_t policy) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "l"(policy)
-                 : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "l"(policy)
+        : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
@@ -335,8 +347,8 @@ __device__ __forceinline__ void send_sums(Shared& s, const float* join, int part
     if (lane == 0) arrive_first(&s.joined);
 }
 template <int kA, int kB, typename GiveUp>
-__device__ __forceinline__ bool add_sums(Shared& s, const float* join, int part_floats, int split, int q, int cols, int lane,
-                                         bool chief, volatile int* abort, GiveUp give_up, float (&v)[kA][kB]) {
+__device__ __forceinline__ bool add_sums(Shared& s, const float* join, int part_floats, int split, int q, int cols,
+                                         int lane, bool chief, volatile int* abort, GiveUp give_up, float (&v)[kA][kB]) {
     if (lane == 0 && !cluster_wait_bounded(&s.joined, 0, abort)) give_up();
     __syncwarp();
     if (chief) s.go[1][0] = !*abort;
@@ -628,8 +640,8 @@ __device__ __forceinline__ int copied_rows(int rows) {
 // they can (maps2) and none of the arithmetic: a dense dW of 16384 rows (K 6144,
 // N 4096) takes 566 us so and 612 without, 64 experts of 384 rows (K 2048, N
 // 2816) 232 and 251.
-__device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, const CUtensorMap* maps2, bool whole, int col,
-                                          int r0, int rows, int R, uint32_t bar, uint64_t policy) {
+__device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, const CUtensorMap* maps2, bool whole,
+                                          int col, int r0, int rows, int R, uint32_t bar, uint64_t policy) {
     if (rows == kBlock) {
         if (whole) {
             copy_columns(at, maps2, col, r0, bar, policy);
@@ -697,8 +709,8 @@ __global__ void __launch_bounds__(threads_of(true), 1)
                         if (rank == 0) mbar_arrive_expect_tx(&s.full[ring.at], 8 * 128 * copied_rows(rows));
                         copy_rows(at, maps.dy, &maps.dy2, a.whole, p.n0 + rank * 128, p.r0 + r, rows, a.plan.R, bar, again);
                     } else {
-                        copy_rows(at + kTileBytes, maps.x, &maps.x2, a.whole, p.k0 + rank * 128, p.r0 + r, rows, a.plan.R, bar,
-                                  again);
+                        copy_rows(at + kTileBytes, maps.x, &maps.x2, a.whole, p.k0 + rank * 128, p.r0 + r, rows, a.plan.R,
+                                  bar, again);
                     }
                     ring.next();
                 }
@@ -868,14 +880,15 @@ cudaError_t launch_rows(const RowsArgs& a, const RowsMaps& maps, int grid, int s
                   kMostSmem, stream);
 }
 
+int64_t most_tiles(int R, int E, int nt) { return E == 1 ? (R + nt - 1) / nt : mx4_max_tiles(R, E, nt); }
+
 // How rows are multiplied: about twice an expert's average of rows a tile, so
 // that most experts are one tile and their weights are read once; from kPairRows
 // on by pairs of CTAs.  Units so few that SMs would be idle are split along
 // their contraction over a cluster instead, eight stages or more a CTA: 16 rows
 // of a dense product (6144 -> 4096, 32 units) take 16.8 us by four CTAs a unit
-// and 23.3 whole, 256 rows 24.6 by two and 34 by pairs.  (Clusters of
-// eight and four leave some SMs out; `clusters` is how many run at once.)
-int64_t most_tiles(int R, int E, int nt) { return E == 1 ? (R + nt - 1) / nt : mx4_max_tiles(R, E, nt); }
+// and 23.3 whole, 256 rows 24.6 by two and 34 by pairs.  (Clusters of eight and
+// four leave some SMs out; `clusters` is how many run at once.)
 struct How {
     Mx4Tiling t;
     int split;
@@ -889,8 +902,8 @@ How how_of(int R, int E, int features, int contraction, int sms) {
     const long long units = most_tiles(R, E, h.t.nt) * ((features + 127) / 128);
     for (int split = 2; split <= 8; split *= 2) {
         const int clusters = split == 8 ? sms * 3 / 32 : split == 4 ? sms * 15 / 64 : sms / 2;
-        if (units <= clusters && (contraction + kBlock - 1) / kBlock >= 8 * split && (split - 1) * h.t.nt * 512 <= 96 * 1024)
-            h.split = split;
+        const bool fits = (split - 1) * h.t.nt * 512 <= 96 * 1024;  // the others' sums
+        if (units <= clusters && fits && (contraction + kBlock - 1) / kBlock >= 8 * split) h.split = split;
     }
     if (h.split == 1 && want >= kPairRows && R >= kPairRows) h.t = {up(rows, 32, kPairTileRows), 32};
     return h;
@@ -922,7 +935,8 @@ cudaError_t launch_expert_product(const void* x, int64_t ld_x, int R, const void
     const int fit = (kMostSmem - rest) / sb;
     a.stages = fit < kMaxStages ? fit : kMaxStages;
     const int smem = a.stages * sb + rest;
-    const int grid = pair ? sms / 2 * 2 : h.split > 1 ? static_cast<int>(most_tiles(R, E, t.nt)) * ((a.N + 127) / 128) * h.split : sms;
+    const int split_grid = static_cast<int>(h.split > 1 ? most_tiles(R, E, t.nt) * ((a.N + 127) / 128) * h.split : 0);
+    const int grid = pair ? sms / 2 * 2 : h.split > 1 ? split_grid : sms;
     const auto by_way = [&](auto f32, auto two, auto cut) {
         constexpr bool kF = decltype(f32)::value, kP = decltype(two)::value, kS = decltype(cut)::value;
         return trans ? launch_rows<kF, kP, true, kS>(a, maps, grid, smem, stream)

@@ -164,7 +164,10 @@ struct Shared {
     int abort, go[2][2];
 };
 
-// Set-up up to the point where memory may be read; ends in a block barrier
+// Set-up up to the point where memory may be read.  (TMEM is taken ahead of the
+// wait for the kernel before: the library's kernels that use it hold 36000
+// registers or more a CTA, so no two of them share an SM, and none waits here
+// for columns that a later one holds.)  Ends in a block barrier
 // (plan_scan's) and, for a pair or a split, one of the cluster.
 template <bool kPair, bool kSplit>
 __device__ __forceinline__ uint32_t set_up(Shared& s, int stages, int split, const Mx4Plan& p, const PlanShared& plan) {

@@ -478,12 +478,16 @@ moeq_status moeq_stack_release_graphs(void);
 
 /* ======================================================================== */
 /* Any number of tokens: the router, the sort of tokens by expert, rows to  */
-/* the experts and back (with gradients), and MXFP4 products.  The calls    */
-/* above stop at MOEQ_MAX_TOKENS; these serve prompts, batches and the      */
-/* training of the routing.  A layer is                                     */
+/* the experts and back (with gradients), MXFP4 products, bf16 products     */
+/* with gradients, and activations kept in 8 bits.  The calls above stop at */
+/* MOEQ_MAX_TOKENS; these serve prompts, batches and training.  A layer is  */
 /*   moeq_route_rows -> moeq_expert_sort ->                                 */
 /*   moeq_mx4_expert_gemm (gate and up) -> moeq_mx4_expert_gemm (down, with */
-/*   MOEQ_ACT_SWIGLU) -> moeq_combine_rows.                                 */
+/*   MOEQ_ACT_SWIGLU) -> moeq_combine_rows,                                 */
+/* and one that trains                                                      */
+/*   moeq_route_rows -> moeq_expert_sort -> moeq_gather_rows ->             */
+/*   moeq_expert_product -> moeq_swiglu_rows -> moeq_expert_product ->      */
+/*   moeq_gather_rows_grad (the sum of a token's rows).                     */
 /* Conventions beyond those above: T, rows and R may be 0; matrices have a  */
 /* leading dimension in elements (rows at least their width apart) and need */
 /* only their elements' alignment (16-byte rows run faster); T * top_k and  */

@@ -888,10 +888,13 @@ int64_t most_tiles(int R, int E, int nt) { return E == 1 ? (R + nt - 1) / nt : m
 // How rows are multiplied: about twice an expert's average of rows a tile, so
 // that most experts are one tile and their weights are read once; from kPairRows
 // on by pairs of CTAs.  Units so few that SMs would be idle are split along
-// their contraction over a cluster instead, eight stages or more a CTA: 16 rows
-// of a dense product (6144 -> 4096, 32 units) take 16.8 us by four CTAs a unit
-// and 23.3 whole, 256 rows 24.6 by two and 34 by pairs.  (Clusters of eight and
-// four leave some SMs out; `clusters` is how many run at once.)
+// their contraction over a cluster instead: a CTA reads about 100 GB/s, and the
+// cluster costs 2 to 4 us, so 40 stages or more, 16 or more a CTA.  16 rows of a
+// dense product of 96 stages (6144 -> 4096, 32 units) take 15.6 us by four CTAs a
+// unit and 22.5 whole, of 44 stages (2816 -> 2048) 12.0 by two and 12.8, of 32
+// stages (2048 -> 6144) 12.1 and 10.6; 256 rows 24 us by two and 33 by pairs.
+// (Clusters of eight and four leave some SMs out; `clusters` is how many run at
+// once.)
 struct How {
     Mx4Tiling t;
     int split;
@@ -903,10 +906,11 @@ How how_of(int R, int E, int features, int contraction, int sms) {
     };
     How h{{up(rows, 16, kSingleTileRows), 16}, 1};
     const long long units = most_tiles(R, E, h.t.nt) * ((features + 127) / 128);
+    const int stages = (contraction + kBlock - 1) / kBlock;
     for (int split = 2; split <= 8; split *= 2) {
         const int clusters = split == 8 ? sms * 3 / 32 : split == 4 ? sms * 15 / 64 : sms / 2;
         const bool fits = (split - 1) * h.t.nt * 512 <= 96 * 1024;  // the others' sums
-        if (units <= clusters && fits && (contraction + kBlock - 1) / kBlock >= 8 * split) h.split = split;
+        if (units <= clusters && fits && stages >= 40 && stages >= 16 * split) h.split = split;
     }
     if (h.split == 1 && want >= kPairRows && R >= kPairRows) h.t = {up(rows, 32, kPairTileRows), 32};
     return h;

@@ -107,7 +107,8 @@ def test_dense(way, rows):
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("counts,C,features", [([1], 4096, 200), ([16], 1024, 136), ([40], 4104, 136), ([100], 2048, 264),
                                                ([128], 4096, 72), ([200], 1032, 520), ([0, 3, 0], 4096, 128), ([1, 0, 2, 5], 2056, 264),
-                                               ([0, 0], 4096, 64)])
+                                               ([0, 0], 4096, 64), ([9], 2568, 2000), ([16], 8192, 136),
+                                               ([64], 8200, 72), ([128], 4096, 4000), ([130, 100], 2560, 2304)])
 def test_few_units_of_long_contraction(way, counts, C, features, dt):
     """Units split over clusters of two, four and eight CTAs; the same result every time."""
     K, N = (C, features) if way == "y" else (features, C)

@@ -131,16 +131,20 @@ def test_only_the_gradients_asked_for():
 
 
 def test_what_is_kept():
-    """Between the passes: x and the gate and up rows in 8 bits, nothing else of their size."""
+    """Between the passes: x and the gate and up rows in 8 bits, nothing else of their size.  (In the bytes that the
+    tensors ask for: an allocation may be handed a whole cached block, up to 1 MB larger, that an earlier test left.)"""
+    def held():
+        return torch.cuda.memory_stats()["requested_bytes.all.current"]
+
     el, lg, x, w_gu, w_d, dout = _setup(T=4096, H=512, I=512)
     ids, w = el.route(lg, 2)
     d = el.Dispatch(ids, lg.shape[1])
     w_gu.requires_grad_()
     x.requires_grad_()
     torch.cuda.synchronize()
-    before = torch.cuda.memory_allocated()
+    before = held()
     out = el.expert_mlp(x, w, w_gu, w_d, d)
-    kept = torch.cuda.memory_allocated() - before - out.numel() * 2
+    kept = held() - before - out.numel() * 2
     T, H, R, I = 4096, 512, 8192, 512
     assert kept <= (T * H + R * 2 * I) * (1 + 4 / 128) + (1 << 16)
 

@@ -429,3 +429,25 @@ def test_refusals():
         moeq.moeq_expert_product(z(8, 60, dt=BF), z(3, 64, 60, dt=BF), offs, z(8, 64))
     with pytest.raises(ValueError, match="x:"):
         moeq.moeq_expert_product_grad_w(z(8, 64, dt=BF), z(7, 64, dt=BF), offs, z(3, 64, 64))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_widest(dt):
+    """Rows of the largest width, and one row less than a block has."""
+    from bandwidth_bound_fp8_gb300 import moeq
+    K = 1 << 20
+    x = _rand(11, 2, K, dt=dt)
+    codes, scales = _quant(x)
+    _same_codes(x, codes, scales)
+    back, xs = torch.empty_like(x), torch.full((4, K), float("nan"), dtype=dt, device="cuda")
+    moeq.moeq_fp8_dequant_rows(codes, scales, back)
+    assert torch.equal(back.cpu(), torch.from_numpy(kp.values(codes.cpu().numpy(), scales.cpu().numpy())).to(dt))
+    offs, pair_row, _ = _pairs(3, 2, 2, 16, 0)
+    moeq.moeq_fp8_gather_rows(codes, scales, offs, pair_row, xs)
+    assert all(torch.equal(xs[pair_row[t, j]], back[t]) for t in range(2) for j in range(2))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,k,I,drop", [(1, 1, 1 << 20, 0), (2, 2, (1 << 20) - 1, 0.3), (700, 3, 1, 0.3), (4000, 2, 24, 0.3)])
+def test_widest_and_narrow_swiglu(T, k, I, drop, dt):
+    test_swiglu_and_its_gradient(T, k, I, drop, dt, True)

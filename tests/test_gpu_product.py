@@ -294,3 +294,25 @@ def test_offsets_past_32_bits():
     _check(y[R - 300:R - 40], x[R - 300:R - 40].double() @ wn[1].double().t(),
            x[R - 300:R - 40].double().abs() @ wn[1].double().abs().t(), 8)
     assert (y[R - 40:] == 0).all()
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("K,N", [(1 << 20, 8), (8, 1 << 20)])
+@pytest.mark.parametrize("counts", [[1], [3, 0, 18]])
+def test_widest(way, K, N, counts):
+    """The largest width: as the contraction, split or not, and as the features."""
+    for dt in (BF, F32):
+        _run(way, counts, K, N, dt, extra=2)
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_many_experts_of_many_rows(way):
+    """The most experts beside the largest tiles: the plan leaves the fewest stages."""
+    _run(way, [(37 * e) % 401 for e in range(1024)], 72, 136, F32, extra=5)
+    _run(way, [(37 * e) % 401 for e in range(1024)], 128, 192, BF)
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_widest_of_many_rows(way):
+    for K, N in ((1 << 18, 64), (64, 1 << 18)):
+        _run(way, [300, 0, 212], K, N, F32)

@@ -300,8 +300,9 @@ unsigned blocks_of(int rows, Split s, int wide, bool vec, int sms) {
 // (The shuffles of the scale want whole warps: rows and groups out of range run
 // along with nothing to load or store.)
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, kVec ? 4 : 5) quant_rows_kernel(const T* x, int64_t ld, int rows, int K, Split sp,
-                                                              uint8_t* __restrict__ codes, float* __restrict__ scales) {
+__global__ void __launch_bounds__(kThreads, kVec ? 4 : 5)
+    quant_rows_kernel(const T* x, int64_t ld, int rows, int K, Split sp, uint8_t* __restrict__ codes,
+                      float* __restrict__ scales) {
     chain();
     const int G = groups_of(K), g = (blockIdx.y << sp.log_groups) + sp.group(), lane16 = threadIdx.x & 15;
     const int c = g * kGroup + col_of<kVec>(lane16), width = min(K, (g + 1) * kGroup) - c;
@@ -392,9 +393,9 @@ __device__ __forceinline__ float weight_of(const SwigluArgs& a, int pair) { retu
 // h[r] = w_r silu(gate) up, and gate and up in 8 bits.  The h, codes and scales
 // of a row that belongs to no expert are zeros, whatever it holds.
 template <typename T, bool kVec, bool kKeep>
-__global__ void __launch_bounds__(kThreads, kVec ? 4 : 5) swiglu_rows_kernel(const SwigluArgs a, const T* gu, int64_t ld, T* __restrict__ h,
-                                                               int64_t ld_h, uint8_t* __restrict__ codes,
-                                                               float* __restrict__ scales) {
+__global__ void __launch_bounds__(kThreads, kVec ? 4 : 5)
+    swiglu_rows_kernel(const SwigluArgs a, const T* gu, int64_t ld, T* __restrict__ h, int64_t ld_h,
+                       uint8_t* __restrict__ codes, float* __restrict__ scales) {
     chain();
     const int G = groups_of(a.I), g = (blockIdx.y << a.sp.log_groups) + a.sp.group(), lane16 = threadIdx.x & 15;
     const int c = g * kGroup + col_of<kVec>(lane16), width = min(a.I, (g + 1) * kGroup) - c;
@@ -443,11 +444,10 @@ __global__ void __launch_bounds__(kThreads, kVec ? 4 : 5) swiglu_rows_kernel(con
 // h again, and d_w[pair] = <dh, silu(gate) up>.  A row's half warps add their
 // parts up in a fixed order.  A pair without a row gets d_w 0.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, 4) swiglu_rows_grad_kernel(const SwigluArgs a, const T* dh, int64_t ld_dh,
-                                                                    const uint8_t* codes, const float* scales,
-                                                                    T* __restrict__ dgu, int64_t ld_dgu, T* __restrict__ h,
-                                                                    int64_t ld_h, const int32_t* pair_row,
-                                                                    float* __restrict__ dw) {
+__global__ void __launch_bounds__(kThreads, 4)
+    swiglu_rows_grad_kernel(const SwigluArgs a, const T* dh, int64_t ld_dh, const uint8_t* codes, const float* scales,
+                            T* __restrict__ dgu, int64_t ld_dgu, T* __restrict__ h, int64_t ld_h,
+                            const int32_t* pair_row, float* __restrict__ dw) {
     chain();
     __shared__ float part[2][kHalves];
     const int G = groups_of(a.I), g0 = a.sp.group(), lane16 = threadIdx.x & 15;

@@ -39,6 +39,9 @@ class Dispatch:
 # gradients alone, and d_y = w d_out depends on w for a constant d_out.)
 # Indices are saved as tensors, so that autograd notices when one is
 # overwritten in place.
+# A step that is captured into a CUDA graph has to be the only one that holds
+# the leaves' gradients: torch's engine ends a capture that meets a node of an
+# eager graph of the same leaves, so drop that graph first.
 def _route_grad(dw, ids, w, E):
     dl = torch.empty((ids.shape[0], E), dtype=w.dtype, device=w.device)
     moeq.moeq_route_rows_grad(dw, ids, w, dl)

@@ -664,53 +664,6 @@ def moeq_mx4_expert_gemm(x, w, w_scales, offs, y, ws: Workspace, row_pair=None, 
 
 
 # ------------------------------------------------------- bf16 products
-def _bf16_rows(t, name: str, R: int, width: int):
-    """Address and leading dimension of bf16 rows [R, width] that tensor copies can read."""
-    if t.dtype is not torch.bfloat16 or t.shape != (R, width):
-        raise ValueError(f"{name}: bf16 rows [{R}, {width}] are wanted, got {t.dtype} {tuple(t.shape)}")
-    ld = _ld(t, name)
-    return t.data_ptr(), ld if R > 1 else (ld + 7) // 8 * 8   # (one row is never stepped over)
-
-
-def _word(status):
-    return None if status is None else _packed(status, torch.int32, (1,), "status")
-
-
-def moeq_expert_product(x, w, offs, y, status=None, stream=None) -> None:
-    """y[r] = w[e(r)] x[r] for rows sorted by expert (offs [E + 1]): x [R, K]
-    bf16, w [E, N, K] bf16, y [R, N] bf16 or fp32.  Rows of y from offs[E] on
-    are zeroed.  status: optional int32 [1] that receives the status word."""
-    R, N = y.shape
-    E, K = offs.shape[0] - 1, x.shape[1]
-    xp, ld = _bf16_rows(x, "x", R, K)
-    _check("moeq_expert_product", (_lib or load()).moeq_expert_product(
-        xp, ld, _packed(w, torch.bfloat16, (E, N, K), "w"), K, N, _offs(offs)[1], E, R, y.data_ptr(), _dtype(y),
-        _ld(y, "y"), _word(status), _queue(stream)))
-
-
-def moeq_expert_product_grad_x(d_y, w, offs, d_x, status=None, stream=None) -> None:
-    """d_x[r] = w[e(r)]^T d_y[r]: d_y [R, N] bf16, d_x [R, K] bf16 or fp32."""
-    R, K = d_x.shape
-    E, N = offs.shape[0] - 1, d_y.shape[1]
-    yp, ld = _bf16_rows(d_y, "d_y", R, N)
-    _check("moeq_expert_product_grad_x", (_lib or load()).moeq_expert_product_grad_x(
-        yp, ld, _packed(w, torch.bfloat16, (E, N, K), "w"), K, N, _offs(offs)[1], E, R, d_x.data_ptr(), _dtype(d_x),
-        _ld(d_x, "d_x"), _word(status), _queue(stream)))
-
-
-def moeq_expert_product_grad_w(d_y, x, offs, d_w, status=None, stream=None) -> None:
-    """d_w[e] = sum of d_y[r] x[r]^T over e's rows: d_y [R, N] and x [R, K]
-    bf16, d_w [E, N, K] bf16 or fp32 (zeros for an expert without rows)."""
-    R, N = d_y.shape
-    E, K = offs.shape[0] - 1, x.shape[1]
-    yp, ld_y = _bf16_rows(d_y, "d_y", R, N)
-    xp, ld_x = _bf16_rows(x, "x", R, K)
-    _check("moeq_expert_product_grad_w", (_lib or load()).moeq_expert_product_grad_w(
-        yp, ld_y, xp, ld_x, K, N, _offs(offs)[1], E, R, _packed(d_w, d_w.dtype, (E, N, K), "d_w"), _dtype(d_w),
-        _word(status), _queue(stream)))
-
-
-# ------------------------------------------------- activations in 8 bits
 # (A small call's time is the host's, and most of that these checks: each
 # property of a tensor is asked for once.)
 def _flat(t, dtype, n: int, name: str):
@@ -724,12 +677,65 @@ def _flat(t, dtype, n: int, name: str):
                      f"strides {t.stride()}")
 
 
+_U8, _F32, _I32 = torch.uint8, torch.float32, torch.int32
+
+
+def _bf16_rows(t, name: str, R: int, width: int):
+    """Address and leading dimension of bf16 rows [R, width] that tensor copies can read."""
+    if t.dtype is not torch.bfloat16 or t.shape != (R, width):
+        raise ValueError(f"{name}: bf16 rows [{R}, {width}] are wanted, got {t.dtype} {tuple(t.shape)}")
+    ld = _ld(t, name)
+    return t.data_ptr(), ld if R > 1 else (ld + 7) // 8 * 8   # (one row is never stepped over)
+
+
+def _word(status):
+    return None if status is None else _flat(status, _I32, 1, "status")
+
+
+def moeq_expert_product(x, w, offs, y, status=None, stream=None) -> None:
+    """y[r] = w[e(r)] x[r] for rows sorted by expert (offs [E + 1]): x [R, K]
+    bf16, w [E, N, K] bf16, y [R, N] bf16 or fp32.  Rows of y from offs[E] on
+    are zeroed.  status: optional int32 [1] that receives the status word."""
+    R, N = y.shape
+    E, K = offs.shape[0] - 1, x.shape[1]
+    xp, ld = _bf16_rows(x, "x", R, K)
+    st = (_lib or load()).moeq_expert_product(
+        xp, ld, _packed(w, torch.bfloat16, (E, N, K), "w"), K, N, _flat(offs, _I32, E + 1, "offs"), E, R, y.data_ptr(), _dtype(y),
+        _ld(y, "y"), _word(status), _queue(stream))
+    if st:
+        raise MoeqError("moeq_expert_product", st)
+
+
+def moeq_expert_product_grad_x(d_y, w, offs, d_x, status=None, stream=None) -> None:
+    """d_x[r] = w[e(r)]^T d_y[r]: d_y [R, N] bf16, d_x [R, K] bf16 or fp32."""
+    R, K = d_x.shape
+    E, N = offs.shape[0] - 1, d_y.shape[1]
+    yp, ld = _bf16_rows(d_y, "d_y", R, N)
+    st = (_lib or load()).moeq_expert_product_grad_x(
+        yp, ld, _packed(w, torch.bfloat16, (E, N, K), "w"), K, N, _flat(offs, _I32, E + 1, "offs"), E, R, d_x.data_ptr(), _dtype(d_x),
+        _ld(d_x, "d_x"), _word(status), _queue(stream))
+    if st:
+        raise MoeqError("moeq_expert_product_grad_x", st)
+
+
+def moeq_expert_product_grad_w(d_y, x, offs, d_w, status=None, stream=None) -> None:
+    """d_w[e] = sum of d_y[r] x[r]^T over e's rows: d_y [R, N] and x [R, K]
+    bf16, d_w [E, N, K] bf16 or fp32 (zeros for an expert without rows)."""
+    R, N = d_y.shape
+    E, K = offs.shape[0] - 1, x.shape[1]
+    yp, ld_y = _bf16_rows(d_y, "d_y", R, N)
+    xp, ld_x = _bf16_rows(x, "x", R, K)
+    st = (_lib or load()).moeq_expert_product_grad_w(
+        yp, ld_y, xp, ld_x, K, N, _flat(offs, _I32, E + 1, "offs"), E, R, _packed(d_w, d_w.dtype, (E, N, K), "d_w"), _dtype(d_w),
+        _word(status), _queue(stream))
+    if st:
+        raise MoeqError("moeq_expert_product_grad_w", st)
+
+
+# ------------------------------------------------- activations in 8 bits
 def fp8_groups(K: int) -> int:
     """Scales of a row of K columns."""
     return (K + 127) >> 7
-
-
-_U8, _F32, _I32 = torch.uint8, torch.float32, torch.int32
 
 
 def moeq_fp8_quant_rows(x, codes, scales, stream=None) -> None:

@@ -643,7 +643,8 @@ moeq_status moeq_expert_product_grad_w(const void* d_y, int64_t ld_dy, const voi
 /*          (the last group of a row is shorter); contiguous                */
 /* A code stands for fl32(code * s), rounded once more to bf16 where that   */
 /* is the type asked for.  Unlike moeq_quant_act, a group with a NaN or an  */
-/* infinity gets the scale NaN and codes 0: it comes back as NaN.           */
+/* infinity gets the scale NaN and codes 0: it comes back as NaN.  No       */
+/* output of these calls and the two below overlaps an input.               */
 /*   moeq_fp8_quant_rows    x [rows, K] bf16 or fp32 -> codes, scales       */
 /*   moeq_fp8_dequant_rows  and back                                        */
 /*   moeq_fp8_gather_rows   xs[pair_row[t, j]] = the values of row t, as    */

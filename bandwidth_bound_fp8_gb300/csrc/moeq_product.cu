@@ -49,6 +49,9 @@ constexpr int kPairRows = 128;
 // summed in registers (over K = 2048 the error against 64 bits is 5.1e-7 of the
 // result, with one accumulator 2.6e-6; a plain fp32 product's is 5e-7).
 constexpr int kRun = 32;
+// The same for a bf16 dW: no thread then waits long for one part of a sum over
+// millions of rows, which fp32 registers also add up better.
+constexpr int kLongRun = 4096;
 // Row tiles that take turns on the same weights, so that a wave of CTAs covers
 // a block of both operands: a dense product of 16384 rows (6144 -> 4096) takes
 // 437 us so, and 503 with all 64 tiles in a row.
@@ -749,7 +752,7 @@ __global__ void __launch_bounds__(threads_of(true), 1)
             for (int u = 0, i = 0; ok && more;) {
                 more = part(u++, p);
                 if (!more) ok = push_part(s, i, 0, abort);
-                const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : steps_n;
+                const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : kLongRun;
                 for (int k0 = 0; ok && more && k0 < steps_n; k0 += run)
                     ok = push_part(s, i++, part_of(256, min(run, steps_n - k0)), abort);
             }
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(threads_of(true), 1)
         bool ok = true;
         for (int u = 0, i = 0; part(u, p); ++u) {
             const int n0 = p.n0 + rank * 128 + q * 32, k0 = p.k0 + group * 128;
-            const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : steps_n;
+            const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : kLongRun;
             float v[128 / kCols][kCols];
             if (p.cnt == 0) {
 #pragma unroll

@@ -316,3 +316,14 @@ def test_many_experts_of_many_rows(way):
 def test_widest_of_many_rows(way):
     for K, N in ((1 << 18, 64), (64, 1 << 18)):
         _run(way, [300, 0, 212], K, N, F32)
+
+
+def test_weight_gradient_of_one_long_expert():
+    """2^29 rows of ones: a sum that one accumulator does not hold, of more stages than one wait lasts."""
+    R = (1 << 29) + 64
+    ones = torch.ones((R, 8), dtype=BF, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dt in (F32, BF):
+        out = torch.empty((2, 8, 8), dtype=dt, device="cuda")
+        _call("dw", ones, ones, torch.tensor([0, R - 64, R], dtype=torch.int32, device="cuda"), out, status=status)
+        assert int(status) == 0 and (out[0] == R - 64).all() and (out[1] == 64).all()

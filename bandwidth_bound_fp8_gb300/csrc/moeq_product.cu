@@ -22,8 +22,7 @@
 // stage may reach past the expert's last row: what follows are another
 // expert's rows (or a NaN in a masked place), and 0 * NaN is not 0.  So the
 // last stage is copied row-exactly, in boxes of a power of two of rows, and
-// filled up to the MMA's 16 rows from beyond the matrix, where a tensor copy
-// reads zeros.
+// filled up to the MMA's 16 rows with zeros.
 #include "moeq_mx4_plan.cuh"
 #include "moeq_pair.cuh"
 #include "moeq_rows.h"
@@ -619,42 +618,28 @@ __device__ __forceinline__ bool wpart_at(const WeightsArgs& a, const PlanShared&
     return true;
 }
 
-// 64 rows of 128 columns, or fewer at the end of an expert's, into a stage.
-// Then the rows up to the next multiple of 16 are zeros, read from beyond the
-// matrix (R).  Two boxes of the largest power of two cover any count, one from
-// each end (what both write is the same); zeros may also run on into rows that
-// no MMA reads.  (A box for each bit of the count: 64 experts of 383 rows, K
-// 6144, N 4096, took 1030 us where 384 take 868.)
+// 64 rows of 128 columns, or fewer at the end of an expert's, into a stage.  Two
+// boxes of the largest power of two cover any count, one from each end (what
+// both write is the same).  (A box for each bit of the count: 64 experts of 383
+// rows, K 6144, N 4096, took 1030 us where 384 take 868.)
 struct Boxes {
-    int m, n;      // maps[m]: 64 >> m rows; how many boxes
-    int at, last;  // rows of the stage where they start
+    int m, n;  // maps[m]: 64 >> m rows; how many boxes
 };
-__device__ __forceinline__ Boxes boxes_of(int at, int rows, bool may_pass) {
-    Boxes b{0, 0, at, at};
-    if (rows == 0) return b;
-    b.m = __clz(rows) - 25;  // the largest box of at most `rows` rows
-    int box = kBlock >> b.m;
-    b.n = box == rows ? 1 : 2;
-    if (may_pass && b.n == 2 && at + 2 * box <= kBlock) {
-        --b.m;
-        b.n = 1;
-        return b;
-    }
-    b.last = at + rows - box;
-    return b;
+__device__ __forceinline__ Boxes boxes_of(int rows) {
+    const int m = __clz(rows) - 25;  // the largest box of at most `rows` rows
+    return {m, kBlock >> m == rows ? 1 : 2};
 }
-// The rows that copy_rows writes, those written twice twice.
+// The rows that arrive, those copied twice twice.
 __device__ __forceinline__ int copied_rows(int rows) {
-    if (rows == kBlock) return kBlock;
-    const Boxes v = boxes_of(0, rows, false), z = boxes_of(rows, (-rows) & 15, true);
-    return v.n * (kBlock >> v.m) + z.n * (kBlock >> z.m);
+    const Boxes v = boxes_of(rows);
+    return v.n * (kBlock >> v.m);
 }
 // The copying threads have little time, so whole stages take one copy where
 // they can (maps2) and none of the arithmetic: a dense dW of 16384 rows (K 6144,
 // N 4096) takes 566 us so and 612 without, 64 experts of 384 rows (K 2048, N
 // 2816) 232 and 251.
 __device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, const CUtensorMap* maps2, bool whole,
-                                          int col, int r0, int rows, int R, uint32_t bar, uint64_t policy) {
+                                          int col, int r0, int rows, uint32_t bar, uint64_t policy) {
     if (rows == kBlock) {
         if (whole) {
             copy_columns(at, maps2, col, r0, bar, policy);
@@ -664,17 +649,24 @@ __device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, 
         }
         return;
     }
-    const Boxes v = boxes_of(0, rows, false), z = boxes_of(rows, (-rows) & 15, true);
+    const Boxes v = boxes_of(rows);
     for (int i = 0; i < v.n; ++i) {
-        const int to = i ? v.last : v.at;
+        const int to = i ? rows - (kBlock >> v.m) : 0;
         copy2<true>(at + to * 128, &maps[v.m], col, r0 + to, bar, policy);
         copy2<true>(at + kTileBytes / 2 + to * 128, &maps[v.m], col + 64, r0 + to, bar, policy);
     }
-    for (int i = 0; i < z.n; ++i) {
-        const int to = i ? z.last : z.at;
-        copy2<true>(at + to * 128, &maps[z.m], col, R, bar, policy);
-        copy2<true>(at + kTileBytes / 2 + to * 128, &maps[z.m], col + 64, R, bar, policy);
-    }
+}
+// The rows behind them up to the next multiple of 16: zeros, written by the warp
+// whose copies into the same stage follow, so that the MMAs that wait for those
+// copies find them.  (Zeros copied from beyond the matrix, or from an array of
+// them, cost more than the rows: 64 experts of 376 rows, K 6144, N 4096, 1046
+// us, so 950.)
+__device__ __forceinline__ void zero_rows(uint8_t* at, int rows, int lane) {
+    uint8_t* const to = at + ((lane >> 3) & 1) * (kTileBytes / 2) + (lane & 7) * 16;
+    for (int r = rows + (lane >> 4); r < ((rows + 15) & ~15); r += 2)
+        *reinterpret_cast<uint4*>(to + r * 128) = make_uint4(0, 0, 0, 0);
+    fence_smem_for_copies();
+    __syncwarp();
 }
 
 template <bool kF32>
@@ -704,35 +696,50 @@ __global__ void __launch_bounds__(threads_of(true), 1)
     if (warp == 0 || warp == 2) {
         // -------------------------------------------------------- copies
         // Warp 0 copies dy, warp 2 x: both come from L2 for every block of dW.
-        if (elect_one()) {
-            const uint64_t again = l2_evict_normal_policy();
-            WPart p;
-            Ring ring{a.stages};
-            int it = 0;
-            bool ok = true;
-            for (int i = 0; ok && part(i, p); ++i)
-                for (int r = 0; r < p.cnt; r += kBlock, ++it) {
+        const uint64_t again = l2_evict_normal_policy();
+        const bool leader = elect_one();
+        const CUtensorMap* const some = warp == 0 ? maps.dy : maps.x;
+        const CUtensorMap* const two = warp == 0 ? &maps.dy2 : &maps.x2;
+        uint8_t* const mine = smem + (warp == 0 ? 0 : kTileBytes);
+        WPart p;
+        Ring ring{a.stages};
+        int it = 0;
+        bool ok = true;
+        for (int i = 0; ok && part(i, p); ++i) {
+            const int col = (warp == 0 ? p.n0 : p.k0) + rank * 128;
+            const auto copies = [&](int r, int rows) {
+                // two CTAs, two operands, two columns of 64
+                if (warp == 0 && rank == 0) mbar_arrive_expect_tx(&s.full[ring.at], 8 * 128 * copied_rows(rows));
+                copy_rows(mine + ring.at * kWStageBytes, some, two, a.whole, col, p.r0 + r, rows, in_first(&s.full[ring.at]),
+                          again);
+            };
+            const int whole = p.cnt & ~(kBlock - 1), rows = p.cnt - whole;
+            if (leader) {
+                for (int r = 0; r < whole; r += kBlock, ++it) {
                     if (it >= a.stages) ok = mbar_wait_bounded(&s.empty[ring.at], ring.phase ^ 1, abort);
                     if (!ok) break;
-                    uint8_t* const at = smem + ring.at * kWStageBytes;
-                    const uint32_t bar = in_first(&s.full[ring.at]);
-                    const int rows = min(p.cnt - r, kBlock);
-                    if (warp == 0) {
-                        // two CTAs, two operands, two columns of 64
-                        if (rank == 0) mbar_arrive_expect_tx(&s.full[ring.at], 8 * 128 * copied_rows(rows));
-                        copy_rows(at, maps.dy, &maps.dy2, a.whole, p.n0 + rank * 128, p.r0 + r, rows, a.plan.R, bar, again);
-                    } else {
-                        copy_rows(at + kTileBytes, maps.x, &maps.x2, a.whole, p.k0 + rank * 128, p.r0 + r, rows, a.plan.R,
-                                  bar, again);
-                    }
+                    copies(r, kBlock);
                     ring.next();
                 }
-            if (!ok) {
-                give_up();
-                const unsigned long long t0 = global_timer_ns();
-                for (int j = max(0, it - a.stages); rank == 0 && j < it; ++j)
-                    drain(&s.full[j % a.stages], (j / a.stages) & 1, t0);
+                if (ok && rows && it >= a.stages) ok = mbar_wait_bounded(&s.empty[ring.at], ring.phase ^ 1, abort);
             }
+            ok = __all_sync(~0u, ok);
+            if (!ok || rows == 0) continue;
+            if (rows & 15) {
+                __syncwarp();  // what the leader waited for
+                zero_rows(mine + __reduce_max_sync(~0u, leader ? ring.at : 0) * kWStageBytes, rows, lane);
+            }
+            if (leader) {
+                copies(whole, rows);
+                ring.next();
+                ++it;
+            }
+        }
+        if (leader && !ok) {
+            give_up();
+            const unsigned long long t0 = global_timer_ns();
+            for (int j = max(0, it - a.stages); rank == 0 && j < it; ++j)
+                drain(&s.full[j % a.stages], (j / a.stages) & 1, t0);
         }
         __syncwarp();
     } else if (warp == 1) {

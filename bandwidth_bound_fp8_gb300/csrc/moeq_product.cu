@@ -17,8 +17,8 @@
 // Whole units, round robin over the CTAs (pairs); none waits for another.  A
 // few units are split along their contraction instead (see how_of).
 //
-// Weights out (dW): a unit is (expert, 256 x 256 of dW) for a pair, the
-// contraction over the expert's rows in stages of 64.  Rows are sorted, so a
+// Weights out (dW): a unit is (expert, 256 x 256 of dW, or 256 x 128 where units
+// are few) for a pair, the contraction over the expert's rows in stages of 64.  Rows are sorted, so a
 // stage may reach past the expert's last row: what follows are another
 // expert's rows (or a NaN in a masked place), and 0 * NaN is not 0.  So the
 // last stage is copied row-exactly, in boxes of a power of two of rows, and
@@ -309,24 +309,24 @@ __device__ __forceinline__ void release_acc(Shared& s, int buf, int rank, int la
             mbar_arrive(&s.acc_empty[buf]);
     }
 }
-// A part's `cols` columns (at most 128) of this thread's lane into registers,
+// A part's `cols` columns (at most kA kB) of this thread's lane into registers,
 // or added to what is there; then the accumulator is free.  All loads of a
 // first part are in flight at once: the MMAs of the part after next wait for
 // them.
 template <bool kPair, int kA, int kB>
 __device__ __forceinline__ void take_acc(Shared& s, int buf, uint32_t acc, int cols, bool first, int rank, int lane,
                                          float (&v)[kA][kB]) {
-    static_assert(kA * kB == 128 && kB % 16 == 0, "128 columns");
+    static_assert(kB % 16 == 0, "loads of 16 columns");
     if (first) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 16)
+        for (int c = 0; c < kA * kB; c += 16)
             if (c < cols) tmem_ld16(acc + c, v[c / kB] + c % kB);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) tmem_use16(v[c / kB] + c % kB);
+        for (int c = 0; c < kA * kB; c += 16) tmem_use16(v[c / kB] + c % kB);
     } else {
 #pragma unroll
-        for (int c = 0; c < 128; c += 16)
+        for (int c = 0; c < kA * kB; c += 16)
             if (c < cols) {
                 float t[16];
                 tmem_ld16(acc + c, t);
@@ -599,26 +599,30 @@ struct WeightsMaps {
     CUtensorMap dy2, x2;      // 64 rows of two columns of 64
     CUtensorMap dw;
 };
-constexpr int kWStageBytes = 2 * kTileBytes;  // a CTA's 128 rows of dW, and half of the 256 columns
+// A unit is 256 rows of dW and kWide columns, 256 or 128 (see wide_units).
+// A stage: a CTA's 128 rows, and half of the columns.
+template <int kWide>
+constexpr int kWStageBytes = kTileBytes + kWide / 2 * 128;
 constexpr int kWEpiBytes = 8 * 4096;          // 128 bytes of 32 rows for each epilogue warp
 
 struct WPart {
     int e, n0, k0, r0, cnt;
 };
+template <int kWide>
 __device__ __forceinline__ bool wpart_at(const WeightsArgs& a, const PlanShared& plan, int i, int worker, int workers,
                                          WPart& p) {
-    const int nbu = (a.N + 255) / 256, kbu = (a.K + 255) / 256, u = worker + i * workers;
+    const int nbu = (a.N + 255) / 256, kbu = (a.K + kWide - 1) / kWide, u = worker + i * workers;
     if (u >= a.plan.E * nbu * kbu) return false;
     p.e = u / (nbu * kbu);
     const int in = u - p.e * nbu * kbu, nb = in / kbu;
     p.n0 = nb * 256;
-    p.k0 = (in - nb * kbu) * 256;
+    p.k0 = (in - nb * kbu) * kWide;
     p.r0 = plan.first[p.e];
     p.cnt = plan.first[p.e + 1] - p.r0;
     return true;
 }
 
-// 64 rows of 128 columns, or fewer at the end of an expert's, into a stage.  Two
+// 64 rows of two columns of 64 (or one), or fewer at the end of an expert's, into a stage.  Two
 // boxes of the largest power of two cover any count, one from each end (what
 // both write is the same).  (A box for each bit of the count: 64 experts of 383
 // rows, K 6144, N 4096, took 1030 us where 384 take 868.)
@@ -639,13 +643,13 @@ __device__ __forceinline__ int copied_rows(int rows) {
 // N 4096) takes 566 us so and 612 without, 64 experts of 384 rows (K 2048, N
 // 2816) 232 and 251.
 __device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, const CUtensorMap* maps2, bool whole,
-                                          int col, int r0, int rows, uint32_t bar, uint64_t policy) {
+                                          bool two, int col, int r0, int rows, uint32_t bar, uint64_t policy) {
     if (rows == kBlock) {
-        if (whole) {
+        if (whole && two) {
             copy_columns(at, maps2, col, r0, bar, policy);
         } else {
             copy2<true>(at, &maps[0], col, r0, bar, policy);
-            copy2<true>(at + kTileBytes / 2, &maps[0], col + 64, r0, bar, policy);
+            if (two) copy2<true>(at + kTileBytes / 2, &maps[0], col + 64, r0, bar, policy);
         }
         return;
     }
@@ -653,7 +657,7 @@ __device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, 
     for (int i = 0; i < v.n; ++i) {
         const int to = i ? rows - (kBlock >> v.m) : 0;
         copy2<true>(at + to * 128, &maps[v.m], col, r0 + to, bar, policy);
-        copy2<true>(at + kTileBytes / 2 + to * 128, &maps[v.m], col + 64, r0 + to, bar, policy);
+        if (two) copy2<true>(at + kTileBytes / 2 + to * 128, &maps[v.m], col + 64, r0 + to, bar, policy);
     }
 }
 // The rows behind them up to the next multiple of 16: zeros, written by the warp
@@ -661,15 +665,15 @@ __device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, 
 // copies find them.  (Zeros copied from beyond the matrix, or from an array of
 // them, cost more than the rows: 64 experts of 376 rows, K 6144, N 4096, 1046
 // us, so 950.)
-__device__ __forceinline__ void zero_rows(uint8_t* at, int rows, int lane) {
-    uint8_t* const to = at + ((lane >> 3) & 1) * (kTileBytes / 2) + (lane & 7) * 16;
-    for (int r = rows + (lane >> 4); r < ((rows + 15) & ~15); r += 2)
+__device__ __forceinline__ void zero_rows(uint8_t* at, bool two, int rows, int lane) {
+    uint8_t* const to = at + (two && (lane & 8) ? kTileBytes / 2 : 0) + (lane & 7) * 16;
+    for (int r = rows + (two ? lane >> 4 : lane >> 3); r < ((rows + 15) & ~15); r += two ? 2 : 4)
         *reinterpret_cast<uint4*>(to + r * 128) = make_uint4(0, 0, 0, 0);
     fence_smem_for_copies();
     __syncwarp();
 }
 
-template <bool kF32>
+template <bool kF32, int kWide>
 __global__ void __launch_bounds__(threads_of(true), 1)
     product_weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ WeightsMaps maps) {
     // (everything is dynamic, and starts where the swizzle's pattern does: six
@@ -677,7 +681,7 @@ __global__ void __launch_bounds__(threads_of(true), 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cluster_rank());
-    uint8_t* const epi_mem = smem + a.stages * kWStageBytes;
+    uint8_t* const epi_mem = smem + a.stages * kWStageBytes<kWide>;
     Shared& s = *reinterpret_cast<Shared*>(epi_mem + kWEpiBytes);
     const PlanShared plan = plan_at(reinterpret_cast<int*>(&s + 1), a.plan.E);
     if (tid == 0) prefetch_map(a.whole ? &maps.dy2 : &maps.dy[0]);
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(threads_of(true), 1)
     const uint32_t tmem = set_up<true, false>(s, a.stages, 1, a.plan, plan);
     volatile int* abort = &s.abort;
     const int workers = gridDim.x / 2, worker = blockIdx.x / 2;
-    auto part = [&](int i, WPart& p) { return wpart_at(a, plan, i, worker, workers, p); };
+    auto part = [&](int i, WPart& p) { return wpart_at<kWide>(a, plan, i, worker, workers, p); };
     auto give_up = [&] {
         *abort = 1;
         if (a.status) atomicExch(a.status, static_cast<int>(MOEQ_ERR_TIMEOUT));
@@ -699,19 +703,21 @@ __global__ void __launch_bounds__(threads_of(true), 1)
         const uint64_t again = l2_evict_normal_policy();
         const bool leader = elect_one();
         const CUtensorMap* const some = warp == 0 ? maps.dy : maps.x;
-        const CUtensorMap* const two = warp == 0 ? &maps.dy2 : &maps.x2;
+        const CUtensorMap* const pairs = warp == 0 ? &maps.dy2 : &maps.x2;
+        const bool two = kWide == 256 || warp == 0;  // columns of 64 that this CTA copies
         uint8_t* const mine = smem + (warp == 0 ? 0 : kTileBytes);
         WPart p;
         Ring ring{a.stages};
         int it = 0;
         bool ok = true;
         for (int i = 0; ok && part(i, p); ++i) {
-            const int col = (warp == 0 ? p.n0 : p.k0) + rank * 128;
+            const int col = (warp == 0 ? p.n0 : p.k0) + rank * (two ? 128 : 64);
             const auto copies = [&](int r, int rows) {
-                // two CTAs, two operands, two columns of 64
-                if (warp == 0 && rank == 0) mbar_arrive_expect_tx(&s.full[ring.at], 8 * 128 * copied_rows(rows));
-                copy_rows(mine + ring.at * kWStageBytes, some, two, a.whole, col, p.r0 + r, rows, in_first(&s.full[ring.at]),
-                          again);
+                // both CTAs' columns of 64 of both operands
+                if (warp == 0 && rank == 0)
+                    mbar_arrive_expect_tx(&s.full[ring.at], (256 + kWide) / 64 * 128 * copied_rows(rows));
+                copy_rows(mine + ring.at * kWStageBytes<kWide>, some, pairs, a.whole, two, col, p.r0 + r, rows,
+                          in_first(&s.full[ring.at]), again);
             };
             const int whole = p.cnt & ~(kBlock - 1), rows = p.cnt - whole;
             if (leader) {
@@ -727,7 +733,7 @@ __global__ void __launch_bounds__(threads_of(true), 1)
             if (!ok || rows == 0) continue;
             if (rows & 15) {
                 __syncwarp();  // what the leader waited for
-                zero_rows(mine + __reduce_max_sync(~0u, leader ? ring.at : 0) * kWStageBytes, rows, lane);
+                zero_rows(mine + __reduce_max_sync(~0u, leader ? ring.at : 0) * kWStageBytes<kWide>, two, rows, lane);
             }
             if (leader) {
                 copies(whole, rows);
@@ -747,7 +753,7 @@ __global__ void __launch_bounds__(threads_of(true), 1)
         if (rank == 0 && elect_one()) {
             const uint32_t base = smem_u32(smem);
             issue_parts<true, 128, 128>(
-                s, a.stages, kWStageBytes, tmem, desc_mn(base), desc_mn(base + kTileBytes),
+                s, a.stages, kWStageBytes<kWide>, tmem, desc_mn(base), desc_mn(base + kTileBytes),
                 [](int n) { return idesc_bf16(256, n, true, true); }, abort, a.status);
         }
         __syncwarp();
@@ -761,7 +767,7 @@ __global__ void __launch_bounds__(threads_of(true), 1)
                 if (!more) ok = push_part(s, i, 0, abort);
                 const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : kLongRun;
                 for (int k0 = 0; ok && more && k0 < steps_n; k0 += run)
-                    ok = push_part(s, i++, part_of(256, min(run, steps_n - k0)), abort);
+                    ok = push_part(s, i++, part_of(kWide, min(run, steps_n - k0)), abort);
             }
             if (!ok) give_up();
         }
@@ -777,29 +783,29 @@ __global__ void __launch_bounds__(threads_of(true), 1)
         const int q = warp & 3, group = (warp >> 2) - 1;
         const bool chief = tid == 128 + group * 128;
         uint8_t* const buf_y = epi_mem + (group * 4 + q) * (kWEpiBytes / 8);
-        constexpr int kCols = kF32 ? 32 : 64;
+        constexpr int kCols = kF32 ? 32 : 64, kMine = kWide / 2;  // a step's and a group's columns
         // dW is not read again here: left to stay in L2 it drives out dy and x (256
         // experts of 128 rows, K 6144, N 4096: 2550 us so, 2385 with this)
         const uint64_t once = l2_evict_first_policy();
         WPart p;
         bool ok = true;
         for (int u = 0, i = 0; part(u, p); ++u) {
-            const int n0 = p.n0 + rank * 128 + q * 32, k0 = p.k0 + group * 128;
+            const int n0 = p.n0 + rank * 128 + q * 32, k0 = p.k0 + group * kMine;
             const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : kLongRun;
-            float v[128 / kCols][kCols];
+            float v[kMine / kCols][kCols];
             if (p.cnt == 0) {
 #pragma unroll
-                for (int c = 0; c < 128; ++c) v[c / kCols][c % kCols] = 0.f;
+                for (int c = 0; c < kMine; ++c) v[c / kCols][c % kCols] = 0.f;
             }
             for (int st = 0; ok && st < steps_n; st += run, ++i) {
                 ok = part_done(s, i, group, lane, chief, abort, give_up);
                 if (!ok) break;
-                const uint32_t acc = tmem + (i & 1) * kAcc1 + group * 128 + (static_cast<uint32_t>(q * 32) << 16);
-                take_acc<true>(s, i & 1, acc, 128, st == 0, rank, lane, v);
+                const uint32_t acc = tmem + (i & 1) * kAcc1 + group * kMine + (static_cast<uint32_t>(q * 32) << 16);
+                take_acc<true>(s, i & 1, acc, kMine, st == 0, rank, lane, v);
             }
             if (!ok) break;
 #pragma unroll
-            for (int c0 = 0; c0 < 128; c0 += kCols) {
+            for (int c0 = 0; c0 < kMine; c0 += kCols) {
                 if (n0 >= a.N || k0 + c0 >= a.K) continue;
                 const float(&w)[kCols] = v[c0 / kCols];
                 if (lane == 0) stores_read();  // the copy before has left the buffer
@@ -933,6 +939,20 @@ How how_of(int R, int E, int features, int contraction, int sms) {
     return h;
 }
 
+// Whether dW's units are 256 x 256, or half of that where twice as many take the
+// pairs no more turns: a dense 1000 x 1064 of 4096 rows takes 33.2 us in 20 wide
+// units and 27.2 in 36, 256 x 6144 25.6 and 20.1 (24 and 48), of 512 rows in fp32
+// 11.4 and 9.6.  With another turn they lose: 2816 x 2048 of 4096 rows 42.3 and
+// 43.9 (two and three), 8 experts of 1024 rows, 1000 x 1064, 31.5 and 35.4 (three
+// and four); 60 experts of 273 rows, 2816 x 2048, 166 and 239.
+bool wide_units(int E, int N, int K, int sms) {
+    const auto turns = [&](int wide) {
+        const long long units = static_cast<long long>(E) * ((N + 255) / 256) * ((K + wide - 1) / wide);
+        return (units + sms / 2 - 1) / (sms / 2);
+    };
+    return turns(128) > turns(256);
+}
+
 }  // namespace
 
 cudaError_t launch_expert_product(const void* x, int64_t ld_x, int R, const void* w, int E, int N, int K, bool trans,
@@ -989,15 +1009,22 @@ cudaError_t launch_expert_product_grad_w(const void* dy, int64_t ld_dy, const vo
     a.whole = N % kBlock == 0 && K % kBlock == 0;
     if (a.whole && (!columns_map(&maps.dy2, dy, N, R, ld_dy) || !columns_map(&maps.x2, x, K, R, ld_x))) return cudaErrorInvalidValue;
     if (!map3(&maps.dw, dw, dw_f32, K, N, E, dw_f32 ? 32 : 64, 32)) return cudaErrorInvalidValue;
-    // six stages up to 340 experts, five beyond: 64 experts of 384 rows (K 6144,
-    // N 4096) take 846 us with six and 915 with five
-    const int rest = kWEpiBytes + static_cast<int>(sizeof(Shared)) + plan_ints(E) * static_cast<int>(sizeof(int));
-    const int fit = (227 * 1024 - rest) / kWStageBytes;
-    a.stages = fit < kMaxStages ? fit : kMaxStages;
-    const int smem = a.stages * kWStageBytes + rest;
-    static OncePerDevice once[2];
-    return dw_f32 ? launch(product_weights_kernel<true>, once[1], a, maps, true, 2, sms / 2 * 2, smem, 227 * 1024, stream)
-                  : launch(product_weights_kernel<false>, once[0], a, maps, true, 2, sms / 2 * 2, smem, 227 * 1024, stream);
+    const auto by_width = [&](auto width) {
+        constexpr int kWide = decltype(width)::value;
+        // six stages of wide units up to 340 experts, five beyond: 64 experts of 384
+        // rows (K 6144, N 4096) take 846 us with six and 915 with five
+        const int rest = kWEpiBytes + static_cast<int>(sizeof(Shared)) + plan_ints(E) * static_cast<int>(sizeof(int));
+        const int fit = (227 * 1024 - rest) / kWStageBytes<kWide>;
+        a.stages = fit < kMaxStages ? fit : kMaxStages;
+        const int smem = a.stages * kWStageBytes<kWide> + rest;
+        static OncePerDevice once[2];
+        return dw_f32 ? launch(product_weights_kernel<true, kWide>, once[1], a, maps, true, 2, sms / 2 * 2, smem, 227 * 1024,
+                               stream)
+                      : launch(product_weights_kernel<false, kWide>, once[0], a, maps, true, 2, sms / 2 * 2, smem,
+                               227 * 1024, stream);
+    };
+    return wide_units(E, N, K, sms) ? by_width(std::integral_constant<int, 256>{})
+                                    : by_width(std::integral_constant<int, 128>{});
 }
 
 }  // namespace moeq

@@ -327,3 +327,12 @@ def test_weight_gradient_of_one_long_expert():
         out = torch.empty((2, 8, 8), dtype=dt, device="cuda")
         _call("dw", ones, ones, torch.tensor([0, R - 64, R], dtype=torch.int32, device="cuda"), out, status=status)
         assert int(status) == 0 and (out[0] == R - 64).all() and (out[1] == 64).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("E,N,K", [(8, 768, 768), (8, 776, 776), (2, 264, 1032), (2, 256, 1024), (1, 1000, 1064),
+                                   (40, 512, 128), (40, 512, 136)])
+def test_weight_gradient_in_units_of_both_widths(E, N, K, dt):
+    """Few units (halves), many (whole ones), and many of one half's columns, with every kind of last stage."""
+    counts = [(0, 1, 15, 16, 17, 63, 64, 65, 127, 600, 31, 47)[(5 * e + E) % 12] for e in range(E)]
+    _run("dw", counts, K, N, dt, extra=3)

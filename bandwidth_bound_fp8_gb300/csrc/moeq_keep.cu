@@ -283,11 +283,18 @@ struct Split {
     __device__ __forceinline__ int group() const { return half() & ((1 << log_groups) - 1); }
 };
 __host__ __device__ constexpr int groups_of(int K) { return (K + kGroup - 1) / kGroup; }
-Split split_of(int groups) {
-    Split s{0};
-    while ((1 << s.log_groups) < groups && (1 << s.log_groups) < kHalves) ++s.log_groups;
+// The most half warps a row, up to 2^most, that leave at most `idle` of them
+// without a group in a row's last turn.
+Split split_of(int groups, int most, int idle) {
+    static_assert(kHalves == 1 << 4, "most is at most 4");
+    Split s{most};
+    while (((groups + (1 << s.log_groups) - 1) >> s.log_groups << s.log_groups) > groups + idle) --s.log_groups;
     return s;
 }
+// Where groups are independent, none idle: 32760 bf16 rows of 2 x 1408 (11
+// groups, kept) take 72 us with one half warp a row and 112 with 16, of 2 x 2816
+// 137 with two and 181, of 2 x 2048 98 with two and with 16.
+Split split_of(int groups) { return split_of(groups, 4, 0); }
 // Blocks for all rows, at most 16 an SM (four of which run at once) over `wide`
 // columns of blocks.  Only accesses of 16 bytes leave registers for loads
 // ahead: the others take a block for every few rows.
@@ -586,17 +593,19 @@ cudaError_t launch_swiglu_rows(RowsIn gu, int R, int I, const int32_t* row_pair,
 cudaError_t launch_swiglu_rows_grad(RowsIn dh, const uint8_t* codes, const float* scales, int R, int I,
                                     const int32_t* row_pair, const float* w, const int32_t* pair_row, RowsOut dgu, RowsOut h,
                                     float* dw, int sms, cudaStream_t stream) {
-    SwigluArgs a = {R, I, split_of(groups_of(I)), row_pair, w};
     const bool vec = I % 8 == 0 && fits8(dh.p, dh.ld, dh.f32) && fits8(dgu.p, dgu.ld, dh.f32) &&
                      (!h.p || fits8(h.p, h.ld, dh.f32));
     // A warp a row where there are rows enough: its part of d_w then needs no
-    // barrier (32760 rows of 2048: 110 us, 133 with one a row).
-    if (vec && R >= 96 * sms && a.sp.log_groups > 1) a.sp.log_groups = 1;
+    // barrier (32760 bf16 rows of 2048: 110 us, 133 with one a row; of 1001: 85 and
+    // 106).  Half a block a row otherwise (2048 rows of 4096: 15.3, 18.1 with a
+    // warp), a block where rows are fewer than SMs.
+    const int G = groups_of(I), most = R >= 96 * sms ? 1 : R > sms ? 3 : 4;
+    const SwigluArgs a = {R, I, split_of(G, most, G / 10), row_pair, w};
     return by_type(dh.f32, [&](auto* tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
         return launch_chained(vec ? swiglu_rows_grad_kernel<T, true> : swiglu_rows_grad_kernel<T, false>,
-                              dim3(blocks_of(R, a.sp, 1, vec, sms)), kThreads, 0, stream, a, static_cast<const T*>(dh.p), dh.ld, codes,
-                              scales, static_cast<T*>(dgu.p), dgu.ld, static_cast<T*>(h.p), h.ld, pair_row, dw);
+                              dim3(blocks_of(R, a.sp, 1, vec, sms)), kThreads, 0, stream, a, static_cast<const T*>(dh.p),
+                              dh.ld, codes, scales, static_cast<T*>(dgu.p), dgu.ld, static_cast<T*>(h.p), h.ld, pair_row, dw);
     });
 }
 

@@ -451,3 +451,11 @@ def test_widest(dt):
 @pytest.mark.parametrize("T,k,I,drop", [(1, 1, 1 << 20, 0), (2, 2, (1 << 20) - 1, 0.3), (700, 3, 1, 0.3), (4000, 2, 24, 0.3)])
 def test_widest_and_narrow_swiglu(T, k, I, drop, dt):
     test_swiglu_and_its_gradient(T, k, I, drop, dt, True)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,k,I", [(16, 3, 1408), (40, 8, 384), (130, 2, 1409), (70, 3, 2816), (20, 2, 2176), (5000, 3, 72),
+                                   (5000, 3, 267)])
+def test_groups_that_do_not_fill_a_block(T, k, I, dt):
+    test_swiglu_and_its_gradient(T, k, I, 0.2, dt, True)
+    test_codes_and_values(T, I, dt)

@@ -336,3 +336,26 @@ def test_weight_gradient_in_units_of_both_widths(E, N, K, dt):
     """Few units (halves), many (whole ones), and many of one half's columns, with every kind of last stage."""
     counts = [(0, 1, 15, 16, 17, 63, 64, 65, 127, 600, 31, 47)[(5 * e + E) % 12] for e in range(E)]
     _run("dw", counts, K, N, dt, extra=3)
+
+
+def test_every_way_at_once():
+    """The three products and SwiGLU on a stream each, of few and of many rows: the same results as one after the other."""
+    from bandwidth_bound_fp8_gb300 import moeq
+    calls = []
+    for i, counts in enumerate(([3, 0, 9], [300, 77, 0, 513], [2] * 40)):
+        E, R, K, N = len(counts), sum(counts), 1024, 520
+        x, dy, w, offs = _rand(i, R, K), _rand(i + 9, R, N), _rand(i + 18, E, N, K, scale=0.1), _offs(counts)
+        for way, a, b, shape in (("y", x, w, (R, N)), ("dx", dy, w, (R, K)), ("dw", dy, x, (E, N, K))):
+            calls.append((lambda out, st, way=way, a=a, b=b, offs=offs: _call(way, a, b, offs, out, stream=st), shape))
+        calls.append((lambda out, st, x=x: moeq.moeq_swiglu_rows(x, out, stream=st), (R, K // 2)))
+    want, got = ([torch.empty(shape, dtype=BF, device="cuda") for _, shape in calls] for _ in range(2))
+    for (f, _), out in zip(calls, want):
+        f(out, None)
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (f, _), out, st in zip(calls, got, streams):
+            f(out, st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(want, got))

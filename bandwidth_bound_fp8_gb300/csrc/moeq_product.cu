@@ -48,9 +48,13 @@ constexpr int kPairRows = 128;
 // summed in registers (over K = 2048 the error against 64 bits is 5.1e-7 of the
 // result, with one accumulator 2.6e-6; a plain fp32 product's is 5e-7).
 constexpr int kRun = 32;
-// The same for a bf16 dW: no thread then waits long for one part of a sum over
-// millions of rows, which fp32 registers also add up better.
-constexpr int kLongRun = 4096;
+// The same where it is bf16: parts of 1024.  An accumulator of the whole
+// contraction tips roundings: of 6144, 0.35 % of the values of y are not the
+// exact sum's nearest, of 65536 terms of one sign 3 %; so 0.07 % at any length
+// (with parts of 512 0.04 %).  The parts cost 0 to 1.4 % (64 experts of 384
+// rows, 6144 -> 4096: 803 us whole, 811 so, 825 in parts of 512).  And no thread
+// waits long for one part of a sum over millions of rows.
+constexpr int kBf16Run = 64;
 // Row tiles that take turns on the same weights, so that a wave of CTAs covers
 // a block of both operands: a dense product of 16384 rows (6144 -> 4096) takes
 // 437 us so, and 503 with all 64 tiles in a row.
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(threads_of(kPair), 1)
     const int each = kPair ? 2 : split, workers = gridDim.x / each, worker = blockIdx.x / each;
     const int nbu = kPair ? (a.N + 255) / 256 : (a.N + 127) / 128, kb_n = (a.C + kBlock - 1) / kBlock;
     const int kb0 = kb_n * srank / split, kb1 = kb_n * (srank + 1) / split;  // (kb_n * 8 < 2^18)
-    const int steps_n = 4 * (kb1 - kb0), run = kF32 ? kRun : steps_n;        // of 16; a part's
+    const int steps_n = 4 * (kb1 - kb0), run = kF32 ? kRun : kBf16Run;       // of 16; a part's
     auto part = [&](int i, Part& p) {
         return (!kSplit || i == 0) && part_at<kPair>(a, plan, i, worker, workers, nbu, rank, p);
     };
@@ -765,7 +769,7 @@ __global__ void __launch_bounds__(threads_of(true), 1)
             for (int u = 0, i = 0; ok && more;) {
                 more = part(u++, p);
                 if (!more) ok = push_part(s, i, 0, abort);
-                const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : kLongRun;
+                const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : kBf16Run;
                 for (int k0 = 0; ok && more && k0 < steps_n; k0 += run)
                     ok = push_part(s, i++, part_of(kWide, min(run, steps_n - k0)), abort);
             }
@@ -791,7 +795,7 @@ __global__ void __launch_bounds__(threads_of(true), 1)
         bool ok = true;
         for (int u = 0, i = 0; part(u, p); ++u) {
             const int n0 = p.n0 + rank * 128 + q * 32, k0 = p.k0 + group * kMine;
-            const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : kLongRun;
+            const int steps_n = (p.cnt + 15) / 16, run = kF32 ? kRun : kBf16Run;
             float v[kMine / kCols][kCols];
             if (p.cnt == 0) {
 #pragma unroll

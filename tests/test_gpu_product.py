@@ -359,3 +359,25 @@ def test_every_way_at_once():
             f(out, st)
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(want, got))
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("C,rows,features", [(8192, 40, 640), (65536, 16, 640), (65536, 200, 264), (1 << 20, 16, 64)])
+def test_long_bf16_sums_are_rounded_once(way, C, rows, features):
+    """Sums of C positive terms: within half a step of bf16 at the exact sum, and what fp32 sums in parts of 1024 indices
+    are off by: 64 accumulations and 8 as above, and half a step for each part that is added."""
+    g = torch.Generator(device="cuda").manual_seed(C + rows)
+    rand = lambda *s: torch.rand(s, generator=g, device="cuda").to(BF)
+    if way == "dw":
+        a, b = rand(C, features), rand(C, rows // 8 * 8)
+        counts, shape = [C], (1, features, rows // 8 * 8)
+    else:
+        a, b = rand(rows, C), rand(1, *((features, C) if way == "y" else (C, features)))
+        counts, shape = [rows], (rows, features)
+    out = torch.empty(shape, dtype=BF, device="cuda")
+    _call(way, a, b, _offs(counts), out)
+    ref, _ = _ref(way, a, b, counts, shape)
+    half = torch.exp2(torch.floor(torch.log2(ref)) - 8)
+    off = (out.double() - ref).abs() - half
+    bound = (72 * 2.0 ** -22 + C / 1024 * 2.0 ** -24) * ref
+    assert (off <= bound).all(), f"{int((off > bound).sum())} of {off.numel()} outside, worst {float((off / ref).max())}"

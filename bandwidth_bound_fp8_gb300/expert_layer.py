@@ -271,6 +271,12 @@ class _Once(torch.autograd.Function):
         raise RuntimeError("swiglu and expert_mlp keep their inputs in 8 bits: they are differentiable once")
 
 
+def _edge(t):
+    """What stands for t, of which only the 8-bit codes are kept, among the tensors that _once ties gradients to: its
+    place in the graph, and nothing of its memory."""
+    return t[:0].clone() if t.requires_grad else None
+
+
 def _once(grads, *of):
     """Gradients as a backward pass returns them; `of`: the tensors they depend on."""
     return _Once.apply(len(grads), *grads, *of) if torch.is_grad_enabled() else grads
@@ -307,16 +313,16 @@ def _swiglu_grad(dh, codes, scales, w, pair_row, row_pair, need_w, again):
 
 class _Swiglu(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, gu, w, pair_row, row_pair, keep):
+    def forward(ctx, gu, w, pair_row, row_pair, keep, edge):
         h, codes, scales = _swiglu(gu, w, row_pair, keep)
-        ctx.save_for_backward(codes, scales, w, pair_row, row_pair)
+        ctx.save_for_backward(codes, scales, w, pair_row, row_pair, edge)
         return h
 
     @staticmethod
     def backward(ctx, dh):
-        codes, scales, w, pair_row, row_pair = ctx.saved_tensors
+        codes, scales, w, pair_row, row_pair, edge = ctx.saved_tensors
         dgu, dw, _ = _swiglu_grad(_rows(dh), codes, scales, w, pair_row, row_pair, ctx.needs_input_grad[1], False)
-        return (*_once((dgu, dw), dh, w), None, None, None)
+        return (*_once((dgu, dw), dh, w, edge), None, None, None, None)
 
 
 class _ExpertMlp(torch.autograd.Function):
@@ -324,17 +330,17 @@ class _ExpertMlp(torch.autograd.Function):
     nor h is kept, and x and its gate and up rows are in 8 bits."""
 
     @staticmethod
-    def forward(ctx, x, w, w_gu, w_d, offs, pair_row, row_pair, keep):
+    def forward(ctx, x, w, w_gu, w_d, offs, pair_row, row_pair, keep, edge):
         gu = _product(_gather(x, offs, pair_row), w_gu, offs)
         h, codes, scales = _swiglu(gu, w, row_pair, keep)
         del gu
         x8 = _keep8(x) if keep and ctx.needs_input_grad[2] else (None, None)
-        ctx.save_for_backward(*x8, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair)
+        ctx.save_for_backward(*x8, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair, edge)
         return _gather_grad(_product(h, w_d, offs), offs, pair_row)
 
     @staticmethod
     def backward(ctx, dout):
-        x_codes, x_scales, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair = ctx.saved_tensors
+        x_codes, x_scales, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair, edge = ctx.saved_tensors
         need_x, need_w, need_gu, need_d = ctx.needs_input_grad[:4]
         with torch.no_grad():
             dy = _gather(_rows(dout), offs, pair_row)
@@ -347,7 +353,7 @@ class _ExpertMlp(torch.autograd.Function):
                 xs = torch.empty((dgu.shape[0], w_gu.shape[2]), dtype=dgu.dtype, device=dgu.device)
                 moeq.moeq_fp8_gather_rows(x_codes, x_scales, offs, pair_row, xs)
                 dw_gu = _product_grad_w(dgu, xs, offs)
-        return (*_once((dx, dw, dw_gu, dw_d), dout, w, w_gu, w_d), None, None, None, None)
+        return (*_once((dx, dw, dw_gu, dw_d), dout, w, w_gu, w_d, edge), None, None, None, None, None)
 
 
 def _experts_fit(what: str, w: torch.Tensor, d: Dispatch, width: int, name: str = "w") -> None:
@@ -376,7 +382,7 @@ def swiglu(gu: torch.Tensor, d: Dispatch, w: torch.Tensor | None = None) -> torc
         _weights_fit("swiglu", w, d)
         w = w.contiguous()
     keep = torch.is_grad_enabled() and (gu.requires_grad or w is not None and w.requires_grad)
-    return _Swiglu.apply(_rows(gu), w, d.pair_row, d.row_pair, keep)
+    return _Swiglu.apply(_rows(gu), w, d.pair_row, d.row_pair, keep, _edge(gu))
 
 
 def expert_mlp(x: torch.Tensor, w: torch.Tensor, w_gu: torch.Tensor, w_d: torch.Tensor, d: Dispatch) -> torch.Tensor:
@@ -394,7 +400,7 @@ def expert_mlp(x: torch.Tensor, w: torch.Tensor, w_gu: torch.Tensor, w_d: torch.
                          f"and {tuple(w_d.shape)}")
     keep = torch.is_grad_enabled() and any(t.requires_grad for t in (x, w, w_gu, w_d))
     return _ExpertMlp.apply(_rows(x), w.contiguous(), w_gu.contiguous(), w_d.contiguous(), d.offs, d.pair_row, d.row_pair,
-                            keep)
+                            keep, _edge(x))
 
 
 # ------------------------------------------------------------------- serving

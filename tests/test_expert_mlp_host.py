@@ -174,3 +174,43 @@ def test_expert_mlp_refuses_what_does_not_fit(el):
         el.swiglu(z(17, 16), d)
     with pytest.raises(ValueError, match="swiglu"):
         el.swiglu(z(18, 16), d, z(9, 2))
+
+
+def _penalised(f, leaf):
+    """A loss that is linear in f(leaf), and the square of its gradient: the latter's gradient has to raise."""
+    (plain,) = torch.autograd.grad(f(leaf).double().sum(), leaf)
+    out = f(leaf).double().sum()
+    (g,) = torch.autograd.grad(out, leaf, create_graph=True)
+    assert torch.equal(g.detach(), plain)
+    penalty = g.double().square().sum()
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        torch.autograd.grad(penalty + leaf.double().sum(), leaf, retain_graph=True)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        (out + penalty).backward()
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_a_second_derivative_through_swiglu_raises(el, weighted):
+    """d_gu depends on gu through its 8-bit codes, also where d_h and the weights need no gradient."""
+    d, _ = _plan(el)
+    g = torch.Generator().manual_seed(5)
+    R, I = d.row_pair.numel(), 24
+    w = _leaf(g, 9, 2, dt=torch.float32).detach() if weighted else None
+    _penalised(lambda gu: el.swiglu(gu, d, w), _leaf(g, R, 2 * I, dt=torch.float32))
+    # ahead of it a function that is differentiable to any order
+    x, ew = _leaf(g, R, 8, dt=torch.float32), _leaf(g, 4, 2 * I, 8, dt=torch.float32)
+    (dx,) = torch.autograd.grad(el.swiglu(el.expert_product(x, ew, d), d, w).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        torch.autograd.grad(dx.square().sum(), ew)
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_a_second_derivative_through_expert_mlp_raises(el, which):
+    """With each of x, w, w_gu and w_d as the only one that needs a gradient."""
+    d, _ = _plan(el)
+    g = torch.Generator().manual_seed(6)
+    bf = torch.bfloat16
+    args = [_leaf(g, *s, dt=dt, scale=0.3).detach() for s, dt in (((9, 16), bf), ((9, 2), torch.float32), ((4, 48, 16), bf),
+                                                                  ((4, 16, 24), bf))]
+    leaf = args[which].clone().requires_grad_()
+    _penalised(lambda t: el.expert_mlp(*args[:which], t, *args[which + 1:], d), leaf)

@@ -266,3 +266,20 @@ def test_a_few_steps_of_training_run():
         loss.backward()
         assert all(torch.isfinite(p.grad).all() and p.grad.abs().sum() > 0 for p in params)
         opt.step()
+
+
+def test_a_penalty_on_what_was_quantised_raises():
+    """A loss linear in the output, with the rows or tokens as the only leaf: their gradient's square has a gradient, which
+    the codes do not give.  What stands for them in the graph keeps no memory."""
+    el, lg, x, w_gu, w_d, _ = _setup()
+    ids, w = el.route(lg, 2)
+    d = el.Dispatch(ids, lg.shape[1])
+    gu = _rand(1, d.row_pair.numel(), 64)
+    for f, t in ((lambda t: el.swiglu(t, d), gu), (lambda t: el.swiglu(t, d, w), gu), (lambda t: el.expert_mlp(t, w, w_gu, w_d, d), x)):
+        leaf = t.detach().clone().requires_grad_()
+        (first,) = torch.autograd.grad(f(leaf).sum(), leaf)
+        out = f(leaf).sum()
+        (g,) = torch.autograd.grad(out, leaf, create_graph=True)
+        assert torch.equal(g.detach(), first)
+        with pytest.raises(RuntimeError, match="differentiable once"):
+            (out + g.float().square().sum()).backward()

@@ -369,7 +369,9 @@ def _weights_fit(what: str, w: torch.Tensor, d: Dispatch) -> None:
 def expert_product(x: torch.Tensor, w: torch.Tensor, d: Dispatch) -> torch.Tensor:
     """w[e] x[r] for the rows [T * k, K] of dispatch, bf16, and w [E, N, K] bf16: [T * k, N], zero rows after the last.
     K and N are multiples of 8."""
-    _experts_fit("expert_product", w, d, x.shape[-1])
+    if x.dim() != 2 or x.shape[0] != d.row_pair.shape[0]:
+        raise ValueError(f"expert_product: x [{d.row_pair.shape[0]}, K] is wanted, got {tuple(x.shape)}")
+    _experts_fit("expert_product", w, d, x.shape[1])
     return _Product.apply(_copied(x), w.contiguous(), d.offs)
 
 

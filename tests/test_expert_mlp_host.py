@@ -214,3 +214,16 @@ def test_a_second_derivative_through_expert_mlp_raises(el, which):
                                                                   ((4, 16, 24), bf))]
     leaf = args[which].clone().requires_grad_()
     _penalised(lambda t: el.expert_mlp(*args[:which], t, *args[which + 1:], d), leaf)
+
+
+def test_product_wants_the_dispatched_rows(el):
+    """Rows that are not the plan's T * k (tokens that were not dispatched, a part of the rows) are refused."""
+    d, _ = _plan(el)
+    w = torch.zeros((4, 8, 16))
+    for rows in (9, 17, 19, 0):
+        with pytest.raises(ValueError, match=r"expert_product: x \[18, K\]"):
+            el.expert_product(torch.zeros((rows, 16)), w, d)
+    for shape in ((18,), (18, 16, 1)):
+        with pytest.raises(ValueError, match="expert_product"):
+            el.expert_product(torch.zeros(shape), w, d)
+    assert el.expert_product(torch.zeros((18, 16)), w, d).shape == (18, 8)

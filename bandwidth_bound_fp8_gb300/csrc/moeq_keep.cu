@@ -244,7 +244,9 @@ __device__ __forceinline__ void scale_two(const Eight<T, kVec>& a, const Eight<T
 template <typename T, bool kVec>
 __device__ __forceinline__ uint2 codes8(const Eight<T, kVec>& e, const F2 (&v)[4], Scale sc) {
     uint32_t c[4];
-    if (sc.s < 1e-30f) {  // remainders could be out of range
+    // A remainder's last bit is ulp(q) ulp(s).  Quotients below 2^-11 all have code
+    // 0, so from s = 2^-92 on it is 2^-34 2^-115 or more: the smallest fp32.
+    if (sc.s < 0x1p-92f) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             c[i] = sc.s == 0.f ? 0u : e4m3x2_from_f32(__fdiv_rn(lo(v[i]), sc.s), __fdiv_rn(hi(v[i]), sc.s));

@@ -459,3 +459,29 @@ def test_widest_and_narrow_swiglu(T, k, I, drop, dt):
 def test_groups_that_do_not_fill_a_block(T, k, I, dt):
     test_swiglu_and_its_gradient(T, k, I, 0.2, dt, True)
     test_codes_and_values(T, I, dt)
+
+
+def test_codes_of_tiny_groups():
+    """fp32 groups whose scale lies between 2^-102 and 2^-86, where the remainder of a quotient may lie below the smallest
+    fp32: two that did get another code, and quotients at the borders of the lowest codes and up to six steps beside."""
+    g = np.random.default_rng(11)
+    x = np.zeros((2048, 128), np.float32)
+    x[0, :3] = 7.068192747815294e-28, 1.5407438636742925e-33, 4.622231131845397e-33
+    mids = ((kp.E4M3[:-1] + kp.E4M3[1:]) / 2)[:9]
+    for i in range(1, len(x)):
+        x[i, 0] = 448 * 2.0 ** g.uniform(-102, -86)
+        s = float(x[i, 0] / np.float32(448))
+        b = (mids[g.integers(0, 9, 127)] * s).astype(np.float32)
+        x[i, 1:] = (b.view(np.int32) + g.integers(-6, 7, 127).astype(np.int32)).view(np.float32)
+    x *= np.where(g.random(x.shape) < 0.5, np.float32(-1), np.float32(1))
+    x[0] = np.abs(x[0])
+    t = torch.from_numpy(x).cuda()
+    codes, scales = _quant(t)
+    _same_codes(t, codes, scales)
+    assert codes[0, :3].tolist() == [126, 1, 1]
+    # the same as gate and up rows
+    from bandwidth_bound_fp8_gb300 import moeq
+    gu = torch.cat((t, t.flip(0)), 1)
+    codes2, scales2 = _kept(len(x), 128, 2)
+    moeq.moeq_swiglu_rows(gu, torch.empty_like(t), codes=codes2, scales=scales2)
+    assert torch.equal(codes2, torch.cat((codes, codes.flip(0)), 1)) and torch.equal(scales2, torch.cat((scales, scales.flip(0)), 1))

@@ -365,23 +365,65 @@ __global__ void __launch_bounds__(kThreads) gather_codes_kernel(const uint8_t* c
 }
 
 // ------------------------------------------------------------------- SwiGLU
-// 1 / (1 + exp(-g)).  For fp32 rows at most four steps off.  For bf16 rows
-// exp(-g) is 2^(-g log2 e) of the rounded product: |g| steps more, which half
-// a step of bf16 (2^15 of fp32's) does not show.
+// 1 / (1 + exp(-g)), also where that is below 2^-126: silu and its products with
+// large numbers are not.  exp(-g) and 1 / (1 + exp(-g)) would leave fp32's normal
+// numbers there; t / (1 + t), t = exp(g), does not (and t is subnormal where the
+// sigmoid is).  For fp32 rows at most four steps off.  For bf16 rows exp(-g) is
+// 2^(-g log2 e) of the rounded product: |g| steps more, which half a step of bf16
+// (2^15 of fp32's) does not show.  (A choice for eight gates at once: 32760 rows
+// of 2048, the gradient in bf16 107 us, by t / (1 + t) alone 111.)
 template <typename T>
-__device__ __forceinline__ F2 sigmoid(F2 g) {
-    float e[2], r[2];
-    if constexpr (sizeof(T) == 2) {
-        const F2 t = g * both(-1.44269504f);
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[0]) : "f"(lo(t)));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[1]) : "f"(hi(t)));
+__device__ __forceinline__ void sigmoids(const F2 (&g)[4], F2 (&o)[4]) {
+    float least = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) least = fminf(least, fminf(lo(g[i]), hi(g[i])));
+    if (least >= -80.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float t[2], r[2];
+            if constexpr (sizeof(T) == 2) {
+                const F2 e = g[i] * both(-1.44269504f);
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t[0]) : "f"(lo(e)));
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t[1]) : "f"(hi(e)));
+            } else {
+                t[0] = expf(-lo(g[i]));
+                t[1] = expf(-hi(g[i]));
+            }
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[0]) : "f"(1.f + t[0]));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[1]) : "f"(1.f + t[1]));
+            o[i] = f2(r[0], r[1]);
+        }
     } else {
-        e[0] = expf(-lo(g));
-        e[1] = expf(-hi(g));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float r[2];
+            const float t = expf(-fabsf(lo(g[i]))), u = expf(-fabsf(hi(g[i])));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[0]) : "f"(1.f + t));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[1]) : "f"(1.f + u));
+            o[i] = f2(lo(g[i]) < 0.f ? t : 1.f, hi(g[i]) < 0.f ? u : 1.f) * f2(r[0], r[1]);
+        }
     }
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[0]) : "f"(1.f + e[0]));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[1]) : "f"(1.f + e[1]));
-    return f2(r[0], r[1]);
+}
+// For outputs in the rows' type alone.  bf16: 2^-24 / (2^-24 + 2^(-g log2 e - 24))
+// is normal throughout, and its exponent's rounding (17 steps) does not show
+// either.  (The forward pass is short of issue slots: the same rows kept in 8 bits
+// 99 us so and 100.5 with a choice; 97.5 with the sigmoid cut off at 2^-126.)
+template <typename T>
+__device__ __forceinline__ void sigmoids_out(const F2 (&g)[4], F2 (&o)[4]) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float t[2], r[2];
+            const F2 e = fma2(g[i], both(-1.44269504f), both(-24.f));
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t[0]) : "f"(lo(e)));
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t[1]) : "f"(hi(e)));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[0]) : "f"(0x1p-24f + t[0]));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[1]) : "f"(0x1p-24f + t[1]));
+            o[i] = f2(r[0], r[1]) * both(0x1p-24f);
+        }
+    } else {
+        sigmoids<T>(g, o);
+    }
 }
 
 struct SwigluArgs {
@@ -443,8 +485,10 @@ __global__ void __launch_bounds__(kThreads, kVec ? 4 : 5)
                 scales[r * 2 * G + G + g] = su.s;
             }
         }
+        F2 sig[4];
+        sigmoids_out<T>(x, sig);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = both(w) * (x[i] * sigmoid<T>(x[i])) * u[i];
+        for (int i = 0; i < 4; ++i) y[i] = both(w) * (x[i] * sig[i]) * u[i];
         store8<kVec>(h + r * ld_h + c, left, y);
     }
 }
@@ -503,9 +547,11 @@ __global__ void __launch_bounds__(kThreads, 4)
             values8(cx, sx, x);
             values8(cu, su, u);
             const F2 one = both(1.f), minus = both(-1.f), ww = both(w);
+            F2 s[4];
+            sigmoids<T>(x, s);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const F2 sig = sigmoid<T>(x[i]), act = x[i] * sig, da = d[i] * act, wu = ww * u[i];
+                const F2 sig = s[i], act = x[i] * sig, da = d[i] * act, wu = ww * u[i];
                 dot = fma2(da, u[i], dot);
                 du[i] = da * ww;
                 y[i] = act * wu;

@@ -485,3 +485,39 @@ def test_codes_of_tiny_groups():
     codes2, scales2 = _kept(len(x), 128, 2)
     moeq.moeq_swiglu_rows(gu, torch.empty_like(t), codes=codes2, scales=scales2)
     assert torch.equal(codes2, torch.cat((codes, codes.flip(0)), 1)) and torch.equal(scales2, torch.cat((scales, scales.flip(0)), 1))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_swiglu_where_the_sigmoid_is_subnormal(dt):
+    """Gates down to -104: a sigmoid below 2^-126 counts where the other factors are large.  It is a multiple of 2^-149, two
+    of them off at most, and so is its product with the gate: (2 |gate| + 1) 2^-149 of the other factors beside the steps."""
+    from bandwidth_bound_fp8_gb300 import moeq
+    R, I = 5, 256
+    gate = torch.linspace(-104, -70, I).to(dt)
+    ups = torch.tensor([1e38, -1e37, 1e30, 1.0, 0.0])
+    gu = torch.cat((gate.expand(R, I), ups[:, None].expand(R, I).to(dt)), 1).contiguous().cuda()
+    half, least = rp.type_half_ulp(dt), 2.0 ** -149
+    h = torch.empty((R, I), dtype=dt, device="cuda")
+    codes, scales = _kept(R, I, 2)
+    moeq.moeq_swiglu_rows(gu, h, codes=codes, scales=scales)
+    z = rp.to64(gu)
+    x, u = z[:, :I], z[:, I:]
+    ref = kp.swiglu(x, u, np.ones(R))
+    tiny = lambda g, f: (2 * np.abs(g) + 1) * least * np.abs(f) + rp.TINY
+    # (the forward pass of bf16 rows has its exponent 24 lower: 24 log 2 steps of rounding more)
+    _within(h, ref, (_steps(dt, x, 12 + 17 * (dt == BF)) + half) * np.abs(ref) + tiny(x, u), "h")
+
+    x, u = (v.astype(np.float64) for v in kp.values_gate_up(codes.cpu().numpy(), scales.cpu().numpy()))
+    pairs = torch.arange(R, dtype=torch.int32, device="cuda")
+    w, dh = torch.full((R, 1), 0.5, device="cuda"), torch.full((R, I), 1.5, dtype=dt, device="cuda")
+    dgu, again, dw = torch.empty_like(gu), torch.empty_like(h), torch.empty_like(w)
+    moeq.moeq_swiglu_rows_grad(dh, codes, scales, dgu, h=again, row_pair=pairs, topk_w=w, pair_row=pairs.view(R, 1), d_topk_w=dw)
+    d, wr = rp.to64(dh), np.full(R, 0.5)
+    dgate, dup, hh, dot = kp.swiglu_grad(d, x, u, wr)
+    sig = 1 / (1 + np.exp(-x))
+    parts = np.abs(0.5 * d * u) * sig * (1 + np.abs(x))
+    _within(dgu[:, :I], dgate, _steps(dt, x, 30, 6) * parts + half * np.abs(dgate) + tiny(x, 0.5 * d * u), "d_gate")
+    _within(dgu[:, I:], dup, (_steps(dt, x) + half) * np.abs(dup) + tiny(x, 0.5 * d), "d_up")
+    _within(again, hh, (_steps(dt, x) + half) * np.abs(hh) + tiny(x, 0.5 * u), "h again")
+    terms = np.abs(d * x * sig * u) * ((I / 8 + 40) * U + _steps(dt, x)) + tiny(x, d * u)
+    _within(dw.reshape(-1), dot, terms.sum(1), "d_topk_w")

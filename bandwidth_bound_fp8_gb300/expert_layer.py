@@ -21,13 +21,22 @@ from . import moeq
 class Dispatch:
     """Where each (token, slot) pair goes: rows of expert e are
     offs[e] .. offs[e + 1] - 1; pair_row [T, k] and row_pair [T * k] map
-    between the two orders (-1: no row)."""
+    between the two orders (-1: no row).  status [1] is 0, or what a product
+    with this plan (or its gradient) reported: ``check`` asks."""
 
     def __init__(self, topk_id: torch.Tensor, E: int):
         T, k = topk_id.shape
         new = lambda *s: torch.empty(s, dtype=torch.int32, device=topk_id.device)
         self.E, self.offs, self.pair_row, self.row_pair = E, new(E + 1), new(T, k), new(T * k)
+        self.status = torch.zeros(1, dtype=torch.int32, device=topk_id.device)
         moeq.moeq_expert_sort(topk_id, E, self.offs, self.pair_row, self.row_pair)
+
+    def check(self) -> None:
+        """Raises MoeqError where a product with this plan gave up a wait inside its kernel: its results are then not
+        valid.  (Waits for the device; a training step asks where it reads its loss.)"""
+        status = int(self.status)
+        if status:
+            raise moeq.MoeqError("a product of the experts", status)
 
 
 # ------------------------------------------------------------------ training
@@ -189,21 +198,21 @@ def combine(y: torch.Tensor, w: torch.Tensor, d: Dispatch, base: torch.Tensor | 
 
 
 # ------------------------------------------------------- training: experts
-def _product(x, w, offs):
+def _product(x, w, offs, status):
     y = torch.empty((x.shape[0], w.shape[1]), dtype=x.dtype, device=x.device)
-    moeq.moeq_expert_product(x, w, offs, y)
+    moeq.moeq_expert_product(x, w, offs, y, status=status)
     return y
 
 
-def _product_grad_x(dy, w, offs):
+def _product_grad_x(dy, w, offs, status):
     dx = torch.empty((dy.shape[0], w.shape[2]), dtype=dy.dtype, device=dy.device)
-    moeq.moeq_expert_product_grad_x(dy, w, offs, dx)
+    moeq.moeq_expert_product_grad_x(dy, w, offs, dx, status=status)
     return dx
 
 
-def _product_grad_w(dy, x, offs):
+def _product_grad_w(dy, x, offs, status):
     dw = torch.empty((offs.shape[0] - 1, dy.shape[1], x.shape[1]), dtype=x.dtype, device=x.device)
-    moeq.moeq_expert_product_grad_w(dy, x, offs, dw)
+    moeq.moeq_expert_product_grad_w(dy, x, offs, dw, status=status)
     return dw
 
 
@@ -215,47 +224,51 @@ def _copied(t: torch.Tensor) -> torch.Tensor:
 
 
 # y = W x, dx = W^T dy and dW = dy x^T are linear in either argument, and each
-# one's derivatives are the other two.
+# one's derivatives are the other two.  (The status word is written, and so not
+# among what autograd watches.)
 class _Product(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, offs):
+    def forward(ctx, x, w, offs, status):
+        ctx.status = status
         ctx.save_for_backward(x, w, offs)
-        return _product(x, w, offs)
+        return _product(x, w, offs, status)
 
     @staticmethod
     def backward(ctx, dy):
         x, w, offs = ctx.saved_tensors
         dy, need = _copied(dy), ctx.needs_input_grad
-        return (_grad(_ProductGradX, _product_grad_x)(dy, w, offs) if need[0] else None,
-                _grad(_ProductGradW, _product_grad_w)(dy, x, offs) if need[1] else None, None)
+        return (_grad(_ProductGradX, _product_grad_x)(dy, w, offs, ctx.status) if need[0] else None,
+                _grad(_ProductGradW, _product_grad_w)(dy, x, offs, ctx.status) if need[1] else None, None, None)
 
 
 class _ProductGradX(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, dy, w, offs):
+    def forward(ctx, dy, w, offs, status):
+        ctx.status = status
         ctx.save_for_backward(dy, w, offs)
-        return _product_grad_x(dy, w, offs)
+        return _product_grad_x(dy, w, offs, status)
 
     @staticmethod
     def backward(ctx, g):
         dy, w, offs = ctx.saved_tensors
         g, need = _copied(g), ctx.needs_input_grad
-        return (_grad(_Product, _product)(g, w, offs) if need[0] else None,
-                _grad(_ProductGradW, _product_grad_w)(dy, g, offs) if need[1] else None, None)
+        return (_grad(_Product, _product)(g, w, offs, ctx.status) if need[0] else None,
+                _grad(_ProductGradW, _product_grad_w)(dy, g, offs, ctx.status) if need[1] else None, None, None)
 
 
 class _ProductGradW(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, dy, x, offs):
+    def forward(ctx, dy, x, offs, status):
+        ctx.status = status
         ctx.save_for_backward(dy, x, offs)
-        return _product_grad_w(dy, x, offs)
+        return _product_grad_w(dy, x, offs, status)
 
     @staticmethod
     def backward(ctx, g):
         dy, x, offs = ctx.saved_tensors
         g, need = g.contiguous(), ctx.needs_input_grad
-        return (_grad(_Product, _product)(x, g, offs) if need[0] else None,
-                _grad(_ProductGradX, _product_grad_x)(dy, g, offs) if need[1] else None, None)
+        return (_grad(_Product, _product)(x, g, offs, ctx.status) if need[0] else None,
+                _grad(_ProductGradX, _product_grad_x)(dy, g, offs, ctx.status) if need[1] else None, None, None)
 
 
 class _Once(torch.autograd.Function):
@@ -330,13 +343,14 @@ class _ExpertMlp(torch.autograd.Function):
     nor h is kept, and x and its gate and up rows are in 8 bits."""
 
     @staticmethod
-    def forward(ctx, x, w, w_gu, w_d, offs, pair_row, row_pair, keep, edge):
-        gu = _product(_gather(x, offs, pair_row), w_gu, offs)
+    def forward(ctx, x, w, w_gu, w_d, offs, pair_row, row_pair, status, keep, edge):
+        ctx.status = status
+        gu = _product(_gather(x, offs, pair_row), w_gu, offs, status)
         h, codes, scales = _swiglu(gu, w, row_pair, keep)
         del gu
         x8 = _keep8(x) if keep and ctx.needs_input_grad[2] else (None, None)
         ctx.save_for_backward(*x8, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair, edge)
-        return _gather_grad(_product(h, w_d, offs), offs, pair_row)
+        return _gather_grad(_product(h, w_d, offs, status), offs, pair_row)
 
     @staticmethod
     def backward(ctx, dout):
@@ -344,16 +358,18 @@ class _ExpertMlp(torch.autograd.Function):
         need_x, need_w, need_gu, need_d = ctx.needs_input_grad[:4]
         with torch.no_grad():
             dy = _gather(_rows(dout), offs, pair_row)
-            dgu, dw, h = _swiglu_grad(_product_grad_x(dy, w_d, offs), codes, scales, w, pair_row, row_pair, need_w, need_d)
-            dw_d = _product_grad_w(dy, h, offs) if need_d else None
+            dh = _product_grad_x(dy, w_d, offs, ctx.status)
+            dgu, dw, h = _swiglu_grad(dh, codes, scales, w, pair_row, row_pair, need_w, need_d)
+            del dh
+            dw_d = _product_grad_w(dy, h, offs, ctx.status) if need_d else None
             del dy, h
-            dx = _gather_grad(_product_grad_x(dgu, w_gu, offs), offs, pair_row) if need_x else None
+            dx = _gather_grad(_product_grad_x(dgu, w_gu, offs, ctx.status), offs, pair_row) if need_x else None
             dw_gu = None
             if need_gu:
                 xs = torch.empty((dgu.shape[0], w_gu.shape[2]), dtype=dgu.dtype, device=dgu.device)
                 moeq.moeq_fp8_gather_rows(x_codes, x_scales, offs, pair_row, xs)
-                dw_gu = _product_grad_w(dgu, xs, offs)
-        return (*_once((dx, dw, dw_gu, dw_d), dout, w, w_gu, w_d, edge), None, None, None, None, None)
+                dw_gu = _product_grad_w(dgu, xs, offs, ctx.status)
+        return (*_once((dx, dw, dw_gu, dw_d), dout, w, w_gu, w_d, edge), None, None, None, None, None, None)
 
 
 def _experts_fit(what: str, w: torch.Tensor, d: Dispatch, width: int, name: str = "w") -> None:
@@ -372,7 +388,7 @@ def expert_product(x: torch.Tensor, w: torch.Tensor, d: Dispatch) -> torch.Tenso
     if x.dim() != 2 or x.shape[0] != d.row_pair.shape[0]:
         raise ValueError(f"expert_product: x [{d.row_pair.shape[0]}, K] is wanted, got {tuple(x.shape)}")
     _experts_fit("expert_product", w, d, x.shape[1])
-    return _Product.apply(_copied(x), w.contiguous(), d.offs)
+    return _Product.apply(_copied(x), w.contiguous(), d.offs, d.status)
 
 
 def swiglu(gu: torch.Tensor, d: Dispatch, w: torch.Tensor | None = None) -> torch.Tensor:
@@ -402,7 +418,7 @@ def expert_mlp(x: torch.Tensor, w: torch.Tensor, w_gu: torch.Tensor, w_d: torch.
                          f"and {tuple(w_d.shape)}")
     keep = torch.is_grad_enabled() and any(t.requires_grad for t in (x, w, w_gu, w_d))
     return _ExpertMlp.apply(_rows(x), w.contiguous(), w_gu.contiguous(), w_d.contiguous(), d.offs, d.pair_row, d.row_pair,
-                            keep, _edge(x))
+                            d.status, keep, _edge(x))
 
 
 # ------------------------------------------------------------------- serving

@@ -227,3 +227,38 @@ def test_product_wants_the_dispatched_rows(el):
         with pytest.raises(ValueError, match="expert_product"):
             el.expert_product(torch.zeros(shape), w, d)
     assert el.expert_product(torch.zeros((18, 16)), w, d).shape == (18, 8)
+
+
+@pytest.mark.parametrize("name", ["expert_product", "expert_product_grad_x", "expert_product_grad_w"])
+@pytest.mark.parametrize("turn", [0, 1])
+def test_a_product_that_gives_up_is_reported(el, monkeypatch, name, turn):
+    """The plan's status word reaches every product, of each pass; check() raises what one of them left there."""
+    from bandwidth_bound_fp8_gb300 import moeq
+    plain, calls = getattr(moeq, "moeq_" + name), []
+
+    def gives_up(a, b, offs, out, status=None, stream=None):
+        plain(a, b, offs, out)
+        assert status is not None and status.dtype is torch.int32 and status.shape == (1,)
+        calls.append(status)
+        if len(calls) == turn + 1:
+            status.data.fill_(moeq.MOEQ_ERR_TIMEOUT)
+    monkeypatch.setattr(moeq, "moeq_" + name, gives_up)
+    g = torch.Generator().manual_seed(7)
+    bf, dx = torch.bfloat16, None
+    d, _ = _plan(el)
+    d.check()
+    args = [_leaf(g, *s, dt=dt) for s, dt in (((9, 16), bf), ((9, 2), torch.float32), ((4, 48, 16), bf), ((4, 16, 24), bf))]
+    el.expert_mlp(*args, d).sum().backward()
+    assert len(calls) == 2 and all(c is d.status for c in calls)
+    with pytest.raises(moeq.MoeqError) as e:
+        d.check()
+    assert e.value.status == moeq.MOEQ_ERR_TIMEOUT
+    # a plan of its own knows nothing of it; the product's own gradients, to second order
+    calls.clear()
+    d, _ = _plan(el)
+    x, w = _leaf(g, 18, 8), _leaf(g, 4, 16, 8)
+    dx, dw = torch.autograd.grad(el.expert_product(x, w, d).square().sum(), (x, w), create_graph=True)
+    (dx.square().sum() + dw.square().sum()).backward()
+    assert len(calls) > 1 and all(c is d.status for c in calls)
+    with pytest.raises(moeq.MoeqError):
+        d.check()

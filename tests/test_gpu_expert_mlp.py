@@ -283,3 +283,19 @@ def test_a_penalty_on_what_was_quantised_raises():
         assert torch.equal(g.detach(), first)
         with pytest.raises(RuntimeError, match="differentiable once"):
             (out + g.float().square().sum()).backward()
+
+
+def test_a_plan_tells_of_its_products():
+    """No product reports anything; what one leaves in the plan's word is raised, and is not the next plan's."""
+    from bandwidth_bound_fp8_gb300 import moeq
+    el, lg, x, w_gu, w_d, dout = _setup()
+    ids, w = el.route(lg, 2)
+    d = el.Dispatch(ids, lg.shape[1])
+    w_gu.requires_grad_()
+    el.expert_mlp(x, w, w_gu, w_d, d).backward(dout)
+    el.expert_product(el.dispatch(x, d), w_gu, d).sum().backward()
+    d.check()
+    d.status.fill_(moeq.MOEQ_ERR_TIMEOUT)
+    with pytest.raises(moeq.MoeqError, match="status 5"):
+        d.check()
+    el.Dispatch(ids, lg.shape[1]).check()

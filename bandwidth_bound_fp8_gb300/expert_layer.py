@@ -14,6 +14,7 @@ function) keep what their backward pass needs in 8 bits.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import moeq
 
@@ -75,9 +76,16 @@ def _combine_grad(dout, y, w, offs, pair_row):
     return dy, dw
 
 
-def _grad(function, plain):
-    """The autograd function where its result may be differentiated again, the plain call where it cannot."""
-    return function.apply if torch.is_grad_enabled() else plain
+def _differentiated(args) -> bool:
+    """Whether a result of args may be differentiated again, or one of them has a tangent."""
+    return torch.is_grad_enabled() or any(
+        isinstance(t, torch.Tensor) and t.is_floating_point() and forward_ad.unpack_dual(t).tangent is not None for t in args)
+
+
+def _grad(function, plain, *args):
+    """The autograd function where its result is differentiated further (in forward mode it raises: it has no rule), the
+    plain call where it is not."""
+    return (function.apply if _differentiated(args) else plain)(*args)
 
 
 class _Route(torch.autograd.Function):
@@ -95,7 +103,7 @@ class _Route(torch.autograd.Function):
     @staticmethod
     def backward(ctx, _, dw):
         ids, w = ctx.saved_tensors
-        return _grad(_RouteGrad, _route_grad)(dw.contiguous(), ids, w, ctx.E), None
+        return _grad(_RouteGrad, _route_grad, dw.contiguous(), ids, w, ctx.E), None
 
 
 class _RouteGrad(torch.autograd.Function):
@@ -126,7 +134,7 @@ class _Dispatch(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dxs):
-        return _grad(_DispatchGrad, _gather_grad)(dxs.contiguous(), *ctx.saved_tensors), None, None
+        return _grad(_DispatchGrad, _gather_grad, dxs.contiguous(), *ctx.saved_tensors), None, None
 
 
 class _DispatchGrad(torch.autograd.Function):
@@ -139,7 +147,7 @@ class _DispatchGrad(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g):
-        return _grad(_Dispatch, _gather)(g.contiguous(), *ctx.saved_tensors), None, None
+        return _grad(_Dispatch, _gather, g.contiguous(), *ctx.saved_tensors), None, None
 
 
 class _Combine(torch.autograd.Function):
@@ -154,7 +162,7 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         dout = dout.contiguous()
-        dy, dw = _grad(_CombineGrad, _combine_grad)(dout, *ctx.saved_tensors)
+        dy, dw = _grad(_CombineGrad, _combine_grad, dout, *ctx.saved_tensors)
         return dy, dw, dout if ctx.has_base else None, None, None
 
 
@@ -172,7 +180,7 @@ class _CombineGrad(torch.autograd.Function):
         dout, y, w, *plan = ctx.saved_tensors
         gy, gw = gy.contiguous(), gw.contiguous()
         d_dout = _Combine.apply(y, gw, _Combine.apply(gy, w, torch.zeros_like(dout), *plan), *plan)
-        dy, dw = _grad(_CombineGrad, _combine_grad)(dout, gy, gw, *plan)
+        dy, dw = _grad(_CombineGrad, _combine_grad, dout, gy, gw, *plan)
         return d_dout, dy, dw, None, None
 
 
@@ -237,8 +245,8 @@ class _Product(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, offs = ctx.saved_tensors
         dy, need = _copied(dy), ctx.needs_input_grad
-        return (_grad(_ProductGradX, _product_grad_x)(dy, w, offs, ctx.status) if need[0] else None,
-                _grad(_ProductGradW, _product_grad_w)(dy, x, offs, ctx.status) if need[1] else None, None, None)
+        return (_grad(_ProductGradX, _product_grad_x, dy, w, offs, ctx.status) if need[0] else None,
+                _grad(_ProductGradW, _product_grad_w, dy, x, offs, ctx.status) if need[1] else None, None, None)
 
 
 class _ProductGradX(torch.autograd.Function):
@@ -252,8 +260,8 @@ class _ProductGradX(torch.autograd.Function):
     def backward(ctx, g):
         dy, w, offs = ctx.saved_tensors
         g, need = _copied(g), ctx.needs_input_grad
-        return (_grad(_Product, _product)(g, w, offs, ctx.status) if need[0] else None,
-                _grad(_ProductGradW, _product_grad_w)(dy, g, offs, ctx.status) if need[1] else None, None, None)
+        return (_grad(_Product, _product, g, w, offs, ctx.status) if need[0] else None,
+                _grad(_ProductGradW, _product_grad_w, dy, g, offs, ctx.status) if need[1] else None, None, None)
 
 
 class _ProductGradW(torch.autograd.Function):
@@ -267,8 +275,8 @@ class _ProductGradW(torch.autograd.Function):
     def backward(ctx, g):
         dy, x, offs = ctx.saved_tensors
         g, need = g.contiguous(), ctx.needs_input_grad
-        return (_grad(_Product, _product)(x, g, offs, ctx.status) if need[0] else None,
-                _grad(_ProductGradX, _product_grad_x)(dy, g, offs, ctx.status) if need[1] else None, None, None)
+        return (_grad(_Product, _product, x, g, offs, ctx.status) if need[0] else None,
+                _grad(_ProductGradX, _product_grad_x, dy, g, offs, ctx.status) if need[1] else None, None, None)
 
 
 class _Once(torch.autograd.Function):
@@ -292,7 +300,7 @@ def _edge(t):
 
 def _once(grads, *of):
     """Gradients as a backward pass returns them; `of`: the tensors they depend on."""
-    return _Once.apply(len(grads), *grads, *of) if torch.is_grad_enabled() else grads
+    return _Once.apply(len(grads), *grads, *of) if _differentiated(of) else grads
 
 
 def _keep8(x):

@@ -262,3 +262,32 @@ def test_a_product_that_gives_up_is_reported(el, monkeypatch, name, turn):
     assert len(calls) > 1 and all(c is d.status for c in calls)
     with pytest.raises(moeq.MoeqError):
         d.check()
+
+
+def test_a_tangent_is_not_dropped(el):
+    """Forward-mode differentiation through a backward pass: none of the functions has a rule for it, so all raise, in
+    place of gradients without their tangent."""
+    from torch.autograd import forward_ad as fwd
+    d, ids = _plan(el)
+    g = torch.Generator().manual_seed(8)
+    f32, bf = torch.float32, torch.bfloat16
+    x, w, lg = _leaf(g, 18, 8), _leaf(g, 9, 2, dt=f32), _leaf(g, 9, 4, dt=f32)
+    ew, gu, t = _leaf(g, 4, 16, 8), _leaf(g, 18, 48, dt=f32), _leaf(g, 9, 8, dt=f32)
+    mlp = [_leaf(g, *s, dt=bf).detach() for s in ((4, 48, 16), (4, 16, 24))]
+    tok = _leaf(g, 9, 16, dt=bf)
+    for out, leaves in ((el.expert_product(x, ew, d), (x, ew)), (el.swiglu(gu, d, w), (gu, w)), (el.swiglu(gu, d), (gu,)),
+                        (el.expert_mlp(tok, w, *mlp, d), (tok, w)), (el.dispatch(t, d), (t,)),
+                        (el.combine(gu, w, d), (gu, w)), (el.route(lg, 2)[1], (lg,))):
+        first = torch.autograd.grad(out, leaves, torch.ones_like(out), retain_graph=True)
+        with fwd.dual_level():
+            dual = fwd.make_dual(torch.ones_like(out), torch.ones_like(out))
+            with pytest.raises(RuntimeError, match="forward"):
+                torch.autograd.grad(out, leaves, dual, retain_graph=True)
+            again = torch.autograd.grad(out, leaves, torch.ones_like(out), retain_graph=True)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+    # and through a second backward pass
+    gx, gw = torch.autograd.grad(el.expert_product(x, ew, d), (x, ew), torch.ones(18, 16, dtype=x.dtype), create_graph=True)
+    for a, leaf in ((gx, ew), (gw, x)):
+        with fwd.dual_level():
+            with pytest.raises(RuntimeError, match="forward"):
+                torch.autograd.grad(a, leaf, fwd.make_dual(torch.ones_like(a), torch.ones_like(a)), retain_graph=True)

@@ -231,6 +231,11 @@ def _copied(t: torch.Tensor) -> torch.Tensor:
     return t if fits else t.clone(memory_format=torch.contiguous_format)
 
 
+def _weights(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy where it is not contiguous or starts off 16 bytes (a slice of a flat buffer)."""
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
 # y = W x, dx = W^T dy and dW = dy x^T are linear in either argument, and each
 # one's derivatives are the other two.  (The status word is written, and so not
 # among what autograd watches.)
@@ -274,7 +279,7 @@ class _ProductGradW(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         dy, x, offs = ctx.saved_tensors
-        g, need = g.contiguous(), ctx.needs_input_grad
+        g, need = _weights(g), ctx.needs_input_grad
         return (_grad(_Product, _product, x, g, offs, ctx.status) if need[0] else None,
                 _grad(_ProductGradX, _product_grad_x, dy, g, offs, ctx.status) if need[1] else None, None, None)
 
@@ -392,11 +397,11 @@ def _weights_fit(what: str, w: torch.Tensor, d: Dispatch) -> None:
 
 def expert_product(x: torch.Tensor, w: torch.Tensor, d: Dispatch) -> torch.Tensor:
     """w[e] x[r] for the rows [T * k, K] of dispatch, bf16, and w [E, N, K] bf16: [T * k, N], zero rows after the last.
-    K and N are multiples of 8."""
+    K and N are multiples of 8; rows and weights that do not start on 16 bytes are copied."""
     if x.dim() != 2 or x.shape[0] != d.row_pair.shape[0]:
         raise ValueError(f"expert_product: x [{d.row_pair.shape[0]}, K] is wanted, got {tuple(x.shape)}")
     _experts_fit("expert_product", w, d, x.shape[1])
-    return _Product.apply(_copied(x), w.contiguous(), d.offs, d.status)
+    return _Product.apply(_copied(x), _weights(w), d.offs, d.status)
 
 
 def swiglu(gu: torch.Tensor, d: Dispatch, w: torch.Tensor | None = None) -> torch.Tensor:
@@ -425,7 +430,7 @@ def expert_mlp(x: torch.Tensor, w: torch.Tensor, w_gu: torch.Tensor, w_d: torch.
         raise ValueError(f"expert_mlp: w_gu [{d.E}, 2I, {H}] and w_d [{d.E}, {H}, I] are wanted, got {tuple(w_gu.shape)} "
                          f"and {tuple(w_d.shape)}")
     keep = torch.is_grad_enabled() and any(t.requires_grad for t in (x, w, w_gu, w_d))
-    return _ExpertMlp.apply(_rows(x), w.contiguous(), w_gu.contiguous(), w_d.contiguous(), d.offs, d.pair_row, d.row_pair,
+    return _ExpertMlp.apply(_rows(x), w.contiguous(), _weights(w_gu), _weights(w_d), d.offs, d.pair_row, d.row_pair,
                             d.status, keep, _edge(x))
 
 

@@ -291,3 +291,40 @@ def test_a_tangent_is_not_dropped(el):
         with fwd.dual_level():
             with pytest.raises(RuntimeError, match="forward"):
                 torch.autograd.grad(a, leaf, fwd.make_dual(torch.ones_like(a), torch.ones_like(a)), retain_graph=True)
+
+
+def _off(t):
+    """t in a buffer, contiguous, off a boundary of 16 bytes."""
+    flat = torch.zeros(t.numel() + 8, dtype=t.dtype)
+    n = 1 if flat.data_ptr() % 16 == 0 else 0
+    out = flat[n:n + t.numel()].view(t.shape)
+    out.copy_(t.detach())
+    assert out.is_contiguous() and out.data_ptr() % 16
+    return out.requires_grad_(t.requires_grad)
+
+
+def test_weights_off_16_bytes_are_copied(el, monkeypatch):
+    """Contiguous weights (and second-order gradients in their place) that are slices of a flat buffer."""
+    from bandwidth_bound_fp8_gb300 import moeq
+    for name in ("moeq_expert_product", "moeq_expert_product_grad_x"):
+        def aligned(a, w, offs, out, status=None, stream=None, plain=getattr(moeq, name)):
+            assert w.is_contiguous() and w.data_ptr() % 16 == 0
+            plain(a, w, offs, out)
+        monkeypatch.setattr(moeq, name, aligned)
+    d, _ = _plan(el)
+    g = torch.Generator().manual_seed(9)
+    bf = torch.bfloat16
+    x, w = _leaf(g, 18, 8), _leaf(g, 4, 16, 8)
+    dy, gw = torch.randn(18, 16, generator=g, dtype=x.dtype), torch.randn(4, 16, 8, generator=g, dtype=x.dtype)
+    def second(w, gw):
+        y = el.expert_product(x, w, d)
+        dx, dw = torch.autograd.grad(y, (x, w), dy, create_graph=True)
+        return (y.detach(), dx.detach(), dw.detach(), *torch.autograd.grad((dx, dw), (x, w), (torch.ones_like(dx), gw)))
+    for a, b in zip(second(w, gw), second(_off(w), _off(gw))):
+        assert torch.equal(a, b)
+    args = [_leaf(g, *s, dt=dt, scale=0.3) for s, dt in (((9, 16), bf), ((9, 2), torch.float32), ((4, 48, 16), bf), ((4, 16, 24), bf))]
+    moved = args[:2] + [_off(t) for t in args[2:]]
+    out, out2 = el.expert_mlp(*args, d), el.expert_mlp(*moved, d)
+    assert torch.equal(out, out2)
+    for a, b in zip(torch.autograd.grad(out.float().sum(), args), torch.autograd.grad(out2.float().sum(), moved)):
+        assert torch.equal(a, b)

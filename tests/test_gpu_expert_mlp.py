@@ -299,3 +299,22 @@ def test_a_plan_tells_of_its_products():
     with pytest.raises(moeq.MoeqError, match="status 5"):
         d.check()
     el.Dispatch(ids, lg.shape[1]).check()
+
+
+def test_weights_in_a_flat_buffer():
+    """Weights that start off 16 bytes: the same results, and gradients in the buffer."""
+    el, lg, x, w_gu, w_d, dout = _setup()
+    ids, w = el.route(lg, 2)
+    d = el.Dispatch(ids, lg.shape[1])
+    plain = [t.detach().clone().requires_grad_() for t in (w_gu, w_d)]
+    out = el.expert_mlp(x, w, *plain, d)
+    want = torch.autograd.grad(out, plain, dout)
+    n = w_gu.numel()
+    flat = torch.cat((torch.zeros(1, dtype=BF, device="cuda"), w_gu.reshape(-1), w_d.reshape(-1))).requires_grad_()
+    gu, dn = flat[1:n + 1].view(w_gu.shape), flat[n + 1:].view(w_d.shape)
+    assert gu.is_contiguous() and gu.data_ptr() % 16
+    out2 = el.expert_mlp(x, w, gu, dn, d)
+    (got,) = torch.autograd.grad(out2, flat, dout)
+    assert torch.equal(out, out2) and torch.equal(got[1:], torch.cat([t.reshape(-1) for t in want])) and got[0] == 0
+    xs = el.dispatch(x, d)
+    assert torch.equal(el.expert_product(xs, gu, d), el.expert_product(xs, w_gu, d))

@@ -381,3 +381,26 @@ def test_long_bf16_sums_are_rounded_once(way, C, rows, features):
     off = (out.double() - ref).abs() - half
     bound = (72 * 2.0 ** -22 + C / 1024 * 2.0 ** -24) * ref
     assert (off <= bound).all(), f"{int((off > bound).sum())} of {off.numel()} outside, worst {float((off / ref).max())}"
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("C,rows,features", [(2048, 40, 640), (2048, 300, 640), (8192, 40, 264)])
+def test_fp32_sums_are_taken_in_parts(way, C, rows, features):
+    """Sums of C positive terms, in parts of 512 indices.  A part is 32 accumulations, each of which truncates up to a step
+    (2^-23) of what is there by then, and that grows evenly: 33/2 2^-23 of the terms, and 8 2^-22 for the products as
+    above; adding the parts up half a step for each.  Truncation loses half as much on average, 33/4 2^-23 at most
+    (9.8e-7); an accumulator of 2048 indices would lose 129/4 2^-24 at least (1.9e-6)."""
+    g = torch.Generator(device="cuda").manual_seed(C + rows)
+    rand = lambda *s: torch.rand(s, generator=g, device="cuda").to(BF)
+    if way == "dw":
+        a, b = rand(C, features), rand(C, rows // 8 * 8)
+        counts, shape = [C], (1, features, rows // 8 * 8)
+    else:
+        a, b = rand(rows, C), rand(1, *((features, C) if way == "y" else (C, features)))
+        counts, shape = [rows], (rows, features)
+    out = torch.empty(shape, dtype=F32, device="cuda")
+    _call(way, a, b, _offs(counts), out)
+    ref, _ = _ref(way, a, b, counts, shape)
+    off = (out.double() - ref) / ref
+    assert float(off.abs().max()) <= 33 / 2 * 2.0 ** -23 + 8 * 2.0 ** -22 + C / 512 * rp.U24
+    assert abs(float(off.mean())) <= 1.4e-6

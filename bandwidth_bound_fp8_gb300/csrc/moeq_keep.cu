@@ -12,9 +12,9 @@
 // quantisation comes close.  Half a warp has a group: eight elements a lane,
 // neighbours where rows allow 16-byte accesses (kVec), else 16 apart, so that
 // neighbouring lanes still touch neighbouring elements.  Measured at 32760 rows
-// (floors at the copy rate): SwiGLU of 2 x 2048 bf16 kept in 8 bits 97 us (79),
-// its gradient 110 (99); 4095 tokens of 6144 quantised 18 (11) and brought back
-// as rows 66 (63).
+// (floors at the copy rate): SwiGLU of 2 x 2048 bf16 kept in 8 bits 99 us (79),
+// its gradient 107 (99); 4095 tokens of 6144 quantised 18 (11), brought back 14
+// (11), and as rows 68 (63).
 #include "moeq_device.cuh"
 #include "moeq_rows.h"
 
@@ -275,7 +275,7 @@ __device__ __forceinline__ void values8(uint2 c, float s, F2 (&v)[4]) {
 
 // A block's half warps over rows and groups: rows of few groups share a block.
 // Blocks walk down the rows, with the next rows' loads in flight behind this
-// one's arithmetic (32760 rows of 2 x 2048 bf16 kept: 97 us so, 124 with a block
+// one's arithmetic (32760 rows of 2 x 2048 bf16 kept: 99 us so, 126 with a block
 // for every row).
 struct Split {
     int log_groups;  // half warps of a row: a power of two, at most kHalves
@@ -294,8 +294,8 @@ Split split_of(int groups, int most, int idle) {
     return s;
 }
 // Where groups are independent, none idle: 32760 bf16 rows of 2 x 1408 (11
-// groups, kept) take 72 us with one half warp a row and 112 with 16, of 2 x 2816
-// 137 with two and 181, of 2 x 2048 98 with two and with 16.
+// groups, kept) take 73 us with one half warp a row and 115 with 16, of 2 x 2816
+// 140 with two and 184, of 2 x 2048 100 with two and 99 with 16.
 Split split_of(int groups) { return split_of(groups, 4, 0); }
 // Blocks for all rows, at most 16 an SM (four of which run at once) over `wide`
 // columns of blocks.  Only accesses of 16 bytes leave registers for loads
@@ -644,9 +644,10 @@ cudaError_t launch_swiglu_rows_grad(RowsIn dh, const uint8_t* codes, const float
     const bool vec = I % 8 == 0 && fits8(dh.p, dh.ld, dh.f32) && fits8(dgu.p, dgu.ld, dh.f32) &&
                      (!h.p || fits8(h.p, h.ld, dh.f32));
     // A warp a row where there are rows enough: its part of d_w then needs no
-    // barrier (32760 bf16 rows of 2048: 110 us, 133 with one a row; of 1001: 85 and
-    // 106).  Half a block a row otherwise (2048 rows of 4096: 15.3, 18.1 with a
-    // warp), a block where rows are fewer than SMs.
+    // barrier (32760 bf16 rows of 2048: 108 us, 117 with half a block a row and 128
+    // with a block; of 1001: 83, 101 and 100).  Half a block otherwise (2048 rows of
+    // 4096: 15.4, 16.4 with a block, 22.9 with a warp), a block where rows are fewer
+    // than SMs.
     const int G = groups_of(I), most = R >= 96 * sms ? 1 : R > sms ? 3 : 4;
     const SwigluArgs a = {R, I, split_of(G, most, G / 10), row_pair, w};
     return by_type(dh.f32, [&](auto* tag) {

@@ -18,11 +18,11 @@
 // few units are split along their contraction instead (see how_of).
 //
 // Weights out (dW): a unit is (expert, 256 x 256 of dW, or 256 x 128 where units
-// are few) for a pair, the contraction over the expert's rows in stages of 64.  Rows are sorted, so a
-// stage may reach past the expert's last row: what follows are another
-// expert's rows (or a NaN in a masked place), and 0 * NaN is not 0.  So the
-// last stage is copied row-exactly, in boxes of a power of two of rows, and
-// filled up to the MMA's 16 rows with zeros.
+// are few) for a pair, the contraction over the expert's rows in stages of 64.
+// Rows are sorted, so a stage may reach past the expert's last row: what follows
+// are another expert's rows (or a NaN in a masked place), and 0 * NaN is not 0.
+// So the last stage is copied row-exactly, in boxes of a power of two of rows,
+// and filled up to the MMA's 16 rows with zeros.
 #include "moeq_mx4_plan.cuh"
 #include "moeq_pair.cuh"
 #include "moeq_rows.h"
@@ -33,9 +33,10 @@ namespace {
 constexpr int kBlock = 64;                      // contraction a stage: 128 bytes of bf16, the swizzle's span
 constexpr int kTileBytes = 128 * kBlock * 2;    // 128 features (or dW rows / columns) of a stage
 constexpr int kAcc1 = 256;                      // TMEM columns of the second accumulator
-// Stages in flight at most: one token over 8 of 256 experts (K 6144, N 4096)
-// takes 70 us with 5, 67 with 7, 66 with 9 and 12; 64 experts of about 6 rows (K
-// 2048, N 2816) 119, 115, 114 and 114.
+// Stages in flight at most.  More gain a little where few CTAs have a long
+// contraction and lose elsewhere; us with 5, 7, 9 and 12: one token over 8 of 256
+// experts (K 6144, N 4096) 67.5, 65.1, 64.0 and 63.6; 6 rows each of 256 experts
+// (K 2048, N 2816) 427, 418, 424 and 422, their gradient 418, 407, 426 and 426.
 constexpr int kMaxStages = 7;
 // Most rows of a tile, for one CTA and for a pair.
 constexpr int kSingleTileRows = 128, kPairTileRows = 256;
@@ -666,7 +667,11 @@ __device__ __forceinline__ void copy_rows(uint8_t* at, const CUtensorMap* maps, 
 }
 // The rows behind them up to the next multiple of 16: zeros, written by the warp
 // whose copies into the same stage follow, so that the MMAs that wait for those
-// copies find them.  (Zeros copied from beyond the matrix, or from an array of
+// copies find them.  Nothing else orders the zeros ahead of the MMAs: every lane's
+// stores are complete for the async proxy at its fence, the copies start behind
+// it, and the MMA thread waits for the bytes of both CTAs' copies, of this warp's
+// among them.  (An arrival of its own, released to the cluster, costs 0.4 us a
+// unit.  Zeros copied from beyond the matrix, or from an array of
 // them, cost more than the rows: 64 experts of 376 rows, K 6144, N 4096, 1046
 // us, so 950.)
 __device__ __forceinline__ void zero_rows(uint8_t* at, bool two, int rows, int lane) {

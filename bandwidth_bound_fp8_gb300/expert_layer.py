@@ -6,8 +6,9 @@ or a prompt.  ``moeq.moeq_moe_layer`` is its FP8 counterpart for up to 16
 tokens in one kernel.
 
 ``route``, ``dispatch`` and ``combine`` train: the same routing and movement
-as autograd functions, around whatever experts the caller's program has, to any order.
-``expert_product`` is the product of bf16 experts for it, to any order too;
+as autograd functions, around whatever experts the caller's program has, to any order (in reverse
+mode: a tangent raises).  ``expert_product`` is the product of bf16 experts for
+it, to any order too;
 ``swiglu`` and ``expert_mlp`` (the experts between dispatch and combine as one
 function) keep what their backward pass needs in 8 bits.
 """
@@ -406,7 +407,8 @@ def expert_product(x: torch.Tensor, w: torch.Tensor, d: Dispatch) -> torch.Tenso
 
 def swiglu(gu: torch.Tensor, d: Dispatch, w: torch.Tensor | None = None) -> torch.Tensor:
     """w silu(gate) up for the rows gu [T * k, 2I] (gate, then up; bf16 or fp32), w [T, k] a pair's weight (None: 1).
-    The backward pass sees gate and up in 8 bits (groups of 128, moeq_fp8_quant_rows): half to a quarter of the bytes."""
+    The backward pass sees gate and up in 8 bits (groups of 128, moeq_fp8_quant_rows): half to a quarter of the bytes.
+    Differentiable once: a second derivative raises."""
     if gu.dim() != 2 or gu.shape[0] != d.row_pair.shape[0] or gu.shape[1] % 2:
         raise ValueError(f"swiglu: gu [{d.row_pair.shape[0]}, 2I] is wanted, got {tuple(gu.shape)}")
     if w is not None:
@@ -420,7 +422,7 @@ def expert_mlp(x: torch.Tensor, w: torch.Tensor, w_gu: torch.Tensor, w_d: torch.
     """out[t] = sum_j w[t, j] expert_j(x[t]), expert = down(silu(gate x) * up x): x [T, H] bf16, w [T, k] fp32 as route
     gives it, w_gu [E, 2I, H] (gate rows, then up rows) and w_d [E, H, I] bf16, H and I multiples of 8.  As
     combine(expert_product(swiglu(expert_product(dispatch(x)))), w), with less kept for the backward pass: x [T, H] and
-    the gate and up rows [T * k, 2I] in 8 bits, and nothing else of its size."""
+    the gate and up rows [T * k, 2I] in 8 bits, and nothing else of its size.  Differentiable once, as swiglu is."""
     if x.dim() != 2 or x.shape[0] != d.pair_row.shape[0] or x.dtype is not torch.bfloat16:
         raise ValueError(f"expert_mlp: x [{d.pair_row.shape[0]}, H] bf16 is wanted, got {x.dtype} {tuple(x.shape)}")
     _weights_fit("expert_mlp", w, d)

@@ -20,6 +20,21 @@ from torch.autograd import forward_ad
 from . import moeq
 
 
+_words: dict = {}   # status words that no plan has yet, by the stream that they were zeroed on
+
+
+def _status_word(device: torch.device) -> torch.Tensor:
+    """An int32 [1] that is 0 on the current stream.  Many are zeroed at once: a fill for each would double a plan's time on
+    the host.  Inside a capture the fill belongs to the graph, so that every replay starts with 0."""
+    if device.type != "cuda" or torch.cuda.is_current_stream_capturing():
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    of = device.index, moeq.current_stream_handle()
+    words = _words.get(of)
+    if not words:
+        words = _words[of] = list(torch.zeros(256, dtype=torch.int32, device=device).split(1))
+    return words.pop()
+
+
 class Dispatch:
     """Where each (token, slot) pair goes: rows of expert e are
     offs[e] .. offs[e + 1] - 1; pair_row [T, k] and row_pair [T * k] map
@@ -30,8 +45,8 @@ class Dispatch:
         T, k = topk_id.shape
         new = lambda *s: torch.empty(s, dtype=torch.int32, device=topk_id.device)
         self.E, self.offs, self.pair_row, self.row_pair = E, new(E + 1), new(T, k), new(T * k)
-        self.status = torch.zeros(1, dtype=torch.int32, device=topk_id.device)
         moeq.moeq_expert_sort(topk_id, E, self.offs, self.pair_row, self.row_pair)
+        self.status = _status_word(topk_id.device)
 
     def check(self) -> None:
         """Raises MoeqError where a product with this plan gave up a wait inside its kernel: its results are then not

@@ -94,7 +94,10 @@ def _combine_grad(dout, y, w, offs, pair_row):
 
 def _differentiated(args) -> bool:
     """Whether a result of args may be differentiated again, or one of them has a tangent."""
-    return torch.is_grad_enabled() or any(
+    if torch.is_grad_enabled():
+        return True
+    # (outside a dual_level, the module's level -1, there are no tangents: 1 us a tensor saved)
+    return getattr(forward_ad, "_current_level", 0) >= 0 and any(
         isinstance(t, torch.Tensor) and t.is_floating_point() and forward_ad.unpack_dual(t).tangent is not None for t in args)
 
 

@@ -6,11 +6,11 @@ or a prompt.  ``moeq.moeq_moe_layer`` is its FP8 counterpart for up to 16
 tokens in one kernel.
 
 ``route``, ``dispatch`` and ``combine`` train: the same routing and movement
-as autograd functions, around whatever experts the caller's program has, to any order (in reverse
-mode: a tangent raises).  ``expert_product`` is the product of bf16 experts for
-it, to any order too;
-``swiglu`` and ``expert_mlp`` (the experts between dispatch and combine as one
-function) keep what their backward pass needs in 8 bits.
+as autograd functions, around whatever experts the caller's program has, to any
+order (in reverse mode: a tangent raises).  ``expert_product`` is the product of
+bf16 experts for it, to any order too; ``swiglu`` and ``expert_mlp`` (the experts
+between dispatch and combine as one function) keep what their backward pass
+needs in 8 bits.
 """
 from __future__ import annotations
 
@@ -316,10 +316,11 @@ class _Once(torch.autograd.Function):
         raise RuntimeError("swiglu and expert_mlp keep their inputs in 8 bits: they are differentiable once")
 
 
-def _edge(t):
-    """What stands for t, of which only the 8-bit codes are kept, among the tensors that _once ties gradients to: its
-    place in the graph, and nothing of its memory."""
-    return t[:0].clone() if t.requires_grad else None
+# What was quantised is not kept, and the gradients depend on it: its place in
+# the graph is held by a second output, empty, whose node is the function's own.
+def _mark(ctx, t, keep):
+    ctx.set_materialize_grads(False)   # (the mark's own gradient would be made each time)
+    return t.new_empty(0) if keep else None
 
 
 def _once(grads, *of):
@@ -358,16 +359,19 @@ def _swiglu_grad(dh, codes, scales, w, pair_row, row_pair, need_w, again):
 
 class _Swiglu(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, gu, w, pair_row, row_pair, keep, edge):
+    def forward(ctx, gu, w, pair_row, row_pair, keep):
         h, codes, scales = _swiglu(gu, w, row_pair, keep)
-        ctx.save_for_backward(codes, scales, w, pair_row, row_pair, edge)
-        return h
+        mark = _mark(ctx, gu, keep)
+        ctx.save_for_backward(codes, scales, w, pair_row, row_pair, mark)
+        return h, mark
 
     @staticmethod
-    def backward(ctx, dh):
-        codes, scales, w, pair_row, row_pair, edge = ctx.saved_tensors
+    def backward(ctx, dh, _):
+        codes, scales, w, pair_row, row_pair, mark = ctx.saved_tensors
+        if dh is None:
+            dh = mark.new_zeros((codes.shape[0], codes.shape[1] // 2))
         dgu, dw, _ = _swiglu_grad(_rows(dh), codes, scales, w, pair_row, row_pair, ctx.needs_input_grad[1], False)
-        return (*_once((dgu, dw), dh, w, edge), None, None, None, None)
+        return (*_once((dgu, dw), dh, w, mark), None, None, None)
 
 
 class _ExpertMlp(torch.autograd.Function):
@@ -375,19 +379,22 @@ class _ExpertMlp(torch.autograd.Function):
     nor h is kept, and x and its gate and up rows are in 8 bits."""
 
     @staticmethod
-    def forward(ctx, x, w, w_gu, w_d, offs, pair_row, row_pair, status, keep, edge):
+    def forward(ctx, x, w, w_gu, w_d, offs, pair_row, row_pair, status, keep):
         ctx.status = status
         gu = _product(_gather(x, offs, pair_row), w_gu, offs, status)
         h, codes, scales = _swiglu(gu, w, row_pair, keep)
         del gu
         x8 = _keep8(x) if keep and ctx.needs_input_grad[2] else (None, None)
-        ctx.save_for_backward(*x8, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair, edge)
-        return _gather_grad(_product(h, w_d, offs, status), offs, pair_row)
+        mark = _mark(ctx, x, keep)
+        ctx.save_for_backward(*x8, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair, mark)
+        return _gather_grad(_product(h, w_d, offs, status), offs, pair_row), mark
 
     @staticmethod
-    def backward(ctx, dout):
-        x_codes, x_scales, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair, edge = ctx.saved_tensors
+    def backward(ctx, dout, _):
+        x_codes, x_scales, codes, scales, w, w_gu, w_d, offs, pair_row, row_pair, mark = ctx.saved_tensors
         need_x, need_w, need_gu, need_d = ctx.needs_input_grad[:4]
+        if dout is None:
+            dout = mark.new_zeros((pair_row.shape[0], w_gu.shape[2]))
         with torch.no_grad():
             dy = _gather(_rows(dout), offs, pair_row)
             dh = _product_grad_x(dy, w_d, offs, ctx.status)
@@ -401,7 +408,7 @@ class _ExpertMlp(torch.autograd.Function):
                 xs = torch.empty((dgu.shape[0], w_gu.shape[2]), dtype=dgu.dtype, device=dgu.device)
                 moeq.moeq_fp8_gather_rows(x_codes, x_scales, offs, pair_row, xs)
                 dw_gu = _product_grad_w(dgu, xs, offs, ctx.status)
-        return (*_once((dx, dw, dw_gu, dw_d), dout, w, w_gu, w_d, edge), None, None, None, None, None, None)
+        return (*_once((dx, dw, dw_gu, dw_d), dout, w, w_gu, w_d, mark), None, None, None, None, None)
 
 
 def _experts_fit(what: str, w: torch.Tensor, d: Dispatch, width: int, name: str = "w") -> None:
@@ -433,7 +440,7 @@ def swiglu(gu: torch.Tensor, d: Dispatch, w: torch.Tensor | None = None) -> torc
         _weights_fit("swiglu", w, d)
         w = w.contiguous()
     keep = torch.is_grad_enabled() and (gu.requires_grad or w is not None and w.requires_grad)
-    return _Swiglu.apply(_rows(gu), w, d.pair_row, d.row_pair, keep, _edge(gu))
+    return _Swiglu.apply(_rows(gu), w, d.pair_row, d.row_pair, keep)[0]
 
 
 def expert_mlp(x: torch.Tensor, w: torch.Tensor, w_gu: torch.Tensor, w_d: torch.Tensor, d: Dispatch) -> torch.Tensor:
@@ -451,7 +458,7 @@ def expert_mlp(x: torch.Tensor, w: torch.Tensor, w_gu: torch.Tensor, w_d: torch.
                          f"and {tuple(w_d.shape)}")
     keep = torch.is_grad_enabled() and any(t.requires_grad for t in (x, w, w_gu, w_d))
     return _ExpertMlp.apply(_rows(x), w.contiguous(), _weights(w_gu), _weights(w_d), d.offs, d.pair_row, d.row_pair,
-                            d.status, keep, _edge(x))
+                            d.status, keep)[0]
 
 
 # ------------------------------------------------------------------- serving

@@ -328,3 +328,22 @@ def test_weights_off_16_bytes_are_copied(el, monkeypatch):
     assert torch.equal(out, out2)
     for a, b in zip(torch.autograd.grad(out.float().sum(), args), torch.autograd.grad(out2.float().sum(), moved)):
         assert torch.equal(a, b)
+
+
+def test_no_gradient_of_the_output_is_zero(el):
+    """What follows has no gradient to give: zeros, as ever."""
+    class Nothing(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, t):
+            return t.clone()
+
+        @staticmethod
+        def backward(ctx, _):
+            return None
+    d, _ = _plan(el)
+    g = torch.Generator().manual_seed(10)
+    gu, w = _leaf(g, 18, 48, dt=torch.float32), _leaf(g, 9, 2, dt=torch.float32)
+    tok, *mlp = (_leaf(g, *s, dt=torch.bfloat16) for s in ((9, 16), (4, 48, 16), (4, 16, 24)))
+    for out, leaves in ((el.swiglu(gu, d, w), (gu, w)), (el.expert_mlp(tok, w, *mlp, d), (tok, w, *mlp))):
+        for got, leaf in zip(torch.autograd.grad(Nothing.apply(out).sum(), leaves), leaves):
+            assert got.shape == leaf.shape and got.dtype is leaf.dtype and (got == 0).all()

@@ -318,3 +318,30 @@ def test_weights_in_a_flat_buffer():
     assert torch.equal(out, out2) and torch.equal(got[1:], torch.cat([t.reshape(-1) for t in want])) and got[0] == 0
     xs = el.dispatch(x, d)
     assert torch.equal(el.expert_product(xs, gu, d), el.expert_product(xs, w_gu, d))
+
+
+def test_plans_have_words_of_their_own():
+    """More plans than are zeroed at once, on two streams; and one inside a graph, whose word every replay clears."""
+    from bandwidth_bound_fp8_gb300 import moeq
+    el, lg, *_ = _setup()
+    ids, _ = el.route(lg, 2)
+    E, side = lg.shape[1], torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    plans = [el.Dispatch(ids, E) for _ in range(300)]
+    with torch.cuda.stream(side):
+        plans += [el.Dispatch(ids, E) for _ in range(300)]
+    torch.cuda.synchronize()
+    assert len({d.status.data_ptr() for d in plans}) == len(plans) and all(int(d.status) == 0 for d in plans)
+    plans[7].status.fill_(moeq.MOEQ_ERR_TIMEOUT)
+    plans[6].check(), plans[8].check()
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            d = el.Dispatch(ids, E)
+    graph.replay()
+    d.check()
+    d.status.fill_(moeq.MOEQ_ERR_TIMEOUT)
+    with pytest.raises(moeq.MoeqError):
+        d.check()
+    graph.replay()
+    d.check()
